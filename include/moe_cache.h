@@ -448,6 +448,93 @@ int moe_set_lookahead(moe_ctx *ctx, int enable);
  */
 int moe_set_router(moe_ctx *ctx, int layer, const float *host_w, const float *host_b);
 
+/* Element types of the activations moe_rms_norm reads and sums. */
+#define MOE_F32 0
+#define MOE_F16 1
+#define MOE_BF16 2
+
+/*
+ * Residual addition, root-mean-square norm and int8 output of token rows, the
+ * step between a layer's experts and what reads them next (no counterpart on
+ * the source pages, which time the expert layers alone; the int8 format is the
+ * q8_1 activation quantization of mx-llama.cpp FEATURES.md).  For each row:
+ *   s = x + res (fp32; s = x without res), d_sum = s rounded to dtype,
+ *   y = s * 1/sqrt(mean(s^2) + eps) * weight,
+ *   per block of 32: d = binary16(max|y| / 127), q = clamp(rint(y / d), -127,
+ *   127), q = 0 where d = 0.
+ * The norm is taken of the unrounded s.  The codes are the ones the forwards
+ * make of the same y, and what moe_linear_forward reads as d_q and d_d.
+ * d_x, d_res, d_sum: [n_tokens][width] of dtype (MOE_F32, MOE_F16, MOE_BF16);
+ * d_res and d_sum may be NULL.  d_weight: fp32 [width].  d_y: fp32
+ * [n_tokens][width] or NULL.  d_q, d_d: int8 [n_tokens][width] and binary16
+ * [n_tokens][width/32], both or neither (both need width % 32 == 0).  At
+ * least one output.  Outputs may be the inputs' own buffers (d_sum = d_res, say).  Infinities and NaN spread as
+ * in the formulas over their row (a block whose max|y| is not a number, or
+ * beyond binary16, has a scale that says so).  Asynchronous on `stream` (NULL:
+ * the context's), any stream; capturable.  Rows whose buffers are 16-byte
+ * aligned and whose width is a multiple of 4 take wide loads.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
+ */
+int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
+                 int width, float eps, void *d_sum, float *d_y, int8_t *d_q, uint16_t *d_d, void *stream);
+
+/*
+ * Register a dense layer with 4-bit weights (no counterpart on the source
+ * pages: the projections and the output head next to the experts, in the
+ * experts' block formats).  host_w: canonical blocks [rows][cols/32][18 B]
+ * (MOE_FMT_Q4_0) or super-blocks [rows][cols/256][144 B] (MOE_FMT_Q4_K), any
+ * host memory, copied.  cols: a multiple of 32 (Q4_K: of 256), at most 65536;
+ * rows: at most 2^26.  The context keeps rows x cols x 18 / 32 bytes of device memory
+ * until moe_destroy (twice that while the call runs).  *linear_id receives the
+ * layer's id.  Synchronous.
+ * Errors: MOE_ERR_ARG, MOE_ERR_OOM, MOE_ERR_CUDA.
+ */
+int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int rows, int cols, int *linear_id);
+
+/*
+ * y = W x of a registered dense layer (no counterpart on the source pages;
+ * the block dots and scales of the pointer-table mat-vec of
+ * Zapdev-labs/a6000-custom-kernels): y[t][r] = the sum over blocks of 32 of
+ * the exact int32 block dot times the weight block's and the activation
+ * block's scales, in fp32, as the expert forwards compute it.  The
+ * activations are either d_x, fp32 [n_tokens][cols], quantized in the call as
+ * the forwards quantize theirs, or d_q and d_d, the codes and scales
+ * moe_rms_norm writes; the other pointers are NULL.  d_x and d_q 16-byte
+ * aligned.  d_y: fp32 [n_tokens][rows].  n_tokens <= cfg.max_tokens.
+ * `stream` must be the context's stream (or NULL).  Asynchronous; capturable.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
+ */
+int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8_t *d_q, const uint16_t *d_d,
+                       int n_tokens, float *d_y, void *stream);
+
+/*
+ * Balance and z loss of a layer's router, the picks of every expert and the
+ * gradient of the logits (no counterpart on the source pages, which take
+ * routing frequencies from a file: the counts are that table's input, and a
+ * router tuned for balance or for fewer experts needs the gradient).  With
+ * p = softmax(logits), n the unmasked tokens and c_e the picks of expert e:
+ *   d_loss[0] = balance_coef * E * sum_e c_e/(n k) * mean_t p_te
+ *   d_loss[1] = z_coef * mean_t logsumexp(logits_t)^2
+ *   d_dlogits = gradient of d_loss[0] + d_loss[1] (the counts are constants)
+ *               + that of the routing weights, whose own gradient is d_gw.
+ * d_logits: fp32 [n_tokens][E]; d_idx: int32 [n_tokens][k] as route_topk
+ * writes them (an id out of range is read as expert 0 and reported by the next
+ * cache_step or miss_drain).  d_mask: uint8 [n_tokens] or NULL, 0 leaves a
+ * token out of everything (its gradient row is zero); all out: losses, counts
+ * and gradients are zero.  d_gw: fp32 [n_tokens][k] or NULL; the routing
+ * weights are route_topk's for cfg.renorm_topk.  d_loss: fp32 [2].  d_counts:
+ * int32 [E], written.  d_dlogits: fp32 [n_tokens][E] or NULL; may not be
+ * d_logits.  A logit of -infinity is an expert the token cannot take; a row of
+ * nothing else adds nothing to the losses, its ids still count and its
+ * gradient is zero.  NaN spreads.  The same inputs give the same bits.
+ * E and k: the context's (of all shards).  `stream` must be the context's
+ * stream (or NULL).  Asynchronous; capturable.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
+ */
+int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, const uint8_t *d_mask,
+                    const float *d_gw, int n_tokens, int n_experts, int k, float balance_coef, float z_coef,
+                    float *d_loss, int32_t *d_counts, float *d_dlogits, void *stream);
+
 /*
  * Snapshot of one tensor's cache state (inspection for tests: the table,
  * slots and stamps of Zapdev-labs/a6000-custom-kernels' pointer-table cache;

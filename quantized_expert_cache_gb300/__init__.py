@@ -23,6 +23,7 @@ MOE_OK = 0
 ERRORS = {-1: "MOE_ERR_ARG", -2: "MOE_ERR_OOM", -3: "MOE_ERR_CUDA", -4: "MOE_ERR_NOT_PINNED",
           -5: "MOE_ERR_TIMEOUT", -6: "MOE_ERR_CAPACITY", -7: "MOE_ERR_STATE", -8: "MOE_ERR_FAULT"}
 KIND_GATE, KIND_UP, KIND_DOWN = 0, 1, 2
+F32, F16, BF16 = 0, 1, 2
 FMT_Q4_0, FMT_Q8_0, FMT_Q5_0, FMT_Q4_K, FMT_Q6_K, FMT_Q5_K = 0, 1, 2, 3, 4, 5
 
 
@@ -45,7 +46,7 @@ class moe_stats_t(ctypes.Structure):
 
 
 # Every symbol include/moe_cache.h declares, with (restype, argtypes).
-_vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "moe_layer_init": (_i32, [ctypes.POINTER(moe_cfg), _vp, ctypes.POINTER(_vp)]),
     "register_expert_tensor": (_i32, [_vp, _i32, _i32, _vp, _i32, _i32, _i32, _vp, _i32, ctypes.POINTER(_i32)]),
@@ -66,6 +67,10 @@ SIGNATURES = {
     "moe_set_preheat": (_i32, [_vp, _i32]),
     "moe_pool_snapshot": (_i32, [_vp, _vp, _vp]),
     "moe_cache_reset": (_i32, [_vp, _i32]),
+    "moe_rms_norm": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "moe_linear_register": (_i32, [_vp, _vp, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
+    "moe_linear_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "moe_router_loss": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _f32, _vp, _vp, _vp, _vp]),
     "moe_cache_snapshot": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp]),
     "moe_cache_layout": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp]),
     "moe_stats": (_i32, [_vp, ctypes.POINTER(moe_stats_t)]),
@@ -247,6 +252,52 @@ def moe_pool_snapshot(ctx, n_slots):
     stamps = np.empty(max(1, n_slots), np.uint32)
     _check(ctx, load().moe_pool_snapshot(ctx, _host(owner), _host(stamps)))
     return dict(owner=owner[:n_slots], stamps=stamps[:n_slots])
+
+
+def _dtype(x) -> int:
+    """MOE_F32 / MOE_F16 / MOE_BF16 of a torch tensor (fp32 for an address)."""
+    if isinstance(x, int) or x is None:
+        return F32
+    name = str(x.dtype)
+    if name not in _DTYPES:
+        raise ValueError(f"expected float32, float16 or bfloat16, got {name}")
+    return _DTYPES[name]
+
+
+_DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+
+
+def moe_rms_norm(ctx, x, res, weight, n_tokens, width, eps, sum, y, q=None, d=None, dtype=None, stream=None):
+    """sum = x + res; y = RMS norm of it times weight; q, d = y's int8 codes and
+    scales.  res, sum, y, (q, d) may be None.  dtype: x's by default."""
+    if dtype is None:
+        dtype = _dtype(x)
+        for o in (res, sum):
+            if o is not None and not isinstance(o, int) and _dtype(o) != dtype:
+                raise ValueError("x, res and sum must have one dtype")
+    return _check(ctx, load().moe_rms_norm(ctx, _dev(x), _dev(res), dtype, _dev(weight), n_tokens, width, eps,
+                                           _dev(sum), _dev(y), _dev(q), _dev(d), _stream(stream)))
+
+
+def moe_linear_register(ctx, host_w: np.ndarray, weight_format, rows, cols) -> int:
+    lid = ctypes.c_int()
+    _check(ctx, load().moe_linear_register(ctx, _host(host_w), weight_format, rows, cols, ctypes.byref(lid)))
+    return lid.value
+
+
+def moe_linear_forward(ctx, linear_id, x, n_tokens, y, q=None, d=None, stream=None):
+    """y = W x from fp32 x, or (x None) from the codes q and scales d."""
+    return _check(ctx, load().moe_linear_forward(ctx, linear_id, _dev(x), _dev(q), _dev(d), n_tokens, _dev(y),
+                                                 _stream(stream)))
+
+
+def moe_router_loss(ctx, logits, idx, mask, gw, n_tokens, n_experts, k, balance_coef, z_coef, loss, counts,
+                    dlogits=None, stream=None):
+    """Balance and z loss, picks per expert and the logits' gradient; mask, gw
+    and dlogits may be None."""
+    return _check(ctx, load().moe_router_loss(ctx, _dev(logits), _dev(idx), _dev(mask), _dev(gw), n_tokens, n_experts,
+                                              k, balance_coef, z_coef, _dev(loss), _dev(counts), _dev(dlogits),
+                                              _stream(stream)))
 
 
 def moe_cache_snapshot(ctx, tensor_id, n_experts, slots_per_tensor):

@@ -151,6 +151,55 @@ struct Update {
     uint64_t value;
 };
 
+// Residual addition, RMS norm and int8 output (kernels_norm.cu).
+struct NormParams {
+    const void *x, *res;        // [n_tokens][width] of dtype; res may be null
+    void *sum;                  // [n_tokens][width] of dtype, or null
+    const float *weight;        // [width]
+    float *y;                   // [n_tokens][width], or null
+    int8_t *q;                  // [n_tokens][width], or null (width % 32 == 0)
+    __half *d;                  // [n_tokens][width / 32] with q
+    int dtype;                  // 0 fp32, 1 binary16, 2 bfloat16
+    int n_tokens, width;
+    float eps;
+};
+
+// Router balance and z loss with the logits' gradient (kernels_router.cu).
+constexpr int kRouterMaxExperts = 4096;
+constexpr int kRouterParts = 1024;  // CTAs of the loss kernel at most
+struct RouterParams {
+    const float *logits;        // [T][E]
+    const int32_t *idx;         // [T][k]
+    const uint8_t *mask;        // [T] or null: 0 leaves the token out
+    const float *gw;            // [T][k] or null: gradient of the routing weights
+    float *loss;                // [2]
+    int32_t *counts;            // [E]
+    float *dlogits;             // [T][E] or null
+    int32_t *ws_count;          // [E + 1], zero between launches
+    int32_t *n_valid;           // [1]
+    unsigned *ticket;           // [1], zero between launches
+    double *ws_part;            // [kRouterParts][2]
+    int *error;                 // bit 0: an id out of range
+    int T, E, k, renorm;
+    float balance, zcoef;
+};
+
+// Dense layer with 4-bit weights (kernels_linear.cu).
+constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
+constexpr int kLinearMaxSmem = 160 * 1024;
+struct LinearParams {
+    const uint8_t *w;           // planes: codes [rows][cols / 32][16], then 2 scale bytes a block
+    const float *x;             // [n_tokens][cols], or null and the codes below
+    const int8_t *q;            // [n_tokens][cols]
+    const __half *d;            // [n_tokens][cols / 32]
+    float *y;                   // [n_tokens][rows]
+    int fmt, rows, cols, n_tokens;
+};
+
+int launch_rms_norm(const NormParams &p, cudaStream_t st);
+int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st);
+int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, size_t nblk, int n_sm, cudaStream_t st);
+int launch_linear(const LinearParams &p, int n_sm, cudaStream_t st);
 int launch_topk(const float *logits, int T, int E, int k, int renorm, int32_t *idx, float *w, cudaStream_t st);
 int launch_quantize(const float *x, int n_blocks, int8_t *q, BlockScale *ds, int n_sm, cudaStream_t st);
 int launch_plan(const PlanParams &p, cudaStream_t st);

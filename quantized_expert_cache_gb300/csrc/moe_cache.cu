@@ -147,6 +147,14 @@ struct moe_ctx {
     // prefill preheat: assignments per (layer, expert) routed while slots are lent
     bool preheat = false;
     uint32_t *d_use = nullptr;
+    // dense 4-bit layers (moe_linear_register), by id
+    struct Linear {
+        int fmt, rows, cols;
+        uint8_t *w;  // device planes
+    };
+    std::vector<Linear> linears;
+    // router loss workspace: picks per expert [4097], tokens, ticket, loss parts
+    uint8_t *router_ws = nullptr;
     moe_stats_t stats{};
     int last_T = -1;
     int fail_nth = 0;
@@ -207,6 +215,11 @@ void set_entry(moe_ctx *c, int tid, int e, uint64_t entry, int32_t slot) {
     push_upd(c, 0, (size_t)tid * c->Et + e, entry);
     push_upd(c, 1, (size_t)tid * c->Et + e, (uint64_t)(int64_t)stamp_index(c, tid, slot));
 }
+
+// Router loss workspace: [loss parts][picks per expert + unmasked tokens][n_valid][ticket]
+constexpr size_t kRouterCountOff = sizeof(double) * 2 * moe::kRouterParts;
+constexpr size_t kRouterTailOff = kRouterCountOff + sizeof(int32_t) * (moe::kRouterMaxExperts + 4);
+constexpr size_t kRouterWsBytes = kRouterTailOff + 16;
 
 constexpr size_t kStepKeys = 256;  // miss keys read back with the hit bitmap
 
@@ -630,6 +643,8 @@ int moe_layer_init(const moe_cfg *cfg, void *cuda_stream, moe_ctx **out) {
         }
     }
 
+    CKI(cudaMalloc(&ctx->router_ws, kRouterWsBytes));
+    CKI(cudaMemset(ctx->router_ws, 0, kRouterWsBytes));
     CKI(cudaHostAlloc(&ctx->h_stamps, sizeof(uint32_t) * (size_t)nt * std::max(1, ctx->spt), cudaHostAllocDefault));
     ctx->upd_cap = 6 * nt * E + 64;
     CKI(cudaHostAlloc(&ctx->h_upd, sizeof(Update) * (size_t)ctx->upd_cap, cudaHostAllocMapped));
@@ -1777,6 +1792,8 @@ void moe_destroy(moe_ctx *ctx) {
     cudaFree(ctx->d_prcount);
     cudaFree(ctx->d_prset);
     cudaFree(ctx->d_prstats);
+    cudaFree(ctx->router_ws);
+    for (auto &l : ctx->linears) cudaFree(l.w);
     cudaFree(ctx->stage_jobs);
     cudaFree(ctx->stage_n);
     for (int b = 0; b < 2; ++b) {
@@ -1796,6 +1813,124 @@ void moe_destroy(moe_ctx *ctx) {
     if (ctx->up) cudaStreamDestroy(ctx->up);
     for (cudaEvent_t e : ctx->ev_layer_up) cudaEventDestroy(e);
     delete ctx;
+}
+
+int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
+                 int width, float eps, void *d_sum, float *d_y, int8_t *d_q, uint16_t *d_d, void *stream) {
+    if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
+    if (dtype != MOE_F32 && dtype != MOE_F16 && dtype != MOE_BF16)
+        return fail(ctx, MOE_ERR_ARG, "rms_norm: dtype must be MOE_F32, MOE_F16 or MOE_BF16");
+    if (n_tokens < 0 || width < 1 || !(eps >= 0.0f))
+        return fail(ctx, MOE_ERR_ARG, "rms_norm: need n_tokens >= 0, width >= 1, eps >= 0");
+    if (!d_q != !d_d) return fail(ctx, MOE_ERR_ARG, "rms_norm: codes and scales come together");
+    if (d_q && width % 32) return fail(ctx, MOE_ERR_ARG, "rms_norm: codes need a width that is a multiple of 32");
+    if (n_tokens == 0) return MOE_OK;
+    if (!d_x || !d_weight || (!d_sum && !d_y && !d_q)) return fail(ctx, MOE_ERR_ARG, "rms_norm: null pointer");
+    moe::NormParams p{};
+    p.x = d_x;
+    p.res = d_res;
+    p.sum = d_sum;
+    p.weight = d_weight;
+    p.y = d_y;
+    p.q = d_q;
+    p.d = (__half *)d_d;
+    p.dtype = dtype;
+    p.n_tokens = n_tokens;
+    p.width = width;
+    p.eps = eps;
+    const int rc = moe::launch_rms_norm(p, stream ? (cudaStream_t)stream : ctx->stream);
+    if (rc) return fail(ctx, MOE_ERR_CUDA, std::string("rms_norm launch: ") + cudaGetErrorString((cudaError_t)rc));
+    return MOE_OK;
+}
+
+int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int rows, int cols, int *linear_id) {
+    if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
+    if (weight_format != MOE_FMT_Q4_0 && weight_format != MOE_FMT_Q4_K)
+        return fail(ctx, MOE_ERR_ARG, "linear: weight_format must be Q4_0 or Q4_K");
+    if (!host_w || !linear_id || rows < 1 || rows > moe::kLinearMaxRows || cols < 32 || cols % (weight_format == MOE_FMT_Q4_K ? 256 : 32) ||
+        cols > moe::kLinearMaxCols)
+        return fail(ctx, MOE_ERR_ARG, "linear: need host_w, linear_id, 1 <= rows <= 2^26, cols % 32 (Q4_K: 256) == 0, cols <= " +
+                                          std::to_string(moe::kLinearMaxCols));
+    CK(cudaSetDevice(ctx->dev));
+    const size_t nblk = (size_t)rows * (cols / 32), bytes = nblk * 18;
+    uint8_t *src = nullptr, *w = nullptr;
+    cudaError_t e = cudaMalloc(&w, bytes);
+    if (e == cudaSuccess) e = cudaMalloc(&src, bytes);
+    if (e == cudaSuccess) e = cudaMemcpy(src, host_w, bytes, cudaMemcpyHostToDevice);
+    const int fmt = weight_format == MOE_FMT_Q4_K ? moe::kFmtQ4K : moe::kFmtQ4;
+    if (e == cudaSuccess) e = (cudaError_t)moe::launch_linear_repack(src, w, fmt, nblk, ctx->n_sm, ctx->stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->stream);
+    cudaFree(src);
+    if (e != cudaSuccess) {
+        cudaFree(w);
+        return fail(ctx, e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA,
+                    std::string("linear upload: ") + cudaGetErrorString(e));
+    }
+    ctx->linears.push_back({fmt, rows, cols, w});
+    *linear_id = (int)ctx->linears.size() - 1;
+    return MOE_OK;
+}
+
+int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8_t *d_q, const uint16_t *d_d,
+                       int n_tokens, float *d_y, void *stream) {
+    if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
+    if (linear_id < 0 || linear_id >= (int)ctx->linears.size() || n_tokens < 0 || n_tokens > ctx->M)
+        return fail(ctx, MOE_ERR_ARG, "linear: bad id or n_tokens (> max_tokens?)");
+    if (stream && (cudaStream_t)stream != ctx->stream)
+        return fail(ctx, MOE_ERR_ARG, "linear: stream must be the context stream");
+    if (n_tokens == 0) return MOE_OK;
+    if (!d_y || (d_x ? (d_q || d_d) : (!d_q || !d_d)))
+        return fail(ctx, MOE_ERR_ARG, "linear: need d_y and either d_x or d_q with d_d");
+    if (((uintptr_t)d_x & 15) || ((uintptr_t)d_q & 15) || ((uintptr_t)d_d & 1) || ((uintptr_t)d_y & 3))
+        return fail(ctx, MOE_ERR_ARG, "linear: d_x and d_q must be 16-byte aligned");
+    const auto &l = ctx->linears[linear_id];
+    moe::LinearParams p{};
+    p.w = l.w;
+    p.x = d_x;
+    p.q = d_q;
+    p.d = (const __half *)d_d;
+    p.y = d_y;
+    p.fmt = l.fmt;
+    p.rows = l.rows;
+    p.cols = l.cols;
+    p.n_tokens = n_tokens;
+    const int rc = moe::launch_linear(p, ctx->n_sm, ctx->stream);
+    if (rc) return fail(ctx, MOE_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString((cudaError_t)rc));
+    return MOE_OK;
+}
+
+int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, const uint8_t *d_mask,
+                    const float *d_gw, int n_tokens, int n_experts, int k, float balance_coef, float z_coef,
+                    float *d_loss, int32_t *d_counts, float *d_dlogits, void *stream) {
+    if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
+    if (n_tokens < 0 || n_experts != ctx->E_route || k != ctx->k)
+        return fail(ctx, MOE_ERR_ARG, "router_loss: n_experts and k must be the context's");
+    if (stream && (cudaStream_t)stream != ctx->stream)
+        return fail(ctx, MOE_ERR_ARG, "router_loss: stream must be the context stream");
+    if (!d_loss || !d_counts || (n_tokens > 0 && (!d_logits || !d_idx)) || (d_dlogits && d_dlogits == d_logits))
+        return fail(ctx, MOE_ERR_ARG, "router_loss: null pointer, or d_dlogits is d_logits");
+    moe::RouterParams p{};
+    p.logits = d_logits;
+    p.idx = d_idx;
+    p.mask = d_mask;
+    p.gw = d_gw;
+    p.loss = d_loss;
+    p.counts = d_counts;
+    p.dlogits = d_dlogits;
+    p.ws_part = (double *)ctx->router_ws;
+    p.ws_count = (int32_t *)(ctx->router_ws + kRouterCountOff);
+    p.n_valid = (int32_t *)(ctx->router_ws + kRouterTailOff);
+    p.ticket = (unsigned *)(ctx->router_ws + kRouterTailOff + 4);
+    p.error = ctx->d_error;
+    p.T = n_tokens;
+    p.E = n_experts;
+    p.k = k;
+    p.renorm = ctx->cfg.renorm_topk;
+    p.balance = balance_coef;
+    p.zcoef = z_coef;
+    const int rc = moe::launch_router_loss(p, ctx->n_sm, ctx->stream);
+    if (rc) return fail(ctx, MOE_ERR_CUDA, std::string("router_loss launch: ") + cudaGetErrorString((cudaError_t)rc));
+    return MOE_OK;
 }
 
 int moe_debug_block_dots(moe_ctx *ctx, int tensor_id, int expert, int row0, int n_rows, const int8_t *d_qa,
