@@ -165,7 +165,6 @@ struct NormParams {
 };
 
 // Router balance and z loss with the logits' gradient (kernels_router.cu).
-constexpr int kRouterMaxExperts = 4096;
 constexpr int kRouterParts = 1024;  // CTAs of the loss kernel at most
 struct RouterParams {
     const float *logits;        // [T][E]
@@ -175,10 +174,9 @@ struct RouterParams {
     float *loss;                // [2]
     int32_t *counts;            // [E]
     float *dlogits;             // [T][E] or null
-    int32_t *ws_count;          // [E + 1], zero between launches
     int32_t *n_valid;           // [1]
-    unsigned *ticket;           // [1], zero between launches
-    double *ws_part;            // [kRouterParts][2]
+    unsigned *ticket;           // [2], zero between launches
+    float *ws_part;             // [kRouterParts][2]
     int *error;                 // bit 0: an id out of range
     int T, E, k, renorm;
     float balance, zcoef;
@@ -197,6 +195,7 @@ struct LinearParams {
 };
 
 int launch_rms_norm(const NormParams &p, cudaStream_t st);
+int router_configure();
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st);
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, size_t nblk, int n_sm, cudaStream_t st);
 int launch_linear(const LinearParams &p, int n_sm, cudaStream_t st);

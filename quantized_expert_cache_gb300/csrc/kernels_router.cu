@@ -12,9 +12,12 @@
 //           p_te (sum_j [idx_tj = e] g_tj - sum_j g_tj p_t,idx_tj))
 // The loss needs only the scalars f . p_t and lse_t that the gradient needs
 // too, so the logits are read once and no E-wide sum over tokens is kept.
-// Counts are integers (their atomics commute exactly); the loss is summed in
-// binary64, per-CTA parts in CTA order: results do not vary from run to run.
+// Counts are integers (their atomics commute exactly); the loss is summed
+// in an order that only the grid size sets: results do not vary from run to run.
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -23,7 +26,16 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr size_t kCountInLoss = 4096;
 constexpr float kNegInf = -__builtin_inff();
+
+// exp(x) for x <= 0 as 2^(x log2 e) by the special-function unit: 2 ulp and
+// |x| 2^-24 of the result, results below 2^-126 are 0.
+__device__ __forceinline__ float exp_neg(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
 
 // An id outside [0, E) is read as expert 0 and reported, as in the forwards.
 __device__ __forceinline__ int checked_id(int e, int E, int *error) {
@@ -34,102 +46,190 @@ __device__ __forceinline__ int checked_id(int e, int E, int *error) {
     return e;
 }
 
-// Picks per expert and unmasked tokens, into counters that are zero between
-// launches; the last CTA publishes them and clears the counters.
-__global__ void __launch_bounds__(kThreads) router_count_kernel(RouterParams p) {
+// Picks of the tokens first, first + step, ... (one a thread) into hist[E]
+// and, at hist[E], the unmasked ones.  A token's picks come by descending
+// logit, so each lane starts at another of them: with one order for all, the
+// warp's atomics would all meet at the popular experts.  Ends with the CTA
+// synchronised.
+__device__ __forceinline__ void count_picks(const RouterParams &p, int *hist, int first, int step) {
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    const int k = p.k;
+    int valid = 0;
+    for (size_t t = first; t < (size_t)p.T; t += step) {
+        const bool on = !p.mask || p.mask[t];
+        const int32_t *id = p.idx + t * k;
+        int j = (int)(t % (unsigned)k);
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            int e[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                e[u] = j0 + u < k ? id[j] : 0;
+                if (++j >= k) j = 0;
+            }
+            if (on)
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (j0 + u < k) atomicAdd(&hist[checked_id(e[u], p.E, p.error)], 1);
+        }
+        valid += on;
+    }
+    valid = __reduce_add_sync(0xffffffffu, valid);
+    if ((threadIdx.x & 31) == 0 && valid) atomicAdd(&hist[p.E], valid);
+    __syncthreads();
+}
+
+// Picks per expert of a long batch: one cluster of kCountCtas CTAs, each with
+// the histogram of its share in shared memory; the CTAs then sum a share of
+// the experts each over the cluster's histograms.
+constexpr int kCountCtas = 16, kCountThreads = 1024;
+__global__ void __launch_bounds__(kCountThreads) router_count_kernel(RouterParams p) {
     extern __shared__ int hist[];
-    __shared__ int last;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int E = p.E, k = p.k;
-    for (int e = threadIdx.x; e <= E; e += kThreads) hist[e] = 0;
-    __syncthreads();
-    const size_t n = (size_t)p.T * k;
-    for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kThreads) {
-        const size_t t = i / k;
-        if (p.mask && !p.mask[t]) continue;
-        atomicAdd(&hist[checked_id(p.idx[i], E, p.error)], 1);
-        if (i == t * k) atomicAdd(&hist[E], 1);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += kThreads)
-        if (hist[e]) atomicAdd(&p.ws_count[e], hist[e]);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    for (int e = threadIdx.x; e <= E; e += kThreads) {
-        const int c = __ldcg(&p.ws_count[e]);
-        p.ws_count[e] = 0;
-        if (e < E)
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int rank = (int)cluster.block_rank();
+    count_picks(p, hist, rank * kCountThreads + threadIdx.x, kCountCtas * kCountThreads);
+    cluster.sync();
+    for (int e = rank * kCountThreads + threadIdx.x; e <= p.E; e += kCountCtas * kCountThreads) {
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < kCountCtas; ++r) c += *cluster.map_shared_rank(hist + e, r);
+        if (e < p.E)
             p.counts[e] = c;
         else
             *p.n_valid = c;
     }
-    if (threadIdx.x == 0) *p.ticket = 0;
+    cluster.sync();  // no CTA leaves while its histogram is read
 }
 
-// One warp a row, ITEMS packs of VEC logits a lane.
-template <int VEC, int ITEMS>
-__global__ void __launch_bounds__(kThreads) router_loss_kernel(RouterParams p) {
-    extern __shared__ float f[];
-    __shared__ double part[2][kThreads / 32];
-    __shared__ int last;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+// One warp a row, ITEMS packs of VEC logits a lane.  COUNT: a short batch, every CTA counts all
+// picks itself (CTA 0 writes them) and no other kernel runs.
+template <int VEC, int ITEMS, bool COUNT>
+__global__ void __launch_bounds__(kThreads, VEC * ITEMS <= 16 ? 4 : 1) router_loss_kernel(RouterParams p) {
+    extern __shared__ __align__(16) float f[];
+    __shared__ float part[2][kThreads / 32];
     const int E = p.E, k = p.k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n_valid = __ldcg(p.n_valid);
-    const float inv_n = n_valid > 0 ? 1.0f / (float)n_valid : 0.0f, inv_nk = inv_n / (float)k;
-    for (int e = threadIdx.x; e < E; e += kThreads) f[e] = (float)__ldcg(&p.counts[e]) * inv_nk;
-    __syncthreads();
-    const float cb = p.balance * (float)E * inv_n, cz = 2.0f * p.zcoef * inv_n;
-    double bal = 0.0, zz = 0.0;
     struct alignas(4 * VEC) Pack {
         float v[VEC];
     };
+    using LoadT = typename std::conditional<VEC == 4, float4, float>::type;
     const int nv = E / VEC;
-    for (size_t t = (size_t)blockIdx.x * (kThreads / 32) + warp; t < (size_t)p.T;
-         t += (size_t)gridDim.x * (kThreads / 32)) {
-        const Pack *zr = (const Pack *)(p.logits + t * E);
-        Pack *dr = p.dlogits ? (Pack *)(p.dlogits + t * E) : nullptr;
-        const bool on = !p.mask || p.mask[t];
+    const size_t step = (size_t)gridDim.x * (kThreads / 32);
+    size_t t = (size_t)blockIdx.x * (kThreads / 32) + warp;
+    // A row's logits, and for lane j < k its pick j with the weight's gradient
+    // and logit.  What a row's loads depend on (its mask, its picks) is
+    // requested a row ahead (meta), the row itself (rows of up to 16 values a
+    // lane) while the one before it is worked on.  All through L2: the first
+    // rows are read before this grid's dependency wait, when L1 may still hold
+    // an earlier launch's lines.
+    constexpr bool kAhead = VEC * ITEMS <= 16;
+    struct Meta {
+        bool on;
+        int e;
+        float g;
+    };
+    struct Row {
         Pack z[ITEMS];
+        Meta m;
+        float zs;
+    };
+    auto meta = [&](size_t row) {
+        Meta m{row < (size_t)p.T, -1, 0.0f};
+        if (!m.on) return m;
+        if (p.gw && lane < k) {
+            m.e = __ldcg(p.idx + row * k + lane);
+            m.g = __ldcg(p.gw + row * k + lane);
+        }
+        if (p.mask) m.on = __ldcg(p.mask + row) != 0;
+        return m;
+    };
+    auto fetch = [&](Row &r, const Meta &m, size_t row) {
+        r.m = m;
+        r.zs = 0.0f;
+        if (!m.on) return;
+        const LoadT *zr = (const LoadT *)(p.logits + row * E);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int v = lane + 32 * i;
+            if (v < nv)
+                *(LoadT *)&r.z[i] = __ldcg(zr + v);
+            else
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) r.z[i].v[j] = kNegInf;
+        }
+        if (p.gw && lane < k) {
+            r.m.e = checked_id(m.e, E, p.error);
+            r.zs = __ldcg(p.logits + row * E + r.m.e);
+        }
+    };
+    Row cur;
+    Meta ahead;
+    auto start = [&]() {
+        const Meta m = meta(t);
+        ahead = meta(t + step);
+        fetch(cur, m, t);
+    };
+    int n_valid;
+    if (COUNT) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
+        start();
+        int *hist = (int *)f;
+        count_picks(p, hist, threadIdx.x, kThreads);
+        n_valid = hist[E];
+        const float inv_nk = n_valid > 0 ? 1.0f / ((float)n_valid * (float)k) : 0.0f;
+        for (int i = threadIdx.x; i < E; i += kThreads) {
+            const int c = hist[i];
+            if (blockIdx.x == 0) p.counts[i] = c;
+            f[i] = (float)c * inv_nk;
+        }
+    } else {
+        // the counting kernel lets this grid start once its own wait is over,
+        // so what earlier work wrote is visible here; its counts are not yet
+        start();
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
+        n_valid = __ldcg(p.n_valid);
+        const float inv_nk = n_valid > 0 ? 1.0f / ((float)n_valid * (float)k) : 0.0f;
+        for (int i = threadIdx.x; i < E; i += kThreads) f[i] = (float)__ldcg(&p.counts[i]) * inv_nk;
+    }
+    __syncthreads();
+    const float inv_n = n_valid > 0 ? 1.0f / (float)n_valid : 0.0f;
+    const float cb = p.balance * (float)E * inv_n, cz = 2.0f * p.zcoef * inv_n;
+    float bal = 0.0f, zz = 0.0f;
+    // One row: its loss terms and its gradient.
+    auto work = [&](Row &r, size_t t) {
+        Pack(&z)[ITEMS] = r.z;
+        const bool on = r.m.on;
+        const int e = r.m.e;
+        const float g = r.m.g, zs = r.zs;
+        Pack *dr = p.dlogits ? (Pack *)(p.dlogits + t * E) : nullptr;
         float top = kNegInf;
+        bool empty = !on;
         if (on) {
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                const int v = lane + 32 * i;
-                if (v < nv)
-                    z[i] = zr[v];
-                else
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) z[i].v[j] = kNegInf;
-            }
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) top = fmaxf(top, z[i].v[j]);
             top = warp_max(top);
-        }
-        bool empty = !on;
-        if (on && top == kNegInf) {
-            // every logit -inf: no expert left.  (A row of NaN has no maximum
-            // either, but stays NaN.)
-            bool nan = false;
+            if (top == kNegInf) {
+                // every logit -inf: no expert left.  (A row of NaN has no
+                // maximum either, but stays NaN.)
+                bool nan = false;
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
+                for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) nan |= z[i].v[j] != z[i].v[j];
-            empty = !__any_sync(0xffffffffu, nan);
+                    for (int j = 0; j < VEC; ++j) nan |= z[i].v[j] != z[i].v[j];
+                empty = !__any_sync(0xffffffffu, nan);
+            }
         }
         if (empty) {
             // masked, or no expert left: nothing to add, a zero gradient
             if (dr) {
                 for (int v = lane; v < nv; v += 32) dr[v] = Pack{};
             }
-            continue;
+            return;
         }
         float tot = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -139,43 +239,45 @@ __global__ void __launch_bounds__(kThreads) router_loss_kernel(RouterParams p) {
                 const Pack fe = *((const Pack *)f + v);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    z[i].v[j] = expf(z[i].v[j] - top);
+                    z[i].v[j] = exp_neg(z[i].v[j] - top);
                     tot += z[i].v[j];
                     dot = fmaf(z[i].v[j], fe.v[j], dot);
                 }
             }
         }
-        tot = warp_sum_f(tot);
-        const float inv = 1.0f / tot;
-        dot = warp_sum_f(dot) * inv;
-        const float lse = top + logf(tot);
-        if (lane == 0) {
-            bal += dot;
-            zz += (double)lse * lse;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            tot += __shfl_xor_sync(0xffffffffu, tot, o);
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        if (!dr) continue;
-        // gradient of the routing weights: lane j < k holds pick j
-        float g = 0.0f, all = 0.0f, zs = 0.0f;
-        int e = -1;
+        const float inv = __frcp_rn(tot);
+        dot *= inv;
+        const float lse = top + logf(tot);
+        bal += dot;
+        zz = fmaf(lse, lse, zz);
+        if (!dr) return;
+        // gradient of the routing weights
+        float own = 0.0f, all = 0.0f;
         if (p.gw) {
-            if (lane < k) {
-                e = checked_id(p.idx[t * k + lane], E, p.error);
-                zs = p.logits[t * E + e];
-                g = p.gw[t * k + lane];
-            }
             if (p.renorm) {
                 const float ts = warp_max(lane < k ? zs : kNegInf);
-                float w = lane < k && ts != kNegInf ? expf(zs - ts) : 0.0f;
-                const float sw = warp_sum_f(w);
-                w = sw > 0.0f ? w / sw : 0.0f;
-                g = w * (g - warp_sum_f(w * g));
+                float w = lane < k && ts != kNegInf ? exp_neg(zs - ts) : 0.0f;
+                float sw = w, swg = w * g;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    sw += __shfl_xor_sync(0xffffffffu, sw, o);
+                    swg += __shfl_xor_sync(0xffffffffu, swg, o);
+                }
+                const float is = sw != 0.0f ? __frcp_rn(sw) : 0.0f;
+                w *= is;
+                own = w * (g - swg * is);
             } else {
-                const float ps = lane < k ? expf(zs - top) * inv : 0.0f;
-                g *= ps;
-                all = warp_sum_f(g);
+                own = lane < k ? g * (exp_neg(zs - top) * inv) : 0.0f;
+                all = warp_sum_f(own);
             }
         }
-        const float base = cz * lse - cb * dot - all;
+        // dz = e^(z - top) (ci f + bi)
+        const float ci = cb * inv, bi = (cz * lse - cb * dot - all) * inv;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int v = lane + 32 * i;
@@ -183,90 +285,131 @@ __global__ void __launch_bounds__(kThreads) router_loss_kernel(RouterParams p) {
                 const Pack fe = *((const Pack *)f + v);
                 Pack o;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) o.v[j] = z[i].v[j] * inv * fmaf(cb, fe.v[j], base);
+                for (int j = 0; j < VEC; ++j) o.v[j] = z[i].v[j] * fmaf(ci, fe.v[j], bi);
                 dr[v] = o;
             }
         }
         if (p.gw) {
             // the picks' elements are written again with their own term (the
             // same element from every lane that holds it)
-            float add = 0.0f;
-            for (int j = 0; j < k; ++j) {
-                const float gj = __shfl_sync(0xffffffffu, g, j);
-                if (__shfl_sync(0xffffffffu, e, j) == e) add += gj;
+            const unsigned same = __match_any_sync(0xffffffffu, lane < k ? e : -1 - lane);
+            float add = own;
+            if (__any_sync(0xffffffffu, same & (same - 1))) {
+                // an id given twice (route_topk writes none)
+                add = 0.0f;
+                for (int j = 0; j < k; ++j) {
+                    const float gj = __shfl_sync(0xffffffffu, own, j);
+                    if (same >> j & 1) add += gj;
+                }
             }
             __syncwarp();
-            if (lane < k) p.dlogits[t * E + e] = expf(zs - top) * inv * fmaf(cb, f[e], base) + add;
+            if (lane < k) p.dlogits[t * E + e] = fmaf(exp_neg(zs - top), fmaf(ci, f[e], bi), add);
         }
+    };
+    // (two buffers in turn: the unrolled loop copies no row)
+    Row next;
+    auto turn = [&](Row &now, Row &then) {
+        const Meta m = ahead;
+        const size_t row = t;
+        t += step;
+        const bool more = t < (size_t)p.T;
+        if (more) ahead = meta(t + step);
+        if (kAhead && more) fetch(then, m, t);
+        work(now, row);
+        if (!kAhead && more) fetch(now, m, t);
+        return more;
+    };
+    if (t < (size_t)p.T) {
+        if constexpr (kAhead)
+            while (turn(cur, next) && turn(next, cur)) {
+            }
+        else
+            while (turn(cur, cur)) {
+            }
     }
     if (lane == 0) {
         part[0][warp] = bal;
         part[1][warp] = zz;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double b = 0.0, z = 0.0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            b += part[0][w];
-            z += part[1][w];
-        }
-        p.ws_part[2 * blockIdx.x] = b;
-        p.ws_part[2 * blockIdx.x + 1] = z;
-        __threadfence();
-        last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-        if (last) {
+    // the CTA's parts, then (the last CTA) all CTAs': warp 0 the balance parts,
+    // warp 1 the z parts, in an order that only the grid size sets
+    if (warp >= 2) return;
+    float sum = lane < kThreads / 32 ? part[warp][lane] : 0.0f;
+    sum = warp_sum_f(sum);
+    if (gridDim.x > 1) {
+        int last = 0;
+        if (lane == 0) {
+            p.ws_part[2 * blockIdx.x + warp] = sum;
             __threadfence();
-            b = z = 0.0;
-            for (unsigned c = 0; c < gridDim.x; ++c) {
-                b += __ldcg(&p.ws_part[2 * c]);
-                z += __ldcg(&p.ws_part[2 * c + 1]);
-            }
-            const double n = n_valid > 0 ? (double)n_valid : 1.0;
-            p.loss[0] = (float)((double)p.balance * E * b / n);
-            p.loss[1] = (float)((double)p.zcoef * z / n);
-            *p.ticket = 0;
+            last = atomicAdd(p.ticket + warp, 1u) == gridDim.x - 1;
+            __threadfence();
         }
+        if (!__shfl_sync(0xffffffffu, last, 0)) return;
+        sum = 0.0f;
+#pragma unroll 8
+        for (unsigned c = lane; c < gridDim.x; c += 32) sum += __ldcg(&p.ws_part[2 * c + warp]);
+        sum = warp_sum_f(sum);
+    }
+    if (lane == 0) {
+        const float n = n_valid > 0 ? (float)n_valid : 1.0f;
+        p.loss[warp] = (warp ? p.zcoef : p.balance * (float)E) * sum / n;
+        p.ticket[warp] = 0;
     }
 }
 
 template <typename K>
-int launch_pdl(K kernel, unsigned grid, size_t smem, const RouterParams &p, cudaStream_t st) {
+int launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, const RouterParams &p, cudaStream_t st,
+               unsigned cluster = 1) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {cluster, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return (int)cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool COUNT>
+int launch_loss(const RouterParams &p, int n_sm, cudaStream_t st) {
+    const size_t rows = kThreads / 32;
+    const unsigned g = (unsigned)std::min<size_t>(((size_t)p.T + rows - 1) / rows + (p.T == 0),
+                                                  (size_t)std::min(n_sm * 4, kRouterParts));
+    const size_t sm = (size_t)(p.E + 1) * 4;
+    const auto a16 = [](const void *q) { return ((uintptr_t)q & 15) == 0; };
+    if (p.E % 4 == 0 && a16(p.logits) && a16(p.dlogits)) {
+        const int nv = p.E / 4;
+        if (nv <= 32) return launch_pdl(router_loss_kernel<4, 1, COUNT>, g, kThreads, sm, p, st);
+        if (nv <= 64) return launch_pdl(router_loss_kernel<4, 2, COUNT>, g, kThreads, sm, p, st);
+        if (nv <= 128) return launch_pdl(router_loss_kernel<4, 4, COUNT>, g, kThreads, sm, p, st);
+        if (nv <= 256) return launch_pdl(router_loss_kernel<4, 8, COUNT>, g, kThreads, sm, p, st);
+        return launch_pdl(router_loss_kernel<4, 32, COUNT>, g, kThreads, sm, p, st);
+    }
+    if (p.E <= 64) return launch_pdl(router_loss_kernel<1, 2, COUNT>, g, kThreads, sm, p, st);
+    if (p.E <= 256) return launch_pdl(router_loss_kernel<1, 8, COUNT>, g, kThreads, sm, p, st);
+    if (p.E <= 512) return launch_pdl(router_loss_kernel<1, 16, COUNT>, g, kThreads, sm, p, st);
+    if (p.E <= 1024) return launch_pdl(router_loss_kernel<1, 32, COUNT>, g, kThreads, sm, p, st);
+    return launch_pdl(router_loss_kernel<1, 128, COUNT>, g, kThreads, sm, p, st);
 }
 
 }  // namespace
 
+// Once per device: a cluster of more than 8 CTAs has to be asked for.
+int router_configure() {
+    return (int)cudaFuncSetAttribute(router_count_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st) {
-    const size_t ids = (size_t)p.T * p.k;
-    const unsigned gc = (unsigned)std::min<size_t>((ids + kThreads - 1) / kThreads + (ids == 0), (size_t)n_sm);
-    int rc = launch_pdl(router_count_kernel, gc, (size_t)(p.E + 1) * 4, p, st);
-    if (rc) return rc;
-    const unsigned g =
-        (unsigned)std::min<size_t>(((size_t)p.T + 7) / 8 + (p.T == 0), (size_t)std::min(n_sm * 4, kRouterParts));
-    const size_t sm = (size_t)p.E * 4;
-    const auto a16 = [](const void *q) { return ((uintptr_t)q & 15) == 0; };
-    if (p.E % 4 == 0 && a16(p.logits) && a16(p.dlogits)) {
-        const int nv = p.E / 4;
-        if (nv <= 32) return launch_pdl(router_loss_kernel<4, 1>, g, sm, p, st);
-        if (nv <= 64) return launch_pdl(router_loss_kernel<4, 2>, g, sm, p, st);
-        if (nv <= 128) return launch_pdl(router_loss_kernel<4, 4>, g, sm, p, st);
-        if (nv <= 256) return launch_pdl(router_loss_kernel<4, 8>, g, sm, p, st);
-        return launch_pdl(router_loss_kernel<4, 32>, g, sm, p, st);
-    }
-    if (p.E <= 64) return launch_pdl(router_loss_kernel<1, 2>, g, sm, p, st);
-    if (p.E <= 256) return launch_pdl(router_loss_kernel<1, 8>, g, sm, p, st);
-    if (p.E <= 1024) return launch_pdl(router_loss_kernel<1, 32>, g, sm, p, st);
-    return launch_pdl(router_loss_kernel<1, 128>, g, sm, p, st);
+    // up to kCountInLoss picks every CTA of the loss kernel counts them all
+    if ((size_t)p.T * p.k <= kCountInLoss) return launch_loss<true>(p, n_sm, st);
+    int rc = launch_pdl(router_count_kernel, kCountCtas, kCountThreads, (size_t)(p.E + 1) * 4, p, st, kCountCtas);
+    return rc ? rc : launch_loss<false>(p, n_sm, st);
 }
 
 }  // namespace moe

@@ -153,7 +153,7 @@ struct moe_ctx {
         uint8_t *w;  // device planes
     };
     std::vector<Linear> linears;
-    // router loss workspace: picks per expert [4097], tokens, ticket, loss parts
+    // router loss workspace: loss parts, unmasked tokens, tickets
     uint8_t *router_ws = nullptr;
     moe_stats_t stats{};
     int last_T = -1;
@@ -216,9 +216,8 @@ void set_entry(moe_ctx *c, int tid, int e, uint64_t entry, int32_t slot) {
     push_upd(c, 1, (size_t)tid * c->Et + e, (uint64_t)(int64_t)stamp_index(c, tid, slot));
 }
 
-// Router loss workspace: [loss parts][picks per expert + unmasked tokens][n_valid][ticket]
-constexpr size_t kRouterCountOff = sizeof(double) * 2 * moe::kRouterParts;
-constexpr size_t kRouterTailOff = kRouterCountOff + sizeof(int32_t) * (moe::kRouterMaxExperts + 4);
+// Router loss workspace: [loss parts][unmasked tokens][tickets]
+constexpr size_t kRouterTailOff = sizeof(float) * 2 * moe::kRouterParts;
 constexpr size_t kRouterWsBytes = kRouterTailOff + 16;
 
 constexpr size_t kStepKeys = 256;  // miss keys read back with the hit bitmap
@@ -643,6 +642,7 @@ int moe_layer_init(const moe_cfg *cfg, void *cuda_stream, moe_ctx **out) {
         }
     }
 
+    CKI((cudaError_t)moe::router_configure());
     CKI(cudaMalloc(&ctx->router_ws, kRouterWsBytes));
     CKI(cudaMemset(ctx->router_ws, 0, kRouterWsBytes));
     CKI(cudaHostAlloc(&ctx->h_stamps, sizeof(uint32_t) * (size_t)nt * std::max(1, ctx->spt), cudaHostAllocDefault));
@@ -1917,8 +1917,7 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
     p.loss = d_loss;
     p.counts = d_counts;
     p.dlogits = d_dlogits;
-    p.ws_part = (double *)ctx->router_ws;
-    p.ws_count = (int32_t *)(ctx->router_ws + kRouterCountOff);
+    p.ws_part = (float *)ctx->router_ws;
     p.n_valid = (int32_t *)(ctx->router_ws + kRouterTailOff);
     p.ticket = (unsigned *)(ctx->router_ws + kRouterTailOff + 4);
     p.error = ctx->d_error;
