@@ -53,6 +53,7 @@ struct LinScale<kFmtQ4> {
     __device__ __forceinline__ float term(int raw, float da, int sa) const {
         return (float)(raw - 8 * sa) * (s * da);
     }
+    __device__ __forceinline__ unsigned bound() const { return __float_as_uint(fabsf(8.0f * s)); }
 };
 template <>
 struct LinScale<kFmtQ4K> {
@@ -69,7 +70,24 @@ struct LinScale<kFmtQ4K> {
     __device__ __forceinline__ float term(int raw, float da, int sa) const {
         return da * (sc * (float)raw - mn * (float)sa);
     }
+    __device__ __forceinline__ unsigned bound() const {
+        return max(__float_as_uint(fabsf(mn)), __float_as_uint(fabsf(15.0f * sc - mn)));
+    }
 };
+
+// Largest magnitude a block's weights can take, over the matrix, as binary32
+// bits (NaN above infinity above all): *out, zero before.
+template <int FMT>
+__global__ void linear_max_kernel(const uint8_t *__restrict__ w, size_t nblk, unsigned *out) {
+    unsigned m = 0;
+    for (size_t b = (size_t)blockIdx.x * blockDim.x + threadIdx.x; b < nblk; b += (size_t)gridDim.x * blockDim.x) {
+        LinScale<FMT> s;
+        s.load(w + 16 * nblk, b);
+        m = max(m, s.bound());
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(out, m);
+}
 
 // Sums V values a lane over the warp's lanes: halves the value set at each
 // of the first log2(V) steps, so the total is V - 1 + 5 - log2(V) shuffles.
@@ -210,6 +228,15 @@ int launch_tokens(const LinearParams &p, int n_sm, cudaStream_t st) {
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, size_t nblk, int n_sm, cudaStream_t st) {
     const unsigned g = (unsigned)std::min<size_t>((nblk + 255) / 256, (size_t)n_sm * 8);
     linear_repack_kernel<<<g, 256, 0, st>>>(src, dst, fmt, nblk);
+    return (int)cudaGetLastError();
+}
+
+int launch_linear_max(const uint8_t *w, int fmt, size_t nblk, unsigned *out, int n_sm, cudaStream_t st) {
+    const unsigned g = (unsigned)std::min<size_t>((nblk + 255) / 256, (size_t)n_sm * 8);
+    if (fmt == kFmtQ4K)
+        linear_max_kernel<kFmtQ4K><<<g, 256, 0, st>>>(w, nblk, out);
+    else
+        linear_max_kernel<kFmtQ4><<<g, 256, 0, st>>>(w, nblk, out);
     return (int)cudaGetLastError();
 }
 

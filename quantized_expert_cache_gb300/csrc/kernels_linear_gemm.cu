@@ -1,0 +1,506 @@
+// y = W x of a dense 4-bit layer for batches: the 5th-generation tensor cores
+// (tcgen05, accumulators in TMEM), with the block scales folded into the
+// operands instead of applied to block sums.
+//
+// Arithmetic.  A Q4_0 weight d (q - 8) has at most 15 significant bits and an
+// activation d_a q_a at most 18, so neither fits one binary16; two do:
+//   w = w_h + w_l,  x 2^-e = x_h + x_l   (each part the binary16 rounding of
+// what is left; w exactly, x to 2^-24 of its token's largest value, e the
+// exponent of the token's largest scale) and
+//   y = 2^e (sum w_h x_h  +  sum (w_l x_h + w_h x_l)),
+// dropping w_l x_l (2^-22 of the product).  Three MMAs a K step replace a
+// scaled epilogue for every 32 columns: the exact-block-sum GEMM of the
+// experts has to read every block's sums back from TMEM and is bound by that.
+// Q4_K weights are formed in binary32 (d sc q - dmin m), scaled by a power of
+// two so that the largest of the layer is below 2^15, and split the same way.
+//
+// The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
+// on a growing sum; so the large products are accumulated for kChunk stages
+// (512 columns) only, then added in registers, rounded to nearest.  The cross
+// products are 2^-11 of them and keep one accumulator for the whole tile.
+#include <cuda.h>
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+using namespace gemm;
+
+constexpr int kBM = 128, kBK = 64, kChunk = 8;
+constexpr int kConv = 8, kEpi = 8;                       // converter and epilogue warps
+constexpr int kWTma = 0, kWMma = 1, kWConv = 2, kWEpi = kWConv + kConv;
+constexpr int kThreads = (kWEpi + kEpi) * 32;
+constexpr int kABytes = kBM * kBK * 2;
+constexpr int kBox = 32;                                 // token rows of one TMA box
+
+template <int BN>
+struct LCfg {
+    static constexpr int B_BYTES = BN * kBK * 2;
+    static constexpr int SLOT = 2 * kABytes + 2 * B_BYTES;
+    static constexpr int STAGES = BN >= 128 ? 3 : 4;
+    static constexpr int BAR_OFF = STAGES * SLOT;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
+    static constexpr int SMEM = MISC_OFF + 16 + 1024;    // + alignment slack
+    // TMEM columns: two buffers of the large products' sums, two of the cross products'
+    static constexpr int COLS = 4 * BN;
+};
+
+// ---- activations: codes and scales -> the two halves -------------------------
+// One CTA a token.  x (quantized here) or q and d.
+__global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ unsigned part[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.cols, nb = K / kBlock;
+    const size_t t = blockIdx.x;
+    const float4 *x = p.x ? (const float4 *)(p.x + t * K) : nullptr;
+    const uint32_t *q = (const uint32_t *)(p.q + t * K);
+    const __half *d = p.d + t * nb;
+    // the token's largest scale (non-negative floats order like their bits)
+    unsigned m = 0;
+    if (x) {
+        for (int i = threadIdx.x; i < K / 4; i += 256) {
+            const float4 v = x[i];
+            m = max(m, max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
+                           max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w)))));
+        }
+    } else {
+        for (int i = threadIdx.x; i < nb; i += 256) m = max(m, __float_as_uint(fabsf(__half2float(d[i]))));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, part[lane & 7]);
+    float top = __uint_as_float(m);
+    if (x) top = __half2float(__float2half_rn(top / 127.0f));
+    // scales times 2^-e; e = 0 for a token of zeros, infinities or NaN
+    const int e = top > 0.0f && top <= 65504.0f ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 : 0;
+    const float up = __uint_as_float((unsigned)(127 + e) << 23), down = __uint_as_float((unsigned)(127 - e) << 23);
+    if (threadIdx.x == 0) p.ws_scale[t] = up * p.w_unscale;
+    // 8 lanes a block, 4 values a lane (whole warps run every round)
+    for (int i0 = warp * 32; i0 < K / 4; i0 += 256) {
+        const int i = i0 + lane;
+        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dd = 0.0f;
+        if (x) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < K / 4) v = x[i];
+            unsigned a = max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
+                             max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            dd = __half2float(__float2half_rn(__uint_as_float(a) / 127.0f));
+            const float w[4] = {v.x, v.y, v.z, v.w};
+            if (dd != 0.0f)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[j] = fminf(fmaxf(rintf(w[j] / dd), -127.0f), 127.0f);
+        } else if (i < K / 4) {
+            const uint32_t w = q[i];
+            dd = __half2float(d[i / 8]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = (float)(int8_t)(w >> (8 * j));
+        }
+        if (i >= K / 4) continue;
+        const float r = dd * down;
+        __half h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = c[j] * r;
+            h[j] = __float2half_rn(v);
+            l[j] = __float2half_rn(v - __half2float(h[j]));
+        }
+        *((uint2 *)(p.ws_hi + t * K) + i) = *(uint2 *)h;
+        *((uint2 *)(p.ws_lo + t * K) + i) = *(uint2 *)l;
+    }
+}
+
+// ---- weights: one block of 32 -> the two halves ------------------------------
+template <int FMT>
+struct WRaw;  // one block in flight
+template <>
+struct WRaw<kFmtQ4> {
+    uint4 c;
+    unsigned short s;
+    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on) {
+        c = on ? __ldg((const uint4 *)p.w + blk) : make_uint4(0, 0, 0, 0);
+        s = on ? __ldg((const unsigned short *)(p.w + p.scale_off) + blk) : (unsigned short)0;
+    }
+};
+template <>
+struct WRaw<kFmtQ4K> {
+    uint4 c, h;
+    int j;
+    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on) {
+        c = on ? __ldg((const uint4 *)p.w + blk) : make_uint4(0, 0, 0, 0);
+        h = on ? __ldg((const uint4 *)(p.w + p.scale_off) + (blk >> 3)) : make_uint4(0, 0, 0, 0);
+        j = (int)(blk & 7);
+    }
+};
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+
+// Two codes of the bytes sel picks from n (one nibble a byte) as binary16
+// 1024 + q, minus 1032: q - 8, exact.
+__device__ __forceinline__ __half2 pair_q(uint32_t n, uint32_t sel) {
+    return __hsub2(u2h(__byte_perm(n, 0x64646464u, sel)), u2h(0x64086408u));
+}
+
+// The block's 32 weights: high parts to row `row` of the tile at hi, low parts
+// at lo, chunks 4 half + 0..3 of the swizzled 128-byte row.
+__device__ __forceinline__ void put(uint8_t *hi, uint8_t *lo, int row, int chunk, const uint32_t (&h)[4],
+                                    const uint32_t (&l)[4]) {
+    const int off = (row >> 3) * 1024 + (row & 7) * 128 + ((chunk ^ (row & 7)) << 4);
+    *(uint4 *)(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+    *(uint4 *)(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, float, uint8_t *hi, uint8_t *lo, int row, int half) {
+    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
+    const __half2 d = u2h((uint32_t)w.s * 0x10001u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // elements 8i..8i+7: low nibbles of bytes 0..15, then the high ones
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t n = (c[(i & 1) * 2 + (j >> 1)] >> (i >> 1 << 2)) & 0x0F0F0F0Fu;
+            const __half2 q = pair_q(n, j & 1 ? 0x5352 : 0x5150);
+            const __half2 v = __hmul2(q, d);
+            h[j] = h2u(v);
+            l[j] = h2u(__hfma2(q, d, __hneg2(v)));  // exact: 15 bits less the 11 above
+        }
+        put(hi, lo, row, half * 4 + i, h, l);
+    }
+}
+
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, float scale, uint8_t *hi, uint8_t *lo, int row,
+                                        int half) {
+    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
+    const int sh = 8 * (w.j & 3);
+    const uint32_t a = w.h.y >> sh, m = w.h.z >> sh, x = w.h.w >> sh;
+    const int s6 = w.j < 4 ? (a & 63) : ((x & 15) | (((a >> 6) & 3) << 4));
+    const int m6 = w.j < 4 ? (m & 63) : (((x >> 4) & 15) | (((m >> 6) & 3) << 4));
+    const float sc = __half2float(__ushort_as_half((unsigned short)(w.h.x & 0xffff))) * (float)s6 * scale;
+    const float mn = __half2float(__ushort_as_half((unsigned short)(w.h.x >> 16))) * (float)m6 * scale;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t n = (c[(i & 1) * 2 + (j >> 1)] >> (i >> 1 << 2)) & 0x0F0F0F0Fu;
+            // a byte under 0x4B0000: 2^23 + q
+            const float q0 = __uint_as_float(__byte_perm(n, 0x4B000000u, j & 1 ? 0x7652 : 0x7650)) - 8388608.0f;
+            const float q1 = __uint_as_float(__byte_perm(n, 0x4B000000u, j & 1 ? 0x7653 : 0x7651)) - 8388608.0f;
+            const float v0 = fmaf(q0, sc, -mn), v1 = fmaf(q1, sc, -mn);
+            const __half2 v = __floats2half2_rn(v0, v1);
+            h[j] = h2u(v);
+            l[j] = h2u(__floats2half2_rn(v0 - __low2float(v), v1 - __high2float(v)));
+        }
+        put(hi, lo, row, half * 4 + i, h, l);
+    }
+}
+
+// ---- the GEMM -----------------------------------------------------------------
+// CTA tile: 128 weight rows (TMEM lanes) x BN tokens.  gridDim.x CTAs walk the
+// tiles (token tiles innermost: they share the weight rows in L2).  A cluster
+// of S > 1 CTAs (one tile each) splits K and joins its sums in shared memory,
+// in rank order.
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap tm_hi, const __grid_constant__ CUtensorMap tm_lo,
+                       const __grid_constant__ LinearParams p) {
+    using C = LCfg<BN>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t full0 = smem_u32(smem + C::BAR_OFF), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES,
+                   acce0 = accf0 + 16;
+    volatile uint32_t *tmem_slot = (volatile uint32_t *)(smem + C::MISC_OFF);
+    volatile int *abort_flag = (volatile int *)(smem + C::MISC_OFF + 4);
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1 + kConv);  // TMA expect-tx arrive + converter warps
+            mbar_init(empty0 + 8 * s, 1);         // MMA commit
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(accf0 + 8 * j, 1);
+            mbar_init(acce0 + 8 * j, kEpi);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kWMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32((const void *)tmem_slot)),
+                     "n"(C::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int nb = p.cols / kBlock, nkt = (p.cols + kBK - 1) / kBK;
+    const int kt0 = nkt * rank / S, kt1 = nkt * (rank + 1) / S;  // this CTA's K stages
+    const int ntt = (p.n_tokens + BN - 1) / BN, nrt = (p.rows + kBM - 1) / kBM;
+    const int tile0 = blockIdx.x / S, total = ntt * nrt, stride = gridDim.x / S;
+    const auto columns = [&](int tt) { return min(BN, p.n_tokens - tt * BN); };
+
+    if (warp == kWTma) {
+        if (lane == 0) {
+            // the split activations are the preceding kernel's
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;");
+            int it = 0;
+            for (int t = tile0; t < total; t += stride) {
+                const int tt = t % ntt, boxes = (columns(tt) + kBox - 1) / kBox;
+                for (int kt = kt0; kt < kt1; ++kt, ++it) {
+                    const int slot = it % STAGES;
+                    if (!mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
+                        goto tma_done;
+                    const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT + 2 * kABytes);
+                    mbar_arrive_tx(full, (uint32_t)(2 * boxes * kBox * kBK * 2));
+                    for (int i = 0; i < boxes; ++i) {
+                        tma_load_2d(b + i * kBox * kBK * 2, &tm_hi, kt * kBK, tt * BN + i * kBox, full);
+                        tma_load_2d(b + C::B_BYTES + i * kBox * kBK * 2, &tm_lo, kt * kBK, tt * BN + i * kBox, full);
+                    }
+                }
+            }
+        tma_done:;
+        }
+    } else if (warp == kWMma) {
+        if (lane == 0) {
+            int it = 0, chunk = 0, n_tile = 0;
+            for (int t = tile0; t < total; t += stride, ++n_tile) {
+                const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15);
+                const uint32_t cross = tmem + (uint32_t)((2 + (n_tile & 1)) * BN);
+                for (int kt = kt0; kt < kt1; ++kt, ++it) {
+                    const int slot = it % STAGES, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
+                    if (in_chunk == 0) {
+                        if (!mbar_wait(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
+                            goto mma_done;
+                    }
+                    if (!mbar_wait(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
+                        goto mma_done;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
+                    const uint64_t ah = sdesc(st), al = sdesc(st + kABytes), bh = sdesc(st + 2 * kABytes),
+                                   bl = sdesc(st + 2 * kABytes + C::B_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t ko = (uint64_t)(kk * 32) >> 4;
+                        mma_f16(main, ah + ko, bh + ko, idesc, in_chunk | kk ? 1u : 0u);
+                        mma_f16(cross, al + ko, bh + ko, idesc, (kt - kt0) | kk ? 1u : 0u);
+                        mma_f16(cross, ah + ko, bl + ko, idesc, 1u);
+                    }
+                    mma_commit(empty0 + 8 * slot);
+                    if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
+                        mma_commit(accf0 + 8 * buf);
+                        ++chunk;
+                    }
+                }
+            }
+        mma_done:;
+        }
+    } else if (warp < kWEpi) {
+        // Converters: a thread owns one block (row, half) of every stage and
+        // holds the next kAhead stages' blocks in registers.
+        constexpr int kAhead = 4;
+        const int c = threadIdx.x - kWConv * 32, row = c >> 1, half = c & 1;
+        int ft = tile0, fk = kt0;  // fetch cursor
+        auto fetch = [&](WRaw<FMT> &w) {
+            const int r = ft / ntt * kBM + row, b = 2 * fk + half;
+            w.load(p, (size_t)r * nb + b, ft < total && r < p.rows && b < nb);
+            if (ft < total && ++fk == kt1) {
+                fk = kt0;
+                ft += stride;
+            }
+        };
+        WRaw<FMT> raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(raw[i]);
+        const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
+        bool ok = true;
+        for (int it0 = 0; it0 < n_it && ok; it0 += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int it = it0 + i, slot = it % STAGES;
+                if (it >= n_it || !ok) break;
+                if (lane == 0)
+                    ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 16);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                uint8_t *st = smem + slot * C::SLOT;
+                convert(raw[i], p.w_scale, st, st + kABytes, row, half);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full0 + 8 * slot);
+                fetch(raw[i]);
+            }
+        }
+    } else {
+        // Epilogue: TMEM lane quarter = warp % 4 (lane = weight row), one half
+        // of the token columns.
+        constexpr int HC = BN / 2;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int quarter = warp & 3, c0 = ((warp - kWEpi) >> 2) * HC, r = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        int chunk = 0, n_tile = 0;
+        for (int t = tile0; t < total; t += stride, ++n_tile) {
+            const int tt = t % ntt, nc = columns(tt) - c0;  // this warp's valid columns
+            float acc[HC];
+#pragma unroll
+            for (int i = 0; i < HC; ++i) acc[i] = 0.0f;
+            auto add = [&](uint32_t col) {
+#pragma unroll
+                for (int i = 0; i < HC; i += 16) {
+                    if (i >= nc) break;  // warp-uniform
+                    uint32_t v[16];
+                    tmem_ld16u(lanes + col + (uint32_t)(c0 + i), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[i + j] += __uint_as_float(v[j]);
+                }
+            };
+            for (int kt = kt0; kt < kt1; kt += kChunk, ++chunk) {
+                const int buf = chunk & 1;
+                bool ok = true;
+                if (lane == 0) ok = mbar_wait(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) goto epi_done;
+                tc_fence_after();
+                add((uint32_t)(buf * BN));
+                if (kt + kChunk >= kt1) add((uint32_t)((2 + (n_tile & 1)) * BN));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+            }
+            if (S == 1) {
+                const int row = t / ntt * kBM + r;
+#pragma unroll
+                for (int i = 0; i < HC; ++i) {
+                    if (i >= nc) break;  // warp-uniform
+                    const size_t tok = (size_t)tt * BN + c0 + i;
+                    if (row < p.rows) p.y[tok * p.rows + row] = acc[i] * __ldcg(p.ws_scale + tok);
+                }
+            } else {
+                // (all MMAs and copies of this CTA's only tile are done: its
+                // stages' memory takes the partial sums [column][row])
+                float *red = (float *)smem;
+#pragma unroll
+                for (int i = 0; i < HC; ++i)
+                    if (i < nc) red[(c0 + i) * kBM + r] = acc[i];
+            }
+        }
+    epi_done:;
+    }
+
+    __syncwarp();
+    if (S > 1) {
+        cluster.sync();
+        if (warp >= kWEpi && !*abort_flag) {
+            const int tt = tile0 % ntt, nc = columns(tt), rt = tile0 / ntt;
+            const float *red = (const float *)smem;
+            for (int i = threadIdx.x - kWEpi * 32 + rank * kEpi * 32; i < nc * kBM; i += S * kEpi * 32) {
+                float sum = 0.0f;
+                for (int s = 0; s < S; ++s) sum += *cluster.map_shared_rank(red + i, s);
+                const size_t tok = (size_t)tt * BN + i / kBM;
+                const int row = rt * kBM + i % kBM;
+                if (row < p.rows) p.y[tok * p.rows + row] = sum * __ldcg(p.ws_scale + tok);
+            }
+        }
+        __syncwarp();
+        cluster.sync();  // no CTA leaves while its sums are read
+    }
+    // drain: after an abort, give the copies and MMAs this CTA issued a
+    // bounded time (about 10 ms) to land, then free TMEM
+    __syncthreads();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 20000000ll) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+}
+
+template <int FMT, int BN>
+int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
+    const LinearParams &p = g.p;
+    auto kernel = linear_gemm_kernel<FMT, BN>;
+    const int ntt = (p.n_tokens + BN - 1) / BN, tiles = ntt * ((p.rows + kBM - 1) / kBM), nkt = (p.cols + kBK - 1) / kBK;
+    // K splits: as many as the SMs take, of at least 4 stages
+    const int S = std::max(1, std::min({8, n_sm / tiles, nkt / 4}));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, n_sm)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = LCfg<BN>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)S, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, g.tm_hi, g.tm_lo, p);
+}
+
+template <int FMT>
+int launch_fmt(const LinearGemm &g, int n_sm, cudaStream_t st) {
+    if (g.p.n_tokens <= 32) return launch_tile<FMT, 32>(g, n_sm, st);
+    if (g.p.n_tokens <= 64) return launch_tile<FMT, 64>(g, n_sm, st);
+    return launch_tile<FMT, 128>(g, n_sm, st);
+}
+
+template <int FMT>
+int configure_fmt() {
+    cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         LCfg<32>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 LCfg<64>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 LCfg<128>::SMEM);
+    return (int)e;
+}
+
+}  // namespace
+
+int linear_gemm_box() { return kBox; }
+
+int linear_gemm_configure() {
+    const int rc = configure_fmt<kFmtQ4>();
+    return rc ? rc : configure_fmt<kFmtQ4K>();
+}
+
+int launch_linear_gemm(const LinearGemm &g, int n_sm, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)g.p.n_tokens);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int rc = (int)cudaLaunchKernelEx(&cfg, linear_split_kernel, g.p);
+    if (rc) return rc;
+    return g.p.fmt == kFmtQ4K ? launch_fmt<kFmtQ4K>(g, n_sm, st) : launch_fmt<kFmtQ4>(g, n_sm, st);
+}
+
+}  // namespace moe
