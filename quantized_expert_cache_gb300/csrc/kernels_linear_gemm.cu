@@ -18,6 +18,11 @@
 // on a growing sum; so the large products are accumulated for kChunk stages
 // (512 columns) only, then added in registers, rounded to nearest.  The cross
 // products are 2^-11 of them and keep one accumulator for the whole tile.
+//
+// The weight halves go from the converters' registers to TMEM (tcgen05.st) and
+// the MMA takes its A operand there.  With A in shared memory the kernel was
+// bound by shared memory: an N = 128 MMA reads 8 KB, and the three of a K step
+// with the stage's writes took 114 cycles an MMA instead of 64.
 #include <cuda.h>
 #include <cooperative_groups.h>
 
@@ -36,19 +41,22 @@ constexpr int kBM = 128, kBK = 64, kChunk = 8;
 constexpr int kConv = 8, kEpi = 8;                       // converter and epilogue warps
 constexpr int kWTma = 0, kWMma = 1, kWConv = 2, kWEpi = kWConv + kConv;
 constexpr int kThreads = (kWEpi + kEpi) * 32;
-constexpr int kABytes = kBM * kBK * 2;
 constexpr int kBox = 32;                                 // token rows of one TMA box
 
 template <int BN>
 struct LCfg {
     static constexpr int B_BYTES = BN * kBK * 2;
-    static constexpr int SLOT = 2 * kABytes + 2 * B_BYTES;
-    static constexpr int STAGES = BN >= 128 ? 3 : 4;
-    static constexpr int BAR_OFF = STAGES * SLOT;
-    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
+    static constexpr int SLOT = 2 * B_BYTES;             // both halves of the tokens' K stage
+    static constexpr int STAGES = BN >= 128 ? 6 : 8;
+    static constexpr int A_STAGES = BN >= 128 ? 2 : 4;   // weight stages in TMEM, 64 columns each
+    static constexpr int RED = BN * kBM * 4;             // a split tile's sums
+    static constexpr int BAR_OFF = STAGES * SLOT > RED ? STAGES * SLOT : RED;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 2 * A_STAGES + 6) * 8;
     static constexpr int SMEM = MISC_OFF + 16 + 1024;    // + alignment slack
-    // TMEM columns: two buffers of the large products' sums, two of the cross products'
-    static constexpr int COLS = 4 * BN;
+    // TMEM columns: two buffers of the large products' sums, the cross
+    // products', the weight stages
+    static constexpr int CROSS = 2 * BN, A_COL = 3 * BN, COLS = 512;
+    static_assert(A_COL + 64 * A_STAGES <= COLS, "TMEM");
 };
 
 // ---- activations: codes and scales -> the two halves -------------------------
@@ -119,25 +127,34 @@ __global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
     }
 }
 
-// ---- weights: one block of 32 -> the two halves ------------------------------
+// ---- weights: a row's two blocks of a K stage -> the two halves ---------------
 template <int FMT>
-struct WRaw;  // one block in flight
+struct WRaw;
 template <>
 struct WRaw<kFmtQ4> {
-    uint4 c;
-    unsigned short s;
-    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on) {
-        c = on ? __ldg((const uint4 *)p.w + blk) : make_uint4(0, 0, 0, 0);
-        s = on ? __ldg((const unsigned short *)(p.w + p.scale_off) + blk) : (unsigned short)0;
+    static constexpr int kAhead = 4;  // stages in registers
+    uint4 c[2];
+    uint32_t s;  // both blocks' scales
+    // block blk is on when on, the next one when on2
+    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on, bool on2) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const unsigned short *d = (const unsigned short *)(p.w + p.scale_off);
+        c[0] = on ? __ldg((const uint4 *)p.w + blk) : z;
+        c[1] = on2 ? __ldg((const uint4 *)p.w + blk + 1) : z;
+        s = on ? __ldg(d + blk) : 0u;
+        if (on2) s |= (uint32_t)__ldg(d + blk + 1) << 16;
     }
 };
 template <>
 struct WRaw<kFmtQ4K> {
-    uint4 c, h;
+    static constexpr int kAhead = 3;
+    uint4 c[2], h;  // both blocks lie in one super-block, blocks j and j + 1
     int j;
-    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on) {
-        c = on ? __ldg((const uint4 *)p.w + blk) : make_uint4(0, 0, 0, 0);
-        h = on ? __ldg((const uint4 *)(p.w + p.scale_off) + (blk >> 3)) : make_uint4(0, 0, 0, 0);
+    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on, bool) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        c[0] = on ? __ldg((const uint4 *)p.w + blk) : z;
+        c[1] = on ? __ldg((const uint4 *)p.w + blk + 1) : z;
+        h = on ? __ldg((const uint4 *)(p.w + p.scale_off) + (blk >> 3)) : z;
         j = (int)(blk & 7);
     }
 };
@@ -151,57 +168,38 @@ __device__ __forceinline__ __half2 pair_q(uint32_t n, uint32_t sel) {
     return __hsub2(u2h(__byte_perm(n, 0x64646464u, sel)), u2h(0x64086408u));
 }
 
-// The block's 32 weights: high parts to row `row` of the tile at hi, low parts
-// at lo, chunks 4 half + 0..3 of the swizzled 128-byte row.
-__device__ __forceinline__ void put(uint8_t *hi, uint8_t *lo, int row, int chunk, const uint32_t (&h)[4],
-                                    const uint32_t (&l)[4]) {
-    const int off = (row >> 3) * 1024 + (row & 7) * 128 + ((chunk ^ (row & 7)) << 4);
-    *(uint4 *)(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-    *(uint4 *)(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-__device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, float, uint8_t *hi, uint8_t *lo, int row, int half) {
-    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
-    const __half2 d = u2h((uint32_t)w.s * 0x10001u);
+// Block b's 32 weights, pairs in K order: high parts h, low parts l.
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, int b, float, uint32_t (&h)[16], uint32_t (&l)[16]) {
+    const uint32_t c[4] = {w.c[b].x, w.c[b].y, w.c[b].z, w.c[b].w};
+    const __half2 d = u2h(__byte_perm(w.s, 0, b ? 0x3232 : 0x1010));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // elements 8i..8i+7: low nibbles of bytes 0..15, then the high ones
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t n = (c[(i & 1) * 2 + (j >> 1)] >> (i >> 1 << 2)) & 0x0F0F0F0Fu;
-            const __half2 q = pair_q(n, j & 1 ? 0x5352 : 0x5150);
-            const __half2 v = __hmul2(q, d);
-            h[j] = h2u(v);
-            l[j] = h2u(__hfma2(q, d, __hneg2(v)));  // exact: 15 bits less the 11 above
-        }
-        put(hi, lo, row, half * 4 + i, h, l);
+    for (int i = 0; i < 16; ++i) {  // pairs 0..7: low nibbles of bytes 0..15, then the high ones
+        const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
+        const __half2 q = pair_q(n, i & 1 ? 0x5352 : 0x5150);
+        const __half2 v = __hmul2(q, d);
+        h[i] = h2u(v);
+        l[i] = h2u(__hfma2(q, d, __hneg2(v)));  // exact: 15 bits less the 11 above
     }
 }
 
-__device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, float scale, uint8_t *hi, uint8_t *lo, int row,
-                                        int half) {
-    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
-    const int sh = 8 * (w.j & 3);
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, int b, float scale, uint32_t (&h)[16], uint32_t (&l)[16]) {
+    const uint32_t c[4] = {w.c[b].x, w.c[b].y, w.c[b].z, w.c[b].w};
+    const int jb = w.j + b, sh = 8 * (jb & 3);
     const uint32_t a = w.h.y >> sh, m = w.h.z >> sh, x = w.h.w >> sh;
-    const int s6 = w.j < 4 ? (a & 63) : ((x & 15) | (((a >> 6) & 3) << 4));
-    const int m6 = w.j < 4 ? (m & 63) : (((x >> 4) & 15) | (((m >> 6) & 3) << 4));
+    const int s6 = jb < 4 ? (a & 63) : ((x & 15) | (((a >> 6) & 3) << 4));
+    const int m6 = jb < 4 ? (m & 63) : (((x >> 4) & 15) | (((m >> 6) & 3) << 4));
     const float sc = __half2float(__ushort_as_half((unsigned short)(w.h.x & 0xffff))) * (float)s6 * scale;
     const float mn = __half2float(__ushort_as_half((unsigned short)(w.h.x >> 16))) * (float)m6 * scale;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t n = (c[(i & 1) * 2 + (j >> 1)] >> (i >> 1 << 2)) & 0x0F0F0F0Fu;
-            // a byte under 0x4B0000: 2^23 + q
-            const float q0 = __uint_as_float(__byte_perm(n, 0x4B000000u, j & 1 ? 0x7652 : 0x7650)) - 8388608.0f;
-            const float q1 = __uint_as_float(__byte_perm(n, 0x4B000000u, j & 1 ? 0x7653 : 0x7651)) - 8388608.0f;
-            const float v0 = fmaf(q0, sc, -mn), v1 = fmaf(q1, sc, -mn);
-            const __half2 v = __floats2half2_rn(v0, v1);
-            h[j] = h2u(v);
-            l[j] = h2u(__floats2half2_rn(v0 - __low2float(v), v1 - __high2float(v)));
-        }
-        put(hi, lo, row, half * 4 + i, h, l);
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
+        // a byte under 0x4B0000: 2^23 + q
+        const float q0 = __uint_as_float(__byte_perm(n, 0x4B000000u, i & 1 ? 0x7652 : 0x7650)) - 8388608.0f;
+        const float q1 = __uint_as_float(__byte_perm(n, 0x4B000000u, i & 1 ? 0x7653 : 0x7651)) - 8388608.0f;
+        const float v0 = fmaf(q0, sc, -mn), v1 = fmaf(q1, sc, -mn);
+        const __half2 v = __floats2half2_rn(v0, v1);
+        h[i] = h2u(v);
+        l[i] = h2u(__floats2half2_rn(v0 - __low2float(v), v1 - __high2float(v)));
     }
 }
 
@@ -218,8 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int STAGES = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t full0 = smem_u32(smem + C::BAR_OFF), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES,
-                   acce0 = accf0 + 16;
+    constexpr int AST = C::A_STAGES;
+    const uint32_t full0 = smem_u32(smem + C::BAR_OFF), empty0 = full0 + 8 * STAGES, afull0 = empty0 + 8 * STAGES,
+                   aempty0 = afull0 + 8 * AST, accf0 = aempty0 + 8 * AST, acce0 = accf0 + 16, crosse = acce0 + 16;
     volatile uint32_t *tmem_slot = (volatile uint32_t *)(smem + C::MISC_OFF);
     volatile int *abort_flag = (volatile int *)(smem + C::MISC_OFF + 4);
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -228,9 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, 1 + kConv);  // TMA expect-tx arrive + converter warps
-            mbar_init(empty0 + 8 * s, 1);         // MMA commit
+            mbar_init(full0 + 8 * s, 1);   // TMA expect-tx arrive
+            mbar_init(empty0 + 8 * s, 1);  // MMA commit
         }
+        for (int s = 0; s < AST; ++s) {
+            mbar_init(afull0 + 8 * s, kConv / 2);  // the stage's converter warps
+            mbar_init(aempty0 + 8 * s, 1);         // MMA commit
+        }
+        mbar_init(crosse, kEpi);
         for (int j = 0; j < 2; ++j) {
             mbar_init(accf0 + 8 * j, 1);
             mbar_init(acce0 + 8 * j, kEpi);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int slot = it % STAGES;
                     if (!mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
                         goto tma_done;
-                    const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT + 2 * kABytes);
+                    const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT);
                     mbar_arrive_tx(full, (uint32_t)(2 * boxes * kBox * kBK * 2));
                     for (int i = 0; i < boxes; ++i) {
                         tma_load_2d(b + i * kBox * kBK * 2, &tm_hi, kt * kBK, tt * BN + i * kBox, full);
@@ -282,27 +286,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int it = 0, chunk = 0, n_tile = 0;
             for (int t = tile0; t < total; t += stride, ++n_tile) {
-                const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15);
-                const uint32_t cross = tmem + (uint32_t)((2 + (n_tile & 1)) * BN);
+                const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15), cross = tmem + C::CROSS;
+                // the cross sums of the tile before are read
+                if (!mbar_wait(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
-                    const int slot = it % STAGES, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
+                    const int slot = it % STAGES, as = it % AST, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
                     if (in_chunk == 0) {
                         if (!mbar_wait(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
                             goto mma_done;
                     }
-                    if (!mbar_wait(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
+                    if (!mbar_wait(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4) ||
+                        !mbar_wait(afull0 + 8 * as, (uint32_t)(it / AST) & 1u, abort_flag, p.error, 4))
                         goto mma_done;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
-                    const uint64_t ah = sdesc(st), al = sdesc(st + kABytes), bh = sdesc(st + 2 * kABytes),
-                                   bl = sdesc(st + 2 * kABytes + C::B_BYTES);
+                    const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN),
+                                   ah = tmem + (uint32_t)(C::A_COL + 64 * as), al = ah + 32;
+                    const uint64_t bh = sdesc(st), bl = sdesc(st + C::B_BYTES);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint64_t ko = (uint64_t)(kk * 32) >> 4;
-                        mma_f16(main, ah + ko, bh + ko, idesc, in_chunk | kk ? 1u : 0u);
-                        mma_f16(cross, al + ko, bh + ko, idesc, (kt - kt0) | kk ? 1u : 0u);
-                        mma_f16(cross, ah + ko, bl + ko, idesc, 1u);
+                        mma_f16_ta(main, ah + 8 * kk, bh + ko, idesc, in_chunk | kk ? 1u : 0u);
+                        mma_f16_ta(cross, al + 8 * kk, bh + ko, idesc, (kt - kt0) | kk ? 1u : 0u);
+                        mma_f16_ta(cross, ah + 8 * kk, bl + ko, idesc, 1u);
                     }
+                    mma_commit(aempty0 + 8 * as);
                     mma_commit(empty0 + 8 * slot);
                     if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
                         mma_commit(accf0 + 8 * buf);
@@ -313,39 +320,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_done:;
         }
     } else if (warp < kWEpi) {
-        // Converters: a thread owns one block (row, half) of every stage and
-        // holds the next kAhead stages' blocks in registers.
-        constexpr int kAhead = 4;
-        const int c = threadIdx.x - kWConv * 32, row = c >> 1, half = c & 1;
-        int ft = tile0, fk = kt0;  // fetch cursor
+        // Converters: two sets of four warps take the stages in turn; a thread
+        // owns a row's two blocks of its set's stages and holds the next kAhead
+        // of them in registers.  The row's halves go to its TMEM lane.
+        constexpr int kAhead = WRaw<FMT>::kAhead;
+        const int set = (warp - kWConv) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL;
+        const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
+        int ft = tile0, fk = kt0, fr = tile0 / ntt * kBM + row;  // fetch cursor
+        auto advance = [&]() {
+            if (++fk < kt1) return;
+            fk = kt0;
+            ft += stride;
+            fr = ft / ntt * kBM + row;
+        };
         auto fetch = [&](WRaw<FMT> &w) {
-            const int r = ft / ntt * kBM + row, b = 2 * fk + half;
-            w.load(p, (size_t)r * nb + b, ft < total && r < p.rows && b < nb);
-            if (ft < total && ++fk == kt1) {
-                fk = kt0;
-                ft += stride;
-            }
+            const bool on = ft < total && fr < p.rows;
+            w.load(p, (size_t)fr * nb + 2 * fk, on, on && 2 * fk + 1 < nb);
+            advance();
+            advance();
         };
         WRaw<FMT> raw[kAhead];
+        if (set) advance();
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) fetch(raw[i]);
-        const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
         bool ok = true;
-        for (int it0 = 0; it0 < n_it && ok; it0 += kAhead) {
+        for (int it0 = set; it0 < n_it && ok; it0 += 2 * kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int it = it0 + i, slot = it % STAGES;
+                const int it = it0 + 2 * i, as = it % AST;
                 if (it >= n_it || !ok) break;
+                uint32_t h[16], l[16];
+                convert(raw[i], 0, p.w_scale, h, l);
                 if (lane == 0)
-                    ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 16);
+                    ok = mbar_wait(aempty0 + 8 * as, ((uint32_t)(it / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
-                uint8_t *st = smem + slot * C::SLOT;
-                convert(raw[i], p.w_scale, st, st + kABytes, row, half);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full0 + 8 * slot);
+                tc_fence_after();
+                tmem_st16(lanes + 64 * as, h);
+                tmem_st16(lanes + 64 * as + 32, l);
+                convert(raw[i], 1, p.w_scale, h, l);
+                tmem_st16(lanes + 64 * as + 16, h);
+                tmem_st16(lanes + 64 * as + 48, l);
                 fetch(raw[i]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(afull0 + 8 * as);
             }
         }
     } else {
@@ -355,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const int quarter = warp & 3, c0 = ((warp - kWEpi) >> 2) * HC, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        int chunk = 0, n_tile = 0;
-        for (int t = tile0; t < total; t += stride, ++n_tile) {
+        int chunk = 0;
+        for (int t = tile0; t < total; t += stride) {
             const int tt = t % ntt, nc = columns(tt) - c0;  // this warp's valid columns
             float acc[HC];
 #pragma unroll
@@ -380,10 +401,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) goto epi_done;
                 tc_fence_after();
                 add((uint32_t)(buf * BN));
-                if (kt + kChunk >= kt1) add((uint32_t)((2 + (n_tile & 1)) * BN));
+                const bool end = kt + kChunk >= kt1;
+                if (end) add(C::CROSS);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+                if (lane == 0) {
+                    mbar_arrive(acce0 + 8 * buf);
+                    if (end) mbar_arrive(crosse);
+                }
             }
             if (S == 1) {
                 const int row = t / ntt * kBM + r;
