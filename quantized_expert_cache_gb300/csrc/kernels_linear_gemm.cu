@@ -41,122 +41,140 @@ constexpr int kBM = 128, kBK = 64, kChunk = 8;
 constexpr int kConv = 8, kEpi = 8;                       // converter and epilogue warps
 constexpr int kWTma = 0, kWMma = 1, kWConv = 2, kWEpi = kWConv + kConv;
 constexpr int kThreads = (kWEpi + kEpi) * 32;
+constexpr int kAhead = 7;                                // K stages of weights in flight
 constexpr int kBox = 32;                                 // token rows of one TMA box
 
-template <int BN>
+template <int FMT, int BN>
 struct LCfg {
     static constexpr int B_BYTES = BN * kBK * 2;
     static constexpr int SLOT = 2 * B_BYTES;             // both halves of the tokens' K stage
-    static constexpr int STAGES = BN >= 128 ? 6 : 8;
-    static constexpr int A_STAGES = BN >= 128 ? 2 : 4;   // weight stages in TMEM, 64 columns each
+    static constexpr int STAGES = 4;
+    static constexpr int A_STAGES = BN >= 128 ? 4 : 8;   // weight blocks (32 of K) in TMEM, 32 columns each
     static constexpr int RED = BN * kBM * 4;             // a split tile's sums
-    static constexpr int BAR_OFF = STAGES * SLOT > RED ? STAGES * SLOT : RED;
+    // weight blocks on their way to the converters, [kAhead + 1] entries of a
+    // thread's 16 code bytes and its scale bytes
+    static constexpr int SC = FMT == kFmtQ4 ? 4 : 16;
+    static constexpr int RAW_OFF = STAGES * SLOT > RED ? STAGES * SLOT : RED;
+    static constexpr int RAW_BYTES = kConv * 32 * (16 + SC);
+    static constexpr int BAR_OFF = RAW_OFF + (kAhead + 1) * RAW_BYTES;
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 2 * A_STAGES + 6) * 8;
     static constexpr int SMEM = MISC_OFF + 16 + 1024;    // + alignment slack
     // TMEM columns: two buffers of the large products' sums, the cross
     // products', the weight stages
     static constexpr int CROSS = 2 * BN, A_COL = 3 * BN, COLS = 512;
-    static_assert(A_COL + 64 * A_STAGES <= COLS, "TMEM");
+    static_assert(A_COL + 32 * A_STAGES <= COLS, "TMEM");
 };
 
 // ---- activations: codes and scales -> the two halves -------------------------
-// One CTA a token.  x (quantized here) or q and d.
+// One CTA a token, four values a thread and round: ITEMS rounds in registers,
+// or (ITEMS 0) any number, read twice.  FP: x, quantized here; else q and d.
+template <bool FP, int ITEMS>
 __global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ unsigned part[8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.cols, nb = K / kBlock;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.cols, n4 = K / 4;
     const size_t t = blockIdx.x;
-    const float4 *x = p.x ? (const float4 *)(p.x + t * K) : nullptr;
-    const uint32_t *q = (const uint32_t *)(p.q + t * K);
-    const __half *d = p.d + t * nb;
-    // the token's largest scale (non-negative floats order like their bits)
-    unsigned m = 0;
-    if (x) {
-        for (int i = threadIdx.x; i < K / 4; i += 256) {
-            const float4 v = x[i];
-            m = max(m, max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
-                           max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w)))));
+    struct Four {
+        float v[4];  // FP: values; else codes
+        float d;     // else: the block's scale
+    };
+    auto load = [&](int i) {
+        Four f{};
+        if (i >= n4) return f;
+        if (FP) {
+            *(float4 *)f.v = *((const float4 *)(p.x + t * K) + i);
+        } else {
+            const uint32_t w = *((const uint32_t *)(p.q + t * K) + i);
+            f.d = __half2float(p.d[t * (n4 / 8) + i / 8]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.v[j] = (float)(int8_t)(w >> (8 * j));
         }
+        return f;
+    };
+    // non-negative floats order like their bits (NaN above all)
+    auto top4 = [](const Four &f) {
+        return FP ? max(max(__float_as_uint(fabsf(f.v[0])), __float_as_uint(fabsf(f.v[1]))),
+                        max(__float_as_uint(fabsf(f.v[2])), __float_as_uint(fabsf(f.v[3]))))
+                  : __float_as_uint(fabsf(f.d));
+    };
+    Four held[ITEMS ? ITEMS : 1];
+    unsigned m = 0;
+    if (ITEMS) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) held[i] = load(threadIdx.x + 256 * i);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) m = max(m, top4(held[i]));
     } else {
-        for (int i = threadIdx.x; i < nb; i += 256) m = max(m, __float_as_uint(fabsf(__half2float(d[i]))));
+        for (int i = threadIdx.x; i < n4; i += 256) m = max(m, top4(load(i)));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) part[warp] = m;
     __syncthreads();
     m = __reduce_max_sync(0xffffffffu, part[lane & 7]);
+    // the token's largest scale; the scales times 2^-e, its exponent (e = 0
+    // for a token of zeros, infinities or NaN)
     float top = __uint_as_float(m);
-    if (x) top = __half2float(__float2half_rn(top / 127.0f));
-    // scales times 2^-e; e = 0 for a token of zeros, infinities or NaN
+    if (FP) top = __half2float(__float2half_rn(top / 127.0f));
     const int e = top > 0.0f && top <= 65504.0f ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 : 0;
     const float up = __uint_as_float((unsigned)(127 + e) << 23), down = __uint_as_float((unsigned)(127 - e) << 23);
     if (threadIdx.x == 0) p.ws_scale[t] = up * p.w_unscale;
-    // 8 lanes a block, 4 values a lane (whole warps run every round)
-    for (int i0 = warp * 32; i0 < K / 4; i0 += 256) {
-        const int i = i0 + lane;
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dd = 0.0f;
-        if (x) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < K / 4) v = x[i];
-            unsigned a = max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
-                             max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+    // 8 lanes a block (whole warps run every round)
+    auto emit = [&](int i, Four f) {
+        if (FP) {
+            unsigned a = top4(f);
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-            dd = __half2float(__float2half_rn(__uint_as_float(a) / 127.0f));
-            const float w[4] = {v.x, v.y, v.z, v.w};
-            if (dd != 0.0f)
+            f.d = __half2float(__float2half_rn(__uint_as_float(a) / 127.0f));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = fminf(fmaxf(rintf(w[j] / dd), -127.0f), 127.0f);
-        } else if (i < K / 4) {
-            const uint32_t w = q[i];
-            dd = __half2float(d[i / 8]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = (float)(int8_t)(w >> (8 * j));
+            for (int j = 0; j < 4; ++j)
+                f.v[j] = f.d != 0.0f ? fminf(fmaxf(rintf(f.v[j] / f.d), -127.0f), 127.0f) : 0.0f;
         }
-        if (i >= K / 4) continue;
-        const float r = dd * down;
+        if (i >= n4) return;
+        const float r = f.d * down;
         __half h[4], l[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float v = c[j] * r;
+            const float v = f.v[j] * r;
             h[j] = __float2half_rn(v);
             l[j] = __float2half_rn(v - __half2float(h[j]));
         }
         *((uint2 *)(p.ws_hi + t * K) + i) = *(uint2 *)h;
         *((uint2 *)(p.ws_lo + t * K) + i) = *(uint2 *)l;
+    };
+    if (ITEMS) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (warp * 32 + 256 * i < n4) emit(threadIdx.x + 256 * i, held[i]);
+    } else {
+        for (int i = threadIdx.x; i - lane < n4; i += 256) emit(i, load(i));
     }
 }
 
-// ---- weights: a row's two blocks of a K stage -> the two halves ---------------
+template <bool FP>
+int launch_split(const LinearParams &p, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.n_tokens);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.cols <= 1024) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 1>, p);
+    if (p.cols <= 2048) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 2>, p);
+    if (p.cols <= 4096) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 4>, p);
+    if (p.cols <= 8192) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 8>, p);
+    return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 0>, p);
+}
+
+// ---- weights: one block of 32 -> the two halves ------------------------------
 template <int FMT>
-struct WRaw;
-template <>
-struct WRaw<kFmtQ4> {
-    static constexpr int kAhead = 4;  // stages in registers
-    uint4 c[2];
-    uint32_t s;  // both blocks' scales
-    // block blk is on when on, the next one when on2
-    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on, bool on2) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        const unsigned short *d = (const unsigned short *)(p.w + p.scale_off);
-        c[0] = on ? __ldg((const uint4 *)p.w + blk) : z;
-        c[1] = on2 ? __ldg((const uint4 *)p.w + blk + 1) : z;
-        s = on ? __ldg(d + blk) : 0u;
-        if (on2) s |= (uint32_t)__ldg(d + blk + 1) << 16;
-    }
-};
-template <>
-struct WRaw<kFmtQ4K> {
-    static constexpr int kAhead = 3;
-    uint4 c[2], h;  // both blocks lie in one super-block, blocks j and j + 1
-    int j;
-    __device__ __forceinline__ void load(const LinearParams &p, size_t blk, bool on, bool) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        c[0] = on ? __ldg((const uint4 *)p.w + blk) : z;
-        c[1] = on ? __ldg((const uint4 *)p.w + blk + 1) : z;
-        h = on ? __ldg((const uint4 *)(p.w + p.scale_off) + (blk >> 3)) : z;
-        j = (int)(blk & 7);
-    }
+struct WRaw {
+    uint4 c;   // codes
+    uint4 h;   // Q4_K: the super-block's header; Q4_0: .x = two adjacent scales
+    int j;     // Q4_K: sub-block; Q4_0: which of the two scales
 };
 
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -168,10 +186,10 @@ __device__ __forceinline__ __half2 pair_q(uint32_t n, uint32_t sel) {
     return __hsub2(u2h(__byte_perm(n, 0x64646464u, sel)), u2h(0x64086408u));
 }
 
-// Block b's 32 weights, pairs in K order: high parts h, low parts l.
-__device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, int b, float, uint32_t (&h)[16], uint32_t (&l)[16]) {
-    const uint32_t c[4] = {w.c[b].x, w.c[b].y, w.c[b].z, w.c[b].w};
-    const __half2 d = u2h(__byte_perm(w.s, 0, b ? 0x3232 : 0x1010));
+// The block's 32 weights, pairs in K order: high parts h, low parts l.
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, float /*scale*/, uint32_t (&h)[16], uint32_t (&l)[16]) {
+    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
+    const __half2 d = u2h(__byte_perm(w.h.x, 0, w.j ? 0x3232 : 0x1010));
 #pragma unroll
     for (int i = 0; i < 16; ++i) {  // pairs 0..7: low nibbles of bytes 0..15, then the high ones
         const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
@@ -182,12 +200,12 @@ __device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, int b, float, uin
     }
 }
 
-__device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, int b, float scale, uint32_t (&h)[16], uint32_t (&l)[16]) {
-    const uint32_t c[4] = {w.c[b].x, w.c[b].y, w.c[b].z, w.c[b].w};
-    const int jb = w.j + b, sh = 8 * (jb & 3);
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, float scale, uint32_t (&h)[16], uint32_t (&l)[16]) {
+    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
+    const int sh = 8 * (w.j & 3);
     const uint32_t a = w.h.y >> sh, m = w.h.z >> sh, x = w.h.w >> sh;
-    const int s6 = jb < 4 ? (a & 63) : ((x & 15) | (((a >> 6) & 3) << 4));
-    const int m6 = jb < 4 ? (m & 63) : (((x >> 4) & 15) | (((m >> 6) & 3) << 4));
+    const int s6 = w.j < 4 ? (a & 63) : ((x & 15) | (((a >> 6) & 3) << 4));
+    const int m6 = w.j < 4 ? (m & 63) : (((x >> 4) & 15) | (((m >> 6) & 3) << 4));
     const float sc = __half2float(__ushort_as_half((unsigned short)(w.h.x & 0xffff))) * (float)s6 * scale;
     const float mn = __half2float(__ushort_as_half((unsigned short)(w.h.x >> 16))) * (float)m6 * scale;
 #pragma unroll
@@ -212,7 +230,7 @@ template <int FMT, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tm_hi, const __grid_constant__ CUtensorMap tm_lo,
                        const __grid_constant__ LinearParams p) {
-    using C = LCfg<BN>;
+    using C = LCfg<FMT, BN>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -224,14 +242,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);   // TMA expect-tx arrive
             mbar_init(empty0 + 8 * s, 1);  // MMA commit
         }
         for (int s = 0; s < AST; ++s) {
-            mbar_init(afull0 + 8 * s, kConv / 2);  // the stage's converter warps
+            mbar_init(afull0 + 8 * s, kConv / 2);  // the block's converter warps
             mbar_init(aempty0 + 8 * s, 1);         // MMA commit
         }
         mbar_init(crosse, kEpi);
@@ -283,36 +301,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_done:;
         }
     } else if (warp == kWMma) {
-        if (lane == 0) {
+        {
             int it = 0, chunk = 0, n_tile = 0;
             for (int t = tile0; t < total; t += stride, ++n_tile) {
                 const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15), cross = tmem + C::CROSS;
                 // the cross sums of the tile before are read
                 if (!mbar_wait(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
-                    const int slot = it % STAGES, as = it % AST, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
+                    const int slot = it % STAGES, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
                     if (in_chunk == 0) {
                         if (!mbar_wait(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
                             goto mma_done;
                     }
-                    if (!mbar_wait(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4) ||
-                        !mbar_wait(afull0 + 8 * as, (uint32_t)(it / AST) & 1u, abort_flag, p.error, 4))
+                    if (!mbar_wait(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
                         goto mma_done;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN),
-                                   ah = tmem + (uint32_t)(C::A_COL + 64 * as), al = ah + 32;
+                    const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
                     const uint64_t bh = sdesc(st), bl = sdesc(st + C::B_BYTES);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ko = (uint64_t)(kk * 32) >> 4;
-                        mma_f16_ta(main, ah + 8 * kk, bh + ko, idesc, in_chunk | kk ? 1u : 0u);
-                        mma_f16_ta(cross, al + 8 * kk, bh + ko, idesc, (kt - kt0) | kk ? 1u : 0u);
-                        mma_f16_ta(cross, ah + 8 * kk, bl + ko, idesc, 1u);
+                    for (int half = 0; half < 2; ++half) {
+                        const int ab = 2 * it + half, as = ab % AST;
+                        if (!mbar_wait(afull0 + 8 * as, (uint32_t)(ab / AST) & 1u, abort_flag, p.error, 4))
+                            goto mma_done;
+                        tc_fence_after();
+                        const uint32_t ah = tmem + (uint32_t)(C::A_COL + 32 * as), al = ah + 16;
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const uint64_t ko = (uint64_t)((2 * half + kk) * 32) >> 4;
+                            mma_f16_ta(main, ah + 8 * kk, bh + ko, idesc, in_chunk | half | kk ? 1u : 0u);
+                            mma_f16_ta(cross, al + 8 * kk, bh + ko, idesc, (kt - kt0) | half | kk ? 1u : 0u);
+                            mma_f16_ta(cross, ah + 8 * kk, bl + ko, idesc, 1u);
+                        }
+                        mma_commit_warp(aempty0 + 8 * as);
                     }
-                    mma_commit(aempty0 + 8 * as);
-                    mma_commit(empty0 + 8 * slot);
+                    mma_commit_warp(empty0 + 8 * slot);
                     if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
-                        mma_commit(accf0 + 8 * buf);
+                        mma_commit_warp(accf0 + 8 * buf);
                         ++chunk;
                     }
                 }
@@ -320,55 +343,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_done:;
         }
     } else if (warp < kWEpi) {
-        // Converters: two sets of four warps take the stages in turn; a thread
-        // owns a row's two blocks of its set's stages and holds the next kAhead
-        // of them in registers.  The row's halves go to its TMEM lane.
-        constexpr int kAhead = WRaw<FMT>::kAhead;
+        // Converters: the two sets of four warps take the two blocks of every
+        // K stage.  A thread owns a row's block; the next kAhead of them are on
+        // their way to its own place in shared memory (asynchronous copies: a
+        // register ring waited for its newest loads), and one is converted
+        // before its place in TMEM (the row's lane) is waited for.
         const int set = (warp - kWConv) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL;
         const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
-        int ft = tile0, fk = kt0, fr = tile0 / ntt * kBM + row;  // fetch cursor
-        auto advance = [&]() {
+        uint8_t *ring = smem + C::RAW_OFF;
+        const int me = threadIdx.x - kWConv * 32;
+        int ft = tile0, fk = kt0, fr = tile0 / ntt * kBM + row, fe = 0;  // fetch cursor
+        auto fetch = [&]() {
+            const int b = 2 * fk + set;
+            const bool on = ft < total && fr < p.rows && b < nb;
+            const size_t blk = on ? (size_t)fr * nb + b : 0;
+            uint8_t *e = ring + fe * C::RAW_BYTES;
+            cp_async(smem_u32(e + me * 16), p.w + 16 * blk, 16, on);
+            if (FMT == kFmtQ4)
+                cp_async(smem_u32(e + kConv * 32 * 16 + me * 4), p.w + p.scale_off + 4 * (blk >> 1), 4, on);
+            else
+                cp_async(smem_u32(e + kConv * 32 * 16 + me * 16), p.w + p.scale_off + 16 * (blk >> 3), 16, on);
+            cp_commit();
+            if (++fe > kAhead) fe = 0;
             if (++fk < kt1) return;
             fk = kt0;
             ft += stride;
             fr = ft / ntt * kBM + row;
         };
-        auto fetch = [&](WRaw<FMT> &w) {
-            const bool on = ft < total && fr < p.rows;
-            w.load(p, (size_t)fr * nb + 2 * fk, on, on && 2 * fk + 1 < nb);
-            advance();
-            advance();
-        };
-        WRaw<FMT> raw[kAhead];
-        if (set) advance();
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(raw[i]);
-        bool ok = true;
-        for (int it0 = set; it0 < n_it && ok; it0 += 2 * kAhead) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int it = it0 + 2 * i, as = it % AST;
-                if (it >= n_it || !ok) break;
-                uint32_t h[16], l[16];
-                convert(raw[i], 0, p.w_scale, h, l);
-                if (lane == 0)
-                    ok = mbar_wait(aempty0 + 8 * as, ((uint32_t)(it / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                tc_fence_after();
-                tmem_st16(lanes + 64 * as, h);
-                tmem_st16(lanes + 64 * as + 32, l);
-                convert(raw[i], 1, p.w_scale, h, l);
-                tmem_st16(lanes + 64 * as + 16, h);
-                tmem_st16(lanes + 64 * as + 48, l);
-                fetch(raw[i]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(afull0 + 8 * as);
+        for (int i = 0; i < kAhead; ++i) fetch();
+        int ce = 0, ck = kt0, cr = tile0 / ntt * kBM + row, ct = tile0;  // cursor of the block converted
+        for (int it = 0; it < n_it; ++it) {
+            const int ab = 2 * it + set, as = ab % AST;
+            fetch();
+            cp_wait<kAhead>();
+            const uint8_t *e = ring + ce * C::RAW_BYTES;
+            WRaw<FMT> raw;
+            raw.c = *(const uint4 *)(e + me * 16);
+            if (FMT == kFmtQ4) {
+                raw.h.x = *(const uint32_t *)(e + kConv * 32 * 16 + me * 4);
+                raw.j = (int)(((size_t)cr * nb + 2 * ck + set) & 1);
+            } else {
+                raw.h = *(const uint4 *)(e + kConv * 32 * 16 + me * 16);
+                raw.j = (2 * ck + set) & 7;
             }
+            if (++ce > kAhead) ce = 0;
+            if (++ck == kt1) {
+                ck = kt0;
+                ct += stride;
+                cr = ct / ntt * kBM + row;
+            }
+            uint32_t h[16], l[16];
+            convert(raw, p.w_scale, h, l);
+            bool ok = true;
+            if (lane == 0)
+                ok = mbar_wait(aempty0 + 8 * as, ((uint32_t)(ab / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            tmem_st16(lanes + 32 * as, h);
+            tmem_st16(lanes + 32 * as + 16, l);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(afull0 + 8 * as);
         }
+        cp_wait<0>();
     } else {
         // Epilogue: TMEM lane quarter = warp % 4 (lane = weight row), one half
         // of the token columns.
@@ -382,6 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float acc[HC];
 #pragma unroll
             for (int i = 0; i < HC; ++i) acc[i] = 0.0f;
+            // the columns' token scales (powers of two): lane i has columns i, i + 32
+            float ts[(HC + 31) / 32];
+#pragma unroll
+            for (int i = 0; i < (HC + 31) / 32; ++i)
+                ts[i] = lane + 32 * i < nc ? __ldcg(p.ws_scale + (size_t)tt * BN + c0 + lane + 32 * i) : 0.0f;
             auto add = [&](uint32_t col) {
 #pragma unroll
                 for (int i = 0; i < HC; i += 16) {
@@ -410,21 +455,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (end) mbar_arrive(crosse);
                 }
             }
-            if (S == 1) {
-                const int row = t / ntt * kBM + r;
+            const int row = t / ntt * kBM + r;
+            float *red = (float *)smem;  // a split tile: its sums [column][row], over the stages it is done with
 #pragma unroll
-                for (int i = 0; i < HC; ++i) {
-                    if (i >= nc) break;  // warp-uniform
-                    const size_t tok = (size_t)tt * BN + c0 + i;
-                    if (row < p.rows) p.y[tok * p.rows + row] = acc[i] * __ldcg(p.ws_scale + tok);
-                }
-            } else {
-                // (all MMAs and copies of this CTA's only tile are done: its
-                // stages' memory takes the partial sums [column][row])
-                float *red = (float *)smem;
-#pragma unroll
-                for (int i = 0; i < HC; ++i)
-                    if (i < nc) red[(c0 + i) * kBM + r] = acc[i];
+            for (int i = 0; i < HC; ++i) {
+                if (i >= nc) break;  // warp-uniform
+                const float v = acc[i] * __shfl_sync(0xffffffffu, ts[i / 32], i % 32);
+                if (S > 1)
+                    red[(c0 + i) * kBM + r] = v;
+                else if (row < p.rows)
+                    p.y[((size_t)tt * BN + c0 + i) * p.rows + row] = v;
             }
         }
     epi_done:;
@@ -441,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int s = 0; s < S; ++s) sum += *cluster.map_shared_rank(red + i, s);
                 const size_t tok = (size_t)tt * BN + i / kBM;
                 const int row = rt * kBM + i % kBM;
-                if (row < p.rows) p.y[tok * p.rows + row] = sum * __ldcg(p.ws_scale + tok);
+                if (row < p.rows) p.y[tok * p.rows + row] = sum;
             }
         }
         __syncwarp();
@@ -472,7 +512,7 @@ int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, n_sm)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = LCfg<BN>::SMEM;
+    cfg.dynamicSmemBytes = LCfg<FMT, BN>::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -494,13 +534,13 @@ int launch_fmt(const LinearGemm &g, int n_sm, cudaStream_t st) {
 template <int FMT>
 int configure_fmt() {
     cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         LCfg<32>::SMEM);
+                                         LCfg<FMT, 32>::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 LCfg<64>::SMEM);
+                                 LCfg<FMT, 64>::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 LCfg<128>::SMEM);
+                                 LCfg<FMT, 128>::SMEM);
     return (int)e;
 }
 
@@ -514,16 +554,7 @@ int linear_gemm_configure() {
 }
 
 int launch_linear_gemm(const LinearGemm &g, int n_sm, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)g.p.n_tokens);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const int rc = (int)cudaLaunchKernelEx(&cfg, linear_split_kernel, g.p);
+    const int rc = g.p.x ? launch_split<true>(g.p, st) : launch_split<false>(g.p, st);
     if (rc) return rc;
     return g.p.fmt == kFmtQ4K ? launch_fmt<kFmtQ4K>(g, n_sm, st) : launch_fmt<kFmtQ4>(g, n_sm, st);
 }
