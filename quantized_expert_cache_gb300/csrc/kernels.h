@@ -185,7 +185,7 @@ struct RouterParams {
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
 constexpr int kLinearSmem = 224 * 1024;             // shared memory of a CTA
-constexpr size_t kLinearResident = 96 * 1024;       // of it, activations held whole
+constexpr size_t kLinearResident = 64 * 1024;       // of it, activations held whole
 struct LinearParams {
     const uint8_t *w;           // the weights in operand order
     const float *x;             // [n_tokens][cols], or null and the codes below

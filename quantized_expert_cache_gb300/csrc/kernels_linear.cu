@@ -18,18 +18,21 @@
 // through TMEM) measured 63 us for 4096 x 4096 at 512 tokens, with larger
 // errors.
 //
-// Weight layout (made at registration): per 16 rows, per group of up to 8
-// blocks: the codes in the instruction's operand order, [block][lane] x 8
-// bytes (lane 4g + t: elements 8t.. of row g, of row g + 8, nibble p of a word
-// element 2p, nibble p + 4 element 2p + 1), then the scales:
-// Q4_0 [block][g] x (binary16 d of rows g, g + 8); Q4_K [block][g] x bytes
-// (sc, m of row g; of row g + 8), then [g] x (d, dmin of row g; of row g + 8).
-// 18 (Q4_K 18.5) bytes to 32 weights, and any run of groups of 16 rows is one
-// contiguous copy.
+// One and two tokens take dp4a on whole blocks instead: 15 warp instructions
+// for 16 x 32 weights and a token against 40 for any 8 tokens.
 //
-// Activation layout: per 8 tokens, per block, 576 bytes: [lane] x 16 (lane
-// 4c + t: the codes 8t.. of token c in binary16), then [t] x 16: d_a of tokens
-// 2t, 2t + 1, and what their products start from.
+// Weight layout (made at registration): per 16 rows, per group of up to 8
+// blocks: the codes [block][row] x 16 bytes in Q4 order, then the scales: Q4_0
+// [block][g] x (binary16 d of rows g, g + 8); Q4_K [block][g] x bytes (sc, m of
+// row g; of row g + 8), then [g] x (d, dmin of row g; of row g + 8).  18 (Q4_K
+// 18.5) bytes to 32 weights, and any run of groups of 16 rows is one contiguous
+// copy.  Lane 4g + t of a product holds word t of rows g and g + 8: elements
+// 4t + (0, 2), 16 + 4t + (0, 2), 4t + (1, 3), 16 + 4t + (1, 3) as its four
+// pairs of K; the sums do not mind the order.
+//
+// Activation layout of the products: per 8 tokens, per block, 576 bytes:
+// [lane] x 16 (lane 4c + t: token c's codes in binary16, in the same order),
+// then [t] x 16: d_a of tokens 2t, 2t + 1, and what their products start from.
 #include <algorithm>
 
 #include "common.cuh"
@@ -89,13 +92,7 @@ __global__ void linear_repack_kernel(const uint8_t *__restrict__ src, uint8_t *_
         }
         sc[0] = s0;
         sc[1] = s1;
-        // element e: byte e % 16, low nibble for e < 16
-        const auto code = [&](int e) { return (w[(e & 15) >> 2] >> (8 * (e & 3) + (e >> 4) * 4)) & 15u; };
-        for (int t = 0; t < 4; ++t) {
-            uint32_t v = 0;
-            for (int k = 0; k < 4; ++k) v |= code(8 * t + 2 * k) << (4 * k) | code(8 * t + 2 * k + 1) << (4 * k + 16);
-            *(uint32_t *)(grp + bi * 256 + (4 * g + t) * 8 + up * 4) = v;
-        }
+        *(uint4 *)(grp + bi * 256 + r * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -130,13 +127,15 @@ __device__ __forceinline__ void code_word(const LinearParams &p, size_t t, int b
 
 // ... into the 576-byte record of its block, token column c of 8.
 __device__ __forceinline__ void put_word(uint8_t *rec, int c, int w, uint32_t code, float dd, int sum, int fmt) {
-    // codes + 128 under the binary16 exponent 0x64: 1152 + q
+    // codes + 128 under the binary16 exponent 0x64: 1152 + q; bytes (0, 2), (1, 3)
     const uint32_t u = code ^ 0x80808080u;
     const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    uint32_t h[2] = {__byte_perm(u, 0x64646464u, 0x4140), __byte_perm(u, 0x64646464u, 0x4342)};
+    uint32_t h[2] = {__byte_perm(u, 0x64646464u, 0x4240), __byte_perm(u, 0x64646464u, 0x4341)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) *(__half2 *)&h[i] = __hsub2(*(__half2 *)&h[i], off);
-    *((uint2 *)(rec + (4 * c + (w >> 1)) * 16) + (w & 1)) = make_uint2(h[0], h[1]);
+    uint32_t *f = (uint32_t *)(rec + (4 * c + (w & 3)) * 16) + (w >> 2);
+    f[0] = h[0];
+    f[2] = h[1];
     if (w == 0) {
         float *s = (float *)(rec + 512 + (c >> 1) * 16) + (c & 1);
         s[0] = dd;
@@ -208,7 +207,9 @@ struct WFrag {
     uint32_t a[8];  // both products' operands
     F2 s[2], m[2];  // scale of each row, twice; Q4_K: its min / 1024, twice
     __device__ __forceinline__ void load(const uint8_t *grp, int n, int b, int lane) {
-        const uint2 c = *(const uint2 *)(grp + b * 256 + lane * 8);
+        uint2 c;
+        c.x = *(const uint32_t *)(grp + b * 256 + lane * 4);
+        c.y = *(const uint32_t *)(grp + b * 256 + 128 + lane * 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             a[2 * k] = ((c.x >> (4 * k)) & 0x000F000Fu) | 0x64006400u;
@@ -236,31 +237,30 @@ struct WFrag {
     }
 };
 
-// where the activations' records come from
-constexpr int kRing = 0;      // workspace, a stage with the weights' stages
-constexpr int kResident = 1;  // workspace, all blocks in shared memory
-constexpr int kStaged = 2;    // x or q and d, made in shared memory
+constexpr int kNW = 16;  // warps of a CTA
 
-// CTA tile: wr x MT x 16 rows, WC x NT x 8 tokens; its NW consumer warps split
-// the rows wr ways, the tokens WC ways and the blocks of a stage wk ways.  CTAs
-// walk the tiles (token tiles innermost: they share the weights in L2).  The
-// producer warp copies group after group into a ring of stages.
-template <int FMT, int MT, int NT, int WC, int NW, int MODE>
-__global__ void __launch_bounds__((NW + 1) * 32, 1) linear_kernel(const __grid_constant__ LinearParams p) {
+// CTA tile: wr x MT x 16 rows, WC x NT x 8 tokens; the warps split the rows wr
+// ways, the tokens WC ways and the blocks of a stage wk ways.  CTAs walk the
+// tiles (token tiles innermost: they share the weights in L2) through a ring of
+// stages of one group of blocks; at each stage another warp requests the stage
+// that the ring has room for.  RES: the records of all blocks stay in shared
+// memory (one token tile), else a stage brings its own.
+template <int FMT, int MT, int NT, int WC, bool RES>
+__global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_constant__ LinearParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const int wr_n = p.wr, wk_n = NW / (WC * wr_n), nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
+    const int wr_n = p.wr, wk_n = kNW / (WC * wr_n), nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
     constexpr int NTC = NT * WC, GB = group_bytes(FMT, kKB), BST = kKB * kBRec;
-    const int a_stage = wr_n * MT * GB, stage = a_stage + (MODE == kRing ? NTC * BST : 0);
+    const int a_stage = wr_n * MT * GB, stage = a_stage + (RES ? 0 : NTC * BST);
     uint8_t *resident = smem + p.stages * stage;
-    float4 *red = (float4 *)(resident + (MODE == kRing ? 0 : (size_t)NTC * nb * kBRec));
-    uint64_t *bars = (uint64_t *)(red + (wk_n > 1 ? NW * MT * NT * 32 : 0));
+    float4 *red = (float4 *)(resident + (RES ? (size_t)NTC * nb * kBRec : 0));
+    uint64_t *bars = (uint64_t *)(red + (wk_n > 1 ? kNW / 2 * MT * NT * 32 : 0));
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * p.stages, bfull = empty0 + 8 * p.stages;
     volatile int *abort_flag = (volatile int *)(bars + 2 * p.stages + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, NW);
+            mbar_init(empty0 + 8 * s, kNW);
         }
         mbar_init(bfull, 1);
         *abort_flag = 0;
@@ -270,14 +270,37 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) linear_kernel(const __grid_c
     const int rt_n = (p.rows + 15) / 16, tile_rt = wr_n * MT, ntt = (p.n_tokens + 8 * NTC - 1) / (8 * NTC);
     const int total = ((rt_n + tile_rt - 1) / tile_rt) * ntt, nt_n = (p.n_tokens + 7) / 8;
     const size_t rt_bytes = tile_bytes(FMT, nb);
+    const int n_it = ((total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * ng;
 
-    if (warp == NW) {
-        // producer: lanes 0..tile_rt-1 copy a row tile's group, and (kRing)
-        // lanes 0..NTC-1 the tokens' records of the group
-        bool waited = MODE != kRing;  // the weights are the context's own; the records the preceding kernel's
-        if (MODE == kResident) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            asm volatile("griddepcontrol.launch_dependents;");
+    // Request stage j: lanes 0..tile_rt-1 a row tile's group each, lanes
+    // 0..NTC-1 the tokens' records of the group.  The weights are the context's
+    // own; the records are the preceding kernel's (part: 1 weights, 2 records).
+    auto request = [&](int j, int part) {
+        const int t = blockIdx.x + j / ng * gridDim.x, g = j % ng, slot = j % p.stages, n = min(kKB, nb - g * kKB);
+        const int rt0 = t / ntt * tile_rt, n_rt = min(tile_rt, rt_n - rt0);
+        const int nt0 = t % ntt * NTC, n_nt = RES ? 0 : min(NTC, nt_n - nt0);
+        const uint32_t full = full0 + 8 * slot, dst = smem_u32(smem + slot * stage);
+        if (part & 1) {
+            bool ok = true;
+            if (lane == 0) {
+                ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(j / p.stages) & 1u) ^ 1u, abort_flag, p.error, 2);
+                if (ok) mbar_arrive_tx(full, (uint32_t)(n_rt * group_bytes(FMT, n) + n_nt * n * kBRec));
+            }
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+            if (lane < n_rt)
+                bulk_load(dst + lane * GB, p.w + (size_t)(rt0 + lane) * rt_bytes + (size_t)g * GB, group_bytes(FMT, n),
+                          full);
+        }
+        if ((part & 2) && lane < n_nt)
+            bulk_load(dst + a_stage + lane * BST, p.ws + ((size_t)(nt0 + lane) * nb + g * kKB) * kBRec,
+                      (uint32_t)(n * kBRec), full);
+    };
+    if (warp == 0) {
+        const int first = min(p.stages - 1, n_it);
+        for (int j = 0; j < first; ++j) request(j, 1);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
+        if (RES) {
             const int n = min(NTC, nt_n);
             if (lane == 0) mbar_arrive_tx(bfull, (uint32_t)(n * nb * kBRec));
             __syncwarp();
@@ -285,148 +308,99 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) linear_kernel(const __grid_c
                 bulk_load(smem_u32(resident + (size_t)lane * nb * kBRec), p.ws + (size_t)lane * nb * kBRec,
                           (uint32_t)(nb * kBRec), bfull);
         }
-        int it = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
-            const int rt0 = t / ntt * tile_rt, n_rt = min(tile_rt, rt_n - rt0);
-            const int nt0 = t % ntt * NTC, n_nt = MODE == kRing ? min(NTC, nt_n - nt0) : 0;
-            for (int g = 0; g < ng; ++g, ++it) {
-                const int slot = it % p.stages, n = min(kKB, nb - g * kKB);
-                const uint32_t full = full0 + 8 * slot, dst = smem_u32(smem + slot * stage);
-                bool ok = true;
-                if (lane == 0) {
-                    ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / p.stages) & 1u) ^ 1u, abort_flag, p.error, 2);
-                    if (ok)
-                        mbar_arrive_tx(full, (uint32_t)(n_rt * group_bytes(FMT, n) + n_nt * n * kBRec));
-                }
-                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) goto done;
-                for (int i = lane; i < n_rt; i += 32)
-                    bulk_load(dst + i * GB, p.w + (size_t)(rt0 + i) * rt_bytes + (size_t)g * GB, group_bytes(FMT, n),
-                              full);
-                if (MODE == kRing) {
-                    if (!waited) {
-                        asm volatile("griddepcontrol.wait;" ::: "memory");
-                        asm volatile("griddepcontrol.launch_dependents;");
-                        waited = true;
-                    }
-                    if (lane < n_nt)
-                        bulk_load(dst + a_stage + lane * BST, p.ws + ((size_t)(nt0 + lane) * nb + g * kKB) * kBRec,
-                                  (uint32_t)(n * kBRec), full);
+        for (int j = 0; j < first; ++j) request(j, 2);
+    }
+    // a wait that expires leaves garbage and an error bit; the warp goes on, so
+    // that the others' barriers complete
+    const int wc = warp % WC, wr = warp / WC % wr_n, wk = warp / (WC * wr_n);
+    if (RES) mbar_wait(bfull, 0, abort_flag, p.error, 4);
+    int it = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        F2 acc[MT][NT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = f2(0.0f, 0.0f);
+        for (int g = 0; g < ng; ++g, ++it) {
+            const int slot = it % p.stages, n = min(kKB, nb - g * kKB);
+            if (warp == it % kNW && it + p.stages - 1 < n_it) request(it + p.stages - 1, 3);
+            mbar_wait(full0 + 8 * slot, (uint32_t)(it / p.stages) & 1u, abort_flag, p.error, 4);
+            const uint8_t *ga = smem + slot * stage + wr * MT * GB;
+            const uint8_t *gb = RES ? resident + (size_t)g * kKB * kBRec : smem + slot * stage + a_stage + wc * NT * BST;
+            const size_t b_tile = RES ? (size_t)nb * kBRec : BST;
+            for (int b = wk; b < n; b += wk_n) {
+                WFrag<FMT> wf[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) wf[m].load(ga + m * GB, n, b, lane);
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    const uint8_t *rec = gb + c * b_tile + b * kBRec;
+                    const uint4 x = *(const uint4 *)(rec + lane * 16);
+                    const float4 sc = *(const float4 *)(rec + 512 + (lane & 3) * 16);
+                    const F2 da = f2(sc.x, sc.y);
+                    float d[MT][4];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma_f16_sync(d[m], wf[m].a, x.x, x.y, sc.z, sc.w, sc.z, sc.w);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        mma_f16_sync(d[m], wf[m].a + 4, x.z, x.w, d[m][0], d[m][1], d[m][2], d[m][3]);
+                    // Q4_K: -1024 d_a sum q_a times min / 1024
+                    const F2 e = FMT == kFmtQ4K ? mul2(da, f2(sc.z, sc.w)) : da;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const F2 v = mul2(f2(d[m][2 * h], d[m][2 * h + 1]), da);
+                            acc[m][c][h] = fma2(wf[m].s[h], v, acc[m][c][h]);
+                            if (FMT == kFmtQ4K) acc[m][c][h] = fma2(wf[m].m[h], e, acc[m][c][h]);
+                        }
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * slot);
         }
-    done:;
-    } else {
-        const int wc = warp % WC, wr = warp / WC % wr_n, wk = warp / (WC * wr_n);
-        if (MODE == kStaged) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            asm volatile("griddepcontrol.launch_dependents;");
-            for (int i0 = warp * 32; i0 < 8 * NTC * nb * 8; i0 += NW * 32) {
-                const int i = i0 + lane, w = i & 7, b = (i >> 3) % nb, t = (i >> 3) / nb;
-                uint32_t code;
-                float dd;
-                int sum;
-                code_word(p, t, b, w, t < p.n_tokens, code, dd, sum);
-                if (t < 8 * NTC) put_word(resident + ((size_t)(t >> 3) * nb + b) * kBRec, t & 7, w, code, dd, sum, FMT);
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
-        } else if (MODE == kResident) {
-            mbar_wait(bfull, 0, abort_flag, p.error, 4);
-        }
-        int it = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
-            F2 acc[MT][NT][2];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = f2(0.0f, 0.0f);
-            for (int g = 0; g < ng; ++g, ++it) {
-                const int slot = it % p.stages, n = min(kKB, nb - g * kKB);
-                // a wait that expires leaves garbage and an error bit; the warp goes on, so that
-                // the others' barriers complete
-                mbar_wait(full0 + 8 * slot, (uint32_t)(it / p.stages) & 1u, abort_flag, p.error, 4);
-                const uint8_t *ga = smem + slot * stage + wr * MT * GB;
-                const uint8_t *gb = MODE == kRing ? smem + slot * stage + a_stage + wc * NT * BST
-                                                  : resident + (size_t)g * kKB * kBRec;
-                const size_t b_tile = MODE == kRing ? BST : (size_t)nb * kBRec;
-#pragma unroll 2
-                for (int b = wk; b < n; b += wk_n) {
-                    WFrag<FMT> wf[MT];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) wf[m].load(ga + m * GB, n, b, lane);
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const uint8_t *rec = gb + c * b_tile + b * kBRec;
-                        const uint4 x = *(const uint4 *)(rec + lane * 16);
-                        const float4 sc = *(const float4 *)(rec + 512 + (lane & 3) * 16);
-                        const F2 da = f2(sc.x, sc.y);
-                        float d[MT][4];
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) mma_f16_sync(d[m], wf[m].a, x.x, x.y, sc.z, sc.w, sc.z, sc.w);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            mma_f16_sync(d[m], wf[m].a + 4, x.z, x.w, d[m][0], d[m][1], d[m][2], d[m][3]);
-                        // Q4_K: -1024 d_a sum q_a times min / 1024
-                        const F2 e = FMT == kFmtQ4K ? mul2(da, f2(sc.z, sc.w)) : da;
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const F2 v = mul2(f2(d[m][2 * h], d[m][2 * h + 1]), da);
-                                acc[m][c][h] = fma2(wf[m].s[h], v, acc[m][c][h]);
-                                if (FMT == kFmtQ4K) acc[m][c][h] = fma2(wf[m].m[h], e, acc[m][c][h]);
-                            }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty0 + 8 * slot);
-            }
-            // lane 4g + q: rows g, g + 8 of a 16-row tile, tokens 2q, 2q + 1
-            const int row0 = (t / ntt * tile_rt + wr * MT) * 16 + (lane >> 2);
-            const int tok0 = (t % ntt * NTC + wc * NT) * 8 + (lane & 3) * 2;
-            auto store = [&](int m, int c, const float4 &v) {
-                const int row = row0 + m * 16, tok = tok0 + c * 8;
-                float *y = p.y + (size_t)tok * p.rows + row;
-                if (tok < p.n_tokens) {
-                    if (row < p.rows) y[0] = v.x;
-                    if (row + 8 < p.rows) y[8] = v.z;
-                }
-                if (tok + 1 < p.n_tokens) {
-                    if (row < p.rows) y[p.rows] = v.y;
-                    if (row + 8 < p.rows) y[(size_t)p.rows + 8] = v.w;
-                }
-            };
-            if (wk_n == 1) {
+        // join the warps of one row and token share: the upper half of them
+        // hands its sums to the lower half, until one is left
+        for (int half = wk_n / 2; half > 0; half /= 2) {
+            float4 *r = red + ((warp - (wk >= half ? half * wr_n * WC : 0)) * MT * NT) * 32 + lane;
+            if (wk >= half && wk < 2 * half) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
                         const float2 u = un2(acc[m][c][0]), v = un2(acc[m][c][1]);
-                        store(m, c, make_float4(u.x, u.y, v.x, v.y));
+                        r[(m * NT + c) * 32] = make_float4(u.x, u.y, v.x, v.y);
                     }
-            } else {
-                // the warps of one row and token share add up in block order
+            }
+            __syncthreads();
+            if (wk < half) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
+                        const float4 o = r[(m * NT + c) * 32];
                         const float2 u = un2(acc[m][c][0]), v = un2(acc[m][c][1]);
-                        red[(warp * MT * NT + m * NT + c) * 32 + lane] = make_float4(u.x, u.y, v.x, v.y);
+                        acc[m][c][0] = f2(u.x + o.x, u.y + o.y);
+                        acc[m][c][1] = f2(v.x + o.z, v.y + o.w);
                     }
-                asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
-                for (int i = wk; i < MT * NT; i += wk_n) {
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int k = 0; k < wk_n; ++k) {
-                        const float4 u = red[(((k * wr_n + wr) * WC + wc) * MT * NT + i) * 32 + lane];
-                        v.x += u.x;
-                        v.y += u.y;
-                        v.z += u.z;
-                        v.w += u.w;
-                    }
-                    store(i / NT, i % NT, v);
-                }
-                asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
             }
+            __syncthreads();
         }
+        if (wk > 0) continue;
+        // lane 4g + q: rows g, g + 8 of a 16-row tile, tokens 2q, 2q + 1
+        const int row0 = (t / ntt * tile_rt + wr * MT) * 16 + (lane >> 2);
+        const int tok0 = (t % ntt * NTC + wc * NT) * 8 + (lane & 3) * 2;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = row0 + m * 16 + h * 8, tok = tok0 + c * 8;
+                    const float2 v = un2(acc[m][c][h]);
+                    if (row < p.rows && tok < p.n_tokens) p.y[(size_t)tok * p.rows + row] = v.x;
+                    if (row < p.rows && tok + 1 < p.n_tokens) p.y[(size_t)(tok + 1) * p.rows + row] = v.y;
+                }
     }
     // after an abort, give the copies in flight a bounded time (about 10 ms) to land
     __syncthreads();
@@ -437,31 +411,107 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) linear_kernel(const __grid_c
     }
 }
 
-// ---- launch ---------------------------------------------------------------------
-template <int FMT, int MT, int NT, int WC, int NW, int MODE>
-int launch_tile(LinearParams p, int wr, int n_sm, cudaStream_t st) {
-    auto kernel = linear_kernel<FMT, MT, NT, WC, NW, MODE>;
-    const int nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
-    const size_t stage = (size_t)wr * MT * group_bytes(FMT, kKB) + (MODE == kRing ? (size_t)NT * WC * kKB * kBRec : 0);
-    const size_t fixed = (MODE == kRing ? 0 : (size_t)NT * WC * nb * kBRec) +
-                         (NW / (WC * wr) > 1 ? (size_t)NW * MT * NT * 512 : 0) + 512;
-    const int tiles = ((p.rows + 16 * MT * wr - 1) / (16 * MT * wr)) * ((p.n_tokens + 8 * NT * WC - 1) / (8 * NT * WC));
-    const int grid = std::min(tiles, n_sm), need = ng * ((tiles + grid - 1) / grid);
-    p.wr = wr;
-    p.stages = (int)std::min<size_t>({(kLinearSmem - fixed) / stage, (size_t)need, (size_t)16});
-    if (p.stages < 1) return (int)cudaErrorInvalidValue;
-    static bool configured[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !configured[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinearSmem);
-        if (e != cudaSuccess) return (int)e;
-        if (dev >= 0 && dev < 64) configured[dev] = true;
+// ---- one and two tokens -----------------------------------------------------------
+// A lane owns a row of the tile and the blocks of its half warp; the CTA's
+// warps take the tile's block pairs in turn, kFly pairs in flight each, the
+// next tile's first ones requested before this tile's sums are joined.
+constexpr int kVecWarps = 8, kFly = 4;
+
+template <int FMT>
+struct VBlock {
+    uint4 c;
+    uint32_t s, dm;  // Q4_0: d; Q4_K: (sc, m) and (d, dmin)
+    __device__ __forceinline__ void load(const uint8_t *tile, int nb, int b, int r) {
+        const int n = min(kKB, nb - b / kKB * kKB), bi = b % kKB;
+        const uint8_t *grp = tile + (size_t)(b / kKB) * group_bytes(FMT, kKB);
+        c = ld_weights((const uint4 *)(grp + bi * 256 + r * 16));
+        s = __ldcs((const unsigned short *)(grp + n * 256 + bi * 32) + (r & 7) * 2 + (r >> 3));
+        if (FMT == kFmtQ4K) dm = __ldg((const uint32_t *)(grp + kKB * kARec) + (r & 7) * 2 + (r >> 3));
     }
+    // acc += the block's term: raw = sum q_w q_a, the activations' scale and code sum
+    __device__ __forceinline__ float term(int raw, const BlockScale &x, float acc) const {
+        if (FMT == kFmtQ4)
+            return fmaf((float)(raw - 8 * x.s), __half2float(__ushort_as_half((unsigned short)s)) * x.d, acc);
+        const float2 d = __half22float2(*(const __half2 *)&dm);
+        acc = fmaf(d.x * (float)(s & 255), x.d * (float)raw, acc);
+        return fmaf(-d.y * (float)(s >> 8), x.d * (float)x.s, acc);
+    }
+};
+
+template <int FMT, int TN>
+__global__ void __launch_bounds__(kVecWarps * 32) linear_vec_kernel(const __grid_constant__ LinearParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[2][kVecWarps][TN][16];
+    const int nb = p.cols / kBlock, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane & 15;
+    int4 *x0 = (int4 *)smem, *x1 = x0 + TN * nb;  // codes: elements 0..15 and 16..31 of a block, [TN][nb]
+    BlockScale *xs = (BlockScale *)(x1 + TN * nb);
+    const int rt_n = (p.rows + 15) / 16, first = 2 * warp + (lane >> 4);
+    const size_t rt_bytes = tile_bytes(FMT, nb);
+    VBlock<FMT> w[kFly];
+    auto fetch = [&](int tile, int b0) {
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            const int b = b0 + i * 2 * kVecWarps;
+            if (b < nb) w[i].load(p.w + tile * rt_bytes, nb, b, r);
+        }
+    };
+    // the weights are the context's own: requested before the wait
+    if ((int)blockIdx.x < rt_n) fetch(blockIdx.x, first);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    // the activations: 8 lanes a block, 4 values a lane (whole warps run every round)
+    for (int i0 = warp * 32; i0 < TN * nb * 8; i0 += kVecWarps * 32) {
+        const int i = i0 + lane, q = i & 7, tb = i >> 3, t = TN > 1 && tb >= nb ? 1 : 0, b = tb - t * nb;
+        uint32_t code;
+        float dd;
+        int sum;
+        code_word(p, t, b, q, tb < TN * nb, code, dd, sum);
+        if (tb >= TN * nb) continue;
+        ((uint32_t *)(q < 4 ? x0 : x1))[tb * 4 + (q & 3)] = code;
+        if (q == 0) xs[tb] = BlockScale{dd, sum};
+    }
+    __syncthreads();
+    int turn = 0;
+    for (int tile = blockIdx.x; tile < rt_n; tile += gridDim.x, turn ^= 1) {
+        float acc[TN];
+#pragma unroll
+        for (int t = 0; t < TN; ++t) acc[t] = 0.0f;
+        for (int b0 = first; b0 - (lane >> 4) < nb; b0 += kFly * 2 * kVecWarps) {
+            if (b0 != first) fetch(tile, b0);
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                const int b = b0 + i * 2 * kVecWarps;
+                if (b < nb)
+#pragma unroll
+                    for (int t = 0; t < TN; ++t)
+                        acc[t] = w[i].term(q4_dot_raw(w[i].c, x0[t * nb + b], x1[t * nb + b]), xs[t * nb + b], acc[t]);
+            }
+        }
+        if (tile + (int)gridDim.x < rt_n) fetch(tile + gridDim.x, first);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], 16);
+            if (lane < 16) red[turn][warp][t][r] = acc[t];
+        }
+        __syncthreads();
+        // (the other buffer of red is free: its readers have passed this barrier)
+        if (threadIdx.x < 16 * TN) {
+            const int t = threadIdx.x / 16, row = tile * 16 + threadIdx.x % 16;
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kVecWarps; ++k) v += red[turn][k][t][threadIdx.x % 16];
+            if (row < p.rows && t < p.n_tokens) p.y[(size_t)t * p.rows + row] = v;
+        }
+    }
+}
+
+// ---- launch ---------------------------------------------------------------------
+template <typename K>
+int launch_pdl(K kernel, dim3 grid, unsigned block, size_t smem, const LinearParams &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((NW + 1) * 32);
-    cfg.dynamicSmemBytes = p.stages * stage + fixed;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -471,65 +521,82 @@ int launch_tile(LinearParams p, int wr, int n_sm, cudaStream_t st) {
     return (int)cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// The row split of the least time: rounds of tiles over the SMs times a tile's
-// rows, a fixed cost of 16 rows' worth for each tile; the tallest of equals.
-int pick_wr(const LinearParams &p, int mt, int nt, int n_sm) {
-    int best = 8;
-    long cost = -1;
-    for (int wr = 8; wr >= 1; wr /= 2) {
-        const long h = 16L * mt * wr, tiles = (p.rows + h - 1) / h * ((p.n_tokens + 8 * nt - 1) / (8 * nt));
-        const long c = (tiles + n_sm - 1) / n_sm * (h + 16);
-        if (cost < 0 || c < cost) {
-            cost = c;
-            best = wr;
-        }
-    }
-    return best;
+// The kernel may use up to kLinearSmem bytes on the current device (asked once).
+template <typename K>
+int allow_smem(K kernel, bool (&done)[64]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && done[dev]) return 0;
+    const int rc = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinearSmem);
+    if (!rc && dev >= 0 && dev < 64) done[dev] = true;
+    return rc;
 }
 
-int launch_prepare(const LinearParams &p, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((p.n_tokens + 7) / 8), (unsigned)((p.cols / kBlock + 3) / 4));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, linear_prepare_kernel, p);
+template <int FMT, int MT, int NT, int WC, bool RES>
+int launch_tile(LinearParams p, int wr, int n_sm, cudaStream_t st) {
+    static bool done[64];
+    auto kernel = linear_kernel<FMT, MT, NT, WC, RES>;
+    int rc = allow_smem(kernel, done);
+    if (rc) return rc;
+    const int nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
+    const size_t stage = (size_t)wr * MT * group_bytes(FMT, kKB) + (RES ? 0 : (size_t)NT * WC * kKB * kBRec);
+    const size_t fixed = (RES ? (size_t)NT * WC * nb * kBRec : 0) +
+                         (kNW / (WC * wr) > 1 ? (size_t)kNW / 2 * MT * NT * 512 : 0) + 512;
+    const int tiles = ((p.rows + 16 * MT * wr - 1) / (16 * MT * wr)) * ((p.n_tokens + 8 * NT * WC - 1) / (8 * NT * WC));
+    const int grid = std::min(tiles, n_sm), need = ng * ((tiles + grid - 1) / grid) + 1;
+    p.wr = wr;
+    p.stages = (int)std::min<size_t>({(kLinearSmem - fixed) / stage, (size_t)need, (size_t)16});
+    if (p.stages < 2) return (int)cudaErrorInvalidValue;
+    rc = launch_pdl(linear_prepare_kernel, dim3((unsigned)((p.n_tokens + 7) / 8), (unsigned)((nb + 3) / 4)), 256, 0, p,
+                    st);
+    return rc ? rc : launch_pdl(kernel, dim3((unsigned)grid), kNW * 32, p.stages * stage + fixed, p, st);
 }
 
-template <int FMT, int MT, int NT, int NW>
+// Time of a row split, in rows: rounds of tiles over the SMs times a tile's
+// rows and 16 rows' worth for each tile.
+long split_cost(const LinearParams &p, int h, int nt, int n_sm) {
+    const long tiles = (p.rows + h - 1L) / h * ((p.n_tokens + 8 * nt - 1) / (8 * nt));
+    return (tiles + n_sm - 1) / n_sm * (h + 16);
+}
+
+template <int FMT, int NT>
 int launch_small(const LinearParams &p, int n_sm, cudaStream_t st) {
-    const int wr = pick_wr(p, MT, NT, n_sm);
-    const size_t records = (size_t)NT * (p.cols / kBlock) * kBRec;
-    if (p.n_tokens <= 8 * NT && records <= kLinearResident) {
-        if (p.n_tokens == 1) return launch_tile<FMT, MT, NT, 1, NW, kStaged>(p, wr, n_sm, st);
-        const int rc = launch_prepare(p, st);
-        return rc ? rc : launch_tile<FMT, MT, NT, 1, NW, kResident>(p, wr, n_sm, st);
+    int best = 256;
+    for (int h = 128; h >= 32; h /= 2)
+        if (split_cost(p, h, NT, n_sm) < split_cost(p, best, NT, n_sm)) best = h;
+    if (p.n_tokens <= 8 * NT && (size_t)NT * (p.cols / kBlock) * kBRec <= kLinearResident) {
+        if (best == 32) return launch_tile<FMT, 1, NT, 1, true>(p, 2, n_sm, st);
+        return launch_tile<FMT, 2, NT, 1, true>(p, best / 32, n_sm, st);
     }
-    const int rc = launch_prepare(p, st);
-    return rc ? rc : launch_tile<FMT, MT, NT, 1, NW, kRing>(p, wr, n_sm, st);
+    if (best == 32) return launch_tile<FMT, 1, NT, 1, false>(p, 2, n_sm, st);
+    return launch_tile<FMT, 2, NT, 1, false>(p, best / 32, n_sm, st);
+}
+
+template <int FMT, int TN>
+int launch_vec(const LinearParams &p, int n_sm, cudaStream_t st) {
+    static bool done[64];
+    const int rc = allow_smem(linear_vec_kernel<FMT, TN>, done);
+    if (rc) return rc;
+    const size_t smem = (size_t)TN * (p.cols / kBlock) * (32 + sizeof(BlockScale));
+    const int fit = (int)std::max<size_t>(1, std::min<size_t>(4, kLinearSmem / (smem + 2048)));
+    return launch_pdl(linear_vec_kernel<FMT, TN>, dim3((unsigned)std::min((p.rows + 15) / 16, n_sm * fit)),
+                      kVecWarps * 32, smem, p, st);
 }
 
 template <int FMT>
 int launch_fmt(const LinearParams &p, int n_sm, cudaStream_t st) {
+    if (p.n_tokens == 1) return launch_vec<FMT, 1>(p, n_sm, st);
+    if (p.n_tokens == 2 && 2 * (p.cols / kBlock) * 40 <= kLinearSmem) return launch_vec<FMT, 2>(p, n_sm, st);
     const int nt = (p.n_tokens + 7) / 8;
-    if (nt == 1) {
-        if (p.rows <= 16 * n_sm) return launch_small<FMT, 1, 1, 16>(p, n_sm, st);
-        return launch_small<FMT, 2, 1, 16>(p, n_sm, st);
-    }
-    if (nt == 2) return launch_small<FMT, 2, 2, 16>(p, n_sm, st);
-    if (nt <= 4) return launch_small<FMT, 2, 4, 8>(p, n_sm, st);
-    // 256 rows x 64 tokens where that fills the SMs
-    if ((long)((p.rows + 255) / 256) * ((nt + 7) / 8) * 4 >= 3L * n_sm) {
-        const int rc = launch_prepare(p, st);
-        return rc ? rc : launch_tile<FMT, 4, 4, 2, 8, kRing>(p, 4, n_sm, st);
-    }
-    if (nt == 5) return launch_small<FMT, 2, 5, 8>(p, n_sm, st);
-    if (nt == 6) return launch_small<FMT, 2, 6, 8>(p, n_sm, st);
-    return launch_small<FMT, 2, 8, 8>(p, n_sm, st);
+    if (nt == 1) return launch_small<FMT, 1>(p, n_sm, st);
+    if (nt == 2) return launch_small<FMT, 2>(p, n_sm, st);
+    if (nt <= 4) return launch_small<FMT, 4>(p, n_sm, st);
+    // 256 rows x 64 tokens where that fills three quarters of the SMs
+    if ((long)((p.rows + 255) / 256) * ((nt + 7) / 8) * 4 >= 3L * n_sm)
+        return launch_tile<FMT, 2, 4, 2, false>(p, 8, n_sm, st);
+    if (nt == 5) return launch_small<FMT, 5>(p, n_sm, st);
+    if (nt == 6) return launch_small<FMT, 6>(p, n_sm, st);
+    return launch_small<FMT, 8>(p, n_sm, st);
 }
 
 }  // namespace
