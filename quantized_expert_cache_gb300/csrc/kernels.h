@@ -195,7 +195,7 @@ struct LinearParams {
     uint8_t *ws;                // linear_ws_bytes(max tokens, cols): the activations in operand order
     int *error;                 // a bit set when a bounded wait expires
     int fmt, rows, cols, n_tokens;
-    int wr, stages;             // set by the launch: row split of a CTA's warps, ring stages
+    int wr, ws_n, stages;       // set by the launch: row and stage split of a CTA's warps, ring stages
 };
 
 int launch_rms_norm(const NormParams &p, cudaStream_t st);

@@ -5,11 +5,13 @@
 //   Q4_0: d_w d_a sum_i (q_w,i - 8) q_a,i
 //   Q4_K: d sc_j d_a sum_i q_w,i q_a,i - dmin m_j d_a sum_i q_a,i
 //
-// Block dots on the tensor cores, exactly: a nibble under the binary16 exponent
-// 0x64 is 1024 + q, an activation code is a binary16 integer, and the two
-// m16n8k16 products of a block start from -1032 (Q4_K: -1024) times the code
-// sum, so that they end at the block's dot; every partial sum is an integer
-// below 2^23, which fp32 holds.  The sums stay in registers and their scaling
+// Block dots on the tensor cores, exactly: a low nibble under the binary16
+// exponent 0x64 is 1024 + q, a high one in its place 1024 + 16 q; the codes of
+// the low nibbles' elements (0..15) are binary16 integers, those of the high
+// ones' (16..31) sixteenths, and the two m16n8k16 products of a block start
+// from minus what the 1024s (and Q4_0's offset 8) add, -(1024 S_lo + 64 S_hi +
+// 8 S) of the code sums, so that they end at the block's dot.  Every partial
+// sum is a multiple of 1 below 2^24 (64 a + a q and the like), which fp32 holds.  The sums stay in registers and their scaling
 // costs two packed fp32 operations for two sums.  That is why this runs on
 // mma.sync (594 TFLOP/s of f16 measured; s8 151, dp4a 149, e4m3 lowered to
 // f16): tcgen05 leaves its sums in TMEM, where reading every block's sums back
@@ -30,9 +32,10 @@
 // 4t + (0, 2), 16 + 4t + (0, 2), 4t + (1, 3), 16 + 4t + (1, 3) as its four
 // pairs of K; the sums do not mind the order.
 //
-// Activation layout of the products: per 8 tokens, per block, 576 bytes:
-// [lane] x 16 (lane 4c + t: token c's codes in binary16, in the same order),
-// then [t] x 16: d_a of tokens 2t, 2t + 1, and what their products start from.
+// Activation layout of the products: per 8 tokens, per block: [lane] x 16
+// bytes (lane 4c + t: token c's codes in binary16, in the same order), then for
+// tokens 2t, 2t + 1: [t] x 16 what their products start from, twice; [t] x 8
+// d_a; Q4_K: [t] x 8 d_a times the code sum.
 #include <algorithm>
 
 #include "common.cuh"
@@ -46,7 +49,8 @@ using namespace gemm;
 
 constexpr int kKB = 8;            // blocks of a group: a pipeline stage
 constexpr int kARec = 16 * 18;    // bytes of 16 rows of a Q4_0 block
-constexpr int kBRec = 576;        // bytes of 8 tokens of a block
+// bytes of 8 tokens of a block: codes, starting values, scales (Q4_K: and sums)
+__host__ __device__ constexpr int act_bytes(int fmt) { return 512 + 64 + 32 + (fmt == kFmtQ4K ? 32 : 0); }
 
 // bytes of a group of n blocks of 16 rows, and of all nb
 __host__ __device__ constexpr int group_bytes(int fmt, int n) { return n * kARec + (fmt == kFmtQ4K ? 64 : 0); }
@@ -98,7 +102,8 @@ __global__ void linear_repack_kernel(const uint8_t *__restrict__ src, uint8_t *_
 
 // ---- activations --------------------------------------------------------------
 // Word w (elements 4w..4w+3) of token t's block b: the code word, the scale
-// and, over the block's 8 lanes, the code sum.  All lanes of a warp call.
+// and, over the 4 lanes of the block's half, the code sum.  All lanes of a warp
+// call.
 __device__ __forceinline__ void code_word(const LinearParams &p, size_t t, int b, int w, bool on, uint32_t &code,
                                           float &dd, int &sum) {
     code = 0;
@@ -121,25 +126,30 @@ __device__ __forceinline__ void code_word(const LinearParams &p, size_t t, int b
         dd = __half2float(__ushort_as_half(__ldcg((const unsigned short *)p.d + t * (p.cols / kBlock) + b)));
     }
     sum = __dp4a((int)code, 0x01010101, 0);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 }
 
-// ... into the 576-byte record of its block, token column c of 8.
+// ... into the record of its block, token column c of 8 (all lanes call).
 __device__ __forceinline__ void put_word(uint8_t *rec, int c, int w, uint32_t code, float dd, int sum, int fmt) {
     // codes + 128 under the binary16 exponent 0x64: 1152 + q; bytes (0, 2), (1, 3)
     const uint32_t u = code ^ 0x80808080u;
     const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const __half2 unit = w < 4 ? __float2half2_rn(1.0f) : __float2half2_rn(0.0625f);
     uint32_t h[2] = {__byte_perm(u, 0x64646464u, 0x4240), __byte_perm(u, 0x64646464u, 0x4341)};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) *(__half2 *)&h[i] = __hsub2(*(__half2 *)&h[i], off);
+    for (int i = 0; i < 2; ++i) *(__half2 *)&h[i] = __hmul2(__hsub2(*(__half2 *)&h[i], off), unit);
     uint32_t *f = (uint32_t *)(rec + (4 * c + (w & 3)) * 16) + (w >> 2);
     f[0] = h[0];
     f[2] = h[1];
+    const int high = __shfl_down_sync(0xffffffffu, sum, 4);
     if (w == 0) {
-        float *s = (float *)(rec + 512 + (c >> 1) * 16) + (c & 1);
-        s[0] = dd;
-        s[2] = (fmt == kFmtQ4K ? -1024.0f : -1032.0f) * (float)sum;
+        const int all = sum + high;
+        const float start = -(float)(1024 * sum + 64 * high + (fmt == kFmtQ4K ? 0 : 8 * all));
+        float *st = (float *)(rec + 512 + (c >> 1) * 16) + (c & 1);
+        st[0] = st[2] = start;
+        *((float *)(rec + 576 + (c >> 1) * 8) + (c & 1)) = dd;
+        if (fmt == kFmtQ4K) *((float *)(rec + 608 + (c >> 1) * 8) + (c & 1)) = dd * (float)all;
     }
 }
 
@@ -148,17 +158,18 @@ __device__ __forceinline__ void put_word(uint8_t *rec, int c, int w, uint32_t co
 __global__ void __launch_bounds__(256) linear_prepare_kernel(LinearParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ __align__(16) uint8_t rec[4 * kBRec];
+    __shared__ __align__(16) uint8_t rec[4 * act_bytes(kFmtQ4K)];
+    const int bytes = act_bytes(p.fmt);
     const int nb = p.cols / kBlock, w = threadIdx.x & 7, c = (threadIdx.x >> 3) & 7, bi = threadIdx.x >> 6;
     const int b = blockIdx.y * 4 + bi, t = blockIdx.x * 8 + c, n = min(4, nb - (int)blockIdx.y * 4);
     uint32_t code;
     float dd;
     int sum;
     code_word(p, t, b, w, t < p.n_tokens && b < nb, code, dd, sum);
-    put_word(rec + bi * kBRec, c, w, code, dd, sum, p.fmt);
+    put_word(rec + bi * bytes, c, w, code, dd, sum, p.fmt);
     __syncthreads();
-    uint4 *out = (uint4 *)(p.ws + ((size_t)blockIdx.x * nb + blockIdx.y * 4) * kBRec);
-    for (int i = threadIdx.x; i < n * (kBRec / 16); i += 256) out[i] = ((const uint4 *)rec)[i];
+    uint4 *out = (uint4 *)(p.ws + ((size_t)blockIdx.x * nb + blockIdx.y * 4) * bytes);
+    for (int i = threadIdx.x; i < n * (bytes / 16); i += 256) out[i] = ((const uint4 *)rec)[i];
 }
 
 // ---- the product ----------------------------------------------------------------
@@ -205,15 +216,15 @@ __device__ __forceinline__ float2 un2(F2 a) {
 template <int FMT>
 struct WFrag {
     uint32_t a[8];  // both products' operands
-    F2 s[2], m[2];  // scale of each row, twice; Q4_K: its min / 1024, twice
+    F2 s[2], m[2];  // scale of each row, twice; Q4_K: minus its min, twice
     __device__ __forceinline__ void load(const uint8_t *grp, int n, int b, int lane) {
-        uint2 c;
-        c.x = *(const uint32_t *)(grp + b * 256 + lane * 4);
-        c.y = *(const uint32_t *)(grp + b * 256 + 128 + lane * 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            a[2 * k] = ((c.x >> (4 * k)) & 0x000F000Fu) | 0x64006400u;
-            a[2 * k + 1] = ((c.y >> (4 * k)) & 0x000F000Fu) | 0x64006400u;
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t c = *(const uint32_t *)(grp + b * 256 + r * 128 + lane * 4);
+            a[r] = (c & 0x000F000Fu) | 0x64006400u;
+            a[2 + r] = (c & 0x00F000F0u) | 0x64006400u;
+            a[4 + r] = ((c >> 8) & 0x000F000Fu) | 0x64006400u;
+            a[6 + r] = ((c >> 8) & 0x00F000F0u) | 0x64006400u;
         }
         const int g = lane >> 2;
         const uint32_t w = *(const uint32_t *)(grp + n * 256 + b * 32 + g * 4);
@@ -227,8 +238,8 @@ struct WFrag {
             const uint32_t b0 = __byte_perm(w, 0x64646464u, 0x5150), b1 = __byte_perm(w, 0x64646464u, 0x5352);
             const float2 d0 = __half22float2(*(const __half2 *)&dm.x), d1 = __half22float2(*(const __half2 *)&dm.y);
             const float2 v0 = __half22float2(*(const __half2 *)&b0), v1 = __half22float2(*(const __half2 *)&b1);
-            const float s0 = d0.x * (v0.x - 1024.0f), m0 = d0.y * (v0.y - 1024.0f) * 0x1p-10f;
-            const float s1 = d1.x * (v1.x - 1024.0f), m1 = d1.y * (v1.y - 1024.0f) * 0x1p-10f;
+            const float s0 = d0.x * (v0.x - 1024.0f), m0 = -d0.y * (v0.y - 1024.0f);
+            const float s1 = d1.x * (v1.x - 1024.0f), m1 = -d1.y * (v1.y - 1024.0f);
             s[0] = f2(s0, s0);
             m[0] = f2(m0, m0);
             s[1] = f2(s1, s1);
@@ -240,19 +251,21 @@ struct WFrag {
 constexpr int kNW = 16;  // warps of a CTA
 
 // CTA tile: wr x MT x 16 rows, WC x NT x 8 tokens; the warps split the rows wr
-// ways, the tokens WC ways and the blocks of a stage wk ways.  CTAs walk the
-// tiles (token tiles innermost: they share the weights in L2) through a ring of
-// stages of one group of blocks; at each stage another warp requests the stage
-// that the ring has room for.  RES: the records of all blocks stay in shared
-// memory (one token tile), else a stage brings its own.
+// ways, the tokens WC ways, the stages of a tile ws ways and the blocks of a
+// stage wb ways.  CTAs walk the tiles (token tiles innermost: they share the
+// weights in L2) through a ring of stages of one group each; a warp that is
+// done with a stage requests the one that takes its place.  The ring's length
+// is a multiple of ws, so that a slot always belongs to the same warps: they
+// see every phase of its barriers in turn.  RES: the records of all blocks stay in shared memory
+// (one token tile), else a stage brings its own.
 template <int FMT, int MT, int NT, int WC, bool RES>
 __global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_constant__ LinearParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const int wr_n = p.wr, wk_n = kNW / (WC * wr_n), nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
-    constexpr int NTC = NT * WC, GB = group_bytes(FMT, kKB), BST = kKB * kBRec;
+    const int wr_n = p.wr, wk_n = kNW / (WC * wr_n), ws_n = p.ws_n, wb_n = wk_n / ws_n, nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
+    constexpr int NTC = NT * WC, GB = group_bytes(FMT, kKB), BST = kKB * act_bytes(FMT);
     const int a_stage = wr_n * MT * GB, stage = a_stage + (RES ? 0 : NTC * BST);
     uint8_t *resident = smem + p.stages * stage;
-    float4 *red = (float4 *)(resident + (RES ? (size_t)NTC * nb * kBRec : 0));
+    float4 *red = (float4 *)(resident + (RES ? (size_t)NTC * nb * act_bytes(FMT) : 0));
     uint64_t *bars = (uint64_t *)(red + (wk_n > 1 ? kNW / 2 * MT * NT * 32 : 0));
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * p.stages, bfull = empty0 + 8 * p.stages;
     volatile int *abort_flag = (volatile int *)(bars + 2 * p.stages + 1);
@@ -260,7 +273,7 @@ __global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, kNW);
+            mbar_init(empty0 + 8 * s, WC * wr_n * wb_n);
         }
         mbar_init(bfull, 1);
         *abort_flag = 0;
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_consta
             bool ok = true;
             if (lane == 0) {
                 ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(j / p.stages) & 1u) ^ 1u, abort_flag, p.error, 2);
-                if (ok) mbar_arrive_tx(full, (uint32_t)(n_rt * group_bytes(FMT, n) + n_nt * n * kBRec));
+                if (ok) mbar_arrive_tx(full, (uint32_t)(n_rt * group_bytes(FMT, n) + n_nt * n * act_bytes(FMT)));
             }
             if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
             if (lane < n_rt)
@@ -292,27 +305,28 @@ __global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_consta
                           full);
         }
         if ((part & 2) && lane < n_nt)
-            bulk_load(dst + a_stage + lane * BST, p.ws + ((size_t)(nt0 + lane) * nb + g * kKB) * kBRec,
-                      (uint32_t)(n * kBRec), full);
+            bulk_load(dst + a_stage + lane * BST, p.ws + ((size_t)(nt0 + lane) * nb + g * kKB) * act_bytes(FMT),
+                      (uint32_t)(n * act_bytes(FMT)), full);
     };
     if (warp == 0) {
-        const int first = min(p.stages - 1, n_it);
+        const int first = min(p.stages, n_it);
         for (int j = 0; j < first; ++j) request(j, 1);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;");
         if (RES) {
             const int n = min(NTC, nt_n);
-            if (lane == 0) mbar_arrive_tx(bfull, (uint32_t)(n * nb * kBRec));
+            if (lane == 0) mbar_arrive_tx(bfull, (uint32_t)(n * nb * act_bytes(FMT)));
             __syncwarp();
             if (lane < n)
-                bulk_load(smem_u32(resident + (size_t)lane * nb * kBRec), p.ws + (size_t)lane * nb * kBRec,
-                          (uint32_t)(nb * kBRec), bfull);
+                bulk_load(smem_u32(resident + (size_t)lane * nb * act_bytes(FMT)), p.ws + (size_t)lane * nb * act_bytes(FMT),
+                          (uint32_t)(nb * act_bytes(FMT)), bfull);
         }
         for (int j = 0; j < first; ++j) request(j, 2);
     }
     // a wait that expires leaves garbage and an error bit; the warp goes on, so
     // that the others' barriers complete
     const int wc = warp % WC, wr = warp / WC % wr_n, wk = warp / (WC * wr_n);
+    const int ws = wk % ws_n, wb = wk / ws_n;
     if (RES) mbar_wait(bfull, 0, abort_flag, p.error, 4);
     int it = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -322,30 +336,37 @@ __global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_consta
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = f2(0.0f, 0.0f);
         for (int g = 0; g < ng; ++g, ++it) {
+            if (it % ws_n != ws) continue;
             const int slot = it % p.stages, n = min(kKB, nb - g * kKB);
-            if (warp == it % kNW && it + p.stages - 1 < n_it) request(it + p.stages - 1, 3);
             mbar_wait(full0 + 8 * slot, (uint32_t)(it / p.stages) & 1u, abort_flag, p.error, 4);
             const uint8_t *ga = smem + slot * stage + wr * MT * GB;
-            const uint8_t *gb = RES ? resident + (size_t)g * kKB * kBRec : smem + slot * stage + a_stage + wc * NT * BST;
-            const size_t b_tile = RES ? (size_t)nb * kBRec : BST;
-            for (int b = wk; b < n; b += wk_n) {
+            const uint8_t *gb = RES ? resident + (size_t)g * kKB * act_bytes(FMT) : smem + slot * stage + a_stage + wc * NT * BST;
+            const size_t b_tile = RES ? (size_t)nb * act_bytes(FMT) : BST;
+            // several blocks at once where one has few products to hide its latency
+            constexpr int kUnroll = MT * NT <= 2 ? 4 : MT * NT <= 4 ? 2 : 1;
+#pragma unroll kUnroll
+            for (int b = wb; b < n; b += wb_n) {
                 WFrag<FMT> wf[MT];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) wf[m].load(ga + m * GB, n, b, lane);
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
-                    const uint8_t *rec = gb + c * b_tile + b * kBRec;
+                    const uint8_t *rec = gb + c * b_tile + b * act_bytes(FMT);
                     const uint4 x = *(const uint4 *)(rec + lane * 16);
-                    const float4 sc = *(const float4 *)(rec + 512 + (lane & 3) * 16);
-                    const F2 da = f2(sc.x, sc.y);
+                    const float4 st = *(const float4 *)(rec + 512 + (lane & 3) * 16);
+                    const float2 dv = *(const float2 *)(rec + 576 + (lane & 3) * 8);
+                    const F2 da = f2(dv.x, dv.y);
                     float d[MT][4];
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) mma_f16_sync(d[m], wf[m].a, x.x, x.y, sc.z, sc.w, sc.z, sc.w);
+                    for (int m = 0; m < MT; ++m) mma_f16_sync(d[m], wf[m].a, x.x, x.y, st.x, st.y, st.z, st.w);
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
                         mma_f16_sync(d[m], wf[m].a + 4, x.z, x.w, d[m][0], d[m][1], d[m][2], d[m][3]);
-                    // Q4_K: -1024 d_a sum q_a times min / 1024
-                    const F2 e = FMT == kFmtQ4K ? mul2(da, f2(sc.z, sc.w)) : da;
+                    F2 e = da;
+                    if (FMT == kFmtQ4K) {
+                        const float2 ev = *(const float2 *)(rec + 608 + (lane & 3) * 8);
+                        e = f2(ev.x, ev.y);
+                    }
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -358,6 +379,7 @@ __global__ void __launch_bounds__(kNW * 32, 1) linear_kernel(const __grid_consta
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+            if ((wb * wr_n + wr) * WC + wc == it / ws_n % (wb_n * wr_n * WC) && it + p.stages < n_it) request(it + p.stages, 3);
         }
         // join the warps of one row and token share: the upper half of them
         // hands its sums to the lower half, until one is left
@@ -466,6 +488,7 @@ __global__ void __launch_bounds__(kVecWarps * 32) linear_vec_kernel(const __grid
         float dd;
         int sum;
         code_word(p, t, b, q, tb < TN * nb, code, dd, sum);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         if (tb >= TN * nb) continue;
         ((uint32_t *)(q < 4 ? x0 : x1))[tb * 4 + (q & 3)] = code;
         if (q == 0) xs[tb] = BlockScale{dd, sum};
@@ -539,14 +562,18 @@ int launch_tile(LinearParams p, int wr, int n_sm, cudaStream_t st) {
     int rc = allow_smem(kernel, done);
     if (rc) return rc;
     const int nb = p.cols / kBlock, ng = (nb + kKB - 1) / kKB;
-    const size_t stage = (size_t)wr * MT * group_bytes(FMT, kKB) + (RES ? 0 : (size_t)NT * WC * kKB * kBRec);
-    const size_t fixed = (RES ? (size_t)NT * WC * nb * kBRec : 0) +
+    const size_t stage = (size_t)wr * MT * group_bytes(FMT, kKB) + (RES ? 0 : (size_t)NT * WC * kKB * act_bytes(FMT));
+    const size_t fixed = (RES ? (size_t)NT * WC * nb * act_bytes(FMT) : 0) +
                          (kNW / (WC * wr) > 1 ? (size_t)kNW / 2 * MT * NT * 512 : 0) + 512;
     const int tiles = ((p.rows + 16 * MT * wr - 1) / (16 * MT * wr)) * ((p.n_tokens + 8 * NT * WC - 1) / (8 * NT * WC));
-    const int grid = std::min(tiles, n_sm), need = ng * ((tiles + grid - 1) / grid) + 1;
+    const int grid = std::min(tiles, n_sm), need = std::max(2, ng * ((tiles + grid - 1) / grid));
     p.wr = wr;
     p.stages = (int)std::min<size_t>({(kLinearSmem - fixed) / stage, (size_t)need, (size_t)16});
     if (p.stages < 2) return (int)cudaErrorInvalidValue;
+    // stages split as many ways as the ring holds whole turns of
+    p.ws_n = kNW / (WC * wr);
+    while (p.ws_n > p.stages) p.ws_n /= 2;
+    p.stages = p.stages / p.ws_n * p.ws_n;
     rc = launch_pdl(linear_prepare_kernel, dim3((unsigned)((p.n_tokens + 7) / 8), (unsigned)((nb + 3) / 4)), 256, 0, p,
                     st);
     return rc ? rc : launch_pdl(kernel, dim3((unsigned)grid), kNW * 32, p.stages * stage + fixed, p, st);
@@ -564,7 +591,7 @@ int launch_small(const LinearParams &p, int n_sm, cudaStream_t st) {
     int best = 256;
     for (int h = 128; h >= 32; h /= 2)
         if (split_cost(p, h, NT, n_sm) < split_cost(p, best, NT, n_sm)) best = h;
-    if (p.n_tokens <= 8 * NT && (size_t)NT * (p.cols / kBlock) * kBRec <= kLinearResident) {
+    if (p.n_tokens <= 8 * NT && (size_t)NT * (p.cols / kBlock) * act_bytes(FMT) <= kLinearResident) {
         if (best == 32) return launch_tile<FMT, 1, NT, 1, true>(p, 2, n_sm, st);
         return launch_tile<FMT, 2, NT, 1, true>(p, best / 32, n_sm, st);
     }
@@ -605,7 +632,7 @@ size_t linear_weight_bytes(int fmt, int rows, int cols) {
     return (size_t)((rows + 15) / 16) * tile_bytes(fmt, cols / kBlock);
 }
 size_t linear_ws_bytes(int max_tokens, int cols) {
-    return (size_t)((max_tokens + 7) / 8) * (cols / kBlock) * kBRec;
+    return (size_t)((max_tokens + 7) / 8) * (cols / kBlock) * act_bytes(kFmtQ4K);
 }
 
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, int cols, int n_sm, cudaStream_t st) {
