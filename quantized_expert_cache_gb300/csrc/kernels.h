@@ -184,27 +184,37 @@ struct RouterParams {
 
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
-constexpr int kLinearSmem = 224 * 1024;             // shared memory of a CTA
-constexpr size_t kLinearResident = 64 * 1024;       // of it, activations held whole
+constexpr int kLinearSmem = 200 * 1024;        // dynamic shared memory of a CTA
+constexpr int kLinearVecTokens = 8;            // above: the tensor cores
 struct LinearParams {
-    const uint8_t *w;           // the weights in operand order
+    const uint8_t *w;           // the weights, layout of linear.cuh
     const float *x;             // [n_tokens][cols], or null and the codes below
     const int8_t *q;            // [n_tokens][cols]
     const __half *d;            // [n_tokens][cols / 32]
     float *y;                   // [n_tokens][rows]
-    uint8_t *ws;                // linear_ws_bytes(max tokens, cols): the activations in operand order
-    int *error;                 // a bit set when a bounded wait expires
     int fmt, rows, cols, n_tokens;
-    int wr, ws_n, stages;       // set by the launch: row and stage split of a CTA's warps, ring stages
+    // batches: the activations' two binary16 halves [max_tokens][cols], their
+    // token scales, the weights' power-of-two scale and its inverse
+    __half *ws_hi, *ws_lo;
+    float *ws_scale;
+    float w_scale, w_unscale;
+    int *error;                 // a bit set when a bounded wait expires
+};
+struct LinearGemm {
+    CUtensorMap tm_hi, tm_lo;   // the halves, 128-B swizzle, boxes of linear_gemm_box() tokens
+    LinearParams p;
 };
 
 int launch_rms_norm(const NormParams &p, cudaStream_t st);
 int router_configure();
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st);
 size_t linear_weight_bytes(int fmt, int rows, int cols);
-size_t linear_ws_bytes(int max_tokens, int cols);
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, int cols, int n_sm, cudaStream_t st);
+int launch_linear_max(const uint8_t *w, int fmt, int rows, int cols, unsigned *out, int n_sm, cudaStream_t st);
 int launch_linear(const LinearParams &p, int n_sm, cudaStream_t st);
+int linear_gemm_box();
+int linear_gemm_configure();
+int launch_linear_gemm(const LinearGemm &g, int n_sm, cudaStream_t st);
 int launch_topk(const float *logits, int T, int E, int k, int renorm, int32_t *idx, float *w, cudaStream_t st);
 int launch_quantize(const float *x, int n_blocks, int8_t *q, BlockScale *ds, int n_sm, cudaStream_t st);
 int launch_plan(const PlanParams &p, cudaStream_t st);

@@ -1,0 +1,571 @@
+// y = W x of a dense 4-bit layer for batches: the 5th-generation tensor cores
+// (tcgen05, accumulators in TMEM), with the block scales folded into the
+// operands instead of applied to block sums.
+//
+// Arithmetic.  A Q4_0 weight d (q - 8) has at most 15 significant bits and an
+// activation d_a q_a at most 18, so neither fits one binary16; two do:
+//   w = w_h + w_l,  x 2^-e = x_h + x_l   (each part the binary16 rounding of
+// what is left; w exactly, x to 2^-24 of its token's largest value, e the
+// exponent of the token's largest scale) and
+//   y = 2^e (sum w_h x_h  +  sum (w_l x_h + w_h x_l)),
+// dropping w_l x_l (2^-22 of the product).  Three MMAs a K step replace a
+// scaled epilogue for every 32 columns: the exact-block-sum GEMM of the
+// experts has to read every block's sums back from TMEM and is bound by that;
+// exact block sums on mma.sync, scaled in registers, measured 88 us for
+// 4096 x 4096 at 512 tokens (its f16 rate is a quarter of tcgen05's).  Q4_K weights are
+// formed in binary32 (d sc q - dmin m), scaled by a power of two so that the
+// largest of the layer is below 2^15, and split the same way.
+//
+// The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
+// on a growing sum; so the large products are accumulated for kChunk stages
+// (512 columns) only, then added in registers, rounded to nearest.  The cross
+// products are 2^-11 of them and keep one accumulator for the whole tile.
+//
+// The weight halves go from the converters' registers to TMEM (tcgen05.st) and
+// the MMA takes its A operand there: with A in shared memory an MMA reads 4 KB
+// more (46 cycles at N = 32 against 26; the measured floor at N = 64 and 128 is
+// 36 and 64), and every stage needs a fence between the converters' stores and
+// the MMA that measured 600 cycles.
+#include <cuda.h>
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "linear.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+using namespace gemm;
+
+constexpr int kBM = 128, kBK = 128, kChunk = 4;          // tile rows, stage columns, stages of a chunk
+constexpr int kConv = 16, kEpi = 8;                      // converter and epilogue warps
+constexpr int kWTma = 0, kWMma = 1, kWConv = 2, kWEpi = kWConv + kConv;
+constexpr int kThreads = (kWEpi + kEpi) * 32;
+constexpr int kBox = 32;                                 // token rows of one TMA box
+constexpr int kAhead = 5;                                // stages of weights in flight
+
+template <int FMT, int BN>
+struct LCfg {
+    static constexpr int ATOM = BN * 128;                // the tokens' 64 columns, a 128-byte swizzled row each
+    static constexpr int SLOT = 4 * ATOM;                // high parts of 128 columns, low parts
+    static constexpr int STAGES = BN > 32 ? 4 : 6;
+    static constexpr int A_STAGES = 8;                   // weight blocks (32 of K) in TMEM, 32 columns each
+    static constexpr int RED = BN * kBM * 4;             // a split tile's sums
+    // weight blocks on their way to the converters, [kAhead + 1] entries of a
+    // thread's 16 code bytes and its scale bytes
+    static constexpr int SC = FMT == kFmtQ4 ? 4 : 8;
+    static constexpr int RAW_OFF = STAGES * SLOT > RED ? STAGES * SLOT : RED;
+    static constexpr int RAW_BYTES = kConv * 32 * (16 + SC);
+    static constexpr int BAR_OFF = RAW_OFF + (kAhead + 1) * RAW_BYTES;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 2 * A_STAGES + 6) * 8;
+    static constexpr int SMEM = MISC_OFF + 16;
+    // TMEM columns: two buffers of the large products' sums, the cross
+    // products', the weight blocks
+    static constexpr int CROSS = 2 * BN, A_COL = 3 * BN, COLS = 512;
+    static_assert(A_COL + 32 * A_STAGES <= COLS, "TMEM");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// ---- activations: codes and scales -> the two halves -------------------------
+// One CTA a token, four values a thread and round: ITEMS rounds in registers,
+// or (ITEMS 0) any number, read twice.  FP: x, quantized here; else q and d.
+template <bool FP, int ITEMS>
+__global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ unsigned part[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.cols, n4 = K / 4;
+    const size_t t = blockIdx.x;
+    struct Four {
+        float v[4];  // FP: values; else codes
+        float d;     // else: the block's scale
+    };
+    auto load = [&](int i) {
+        Four f{};
+        if (i >= n4) return f;
+        if (FP) {
+            *(float4 *)f.v = *((const float4 *)(p.x + t * K) + i);
+        } else {
+            const uint32_t w = *((const uint32_t *)(p.q + t * K) + i);
+            f.d = __half2float(p.d[t * (n4 / 8) + i / 8]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.v[j] = (float)(int8_t)(w >> (8 * j));
+        }
+        return f;
+    };
+    // non-negative floats order like their bits (NaN above all)
+    auto top4 = [](const Four &f) {
+        return FP ? max(max(__float_as_uint(fabsf(f.v[0])), __float_as_uint(fabsf(f.v[1]))),
+                        max(__float_as_uint(fabsf(f.v[2])), __float_as_uint(fabsf(f.v[3]))))
+                  : __float_as_uint(fabsf(f.d));
+    };
+    Four held[ITEMS ? ITEMS : 1];
+    unsigned m = 0;
+    if (ITEMS) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) held[i] = load(threadIdx.x + 256 * i);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) m = max(m, top4(held[i]));
+    } else {
+        for (int i = threadIdx.x; i < n4; i += 256) m = max(m, top4(load(i)));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, part[lane & 7]);
+    // the token's largest scale; the scales times 2^-e, its exponent (e = 0
+    // for a token of zeros, infinities or NaN)
+    float top = __uint_as_float(m);
+    if (FP) top = __half2float(__float2half_rn(top / 127.0f));
+    const int e = top > 0.0f && top <= 65504.0f ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 : 0;
+    const float up = __uint_as_float((unsigned)(127 + e) << 23), down = __uint_as_float((unsigned)(127 - e) << 23);
+    if (threadIdx.x == 0) p.ws_scale[t] = up * p.w_unscale;
+    // 8 lanes a block (whole warps run every round)
+    auto emit = [&](int i, Four f) {
+        if (FP) {
+            unsigned a = top4(f);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            f.d = __half2float(__float2half_rn(__uint_as_float(a) / 127.0f));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f.v[j] = f.d != 0.0f ? fminf(fmaxf(rintf(f.v[j] / f.d), -127.0f), 127.0f) : 0.0f;
+        }
+        if (i >= n4) return;
+        const float r = f.d * down;
+        __half h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = f.v[j] * r;
+            h[j] = __float2half_rn(v);
+            l[j] = __float2half_rn(v - __half2float(h[j]));
+        }
+        *((uint2 *)(p.ws_hi + t * K) + i) = *(uint2 *)h;
+        *((uint2 *)(p.ws_lo + t * K) + i) = *(uint2 *)l;
+    };
+    if (ITEMS) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (warp * 32 + 256 * i < n4) emit(threadIdx.x + 256 * i, held[i]);
+    } else {
+        for (int i = threadIdx.x; i - lane < n4; i += 256) emit(i, load(i));
+    }
+}
+
+template <bool FP>
+int launch_split(const LinearParams &p, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.n_tokens);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.cols <= 1024) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 1>, p);
+    if (p.cols <= 2048) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 2>, p);
+    if (p.cols <= 4096) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 4>, p);
+    if (p.cols <= 8192) return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 8>, p);
+    return (int)cudaLaunchKernelEx(&cfg, linear_split_kernel<FP, 0>, p);
+}
+
+// ---- weights: one block of 32 -> the two halves ------------------------------
+template <int FMT>
+struct WRaw {
+    uint4 c;      // codes
+    uint32_t s;   // scale bytes of rows g and g + 8
+    uint32_t dm;  // Q4_K: this row's d and dmin
+    int up;       // this row is the second of the two
+    __device__ __forceinline__ void load(uint32_t codes, uint32_t scales) {
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                     : "r"(codes)
+                     : "memory");
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s) : "r"(scales) : "memory");
+        if (FMT == kFmtQ4K) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(dm) : "r"(scales + 4) : "memory");
+    }
+};
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+
+// Two codes of the bytes sel picks from n (one nibble a byte) as binary16
+// 1024 + q, minus 1032: q - 8, exact.
+__device__ __forceinline__ __half2 pair_q(uint32_t n, uint32_t sel) {
+    return __hsub2(u2h(__byte_perm(n, 0x64646464u, sel)), u2h(0x64086408u));
+}
+
+// The block's 32 weights, pairs in K order: high parts h, low parts l.
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, float /*scale*/, uint32_t (&h)[16], uint32_t (&l)[16]) {
+    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
+    const __half2 d = u2h(__byte_perm(w.s, 0, w.up ? 0x3232 : 0x1010));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {  // pairs 0..7: low nibbles of bytes 0..15, then the high ones
+        const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
+        const __half2 q = pair_q(n, i & 1 ? 0x5352 : 0x5150);
+        const __half2 v = __hmul2(q, d);
+        h[i] = h2u(v);
+        l[i] = h2u(__hfma2(q, d, __hneg2(v)));  // exact: 15 bits less the 11 above
+    }
+}
+
+__device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, float scale, uint32_t (&h)[16], uint32_t (&l)[16]) {
+    const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w}, s = w.up ? w.s >> 16 : w.s;
+    const float2 dm = __half22float2(u2h(w.dm));
+    const float sc = dm.x * (float)(s & 255u) * scale, mn = dm.y * (float)((s >> 8) & 255u) * scale;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
+        // a byte under 0x4B0000: 2^23 + q
+        const float q0 = __uint_as_float(__byte_perm(n, 0x4B000000u, i & 1 ? 0x7652 : 0x7650)) - 8388608.0f;
+        const float q1 = __uint_as_float(__byte_perm(n, 0x4B000000u, i & 1 ? 0x7653 : 0x7651)) - 8388608.0f;
+        const float v0 = fmaf(q0, sc, -mn), v1 = fmaf(q1, sc, -mn);
+        const __half2 v = __floats2half2_rn(v0, v1);
+        h[i] = h2u(v);
+        l[i] = h2u(__floats2half2_rn(v0 - __low2float(v), v1 - __high2float(v)));
+    }
+}
+
+// ---- the GEMM -----------------------------------------------------------------
+// CTA tile: 128 weight rows (TMEM lanes) x BN tokens.  gridDim.x CTAs walk the
+// tiles (token tiles innermost: they share the weight rows in L2).  A cluster
+// of S > 1 CTAs (one tile each) splits K and joins its sums in shared memory,
+// in rank order.
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap tm_hi, const __grid_constant__ CUtensorMap tm_lo,
+                       const __grid_constant__ LinearParams p) {
+    using C = LCfg<FMT, BN>;
+    constexpr int STAGES = C::STAGES;
+    // (aligned by the declaration, so that addresses in it are constants: the
+    // kernel has no other shared memory)
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int AST = C::A_STAGES;
+    const uint32_t full0 = smem_u32(smem + C::BAR_OFF), empty0 = full0 + 8 * STAGES, afull0 = empty0 + 8 * STAGES,
+                   aempty0 = afull0 + 8 * AST, accf0 = aempty0 + 8 * AST, acce0 = accf0 + 16, crosse = acce0 + 16;
+    volatile uint32_t *tmem_slot = (volatile uint32_t *)(smem + C::MISC_OFF);
+    volatile int *abort_flag = (volatile int *)(smem + C::MISC_OFF + 4);
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);   // TMA expect-tx arrive
+            mbar_init(empty0 + 8 * s, 1);  // MMA commit
+        }
+        for (int s = 0; s < AST; ++s) {
+            mbar_init(afull0 + 8 * s, 4);   // the block's converter warps
+            mbar_init(aempty0 + 8 * s, 1);         // MMA commit
+        }
+        mbar_init(crosse, kEpi);
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(accf0 + 8 * j, 1);
+            mbar_init(acce0 + 8 * j, kEpi);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kWMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32((const void *)tmem_slot)),
+                     "n"(C::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // all 512 columns: the allocation starts at column 0, a constant
+    constexpr uint32_t tmem = 0;
+    const bool off = *tmem_slot != 0 || (smem_u32(smem) & 1023);  // never: then nothing is computed
+    __syncthreads();
+    if (off && threadIdx.x == 0) {
+        *abort_flag = 1;
+        atomicOr(p.error, 64);
+    }
+
+    const int nb = p.cols / kBlock, rt_n = (p.rows + 15) / 16, nkt = (p.cols + kBK - 1) / kBK;
+    const int kt0 = nkt * rank / S, kt1 = nkt * (rank + 1) / S;  // this CTA's K stages
+    const int ntt = (p.n_tokens + BN - 1) / BN, nrt = (p.rows + kBM - 1) / kBM;
+    const int tile0 = blockIdx.x / S, total = off ? 0 : ntt * nrt, stride = gridDim.x / S;
+    const auto columns = [&](int tt) { return min(BN, p.n_tokens - tt * BN); };
+
+    if (warp == kWTma) {
+        if (lane == 0) {
+            // the split activations are the preceding kernel's
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;");
+            int it = 0;
+            for (int t = tile0; t < total; t += stride) {
+                const int tt = t % ntt, boxes = (columns(tt) + kBox - 1) / kBox;
+                for (int kt = kt0; kt < kt1; ++kt, ++it) {
+                    const int slot = it % STAGES;
+                    if (!mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
+                        goto tma_done;
+                    const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT);
+                    mbar_arrive_tx(full, (uint32_t)(4 * boxes * kBox * 128));
+                    for (int a = 0; a < 2; ++a)  // 64 columns each; past the last they read zeros
+                        for (int i = 0; i < boxes; ++i) {
+                            const uint32_t dst = b + a * C::ATOM + i * kBox * 128;
+                            tma_load_2d(dst, &tm_hi, kt * kBK + a * 64, tt * BN + i * kBox, full);
+                            tma_load_2d(dst + 2 * C::ATOM, &tm_lo, kt * kBK + a * 64, tt * BN + i * kBox, full);
+                        }
+                }
+            }
+        tma_done:;
+        }
+    } else if (warp == kWMma) {
+        {
+            int it = 0, chunk = 0, n_tile = 0;
+            for (int t = tile0; t < total; t += stride, ++n_tile) {
+                const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15), cross = tmem + C::CROSS;
+                // the cross sums of the tile before are read
+                if (!mbar_wait(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
+                for (int kt = kt0; kt < kt1; ++kt, ++it) {
+                    const int slot = it % STAGES, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
+                    if (in_chunk == 0) {
+                        if (!mbar_wait(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
+                            goto mma_done;
+                    }
+                    if (!mbar_wait_ready(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
+                        goto mma_done;
+                    const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
+                    const uint64_t bh = sdesc(st), bl = sdesc(st + 2 * C::ATOM);
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk) {
+                        const int ab = 4 * it + blk, as = ab % AST;
+                        if (!mbar_wait_ready(afull0 + 8 * as, (uint32_t)(ab / AST) & 1u, abort_flag, p.error, 4))
+                            goto mma_done;
+                        tc_fence_after();
+                        const uint32_t ah = tmem + (uint32_t)(C::A_COL + 32 * as), al = ah + 16;
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const uint64_t ko = (uint64_t)((blk >> 1) * C::ATOM + (blk & 1) * 64 + kk * 32) >> 4;
+                            mma_f16_ta(main, ah + 8 * kk, bh + ko, idesc, in_chunk | blk | kk ? 1u : 0u);
+                            mma_f16_ta(cross, al + 8 * kk, bh + ko, idesc, (kt - kt0) | blk | kk ? 1u : 0u);
+                            mma_f16_ta(cross, ah + 8 * kk, bl + ko, idesc, 1u);
+                        }
+                        mma_commit_warp(aempty0 + 8 * as);
+                    }
+                    mma_commit_warp(empty0 + 8 * slot);
+                    if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
+                        mma_commit_warp(accf0 + 8 * buf);
+                        ++chunk;
+                    }
+                }
+            }
+        mma_done:;
+        }
+    } else if (warp < kWEpi) {
+        // Converters: the four sets of four warps take the four blocks of every
+        // stage.  A thread owns a row's block; the next kAhead of them are on
+        // their way to its own place in shared memory (asynchronous copies: a
+        // register ring waited for its newest loads), and one is converted
+        // before its place in TMEM (the row's lane) is waited for.
+        const int set = (warp - kWConv) >> 2, quarter = warp & 3, row = quarter * 32 + lane, r = row & 15;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL;
+        const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
+        const size_t rt_bytes = tile_bytes(FMT, nb);
+        const int me = threadIdx.x - kWConv * 32;
+        const uint32_t codes = smem_u32(smem + C::RAW_OFF) + me * 16,
+                       scales = smem_u32(smem + C::RAW_OFF) + kConv * 32 * 16 + me * C::SC;
+        int ft = tile0, fk = kt0, fe = 0;  // fetch cursor
+        const uint8_t *src = nullptr;      // its row tile, null past the last
+        auto aim = [&]() {
+            const int rt = ft / ntt * (kBM / 16) + (row >> 4);
+            src = ft < total && rt < rt_n ? p.w + rt * rt_bytes : nullptr;
+        };
+        aim();
+        auto fetch = [&]() {
+            const int b = 4 * fk + set, bi = b % kKB, n = min(kKB, nb - (b - bi));
+            const bool on = src && b < nb;
+            const uint8_t *grp = on ? src + (size_t)(b / kKB) * group_bytes(FMT, kKB) : p.w;
+            cp_async(codes + fe * C::RAW_BYTES, grp + (on ? bi * 256 + r * 16 : 0), 16, on);
+            cp_async(scales + fe * C::RAW_BYTES, grp + (on ? n * 256 + bi * 32 + (r & 7) * 4 : 0), 4, on);
+            if (FMT == kFmtQ4K)
+                cp_async(scales + fe * C::RAW_BYTES + 4, grp + (on ? kKB * kARec + (r & 7) * 8 + (r >> 3) * 4 : 0), 4,
+                         on);
+            cp_commit();
+            if (++fe > kAhead) fe = 0;
+            if (++fk < kt1) return;
+            fk = kt0;
+            ft += stride;
+            aim();
+        };
+        for (int i = 0; i < kAhead; ++i) fetch();
+        int ce = 0;
+        for (int it = 0; it < n_it; ++it) {
+            const int ab = 4 * it + set, as = ab % AST;
+            fetch();
+            cp_wait<kAhead>();
+            WRaw<FMT> raw;
+            raw.load(codes + ce * C::RAW_BYTES, scales + ce * C::RAW_BYTES);
+            if (++ce > kAhead) ce = 0;
+            raw.up = r >> 3;
+            uint32_t h[16], l[16];
+            convert(raw, p.w_scale, h, l);
+            bool ok = true;
+            if (lane == 0)
+                ok = mbar_wait(aempty0 + 8 * as, ((uint32_t)(ab / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            tmem_st16(lanes + 32 * as, h);
+            tmem_st16(lanes + 32 * as + 16, l);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(afull0 + 8 * as);
+        }
+        cp_wait<0>();
+    } else {
+        // Epilogue: TMEM lane quarter = warp % 4 (lane = weight row), one half
+        // of the token columns.
+        constexpr int HC = BN / 2;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int quarter = warp & 3, c0 = ((warp - kWEpi) >> 2) * HC, r = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        int chunk = 0;
+        for (int t = tile0; t < total; t += stride) {
+            const int tt = t % ntt, nc = columns(tt) - c0;  // this warp's valid columns
+            float acc[HC];
+#pragma unroll
+            for (int i = 0; i < HC; ++i) acc[i] = 0.0f;
+            // the columns' token scales (powers of two): lane i has columns i, i + 32
+            float ts[(HC + 31) / 32];
+#pragma unroll
+            for (int i = 0; i < (HC + 31) / 32; ++i)
+                ts[i] = lane + 32 * i < nc ? __ldcg(p.ws_scale + (size_t)tt * BN + c0 + lane + 32 * i) : 0.0f;
+            auto add = [&](uint32_t col) {
+#pragma unroll
+                for (int i = 0; i < HC; i += 16) {
+                    if (i >= nc) break;  // warp-uniform
+                    uint32_t v[16];
+                    tmem_ld16u(lanes + col + (uint32_t)(c0 + i), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[i + j] += __uint_as_float(v[j]);
+                }
+            };
+            for (int kt = kt0; kt < kt1; kt += kChunk, ++chunk) {
+                const int buf = chunk & 1;
+                bool ok = true;
+                if (lane == 0) ok = mbar_wait(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) goto epi_done;
+                tc_fence_after();
+                add((uint32_t)(buf * BN));
+                const bool end = kt + kChunk >= kt1;
+                if (end) add(C::CROSS);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(acce0 + 8 * buf);
+                    if (end) mbar_arrive(crosse);
+                }
+            }
+            const int row = t / ntt * kBM + r;
+            float *red = (float *)smem;  // a split tile: its sums [column][row], over the stages it is done with
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                if (i >= nc) break;  // warp-uniform
+                const float v = acc[i] * __shfl_sync(0xffffffffu, ts[i / 32], i % 32);
+                if (S > 1)
+                    red[(c0 + i) * kBM + r] = v;
+                else if (row < p.rows)
+                    p.y[((size_t)tt * BN + c0 + i) * p.rows + row] = v;
+            }
+        }
+    epi_done:;
+    }
+
+    __syncwarp();
+    if (S > 1) {
+        cluster.sync();
+        if (warp >= kWEpi && !*abort_flag) {
+            const int tt = tile0 % ntt, nc = columns(tt), rt = tile0 / ntt;
+            const float *red = (const float *)smem;
+            for (int i = threadIdx.x - kWEpi * 32 + rank * kEpi * 32; i < nc * kBM; i += S * kEpi * 32) {
+                float sum = 0.0f;
+                for (int s = 0; s < S; ++s) sum += *cluster.map_shared_rank(red + i, s);
+                const size_t tok = (size_t)tt * BN + i / kBM;
+                const int row = rt * kBM + i % kBM;
+                if (row < p.rows) p.y[tok * p.rows + row] = sum;
+            }
+        }
+        __syncwarp();
+        cluster.sync();  // no CTA leaves while its sums are read
+    }
+    // drain: after an abort, give the copies and MMAs this CTA issued a
+    // bounded time (about 10 ms) to land, then free TMEM
+    __syncthreads();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 20000000ll) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "n"(C::COLS) : "memory");
+}
+
+template <int FMT, int BN>
+int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
+    const LinearParams &p = g.p;
+    auto kernel = linear_gemm_kernel<FMT, BN>;
+    const int ntt = (p.n_tokens + BN - 1) / BN, tiles = ntt * ((p.rows + kBM - 1) / kBM), nkt = (p.cols + kBK - 1) / kBK;
+    // K splits: as many as the SMs take, of at least 2 stages
+    const int S = std::max(1, std::min({8, n_sm / tiles, nkt / 2}));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, n_sm)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = LCfg<FMT, BN>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)S, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, g.tm_hi, g.tm_lo, p);
+}
+
+template <int FMT>
+int launch_fmt(const LinearGemm &g, int n_sm, cudaStream_t st) {
+    return g.p.n_tokens <= 32 ? launch_tile<FMT, 32>(g, n_sm, st) : launch_tile<FMT, 64>(g, n_sm, st);
+}
+
+template <int FMT>
+int configure_fmt() {
+    cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         LCfg<FMT, 32>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 LCfg<FMT, 64>::SMEM);
+    return (int)e;
+}
+
+}  // namespace
+
+int linear_gemm_box() { return kBox; }
+
+int linear_gemm_configure() {
+    const int rc = configure_fmt<kFmtQ4>();
+    return rc ? rc : configure_fmt<kFmtQ4K>();
+}
+
+int launch_linear_gemm(const LinearGemm &g, int n_sm, cudaStream_t st) {
+    const int rc = g.p.x ? launch_split<true>(g.p, st) : launch_split<false>(g.p, st);
+    if (rc) return rc;
+    return g.p.fmt == kFmtQ4K ? launch_fmt<kFmtQ4K>(g, n_sm, st) : launch_fmt<kFmtQ4>(g, n_sm, st);
+}
+
+}  // namespace moe

@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <chrono>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <string>
@@ -150,8 +151,13 @@ struct moe_ctx {
     // dense 4-bit layers (moe_linear_register), by id
     struct Linear {
         int fmt, rows, cols;
-        uint8_t *w;   // weights in operand order
-        uint8_t *ws;  // the activations' workspace of its calls
+        uint8_t *w;
+        // batches: power-of-two scale of the weights, the split activations'
+        // workspace and its tensor maps (gemm: the tensor cores can take them)
+        bool gemm;
+        float w_scale;
+        uint8_t *ws;
+        CUtensorMap tm_hi, tm_lo;
     };
     std::vector<Linear> linears;
     // workspaces, the last one the largest: a layer keeps the one it was
@@ -1849,6 +1855,38 @@ int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, co
     return MOE_OK;
 }
 
+// What batches through the tensor cores need of a layer: the weights' range
+// and the workspace of the split activations.
+static int linear_batch_setup(moe_ctx *ctx, moe_ctx::Linear &l) {
+    const size_t rows = ((size_t)ctx->M + 31) / 32 * 32, half = rows * l.cols * sizeof(__half);
+    const size_t bytes = 2 * half + rows * sizeof(float);
+    if (bytes > ctx->lin_ws_bytes) {
+        uint8_t *ws = nullptr;
+        CK(cudaMalloc(&ws, bytes));
+        ctx->lin_ws.push_back(ws);
+        ctx->lin_ws_bytes = bytes;
+    }
+    l.ws = ctx->lin_ws.back();
+    unsigned bits = 0, *d_max = (unsigned *)l.ws;
+    CK(cudaMemsetAsync(d_max, 0, sizeof(unsigned), ctx->stream));
+    const int rc = moe::launch_linear_max(l.w, l.fmt, l.rows, l.cols, d_max, ctx->n_sm, ctx->stream);
+    if (rc) return fail(ctx, MOE_ERR_CUDA, "linear: range launch failed");
+    CK(cudaMemcpyAsync(&bits, d_max, sizeof bits, cudaMemcpyDeviceToHost, ctx->stream));
+    CK(cudaStreamSynchronize(ctx->stream));
+    float top;
+    memcpy(&top, &bits, sizeof top);
+    // Q4_0 weights are split as they are; Q4_K ones scaled to below 2^15.
+    // Weights out of binary16's range (infinities, NaN) stay with dp4a.
+    l.gemm = top <= 65504.0f || (l.fmt == moe::kFmtQ4K && top <= 1e30f);
+    l.w_scale = 1.0f;
+    if (l.fmt == moe::kFmtQ4K && l.gemm && top > 0.0f) l.w_scale = std::ldexp(1.0f, std::min(14 - std::ilogb(top), 100));
+    if (make_tmap(ctx, &l.tm_hi, l.ws, rows, l.cols, (uint32_t)moe::linear_gemm_box()) ||
+        make_tmap(ctx, &l.tm_lo, l.ws + half, rows, l.cols, (uint32_t)moe::linear_gemm_box()))
+        return MOE_ERR_CUDA;
+    CK((cudaError_t)moe::linear_gemm_configure());
+    return MOE_OK;
+}
+
 int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int rows, int cols, int *linear_id) {
     if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
     if (weight_format != MOE_FMT_Q4_0 && weight_format != MOE_FMT_Q4_K)
@@ -1859,13 +1897,7 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
                                           std::to_string(moe::kLinearMaxCols));
     CK(cudaSetDevice(ctx->dev));
     const int fmt = weight_format == MOE_FMT_Q4_K ? moe::kFmtQ4K : moe::kFmtQ4;
-    const size_t ws_bytes = moe::linear_ws_bytes(ctx->M, cols), bytes = (size_t)rows * (cols / 32) * 18;
-    if (ws_bytes > ctx->lin_ws_bytes) {
-        uint8_t *ws = nullptr;
-        CK(cudaMalloc(&ws, ws_bytes));
-        ctx->lin_ws.push_back(ws);
-        ctx->lin_ws_bytes = ws_bytes;
-    }
+    const size_t bytes = (size_t)rows * (cols / 32) * 18;
     uint8_t *src = nullptr, *w = nullptr;
     cudaError_t e = cudaMalloc(&w, moe::linear_weight_bytes(fmt, rows, cols));
     if (e == cudaSuccess) e = cudaMalloc(&src, bytes);
@@ -1878,7 +1910,19 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
         return fail(ctx, e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA,
                     std::string("linear upload: ") + cudaGetErrorString(e));
     }
-    ctx->linears.push_back({fmt, rows, cols, w, ctx->lin_ws.back()});
+    moe_ctx::Linear l{};
+    l.fmt = fmt;
+    l.rows = rows;
+    l.cols = cols;
+    l.w = w;
+    if (ctx->M > moe::kLinearVecTokens) {
+        const int rc = linear_batch_setup(ctx, l);
+        if (rc) {
+            cudaFree(w);
+            return rc;
+        }
+    }
+    ctx->linears.push_back(l);
     *linear_id = (int)ctx->linears.size() - 1;
     return MOE_OK;
 }
@@ -1906,9 +1950,20 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
     p.rows = l.rows;
     p.cols = l.cols;
     p.n_tokens = n_tokens;
-    p.ws = l.ws;
     p.error = ctx->d_error;
-    const int rc = moe::launch_linear(p, ctx->n_sm, ctx->stream);
+    int rc;
+    if (n_tokens > moe::kLinearVecTokens && l.gemm) {
+        const size_t rows = ((size_t)ctx->M + 31) / 32 * 32;
+        p.ws_hi = (__half *)l.ws;
+        p.ws_lo = p.ws_hi + rows * l.cols;
+        p.ws_scale = (float *)(p.ws_lo + rows * l.cols);
+        p.w_scale = l.w_scale;
+        p.w_unscale = 1.0f / l.w_scale;
+        const moe::LinearGemm g{l.tm_hi, l.tm_lo, p};
+        rc = moe::launch_linear_gemm(g, ctx->n_sm, ctx->stream);
+    } else {
+        rc = moe::launch_linear(p, ctx->n_sm, ctx->stream);
+    }
     if (rc) return fail(ctx, MOE_ERR_CUDA, std::string("linear launch: ") + cudaGetErrorString((cudaError_t)rc));
     return MOE_OK;
 }
