@@ -52,7 +52,7 @@ struct LCfg {
     static constexpr int ATOM = BN * 128;                // the tokens' 64 columns, a 128-byte swizzled row each
     static constexpr int SLOT = 4 * ATOM;                // high parts of 128 columns, low parts
     static constexpr int STAGES = BN > 32 ? 4 : 6;
-    static constexpr int A_STAGES = 8;                   // weight blocks (32 of K) in TMEM, 32 columns each
+    static constexpr int A_STAGES = 2;                   // stages of weights in TMEM, 4 blocks of 32 columns each
     static constexpr int RED = BN * kBM * 4;             // a split tile's sums
     // weight blocks on their way to the converters, [kAhead + 1] entries of a
     // thread's 16 code bytes and its scale bytes
@@ -65,7 +65,7 @@ struct LCfg {
     // TMEM columns: two buffers of the large products' sums, the cross
     // products', the weight blocks
     static constexpr int CROSS = 2 * BN, A_COL = 3 * BN, COLS = 512;
-    static_assert(A_COL + 32 * A_STAGES <= COLS, "TMEM");
+    static_assert(A_COL + 128 * A_STAGES <= COLS, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(empty0 + 8 * s, 1);  // MMA commit
         }
         for (int s = 0; s < AST; ++s) {
-            mbar_init(afull0 + 8 * s, 4);   // the block's converter warps
-            mbar_init(aempty0 + 8 * s, 1);         // MMA commit
+            mbar_init(afull0 + 8 * s, kConv);  // the converter warps
+            mbar_init(aempty0 + 8 * s, 1);     // MMA commit
         }
         mbar_init(crosse, kEpi);
         for (int j = 0; j < 2; ++j) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tt = t % ntt, boxes = (columns(tt) + kBox - 1) / kBox;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
                     const int slot = it % STAGES;
-                    if (!mbar_wait(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
+                    if (!mbar_wait_spin(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
                         goto tma_done;
                     const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT);
                     mbar_arrive_tx(full, (uint32_t)(4 * boxes * kBox * 128));
@@ -325,33 +325,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = tile0; t < total; t += stride, ++n_tile) {
                 const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15), cross = tmem + C::CROSS;
                 // the cross sums of the tile before are read
-                if (!mbar_wait(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
+                if (!mbar_wait_spin(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
                     const int slot = it % STAGES, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
                     if (in_chunk == 0) {
-                        if (!mbar_wait(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
+                        if (!mbar_wait_spin(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
                             goto mma_done;
                     }
-                    if (!mbar_wait_ready(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
+                    const int as = it % AST;
+                    if (!mbar_wait_spin(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4) ||
+                        !mbar_wait_spin(afull0 + 8 * as, (uint32_t)(it / AST) & 1u, abort_flag, p.error, 4))
                         goto mma_done;
+                    tc_fence_after();
                     const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
+                    const uint32_t a = tmem + (uint32_t)(C::A_COL + 128 * as);
                     const uint64_t bh = sdesc(st), bl = sdesc(st + 2 * C::ATOM);
 #pragma unroll
-                    for (int blk = 0; blk < 4; ++blk) {
-                        const int ab = 4 * it + blk, as = ab % AST;
-                        if (!mbar_wait_ready(afull0 + 8 * as, (uint32_t)(ab / AST) & 1u, abort_flag, p.error, 4))
-                            goto mma_done;
-                        tc_fence_after();
-                        const uint32_t ah = tmem + (uint32_t)(C::A_COL + 32 * as), al = ah + 16;
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            const uint64_t ko = (uint64_t)((blk >> 1) * C::ATOM + (blk & 1) * 64 + kk * 32) >> 4;
-                            mma_f16_ta(main, ah + 8 * kk, bh + ko, idesc, in_chunk | blk | kk ? 1u : 0u);
-                            mma_f16_ta(cross, al + 8 * kk, bh + ko, idesc, (kt - kt0) | blk | kk ? 1u : 0u);
-                            mma_f16_ta(cross, ah + 8 * kk, bl + ko, idesc, 1u);
-                        }
-                        mma_commit_warp(aempty0 + 8 * as);
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t ah = a + 32 * (kk >> 1) + 8 * (kk & 1), al = ah + 16;
+                        const uint64_t ko = (uint64_t)((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
+                        mma_f16_ta(main, ah, bh + ko, idesc, in_chunk | kk ? 1u : 0u);
+                        mma_f16_ta(cross, al, bh + ko, idesc, (kt - kt0) | kk ? 1u : 0u);
+                        mma_f16_ta(cross, ah, bl + ko, idesc, 1u);
                     }
+                    mma_commit_warp(aempty0 + 8 * as);
                     mma_commit_warp(empty0 + 8 * slot);
                     if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
                         mma_commit_warp(accf0 + 8 * buf);
@@ -368,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // register ring waited for its newest loads), and one is converted
         // before its place in TMEM (the row's lane) is waited for.
         const int set = (warp - kWConv) >> 2, quarter = warp & 3, row = quarter * 32 + lane, r = row & 15;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL + 32 * set;
         const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
         const size_t rt_bytes = tile_bytes(FMT, nb);
         const int me = threadIdx.x - kWConv * 32;
@@ -400,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kAhead; ++i) fetch();
         int ce = 0;
         for (int it = 0; it < n_it; ++it) {
-            const int ab = 4 * it + set, as = ab % AST;
+            const int as = it % AST;
             fetch();
             cp_wait<kAhead>();
             WRaw<FMT> raw;
@@ -411,12 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             convert(raw, p.w_scale, h, l);
             bool ok = true;
             if (lane == 0)
-                ok = mbar_wait(aempty0 + 8 * as, ((uint32_t)(ab / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
+                ok = mbar_wait_spin(aempty0 + 8 * as, ((uint32_t)(it / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
             tc_fence_after();
-            tmem_st16(lanes + 32 * as, h);
-            tmem_st16(lanes + 32 * as + 16, l);
+            tmem_st16(lanes + 128 * as, h);
+            tmem_st16(lanes + 128 * as + 16, l);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -455,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kt = kt0; kt < kt1; kt += kChunk, ++chunk) {
                 const int buf = chunk & 1;
                 bool ok = true;
-                if (lane == 0) ok = mbar_wait(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
+                if (lane == 0) ok = mbar_wait_spin(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) goto epi_done;
                 tc_fence_after();

@@ -57,16 +57,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// The same where the phase is mostly complete already: one test without
-// suspension first.
-__device__ __forceinline__ bool mbar_wait_ready(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                                int code) {
+// The same by testing without suspension: a suspended thread takes some
+// hundreds of cycles to wake, which a short wait in a pipeline cannot afford.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n.reg .pred P;\nmbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\nselp.u32 %0, 1, 0, P;\n}"
                  : "=r"(ok)
                  : "r"(bar), "r"(parity)
                  : "memory");
-    return ok || mbar_wait(bar, parity, abort_flag, err, code);
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
+                                               int code) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_test(bar, parity)) return true;
+    return mbar_wait(bar, parity, abort_flag, err, code);
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar) {
