@@ -45,7 +45,7 @@ constexpr int kConv = 16, kEpi = 8;                      // converter and epilog
 constexpr int kWTma = 0, kWMma = 1, kWConv = 2, kWEpi = kWConv + kConv;
 constexpr int kThreads = (kWEpi + kEpi) * 32;
 constexpr int kBox = 32;                                 // token rows of one TMA box
-constexpr int kAhead = 5;                                // stages of weights in flight
+constexpr int kAhead = 3;                                // groups of weights (two stages) in flight
 
 template <int FMT, int BN>
 struct LCfg {
@@ -54,18 +54,19 @@ struct LCfg {
     static constexpr int STAGES = BN > 32 ? 4 : 6;
     static constexpr int A_STAGES = 2;                   // stages of weights in TMEM, 4 blocks of 32 columns each
     static constexpr int RED = BN * kBM * 4;             // a split tile's sums
-    // weight blocks on their way to the converters, [kAhead + 1] entries of a
-    // thread's 16 code bytes and its scale bytes
-    static constexpr int SC = FMT == kFmtQ4 ? 4 : 8;
+    // weights on their way to the converters, [kAhead + 1] groups: of a thread's
+    // two blocks the codes [2][thread] x 16, the scale words [2][thread] x 4 and
+    // (Q4_K) d and dmin [thread] x 4
+    static constexpr int CODES = 2 * kConv * 32 * 16, SCALES = 2 * kConv * 32 * 4;
     static constexpr int RAW_OFF = STAGES * SLOT > RED ? STAGES * SLOT : RED;
-    static constexpr int RAW_BYTES = kConv * 32 * (16 + SC);
+    static constexpr int RAW_BYTES = CODES + SCALES + (FMT == kFmtQ4K ? kConv * 32 * 4 : 0);
     static constexpr int BAR_OFF = RAW_OFF + (kAhead + 1) * RAW_BYTES;
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 2 * A_STAGES + 6) * 8;
     static constexpr int SMEM = MISC_OFF + 16;
     // TMEM columns: two buffers of the large products' sums, the cross
     // products', the weight blocks
     static constexpr int CROSS = 2 * BN, A_COL = 3 * BN, COLS = 512;
-    static_assert(A_COL + 128 * A_STAGES <= COLS, "TMEM");
+    static_assert(A_COL + 128 * A_STAGES <= COLS && A_STAGES == 2, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -180,13 +181,13 @@ struct WRaw {
     uint32_t s;   // scale bytes of rows g and g + 8
     uint32_t dm;  // Q4_K: this row's d and dmin
     int up;       // this row is the second of the two
-    __device__ __forceinline__ void load(uint32_t codes, uint32_t scales) {
+    __device__ __forceinline__ void load(uint32_t codes, uint32_t scales, uint32_t mins) {
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
                      : "r"(codes)
                      : "memory");
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s) : "r"(scales) : "memory");
-        if (FMT == kFmtQ4K) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(dm) : "r"(scales + 4) : "memory");
+        if (FMT == kFmtQ4K) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(dm) : "r"(mins) : "memory");
     }
 };
 
@@ -289,8 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(p.error, 64);
     }
 
-    const int nb = p.cols / kBlock, rt_n = (p.rows + 15) / 16, nkt = (p.cols + kBK - 1) / kBK;
-    const int kt0 = nkt * rank / S, kt1 = nkt * (rank + 1) / S;  // this CTA's K stages
+    const int nb = p.cols / kBlock, rt_n = (p.rows + 15) / 16, ng = (nb + kKB - 1) / kKB;
+    // this CTA's K stages, two to a group of blocks (columns past the last are zeros)
+    const int kt0 = 2 * (ng * rank / S), kt1 = 2 * (ng * (rank + 1) / S);
     const int ntt = (p.n_tokens + BN - 1) / BN, nrt = (p.rows + kBM - 1) / kBM;
     const int tile0 = blockIdx.x / S, total = off ? 0 : ntt * nrt, stride = gridDim.x / S;
     const auto columns = [&](int tt) { return min(BN, p.n_tokens - tt * BN); };
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kWEpi) {
         // Converters: the four sets of four warps take the four blocks of every
-        // stage.  A thread owns a row's block; the next kAhead of them are on
+        // stage.  A thread owns a row's block; the next kAhead groups' are on
         // their way to its own place in shared memory (asynchronous copies: a
         // register ring waited for its newest loads), and one is converted
         // before its place in TMEM (the row's lane) is waited for.
@@ -370,54 +372,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t rt_bytes = tile_bytes(FMT, nb);
         const int me = threadIdx.x - kWConv * 32;
         const uint32_t codes = smem_u32(smem + C::RAW_OFF) + me * 16,
-                       scales = smem_u32(smem + C::RAW_OFF) + kConv * 32 * 16 + me * C::SC;
-        int ft = tile0, fk = kt0, fe = 0;  // fetch cursor
-        const uint8_t *src = nullptr;      // its row tile, null past the last
+                       scales = smem_u32(smem + C::RAW_OFF) + C::CODES + me * 4;
+        int ft = tile0, fg = kt0 / 2, fe = 0;  // fetch cursor
+        const uint8_t *grp = nullptr;          // its group of its row tile
+        bool live = false;                     // there is one
         auto aim = [&]() {
             const int rt = ft / ntt * (kBM / 16) + (row >> 4);
-            src = ft < total && rt < rt_n ? p.w + rt * rt_bytes : nullptr;
+            live = ft < total && rt < rt_n;
+            grp = live ? p.w + rt * rt_bytes + (size_t)(kt0 / 2) * group_bytes(FMT, kKB) : p.w;
         };
         aim();
         auto fetch = [&]() {
-            const int b = 4 * fk + set, bi = b % kKB, n = min(kKB, nb - (b - bi));
-            const bool on = src && b < nb;
-            const uint8_t *grp = on ? src + (size_t)(b / kKB) * group_bytes(FMT, kKB) : p.w;
-            cp_async(codes + fe * C::RAW_BYTES, grp + (on ? bi * 256 + r * 16 : 0), 16, on);
-            cp_async(scales + fe * C::RAW_BYTES, grp + (on ? n * 256 + bi * 32 + (r & 7) * 4 : 0), 4, on);
-            if (FMT == kFmtQ4K)
-                cp_async(scales + fe * C::RAW_BYTES + 4, grp + (on ? kKB * kARec + (r & 7) * 8 + (r >> 3) * 4 : 0), 4,
-                         on);
+            // blocks set and set + 4 of the group (its first n)
+            const int n = min(kKB, nb - kKB * fg);
+            const bool on0 = live && set < n, on1 = live && set + 4 < n;
+            const uint8_t *c = grp + set * 256 + r * 16, *sc = grp + n * 256 + set * 32 + (r & 7) * 4;
+            const uint32_t dc = codes + fe * C::RAW_BYTES, ds = scales + fe * C::RAW_BYTES;
+            cp_async(dc, c, 16, on0);
+            cp_async(dc + C::CODES / 2, c + 4 * 256, 16, on1);
+            cp_async(ds, sc, 4, on0);
+            cp_async(ds + C::SCALES / 2, sc + 4 * 32, 4, on1);
+            if (FMT == kFmtQ4K) cp_async(ds + C::SCALES, grp + kKB * kARec + (r & 7) * 8 + (r >> 3) * 4, 4, live);
             cp_commit();
-            if (++fe > kAhead) fe = 0;
-            if (++fk < kt1) return;
-            fk = kt0;
+            fe = fe == kAhead ? 0 : fe + 1;
+            if (live) grp += group_bytes(FMT, kKB);
+            if (2 * ++fg < kt1) return;
+            fg = kt0 / 2;
             ft += stride;
             aim();
         };
         for (int i = 0; i < kAhead; ++i) fetch();
         int ce = 0;
-        for (int it = 0; it < n_it; ++it) {
-            const int as = it % AST;
+        bool ok = true;
+        for (int it0 = 0; it0 < n_it && ok; it0 += 2) {
             fetch();
             cp_wait<kAhead>();
-            WRaw<FMT> raw;
-            raw.load(codes + ce * C::RAW_BYTES, scales + ce * C::RAW_BYTES);
-            if (++ce > kAhead) ce = 0;
-            raw.up = r >> 3;
-            uint32_t h[16], l[16];
-            convert(raw, p.w_scale, h, l);
-            bool ok = true;
-            if (lane == 0)
-                ok = mbar_wait_spin(aempty0 + 8 * as, ((uint32_t)(it / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
-            tc_fence_after();
-            tmem_st16(lanes + 128 * as, h);
-            tmem_st16(lanes + 128 * as + 16, l);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(afull0 + 8 * as);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // stage it0 + j: weight stage j of two in TMEM
+                WRaw<FMT> raw;
+                raw.load(codes + ce * C::RAW_BYTES + j * (C::CODES / 2), scales + ce * C::RAW_BYTES + j * (C::SCALES / 2),
+                         scales + ce * C::RAW_BYTES + C::SCALES);
+                raw.up = r >> 3;
+                uint32_t h[16], l[16];
+                convert(raw, p.w_scale, h, l);
+                if (lane == 0) ok = mbar_wait_spin(aempty0 + 8 * j, ((uint32_t)(it0 / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                tc_fence_after();
+                tmem_st16(lanes + 128 * j, h);
+                tmem_st16(lanes + 128 * j + 16, l);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(afull0 + 8 * j);
+            }
+            ce = ce == kAhead ? 0 : ce + 1;
         }
         cp_wait<0>();
     } else {
@@ -517,9 +526,9 @@ template <int FMT, int BN>
 int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
     const LinearParams &p = g.p;
     auto kernel = linear_gemm_kernel<FMT, BN>;
-    const int ntt = (p.n_tokens + BN - 1) / BN, tiles = ntt * ((p.rows + kBM - 1) / kBM), nkt = (p.cols + kBK - 1) / kBK;
-    // K splits: as many as the SMs take, of at least 2 stages
-    const int S = std::max(1, std::min({8, n_sm / tiles, nkt / 2}));
+    const int ntt = (p.n_tokens + BN - 1) / BN, tiles = ntt * ((p.rows + kBM - 1) / kBM);
+    // K splits: as many as the SMs take, of at least a group of blocks
+    const int S = std::max(1, std::min({8, n_sm / tiles, (p.cols + kKB * kBlock - 1) / (kKB * kBlock)}));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, n_sm)));
     cfg.blockDim = dim3(kThreads);
