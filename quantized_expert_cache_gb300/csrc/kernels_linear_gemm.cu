@@ -4,11 +4,12 @@
 //
 // Arithmetic.  A Q4_0 weight d (q - 8) has at most 15 significant bits and an
 // activation d_a q_a at most 18, so neither fits one binary16; two do:
-//   w = w_h + w_l,  x 2^-e = x_h + x_l   (each part the binary16 rounding of
-// what is left; w exactly, x to 2^-24 of its token's largest value, e the
-// exponent of the token's largest scale) and
+//   w = w_h + w_l,  x 2^-e = x_h + x_l   (w exactly, w_l below 2^-8 of it; x to
+// 2^-24 of its token's largest value, each part the binary16 rounding of what
+// is left, e the exponent of the token's largest scale) and
 //   y = 2^e (sum w_h x_h  +  sum (w_l x_h + w_h x_l)),
-// dropping w_l x_l (2^-22 of the product).  Three MMAs a K step replace a
+// dropping w_l x_l (below 2^-19 of the product; 1e-6 of the result measured with
+// what the accumulation loses, 1.1e-6 for an fp32 library product).  Three MMAs a K step replace a
 // scaled epilogue for every 32 columns: the exact-block-sum GEMM of the
 // experts has to read every block's sums back from TMEM and is bound by that;
 // exact block sums on mma.sync, scaled in registers, measured 88 us for
@@ -19,7 +20,7 @@
 // The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
 // on a growing sum; so the large products are accumulated for kChunk stages
 // (512 columns) only, then added in registers, rounded to nearest.  The cross
-// products are 2^-11 of them and keep one accumulator for the whole tile.
+// products are 2^-8 of them and keep one accumulator for the whole tile.
 //
 // The weight halves go from the converters' registers to TMEM (tcgen05.st) and
 // the MMA takes its A operand there: with A in shared memory an MMA reads 4 KB
@@ -51,7 +52,7 @@ template <int FMT, int BN>
 struct LCfg {
     static constexpr int ATOM = BN * 128;                // the tokens' 64 columns, a 128-byte swizzled row each
     static constexpr int SLOT = 4 * ATOM;                // high parts of 128 columns, low parts
-    static constexpr int STAGES = BN > 32 ? 4 : 6;
+    static constexpr int STAGES = 4;
     static constexpr int A_STAGES = 2;                   // stages of weights in TMEM, 4 blocks of 32 columns each
     static constexpr int RED = BN * kBM * 4;             // a split tile's sums
     // weights on their way to the converters, [kAhead + 1] groups: of a thread's
@@ -61,7 +62,7 @@ struct LCfg {
     static constexpr int RAW_OFF = STAGES * SLOT > RED ? STAGES * SLOT : RED;
     static constexpr int RAW_BYTES = CODES + SCALES + (FMT == kFmtQ4K ? kConv * 32 * 4 : 0);
     static constexpr int BAR_OFF = RAW_OFF + (kAhead + 1) * RAW_BYTES;
-    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 2 * A_STAGES + 6) * 8;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 6) * 8;
     static constexpr int SMEM = MISC_OFF + 16;
     // TMEM columns: two buffers of the large products' sums, the cross
     // products', the weight blocks
@@ -144,8 +145,12 @@ __global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
             h[j] = __float2half_rn(v);
             l[j] = __float2half_rn(v - __half2float(h[j]));
         }
-        *((uint2 *)(p.ws_hi + t * K) + i) = *(uint2 *)h;
-        *((uint2 *)(p.ws_lo + t * K) + i) = *(uint2 *)l;
+        // the weights' order within a block: elements (0, 2) of word w & 3 at pair w >> 2, (1, 3) two pairs on
+        const size_t o = (t * K + (size_t)(i & ~7) * 4) / 2 + (i & 3) * 4 + ((i >> 2) & 1);
+        ((__half2 *)p.ws_hi)[o] = __halves2half2(h[0], h[2]);
+        ((__half2 *)p.ws_hi)[o + 2] = __halves2half2(h[1], h[3]);
+        ((__half2 *)p.ws_lo)[o] = __halves2half2(l[0], l[2]);
+        ((__half2 *)p.ws_lo)[o + 2] = __halves2half2(l[1], l[3]);
     };
     if (ITEMS) {
 #pragma unroll
@@ -194,23 +199,26 @@ struct WRaw {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
-// Two codes of the bytes sel picks from n (one nibble a byte) as binary16
-// 1024 + q, minus 1032: q - 8, exact.
-__device__ __forceinline__ __half2 pair_q(uint32_t n, uint32_t sel) {
-    return __hsub2(u2h(__byte_perm(n, 0x64646464u, sel)), u2h(0x64086408u));
+// Pair j of a code word (nibbles j and j + 4) as binary16 64 + q, exact.
+__device__ __forceinline__ __half2 pair_q(uint32_t c, int j) {
+    const uint32_t n = j == 0 ? c << 4 : c >> (4 * j - 4);
+    return u2h((n & 0x00F000F0u) | 0x54005400u);
 }
 
-// The block's 32 weights, pairs in K order: high parts h, low parts l.
+// The block's 32 weights: word i's four pairs in turn (elements 4i + (0, 2),
+// 16 + 4i + (0, 2), 4i + (1, 3), 16 + 4i + (1, 3)), high parts h, low parts l.
+// Q4_0: the scale is split instead of the weight, into its upper 7 bits, rounded,
+// and the 4 below, so that (64 + q) d' - 72 d' is exact for both: two operations a pair.
 __device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, float /*scale*/, uint32_t (&h)[16], uint32_t (&l)[16]) {
     const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
-    const __half2 d = u2h(__byte_perm(w.s, 0, w.up ? 0x3232 : 0x1010));
+    const uint32_t d = __byte_perm(w.s, 0, w.up ? 0x3232 : 0x1010);
+    const __half2 dh = u2h((d + 0x00080008u) & 0xFFF0FFF0u), dl = __hsub2(u2h(d), dh), m72 = __float2half2_rn(-72.0f);
+    const __half2 ch = __hmul2(dh, m72), cl = __hmul2(dl, m72);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {  // pairs 0..7: low nibbles of bytes 0..15, then the high ones
-        const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
-        const __half2 q = pair_q(n, i & 1 ? 0x5352 : 0x5150);
-        const __half2 v = __hmul2(q, d);
-        h[i] = h2u(v);
-        l[i] = h2u(__hfma2(q, d, __hneg2(v)));  // exact: 15 bits less the 11 above
+    for (int i = 0; i < 16; ++i) {
+        const __half2 q = pair_q(c[i >> 2], i & 3);
+        h[i] = h2u(__hfma2(q, dh, ch));
+        l[i] = h2u(__hfma2(q, dl, cl));
     }
 }
 
@@ -220,11 +228,8 @@ __device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, float scale, uin
     const float sc = dm.x * (float)(s & 255u) * scale, mn = dm.y * (float)((s >> 8) & 255u) * scale;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const uint32_t n = (c[(i >> 1) & 3] >> (i >> 3 << 2)) & 0x0F0F0F0Fu;
-        // a byte under 0x4B0000: 2^23 + q
-        const float q0 = __uint_as_float(__byte_perm(n, 0x4B000000u, i & 1 ? 0x7652 : 0x7650)) - 8388608.0f;
-        const float q1 = __uint_as_float(__byte_perm(n, 0x4B000000u, i & 1 ? 0x7653 : 0x7651)) - 8388608.0f;
-        const float v0 = fmaf(q0, sc, -mn), v1 = fmaf(q1, sc, -mn);
+        const float2 q = __half22float2(pair_q(c[i >> 2], i & 3));
+        const float v0 = fmaf(q.x - 64.0f, sc, -mn), v1 = fmaf(q.y - 64.0f, sc, -mn);
         const __half2 v = __floats2half2_rn(v0, v1);
         h[i] = h2u(v);
         l[i] = h2u(__floats2half2_rn(v0 - __low2float(v), v1 - __high2float(v)));
@@ -245,9 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (aligned by the declaration, so that addresses in it are constants: the
     // kernel has no other shared memory)
     extern __shared__ __align__(1024) uint8_t smem[];
+    // full: a stage's tokens and weights are in place; done: its products are
     constexpr int AST = C::A_STAGES;
-    const uint32_t full0 = smem_u32(smem + C::BAR_OFF), empty0 = full0 + 8 * STAGES, afull0 = empty0 + 8 * STAGES,
-                   aempty0 = afull0 + 8 * AST, accf0 = aempty0 + 8 * AST, acce0 = accf0 + 16, crosse = acce0 + 16;
+    const uint32_t full0 = smem_u32(smem + C::BAR_OFF), done0 = full0 + 8 * STAGES, accf0 = done0 + 8 * STAGES,
+                   acce0 = accf0 + 16, crosse = acce0 + 16;
     volatile uint32_t *tmem_slot = (volatile uint32_t *)(smem + C::MISC_OFF);
     volatile int *abort_flag = (volatile int *)(smem + C::MISC_OFF + 4);
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -256,12 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, 1);   // TMA expect-tx arrive
-            mbar_init(empty0 + 8 * s, 1);  // MMA commit
-        }
-        for (int s = 0; s < AST; ++s) {
-            mbar_init(afull0 + 8 * s, kConv);  // the converter warps
-            mbar_init(aempty0 + 8 * s, 1);     // MMA commit
+            mbar_init(full0 + 8 * s, 1 + kConv);  // TMA expect-tx arrive + the converter warps
+            mbar_init(done0 + 8 * s, 1);          // MMA commit
         }
         mbar_init(crosse, kEpi);
         for (int j = 0; j < 2; ++j) {
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tt = t % ntt, boxes = (columns(tt) + kBox - 1) / kBox;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
                     const int slot = it % STAGES;
-                    if (!mbar_wait_spin(empty0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
+                    if (!mbar_wait(done0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
                         goto tma_done;
                     const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT);
                     mbar_arrive_tx(full, (uint32_t)(4 * boxes * kBox * 128));
@@ -334,13 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!mbar_wait_spin(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
                             goto mma_done;
                     }
-                    const int as = it % AST;
-                    if (!mbar_wait_spin(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4) ||
-                        !mbar_wait_spin(afull0 + 8 * as, (uint32_t)(it / AST) & 1u, abort_flag, p.error, 4))
+                    if (!mbar_wait_spin(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
                         goto mma_done;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
-                    const uint32_t a = tmem + (uint32_t)(C::A_COL + 128 * as);
+                    const uint32_t a = tmem + (uint32_t)(C::A_COL + 128 * (it % AST));
                     const uint64_t bh = sdesc(st), bl = sdesc(st + 2 * C::ATOM);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
@@ -350,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_f16_ta(cross, al, bh + ko, idesc, (kt - kt0) | kk ? 1u : 0u);
                         mma_f16_ta(cross, ah, bl + ko, idesc, 1u);
                     }
-                    mma_commit_warp(aempty0 + 8 * as);
-                    mma_commit_warp(empty0 + 8 * slot);
+                    mma_commit_warp(done0 + 8 * slot);
                     if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
                         mma_commit_warp(accf0 + 8 * buf);
                         ++chunk;
@@ -415,7 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 raw.up = r >> 3;
                 uint32_t h[16], l[16];
                 convert(raw, p.w_scale, h, l);
-                if (lane == 0) ok = mbar_wait_spin(aempty0 + 8 * j, ((uint32_t)(it0 / AST) & 1u) ^ 1u, abort_flag, p.error, 16);
+                // its place in TMEM was the stage's before last
+                const int it = it0 + j, prev = it - AST;
+                if (lane == 0 && prev >= 0)
+                    ok = mbar_wait(done0 + 8 * (prev % STAGES), (uint32_t)(prev / STAGES) & 1u, abort_flag, p.error, 16);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
                 tc_fence_after();
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(afull0 + 8 * j);
+                if (lane == 0) mbar_arrive(full0 + 8 * (it % STAGES));
             }
             ce = ce == kAhead ? 0 : ce + 1;
         }
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kt = kt0; kt < kt1; kt += kChunk, ++chunk) {
                 const int buf = chunk & 1;
                 bool ok = true;
-                if (lane == 0) ok = mbar_wait_spin(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
+                if (lane == 0) ok = mbar_wait(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) goto epi_done;
                 tc_fence_after();
