@@ -185,7 +185,7 @@ struct RouterParams {
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
 constexpr int kLinearSmem = 200 * 1024;        // dynamic shared memory of a CTA
-constexpr int kLinearVecTokens = 8;            // above: the tensor cores
+constexpr int kLinearVecTokens = 2;            // above: the tensor cores
 struct LinearParams {
     const uint8_t *w;           // the weights, layout of linear.cuh
     const float *x;             // [n_tokens][cols], or null and the codes below

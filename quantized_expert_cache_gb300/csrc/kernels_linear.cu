@@ -1,13 +1,16 @@
 // y = W x of a dense layer with 4-bit weights and group scales, on the library's
-// int8 blocks: registration, and the kernel of up to 8 tokens (more:
+// int8 blocks: registration, and the kernel of one or two tokens (more:
 // kernels_linear_gemm.cu).
 //
 //   y[t][r] = sum_b term(W block (r, b), x block (t, b)), block dots exact in
 //   int32, Q4_0: d_w d_a sum_i (q_w,i - 8) q_a,i
 //   Q4_K: d sc_j d_a sum_i q_w,i q_a,i - dmin m_j d_a sum_i q_a,i
 //
-// Bound: the weights' one read from HBM at one token; from about four tokens on
-// the dot instructions (8 dp4a and 6 others to a block and a token).
+// Bound: the weights' one read from HBM.  65536 x 2048 at one token (75.5 MB)
+// 14.6 us = 5.2 TB/s, 0.76 of a copy's rate.  At 8 tokens the dots (8 dp4a and 6
+// others to a block and a token) and the activations' shared-memory reads took
+// 53 us here, 39 with two rows a lane; the tensor cores' path takes 45, and
+// 8.6 us against 13.5 for 2880 x 2880.
 //
 // Weight layout (made at registration): per 16 rows, per group of up to 8
 // blocks: the codes [block][row] x 16 bytes in Q4 order, then the scales: Q4_0
@@ -94,7 +97,7 @@ __device__ __forceinline__ void code_word(const LinearParams &p, size_t t, int b
     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 }
 
-// ---- up to 8 tokens ---------------------------------------------------------------
+// ---- one and two tokens -----------------------------------------------------------
 // A lane owns a row of the tile and the blocks of its half warp; the CTA's
 // warps take the tile's block pairs in turn, kFly pairs in flight each, the
 // next tile's first ones requested before this tile's sums are joined.
@@ -261,12 +264,9 @@ int launch_vec(const LinearParams &p, int n_sm, cudaStream_t st) {
 
 template <int FMT>
 int launch_fmt(const LinearParams &p, int n_sm, cudaStream_t st) {
-    // tokens a pass over the weights: what their activations' shared memory allows
+    // two tokens a pass over the weights where their activations fit
     const size_t one = (size_t)(p.cols / kBlock) * (32 + sizeof(BlockScale));
-    const int n = (int)std::min<size_t>((size_t)p.n_tokens, kLinearSmem / one);
-    if (n >= 5 && 8 * one <= (size_t)kLinearSmem) return launch_vec<FMT, 8>(p, n_sm, st);
-    if (n >= 3 && 4 * one <= (size_t)kLinearSmem) return launch_vec<FMT, 4>(p, n_sm, st);
-    if (n >= 2) return launch_vec<FMT, 2>(p, n_sm, st);
+    if (p.n_tokens >= 2 && 2 * one <= (size_t)kLinearSmem) return launch_vec<FMT, 2>(p, n_sm, st);
     return launch_vec<FMT, 1>(p, n_sm, st);
 }
 
