@@ -38,7 +38,7 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 template <typename T, int N>
-struct alignas(sizeof(T) * N) Pack {
+struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack {
     T v[N];
 };
 
@@ -194,8 +194,12 @@ int launch_typed(const NormParams &p, cudaStream_t st) {
     if (nv <= 32) return launch_pdl(rms_norm_kernel<T, VEC, 1, true>, (T_ + 7) / 8, 256, p, st);
     if (nv <= 64) return launch_pdl(rms_norm_kernel<T, VEC, 2, true>, (T_ + 7) / 8, 256, p, st);
     if (nv <= 128) return launch_pdl(rms_norm_kernel<T, VEC, 4, true>, (T_ + 7) / 8, 256, p, st);
+    if (nv <= 256 && p.n_tokens > 256) return launch_pdl(rms_norm_kernel<T, VEC, 8, true>, (T_ + 7) / 8, 256, p, st);
+    if (VEC == 1 && nv <= 512 && p.n_tokens > 256)
+        return launch_pdl(rms_norm_kernel<T, VEC, 16, true>, (T_ + 7) / 8, 256, p, st);
     // one CTA a row
     auto threads = [&](int items) { return (unsigned)(((nv + items - 1) / items + 31) / 32 * 32); };
+    if (p.n_tokens <= 256 && nv <= 1024) return launch_pdl(rms_norm_kernel<T, VEC, 1, false>, T_, threads(1), p, st);
     if (nv <= 256) return launch_pdl(rms_norm_kernel<T, VEC, 1, false>, T_, threads(1), p, st);
     if (nv <= 512) return launch_pdl(rms_norm_kernel<T, VEC, 2, false>, T_, threads(2), p, st);
     if (nv <= 2048) return launch_pdl(rms_norm_kernel<T, VEC, 4, false>, T_, threads(4), p, st);
@@ -206,6 +210,9 @@ int launch_typed(const NormParams &p, cudaStream_t st) {
 template <typename T>
 int launch_rows(const NormParams &p, cudaStream_t st) {
     const auto aligned = [](const void *q, size_t a) { return ((uintptr_t)q & (a - 1)) == 0; };
+    if (sizeof(T) == 2 && p.width % 8 == 0 && p.n_tokens > 256 && aligned(p.x, 16) && aligned(p.res, 16) &&
+        aligned(p.sum, 16) && aligned(p.weight, 16) && aligned(p.y, 16) && aligned(p.q, 8))
+        return launch_typed<T, 8>(p, st);
     const size_t e = 4 * sizeof(T);
     const bool vec = p.width % 4 == 0 && aligned(p.x, e) && aligned(p.res, e) && aligned(p.sum, e) &&
                      aligned(p.weight, 16) && aligned(p.y, 16) && aligned(p.q, 4);
