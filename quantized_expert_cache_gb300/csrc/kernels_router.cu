@@ -46,33 +46,33 @@ __device__ __forceinline__ int checked_id(int e, int E, int *error) {
     return e;
 }
 
-// Picks of the tokens first, first + step, ... (one a thread) into hist[E]
-// and, at hist[E], the unmasked ones.  A token's picks come by descending
-// logit, so each lane starts at another of them: with one order for all, the
-// warp's atomics would all meet at the popular experts.  Ends with the CTA
+// Picks first, first + step, ... into hist[E] and, at hist[E], the unmasked
+// tokens.  Neighbouring lanes take neighbouring picks, of few tokens, so that a
+// warp's atomics seldom meet at a popular expert.  Ends with the CTA
 // synchronised.
 __device__ __forceinline__ void count_picks(const RouterParams &p, int *hist, int first, int step) {
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
-    const int k = p.k;
+    const size_t n = (size_t)p.T * p.k;
+    constexpr int kBatch = 4;  // loads in flight
     int valid = 0;
-    for (size_t t = first; t < (size_t)p.T; t += step) {
-        const bool on = !p.mask || p.mask[t];
-        const int32_t *id = p.idx + t * k;
-        int j = (int)(t % (unsigned)k);
-        for (int j0 = 0; j0 < k; j0 += 8) {
-            int e[8];
+    for (size_t i0 = first; i0 < n; i0 += (size_t)kBatch * step) {
+        int e[kBatch];
+        bool on[kBatch], head[kBatch];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                e[u] = j0 + u < k ? id[j] : 0;
-                if (++j >= k) j = 0;
-            }
-            if (on)
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (j0 + u < k) atomicAdd(&hist[checked_id(e[u], p.E, p.error)], 1);
+        for (int j = 0; j < kBatch; ++j) {
+            const size_t i = i0 + (size_t)j * step;
+            const size_t t = n <= 0xffffffffu ? (unsigned)i / (unsigned)p.k : i / p.k;
+            e[j] = i < n ? p.idx[i] : 0;
+            on[j] = i < n && (!p.mask || p.mask[t]);
+            head[j] = i == t * p.k;
         }
-        valid += on;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (on[j]) {
+                atomicAdd(&hist[checked_id(e[j], p.E, p.error)], 1);
+                valid += head[j];
+            }
     }
     valid = __reduce_add_sync(0xffffffffu, valid);
     if ((threadIdx.x & 31) == 0 && valid) atomicAdd(&hist[p.E], valid);
