@@ -4,12 +4,13 @@
 //
 // Arithmetic.  A Q4_0 weight d (q - 8) has at most 15 significant bits and an
 // activation d_a q_a at most 18, so neither fits one binary16; two do:
-//   w = w_h + w_l,  x 2^-e = x_h + x_l   (w exactly, w_l below 2^-8 of it; x to
+//   w = w_h + w_l,  x 2^-e = x_h + x_l   (w exactly, w_l below 2^-11 of it; x to
 // 2^-24 of its token's largest value, each part the binary16 rounding of what
 // is left, e the exponent of the token's largest scale) and
 //   y = 2^e (sum w_h x_h  +  sum (w_l x_h + w_h x_l)),
-// dropping w_l x_l (below 2^-19 of the product; 1e-6 of the result measured with
-// what the accumulation loses, 1.1e-6 for an fp32 library product).  Three MMAs a K step replace a
+// dropping w_l x_l (below 2^-22 of the product; with what the accumulation loses
+// 6e-7 of the result measured at 4096 columns, 1.1e-6 for an fp32 library
+// product).  Three MMAs a K step replace a
 // scaled epilogue for every 32 columns: the exact-block-sum GEMM of the
 // experts has to read every block's sums back from TMEM and is bound by that;
 // exact block sums on mma.sync, scaled in registers, measured 88 us for
@@ -20,7 +21,7 @@
 // The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
 // on a growing sum; so the large products are accumulated for kChunk stages
 // (512 columns) only, then added in registers, rounded to nearest.  The cross
-// products are 2^-8 of them and keep one accumulator for the whole tile.
+// products are 2^-11 of them and keep one accumulator for the whole tile.
 //
 // The weight halves go from the converters' registers to TMEM (tcgen05.st) and
 // the MMA takes its A operand there: with A in shared memory an MMA reads 4 KB
@@ -207,18 +208,18 @@ __device__ __forceinline__ __half2 pair_q(uint32_t c, int j) {
 
 // The block's 32 weights: word i's four pairs in turn (elements 4i + (0, 2),
 // 16 + 4i + (0, 2), 4i + (1, 3), 16 + 4i + (1, 3)), high parts h, low parts l.
-// Q4_0: the scale is split instead of the weight, into its upper 7 bits, rounded,
-// and the 4 below, so that (64 + q) d' - 72 d' is exact for both: two operations a pair.
+// (Splitting Q4_0's scale into its upper 7 bits and the 4 below instead takes
+// two operations a pair and not three, but makes w_l x_l 2^-20 of the product:
+// 9e-7 of the result off instead of 6e-7, or a fourth product.)
 __device__ __forceinline__ void convert(const WRaw<kFmtQ4> &w, float /*scale*/, uint32_t (&h)[16], uint32_t (&l)[16]) {
     const uint32_t c[4] = {w.c.x, w.c.y, w.c.z, w.c.w};
-    const uint32_t d = __byte_perm(w.s, 0, w.up ? 0x3232 : 0x1010);
-    const __half2 dh = u2h((d + 0x00080008u) & 0xFFF0FFF0u), dl = __hsub2(u2h(d), dh), m72 = __float2half2_rn(-72.0f);
-    const __half2 ch = __hmul2(dh, m72), cl = __hmul2(dl, m72);
+    const __half2 d = u2h(__byte_perm(w.s, 0, w.up ? 0x3232 : 0x1010)), m72 = __float2half2_rn(-72.0f);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const __half2 q = pair_q(c[i >> 2], i & 3);
-        h[i] = h2u(__hfma2(q, dh, ch));
-        l[i] = h2u(__hfma2(q, dl, cl));
+        const __half2 q = __hadd2(pair_q(c[i >> 2], i & 3), m72);  // q - 8
+        const __half2 v = __hmul2(q, d);
+        h[i] = h2u(v);
+        l[i] = h2u(__hfma2(q, d, __hneg2(v)));  // exact: 15 bits less the 11 above
     }
 }
 
@@ -416,17 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 convert(raw, p.w_scale, h, l);
                 // its place in TMEM was the stage's before last
                 const int it = it0 + j, prev = it - AST;
-                if (lane == 0 && prev >= 0)
-                    ok = mbar_wait(done0 + 8 * (prev % STAGES), (uint32_t)(prev / STAGES) & 1u, abort_flag, p.error, 16);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
+                if (prev >= 0) {
+                    const uint32_t bar = done0 + 8 * (prev % STAGES), parity = (uint32_t)(prev / STAGES) & 1u;
+                    if (!mbar_test(bar, parity)) {
+                        if (lane == 0) ok = mbar_wait(bar, parity, abort_flag, p.error, 16);
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                        if (!ok) break;
+                    }
+                }
                 tc_fence_after();
                 tmem_st16(lanes + 128 * j, h);
                 tmem_st16(lanes + 128 * j + 16, l);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full0 + 8 * (it % STAGES));
+                mbar_arrive_warp(full0 + 8 * (it % STAGES), lane);
             }
             ce = ce == kAhead ? 0 : ce + 1;
         }

@@ -1875,10 +1875,9 @@ static int linear_batch_setup(moe_ctx *ctx, moe_ctx::Linear &l) {
     CK(cudaStreamSynchronize(ctx->stream));
     float top;
     memcpy(&top, &bits, sizeof top);
-    // Q4_0 weights are split as they are, through values up to 72 d; Q4_K ones
-    // scaled to below 2^15.  Weights out of that range (or infinite, or NaN)
-    // stay with dp4a.
-    l.gemm = l.fmt == moe::kFmtQ4K ? top <= 1e30f : 9.0f * top <= 65504.0f;
+    // Q4_0 weights are split as they are; Q4_K ones scaled to below 2^15.
+    // Weights out of binary16's range (or infinite, or NaN) stay with dp4a.
+    l.gemm = top <= (l.fmt == moe::kFmtQ4K ? 1e30f : 65504.0f);
     l.w_scale = 1.0f;
     if (l.fmt == moe::kFmtQ4K && l.gemm && top > 0.0f) l.w_scale = std::ldexp(1.0f, std::min(14 - std::ilogb(top), 100));
     if (make_tmap(ctx, &l.tm_hi, l.ws, rows, l.cols, (uint32_t)moe::linear_gemm_box()) ||

@@ -23,6 +23,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t tx) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(tx) : "memory");
 }
+// Arrival of a warp: its lane 0's, by predication (a branch on the lane costs
+// the converged warp more than the arrival).
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar, int lane) {
+    asm volatile("{\n.reg .pred p;\nsetp.eq.s32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar),
+                 "r"(lane)
+                 : "memory");
+}
 // One try: the thread is suspended (not spinning) until the phase completes
 // or about kSuspendNs pass, so waiting warps leave their issue slots to the
 // converter and epilogue warps.
