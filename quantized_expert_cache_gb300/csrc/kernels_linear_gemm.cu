@@ -19,8 +19,8 @@
 // largest of the layer is below 2^15, and split the same way.
 //
 // The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
-// on a growing sum; so the large products are accumulated for kChunk stages
-// (512 columns) only, then added in registers, rounded to nearest.  The cross
+// on a growing sum; so the large products are accumulated for 512 columns
+// only, then added in registers, rounded to nearest.  The cross
 // products are 2^-11 of them and keep one accumulator for the whole tile.
 //
 // The weight halves go from the converters' registers to TMEM (tcgen05.st) and
@@ -42,19 +42,26 @@ namespace {
 
 using namespace gemm;
 
-constexpr int kBM = 128, kBK = 128, kChunk = 4;          // tile rows, stage columns, stages of a chunk
-constexpr int kConv = 16, kEpi = 8;                      // converter and epilogue warps
-constexpr int kWTma = 0, kWMma = 1, kWConv = 2, kWEpi = kWConv + kConv;
-constexpr int kThreads = (kWEpi + kEpi) * 32;
-constexpr int kBox = 32;                                 // token rows of one TMA box
-constexpr int kAhead = 3;                                // groups of weights (two stages) in flight
+constexpr int kBM = 128;         // tile rows
+constexpr int kConv = 16, kEpi = 8;  // converter and epilogue warps
+constexpr int kWTma = 0, kWMma = 1;
+constexpr int kBox = 32;         // token rows of one TMA box
+constexpr int kAhead = 3;        // groups of weights (256 columns) in flight
 
+// BN tokens a tile: 32, 64 or 128.  128 halves the conversions a token costs and
+// leaves TMEM room for one buffer of the large products' sums only; its 64 sums
+// an epilogue thread take registers from the other warps.
 template <int FMT, int BN>
 struct LCfg {
-    static constexpr int ATOM = BN * 128;                // the tokens' 64 columns, a 128-byte swizzled row each
-    static constexpr int SLOT = 4 * ATOM;                // high parts of 128 columns, low parts
+    static constexpr bool WIDE = BN == 128;
+    static constexpr int BK = WIDE ? 64 : 128;           // columns of a stage
+    static constexpr int BPS = BK / 32, SPG = 256 / BK;  // blocks of a stage, stages of a group
+    static constexpr int CHUNK = 512 / BK;               // stages of a chunk
+    static constexpr int WCONV = WIDE ? 4 : 2, WEPI = WCONV + kConv, THREADS = (WEPI + kEpi) * 32;
+    static constexpr int ATOM = BN * 128, ATOMS = BK / 64;  // the tokens' 64 columns, a 128-byte swizzled row each
+    static constexpr int SLOT = 2 * ATOMS * ATOM;        // high parts, low parts
     static constexpr int STAGES = 4;
-    static constexpr int A_STAGES = 2;                   // stages of weights in TMEM, 4 blocks of 32 columns each
+    static constexpr int A_STAGES = WIDE ? 4 : 2;        // stages of weights in TMEM, BPS blocks of 32 columns each
     static constexpr int RED = BN * kBM * 4;             // a split tile's sums
     // weights on their way to the converters, [kAhead + 1] groups: of a thread's
     // two blocks the codes [2][thread] x 16, the scale words [2][thread] x 4 and
@@ -65,12 +72,25 @@ struct LCfg {
     static constexpr int BAR_OFF = RAW_OFF + (kAhead + 1) * RAW_BYTES;
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 6) * 8;
     static constexpr int SMEM = MISC_OFF + 16;
-    // TMEM columns: two buffers of the large products' sums, the cross
-    // products', the weight blocks
-    static constexpr int CROSS = 2 * BN, A_COL = 3 * BN, COLS = 512;
-    static_assert(A_COL + 128 * A_STAGES <= COLS && A_STAGES == 2, "TMEM");
+    // TMEM columns: the large products' sums (two buffers if they fit), the
+    // cross products', the weight blocks
+    static constexpr int MAINS = WIDE ? 1 : 2;
+    static constexpr int CROSS = MAINS * BN, A_COL = CROSS + BN, COLS = 512;
+    static_assert(A_COL + 32 * BPS * A_STAGES <= COLS && A_STAGES <= STAGES, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// Register shares of the wide tile's warpgroups (28 warps of kRegs at launch):
+// TMA and MMA, four of converters, two of the epilogue.
+constexpr int kRegs = 72, kRegsLead = 40, kRegsConv = 64, kRegsEpi = 104;
+static_assert(kRegsLead + 4 * kRegsConv + 2 * kRegsEpi <= 7 * kRegs, "registers");
+template <int N, bool UP>
+__device__ __forceinline__ void set_regs() {
+    if (UP)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // ---- activations: codes and scales -> the two halves -------------------------
 // One CTA a token, four values a thread and round: ITEMS rounds in registers,
@@ -243,7 +263,7 @@ __device__ __forceinline__ void convert(const WRaw<kFmtQ4K> &w, float scale, uin
 // of S > 1 CTAs (one tile each) splits K and joins its sums in shared memory,
 // in rank order.
 template <int FMT, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tm_hi, const __grid_constant__ CUtensorMap tm_lo,
                        const __grid_constant__ LinearParams p) {
     using C = LCfg<FMT, BN>;
@@ -263,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, 1 + kConv);  // TMA expect-tx arrive + the converter warps
-            mbar_init(done0 + 8 * s, 1);          // MMA commit
+            mbar_init(full0 + 8 * s, 1 + 4 * C::BPS);  // TMA expect-tx arrive + the blocks' converter warps
+            mbar_init(done0 + 8 * s, 1);               // MMA commit
         }
         mbar_init(crosse, kEpi);
         for (int j = 0; j < 2; ++j) {
@@ -294,12 +314,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     const int nb = p.cols / kBlock, rt_n = (p.rows + 15) / 16, ng = (nb + kKB - 1) / kKB;
-    // this CTA's K stages, two to a group of blocks (columns past the last are zeros)
-    const int kt0 = 2 * (ng * rank / S), kt1 = 2 * (ng * (rank + 1) / S);
+    // this CTA's K stages, whole groups of blocks (columns past the last are zeros)
+    const int kt0 = C::SPG * (ng * rank / S), kt1 = C::SPG * (ng * (rank + 1) / S);
     const int ntt = (p.n_tokens + BN - 1) / BN, nrt = (p.rows + kBM - 1) / kBM;
     const int tile0 = blockIdx.x / S, total = off ? 0 : ntt * nrt, stride = gridDim.x / S;
     const auto columns = [&](int tt) { return min(BN, p.n_tokens - tt * BN); };
 
+    if (C::WIDE && warp < C::WCONV) set_regs<kRegsLead, false>();
     if (warp == kWTma) {
         if (lane == 0) {
             // the split activations are the preceding kernel's
@@ -313,12 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!mbar_wait(done0 + 8 * slot, ((uint32_t)(it / STAGES) & 1u) ^ 1u, abort_flag, p.error, 2))
                         goto tma_done;
                     const uint32_t full = full0 + 8 * slot, b = smem_u32(smem + slot * C::SLOT);
-                    mbar_arrive_tx(full, (uint32_t)(4 * boxes * kBox * 128));
-                    for (int a = 0; a < 2; ++a)  // 64 columns each; past the last they read zeros
+                    mbar_arrive_tx(full, (uint32_t)(2 * C::ATOMS * boxes * kBox * 128));
+                    for (int a = 0; a < C::ATOMS; ++a)  // 64 columns each; past the last they read zeros
                         for (int i = 0; i < boxes; ++i) {
                             const uint32_t dst = b + a * C::ATOM + i * kBox * 128;
-                            tma_load_2d(dst, &tm_hi, kt * kBK + a * 64, tt * BN + i * kBox, full);
-                            tma_load_2d(dst + 2 * C::ATOM, &tm_lo, kt * kBK + a * 64, tt * BN + i * kBox, full);
+                            tma_load_2d(dst, &tm_hi, kt * C::BK + a * 64, tt * BN + i * kBox, full);
+                            tma_load_2d(dst + C::ATOMS * C::ATOM, &tm_lo, kt * C::BK + a * 64, tt * BN + i * kBox, full);
                         }
                 }
             }
@@ -332,19 +353,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the cross sums of the tile before are read
                 if (!mbar_wait_spin(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
-                    const int slot = it % STAGES, in_chunk = (kt - kt0) % kChunk, buf = chunk & 1;
+                    const int slot = it % STAGES, in_chunk = (kt - kt0) % C::CHUNK, buf = chunk % C::MAINS;
                     if (in_chunk == 0) {
-                        if (!mbar_wait_spin(acce0 + 8 * buf, ((uint32_t)(chunk / 2) & 1u) ^ 1u, abort_flag, p.error, 8))
+                        if (!mbar_wait_spin(acce0 + 8 * buf, ((uint32_t)(chunk / C::MAINS) & 1u) ^ 1u, abort_flag, p.error, 8))
                             goto mma_done;
                     }
                     if (!mbar_wait_spin(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
                         goto mma_done;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
-                    const uint32_t a = tmem + (uint32_t)(C::A_COL + 128 * (it % AST));
-                    const uint64_t bh = sdesc(st), bl = sdesc(st + 2 * C::ATOM);
+                    const uint32_t a = tmem + (uint32_t)(C::A_COL + 32 * C::BPS * (it % AST));
+                    const uint64_t bh = sdesc(st), bl = sdesc(st + C::ATOMS * C::ATOM);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
+                    for (int kk = 0; kk < C::BK / 16; ++kk) {
                         const uint32_t ah = a + 32 * (kk >> 1) + 8 * (kk & 1), al = ah + 16;
                         const uint64_t ko = (uint64_t)((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
                         mma_f16_ta(main, ah, bh + ko, idesc, in_chunk | kk ? 1u : 0u);
@@ -352,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_f16_ta(cross, ah, bl + ko, idesc, 1u);
                     }
                     mma_commit_warp(done0 + 8 * slot);
-                    if (in_chunk == kChunk - 1 || kt == kt1 - 1) {
+                    if (in_chunk == C::CHUNK - 1 || kt == kt1 - 1) {
                         mma_commit_warp(accf0 + 8 * buf);
                         ++chunk;
                     }
@@ -360,26 +381,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         mma_done:;
         }
-    } else if (warp < kWEpi) {
-        // Converters: the four sets of four warps take the four blocks of every
-        // stage.  A thread owns a row's block; the next kAhead groups' are on
+    } else if (warp < C::WCONV) {
+        // (fills the first warpgroup)
+    } else if (warp < C::WEPI) {
+        // Converters: the four sets of four warps take blocks set and set + 4 of
+        // every group.  A thread owns a row's block; the next kAhead groups' are on
         // their way to its own place in shared memory (asynchronous copies: a
         // register ring waited for its newest loads), and one is converted
         // before its place in TMEM (the row's lane) is waited for.
-        const int set = (warp - kWConv) >> 2, quarter = warp & 3, row = quarter * 32 + lane, r = row & 15;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL + 32 * set;
+        if (C::WIDE) set_regs<kRegsConv, false>();
+        const int set = (warp - C::WCONV) >> 2, quarter = warp & 3, row = quarter * 32 + lane, r = row & 15;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL + 32 * (set % C::BPS);
         const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
         const size_t rt_bytes = tile_bytes(FMT, nb);
-        const int me = threadIdx.x - kWConv * 32;
+        const int me = threadIdx.x - C::WCONV * 32;
         const uint32_t codes = smem_u32(smem + C::RAW_OFF) + me * 16,
                        scales = smem_u32(smem + C::RAW_OFF) + C::CODES + me * 4;
-        int ft = tile0, fg = kt0 / 2, fe = 0;  // fetch cursor
+        int ft = tile0, fg = kt0 / C::SPG, fe = 0;  // fetch cursor
         const uint8_t *grp = nullptr;          // its group of its row tile
         bool live = false;                     // there is one
         auto aim = [&]() {
             const int rt = ft / ntt * (kBM / 16) + (row >> 4);
             live = ft < total && rt < rt_n;
-            grp = live ? p.w + rt * rt_bytes + (size_t)(kt0 / 2) * group_bytes(FMT, kKB) : p.w;
+            grp = live ? p.w + rt * rt_bytes + (size_t)(kt0 / C::SPG) * group_bytes(FMT, kKB) : p.w;
         };
         aim();
         auto fetch = [&]() {
@@ -396,27 +420,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_commit();
             fe = fe == kAhead ? 0 : fe + 1;
             if (live) grp += group_bytes(FMT, kKB);
-            if (2 * ++fg < kt1) return;
-            fg = kt0 / 2;
+            if (C::SPG * ++fg < kt1) return;
+            fg = kt0 / C::SPG;
             ft += stride;
             aim();
         };
         for (int i = 0; i < kAhead; ++i) fetch();
         int ce = 0;
         bool ok = true;
-        for (int it0 = 0; it0 < n_it && ok; it0 += 2) {
+        for (int it0 = 0; it0 < n_it && ok; it0 += C::SPG) {
             fetch();
             cp_wait<kAhead>();
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // stage it0 + j: weight stage j of two in TMEM
+            for (int j = 0; j < 2; ++j) {
                 WRaw<FMT> raw;
                 raw.load(codes + ce * C::RAW_BYTES + j * (C::CODES / 2), scales + ce * C::RAW_BYTES + j * (C::SCALES / 2),
                          scales + ce * C::RAW_BYTES + C::SCALES);
                 raw.up = r >> 3;
                 uint32_t h[16], l[16];
                 convert(raw, p.w_scale, h, l);
-                // its place in TMEM was the stage's before last
-                const int it = it0 + j, prev = it - AST;
+                // block set + 4 j's stage; its place in TMEM was that of AST stages ago
+                const int it = it0 + (set + 4 * j) / C::BPS, prev = it - AST;
                 if (prev >= 0) {
                     const uint32_t bar = done0 + 8 * (prev % STAGES), parity = (uint32_t)(prev / STAGES) & 1u;
                     if (!mbar_test(bar, parity)) {
@@ -426,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_after();
-                tmem_st16(lanes + 128 * j, h);
-                tmem_st16(lanes + 128 * j + 16, l);
+                tmem_st16(lanes + 32 * C::BPS * (it % AST), h);
+                tmem_st16(lanes + 32 * C::BPS * (it % AST) + 16, l);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -439,9 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // Epilogue: TMEM lane quarter = warp % 4 (lane = weight row), one half
         // of the token columns.
+        if (C::WIDE) set_regs<kRegsEpi, true>();
         constexpr int HC = BN / 2;
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        const int quarter = warp & 3, c0 = ((warp - kWEpi) >> 2) * HC, r = quarter * 32 + lane;
+        const int quarter = warp & 3, c0 = ((warp - C::WEPI) >> 2) * HC, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int chunk = 0;
         for (int t = tile0; t < total; t += stride) {
@@ -465,21 +490,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 16; ++j) acc[i + j] += __uint_as_float(v[j]);
                 }
             };
-            for (int kt = kt0; kt < kt1; kt += kChunk, ++chunk) {
-                const int buf = chunk & 1;
+            for (int kt = kt0; kt < kt1; kt += C::CHUNK, ++chunk) {
+                const int buf = chunk % C::MAINS;
                 bool ok = true;
-                if (lane == 0) ok = mbar_wait(accf0 + 8 * buf, (uint32_t)(chunk / 2) & 1u, abort_flag, p.error, 32);
+                if (lane == 0) ok = mbar_wait(accf0 + 8 * buf, (uint32_t)(chunk / C::MAINS) & 1u, abort_flag, p.error, 32);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) goto epi_done;
                 tc_fence_after();
                 add((uint32_t)(buf * BN));
-                const bool end = kt + kChunk >= kt1;
-                if (end) add(C::CROSS);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(acce0 + 8 * buf);
-                    if (end) mbar_arrive(crosse);
+                mbar_arrive_warp(acce0 + 8 * buf, lane);
+                if (kt + C::CHUNK >= kt1) {
+                    add(C::CROSS);
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_warp(crosse, lane);
                 }
             }
             const int row = t / ntt * kBM + r;
@@ -500,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (S > 1) {
         cluster.sync();
-        if (warp >= kWEpi && !*abort_flag) {
+        if (warp >= C::WEPI && !*abort_flag) {
             const int tt = tile0 % ntt, nc = columns(tt), rt = tile0 / ntt;
             const float *red = (const float *)smem;
-            for (int i = threadIdx.x - kWEpi * 32 + rank * kEpi * 32; i < nc * kBM; i += S * kEpi * 32) {
+            for (int i = threadIdx.x - C::WEPI * 32 + rank * kEpi * 32; i < nc * kBM; i += S * kEpi * 32) {
                 float sum = 0.0f;
                 for (int s = 0; s < S; ++s) sum += *cluster.map_shared_rank(red + i, s);
                 const size_t tok = (size_t)tt * BN + i / kBM;
@@ -538,7 +564,7 @@ int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
     const int S = std::max(1, std::min({8, n_sm / tiles, (p.cols + kKB * kBlock - 1) / (kKB * kBlock)}));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, n_sm)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(LCfg<FMT, BN>::THREADS);
     cfg.dynamicSmemBytes = LCfg<FMT, BN>::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -551,9 +577,22 @@ int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
     return (int)cudaLaunchKernelEx(&cfg, kernel, g.tm_hi, g.tm_lo, p);
 }
 
+// The wide tile's kernel has the registers that its warpgroups share out.
+template <int FMT>
+bool wide_ok() {
+    static int regs = -1;
+    if (regs < 0) {
+        cudaFuncAttributes a{};
+        regs = cudaFuncGetAttributes(&a, linear_gemm_kernel<FMT, 128>) == cudaSuccess ? a.numRegs : 0;
+    }
+    return regs == kRegs;
+}
+
 template <int FMT>
 int launch_fmt(const LinearGemm &g, int n_sm, cudaStream_t st) {
-    return g.p.n_tokens <= 32 ? launch_tile<FMT, 32>(g, n_sm, st) : launch_tile<FMT, 64>(g, n_sm, st);
+    if (g.p.n_tokens <= 32) return launch_tile<FMT, 32>(g, n_sm, st);
+    if (g.p.n_tokens <= 64 || !wide_ok<FMT>()) return launch_tile<FMT, 64>(g, n_sm, st);
+    return launch_tile<FMT, 128>(g, n_sm, st);
 }
 
 template <int FMT>
@@ -563,6 +602,9 @@ int configure_fmt() {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  LCfg<FMT, 64>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_gemm_kernel<FMT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 LCfg<FMT, 128>::SMEM);
     return (int)e;
 }
 

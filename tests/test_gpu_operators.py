@@ -253,7 +253,9 @@ def check_linear(w, fmt, q, d, y):
 SHAPES = [(1, 512, 2048), (1, 33, 64), (1, 1, 256), (2, 2880, 2880), (3, 1000, 512), (4, 129, 2080), (5, 64, 32),
           (7, 2050, 1152), (8, 300, 4096), (9, 257, 2304), (16, 640, 1024), (17, 1, 2048), (31, 200, 288),
           (32, 1280, 2048), (33, 77, 1536), (64, 2880, 2880), (100, 65, 320), (1, 24, 65536), (6, 24, 16384),
-          (130, 384, 1280), (257, 130, 2048), (512, 1000, 512)]
+          (130, 384, 1280), (257, 130, 2048), (512, 1000, 512),
+          # more tiles than SMs: a CTA walks several
+          (20, 20000, 288), (40, 20001, 256), (300, 8100, 544)]
 
 
 @pytest.mark.parametrize("fmt", [qec.FMT_Q4_0, qec.FMT_Q4_K])
