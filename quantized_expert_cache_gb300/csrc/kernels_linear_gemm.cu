@@ -528,13 +528,27 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
         cluster.sync();
         if (warp >= C::WEPI && !*abort_flag) {
             const int tt = tile0 % ntt, nc = columns(tt), rt = tile0 / ntt;
-            const float *red = (const float *)smem;
-            for (int i = threadIdx.x - C::WEPI * 32 + rank * kEpi * 32; i < nc * kBM; i += S * kEpi * 32) {
-                float sum = 0.0f;
-                for (int s = 0; s < S; ++s) sum += *cluster.map_shared_rank(red + i, s);
-                const size_t tok = (size_t)tt * BN + i / kBM;
-                const int row = rt * kBM + i % kBM;
-                if (row < p.rows) p.y[tok * p.rows + row] = sum;
+            // four rows of a column a thread and round, all ranks' loads in flight
+            const float4 *red = (const float4 *)smem;
+            for (int i = threadIdx.x - C::WEPI * 32 + rank * kEpi * 32; i < nc * kBM / 4; i += S * kEpi * 32) {
+                float4 v[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < S) v[s] = *cluster.map_shared_rank(red + i, s);
+                float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+                for (int s = 1; s < 8; ++s)
+                    if (s < S) {
+                        sum[0] += v[s].x;
+                        sum[1] += v[s].y;
+                        sum[2] += v[s].z;
+                        sum[3] += v[s].w;
+                    }
+                const int row = rt * kBM + i % (kBM / 4) * 4;
+                float *y = p.y + ((size_t)tt * BN + i / (kBM / 4)) * p.rows + row;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (row + j < p.rows) y[j] = sum[j];
             }
         }
         __syncwarp();
@@ -555,13 +569,21 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "n"(C::COLS) : "memory");
 }
 
+// Tiles of BN tokens, and the K splits of one: as many as the SMs take, of at
+// least a group of blocks.
+int tiles_of(const LinearParams &p, int bn) {
+    return (p.n_tokens + bn - 1) / bn * ((p.rows + kBM - 1) / kBM);
+}
+int groups_of(const LinearParams &p) { return (p.cols + kKB * kBlock - 1) / (kKB * kBlock); }
+int splits_of(const LinearParams &p, int bn, int n_sm) {
+    return std::max(1, std::min({8, n_sm / tiles_of(p, bn), groups_of(p)}));
+}
+
 template <int FMT, int BN>
 int launch_tile(const LinearGemm &g, int n_sm, cudaStream_t st) {
     const LinearParams &p = g.p;
     auto kernel = linear_gemm_kernel<FMT, BN>;
-    const int ntt = (p.n_tokens + BN - 1) / BN, tiles = ntt * ((p.rows + kBM - 1) / kBM);
-    // K splits: as many as the SMs take, of at least a group of blocks
-    const int S = std::max(1, std::min({8, n_sm / tiles, (p.cols + kKB * kBlock - 1) / (kKB * kBlock)}));
+    const int tiles = tiles_of(p, BN), S = splits_of(p, BN, n_sm);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, n_sm)));
     cfg.blockDim = dim3(LCfg<FMT, BN>::THREADS);
@@ -588,11 +610,26 @@ bool wide_ok() {
     return regs == kRegs;
 }
 
+// Clocks of the longest CTA: rounds of tiles x groups x a group's clocks (Q4_0:
+// 2600 in a tile of 64 tokens, 4960 in one of 128, whose MMAs bound it; Q4_K:
+// 3900, bound by the conversions, and 5000), and 3000 to join a split tile.
+long clocks_of(const LinearParams &p, int bn, int n_sm, long group) {
+    const int tiles = tiles_of(p, bn), S = splits_of(p, bn, n_sm);
+    return (tiles * S + n_sm - 1L) / n_sm * ((groups_of(p) + S - 1) / S) * group + (S > 1 ? 3000 : 0);
+}
+
+// Up to 128 tokens one tile holds them all: weights are converted once (80 x
+// 1000 x 2048 13.0 us against 15.2 in tiles of 64, 128 x 8192 x 8192 47.8
+// against 49.1); above, the shorter schedule (512 x 4096 x 4096 48.6 in tiles of
+// 128 against 53.4, 512 x 16384 x 1024 57.0 against 51.6).
 template <int FMT>
 int launch_fmt(const LinearGemm &g, int n_sm, cudaStream_t st) {
     if (g.p.n_tokens <= 32) return launch_tile<FMT, 32>(g, n_sm, st);
-    if (g.p.n_tokens <= 64 || !wide_ok<FMT>()) return launch_tile<FMT, 64>(g, n_sm, st);
-    return launch_tile<FMT, 128>(g, n_sm, st);
+    const bool q4k = FMT == kFmtQ4K;
+    const bool wide = g.p.n_tokens > 64 && wide_ok<FMT>() &&
+                      (g.p.n_tokens <= 128 ||
+                       clocks_of(g.p, 128, n_sm, q4k ? 5000 : 4960) <= clocks_of(g.p, 64, n_sm, q4k ? 3900 : 2600));
+    return wide ? launch_tile<FMT, 128>(g, n_sm, st) : launch_tile<FMT, 64>(g, n_sm, st);
 }
 
 template <int FMT>
