@@ -185,7 +185,11 @@ struct RouterParams {
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
 constexpr int kLinearSmem = 200 * 1024;        // dynamic shared memory of a CTA
-constexpr int kLinearVecTokens = 2;            // above: the tensor cores
+// Whether a batch goes to the tensor cores: from 5 tokens on, and 3 or 4 of more
+// than 2048 columns (what the dp4a kernel's CTAs all stage and read from shared
+// memory; 3 tokens: 65536 x 2048 27 us there, 44 on the tensor cores, 8192 x
+// 8192 35 and 25).
+inline bool linear_takes_gemm(int n_tokens, int cols) { return n_tokens > 4 || (n_tokens > 2 && cols > 2048); }
 struct LinearParams {
     const uint8_t *w;           // the weights, layout of linear.cuh
     const float *x;             // [n_tokens][cols], or null and the codes below

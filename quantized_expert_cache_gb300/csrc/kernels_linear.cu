@@ -69,35 +69,46 @@ __global__ void linear_repack_kernel(const uint8_t *__restrict__ src, uint8_t *_
 }
 
 // ---- activations --------------------------------------------------------------
-// Word w (elements 4w..4w+3) of token t's block b: the code word, the scale
-// and, over the block's 8 lanes, the code sum.  All lanes of a warp call.
-__device__ __forceinline__ void code_word(const LinearParams &p, size_t t, int b, int w, bool on, uint32_t &code,
-                                          float &dd, int &sum) {
-    code = 0;
-    dd = 0.0f;
-    if (p.x) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (on) v = __ldcg((const float4 *)(p.x + t * p.cols) + b * 8 + w);
-        unsigned m = max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
-                         max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        dd = __half2float(__float2half_rn(__uint_as_float(m) / 127.0f));
-        const float e[4] = {v.x, v.y, v.z, v.w};
-        if (dd != 0.0f)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                code |= ((uint32_t)(int)fminf(fmaxf(rintf(e[j] / dd), -127.0f), 127.0f) & 255u) << (8 * j);
-    } else if (on) {
-        code = __ldcg((const uint32_t *)(p.q + t * p.cols) + b * 8 + w);
-        dd = __half2float(__ushort_as_half(__ldcg((const unsigned short *)p.d + t * (p.cols / kBlock) + b)));
+// Word w (elements 4w..4w+3) of token t's block b as it is in memory: four fp32
+// values, or the code word and the scale.
+struct RawWord {
+    float4 v;
+    __device__ __forceinline__ void load(const LinearParams &p, size_t t, int b, int w, bool on) {
+        v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!on) return;
+        if (p.x) {
+            v = __ldcg((const float4 *)(p.x + t * p.cols) + b * 8 + w);
+        } else {
+            v.x = __uint_as_float(__ldcg((const uint32_t *)(p.q + t * p.cols) + b * 8 + w));
+            v.y = __half2float(__ushort_as_half(__ldcg((const unsigned short *)p.d + t * (p.cols / kBlock) + b)));
+        }
     }
-    sum = __dp4a((int)code, 0x01010101, 0);
+    // The code word, the scale and, over the block's 8 lanes, the code sum.
+    // All lanes of a warp call.
+    __device__ __forceinline__ void finish(bool fp, uint32_t &code, float &dd, int &sum) const {
+        if (fp) {
+            code = 0;
+            unsigned m = max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
+                             max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-}
+            for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            dd = __half2float(__float2half_rn(__uint_as_float(m) / 127.0f));
+            const float e[4] = {v.x, v.y, v.z, v.w};
+            if (dd != 0.0f)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    code |= ((uint32_t)(int)fminf(fmaxf(rintf(e[j] / dd), -127.0f), 127.0f) & 255u) << (8 * j);
+        } else {
+            code = __float_as_uint(v.x);
+            dd = v.y;
+        }
+        sum = __dp4a((int)code, 0x01010101, 0);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+};
 
-// ---- one and two tokens -----------------------------------------------------------
+// ---- up to four tokens ------------------------------------------------------------
 // A lane owns a row of the tile and the blocks of its half warp; the CTA's
 // warps take the tile's block pairs in turn, kFly pairs in flight each, the
 // next tile's first ones requested before this tile's sums are joined.
@@ -147,8 +158,8 @@ __device__ __forceinline__ float add_term(const uint4 &c, const float2 &w, const
     return fmaf((float)x.s * x.d, w.y, acc);
 }
 
-template <int FMT, int TN>
-__global__ void __launch_bounds__(kVecWarps * 32) linear_vec_kernel(const __grid_constant__ LinearParams p) {
+template <int FMT, int TN, int kBatch>
+__global__ void __launch_bounds__(kVecWarps * 32, TN > 2 ? 3 : 4) linear_vec_kernel(const __grid_constant__ LinearParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][kVecWarps][TN][16];
     const int nb = p.cols / kBlock, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane & 15;
@@ -169,16 +180,26 @@ __global__ void __launch_bounds__(kVecWarps * 32) linear_vec_kernel(const __grid
     if ((int)blockIdx.x < rt_n) fetch(blockIdx.x, first);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    // the activations: 8 lanes a block, 4 values a lane (whole warps run every round)
-    for (int i0 = warp * 32; i0 < TN * nb * 8; i0 += kVecWarps * 32) {
-        const int i = i0 + lane, q = i & 7, tb = i >> 3, t = TN > 1 ? tb / nb : 0, b = tb - t * nb;
-        uint32_t code;
-        float dd;
-        int sum;
-        code_word(p, t0 + t, b, q, t < nt, code, dd, sum);
-        if (tb >= TN * nb) continue;
-        ((uint32_t *)(q < 4 ? x0 : x1))[tb * 4 + (q & 3)] = code;
-        if (q == 0) xs[tb] = BlockScale{dd, FMT == kFmtQ4 ? kMagic - 8 * sum : sum};
+    // the activations: 8 lanes a block, 4 values a lane, kBatch rounds' loads in
+    // flight (whole warps run every round)
+    for (int i0 = warp * 32; i0 < TN * nb * 8; i0 += kBatch * kVecWarps * 32) {
+        RawWord raw[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kVecWarps * 32 + lane, tb = i >> 3, t = TN > 1 ? tb / nb : 0;
+            raw[k].load(p, t0 + t, tb - t * nb, i & 7, tb < nt * nb);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kVecWarps * 32 + lane, q = i & 7, tb = i >> 3;
+            uint32_t code;
+            float dd;
+            int sum;
+            raw[k].finish(p.x != nullptr, code, dd, sum);
+            if (tb >= TN * nb) continue;
+            ((uint32_t *)(q < 4 ? x0 : x1))[tb * 4 + (q & 3)] = code;
+            if (q == 0) xs[tb] = BlockScale{dd, FMT == kFmtQ4 ? kMagic - 8 * sum : sum};
+        }
     }
     __syncthreads();
     int turn = 0;
@@ -236,9 +257,9 @@ __global__ void linear_max_kernel(const uint8_t *__restrict__ w, int rows, int n
 }
 
 // ---- launch ---------------------------------------------------------------------
-template <int FMT, int TN>
-int launch_vec(const LinearParams &p, int n_sm, cudaStream_t st) {
-    auto kernel = linear_vec_kernel<FMT, TN>;
+template <int FMT, int TN, int BATCH>
+int launch_batch(const LinearParams &p, int n_sm, cudaStream_t st) {
+    auto kernel = linear_vec_kernel<FMT, TN, BATCH>;
     static bool done[64];  // the shared memory limit, raised once a device
     int dev = 0;
     cudaGetDevice(&dev);
@@ -248,7 +269,7 @@ int launch_vec(const LinearParams &p, int n_sm, cudaStream_t st) {
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
     const size_t smem = (size_t)TN * (p.cols / kBlock) * (32 + sizeof(BlockScale));
-    const int fit = (int)std::max<size_t>(1, std::min<size_t>(4, 220 * 1024 / (smem + 10 * 1024)));
+    const int fit = (int)std::max<size_t>(1, std::min<size_t>(TN > 2 ? 3 : 4, 220 * 1024 / (smem + 10 * 1024)));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)std::min((p.rows + 15) / 16, n_sm * fit), (unsigned)((p.n_tokens + TN - 1) / TN));
     cfg.blockDim = dim3(kVecWarps * 32);
@@ -262,10 +283,17 @@ int launch_vec(const LinearParams &p, int n_sm, cudaStream_t st) {
     return (int)cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int FMT, int TN>
+int launch_vec(const LinearParams &p, int n_sm, cudaStream_t st) {
+    // rounds of the activations' staging: 1024 values each
+    return TN * p.cols > 2048 ? launch_batch<FMT, TN, 4>(p, n_sm, st) : launch_batch<FMT, TN, 2>(p, n_sm, st);
+}
+
 template <int FMT>
 int launch_fmt(const LinearParams &p, int n_sm, cudaStream_t st) {
     // two tokens a pass over the weights where their activations fit
     const size_t one = (size_t)(p.cols / kBlock) * (32 + sizeof(BlockScale));
+    if (p.n_tokens >= 3 && 4 * one <= (size_t)kLinearSmem) return launch_vec<FMT, 4>(p, n_sm, st);
     if (p.n_tokens >= 2 && 2 * one <= (size_t)kLinearSmem) return launch_vec<FMT, 2>(p, n_sm, st);
     return launch_vec<FMT, 1>(p, n_sm, st);
 }

@@ -1915,7 +1915,7 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
     l.rows = rows;
     l.cols = cols;
     l.w = w;
-    if (ctx->M > moe::kLinearVecTokens) {
+    if (moe::linear_takes_gemm(ctx->M, cols)) {
         const int rc = linear_batch_setup(ctx, l);
         if (rc) {
             cudaFree(w);
@@ -1952,7 +1952,7 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
     p.n_tokens = n_tokens;
     p.error = ctx->d_error;
     int rc;
-    if (n_tokens > moe::kLinearVecTokens && l.gemm) {
+    if (moe::linear_takes_gemm(n_tokens, l.cols) && l.gemm) {
         const size_t rows = ((size_t)ctx->M + 31) / 32 * 32;
         p.ws_hi = (__half *)l.ws;
         p.ws_lo = p.ws_hi + rows * l.cols;
