@@ -174,7 +174,7 @@ struct RouterParams {
     float *loss;                // [2]
     int32_t *counts;            // [E]
     float *dlogits;             // [T][E] or null
-    int32_t *n_valid;           // [1]
+    int32_t *ws_count;          // [E + 1]: picks and unmasked tokens, zero between calls
     unsigned *ticket;           // [2], zero between launches
     float *ws_part;             // [kRouterParts][2]
     int *error;                 // bit 0: an id out of range
@@ -210,7 +210,6 @@ struct LinearGemm {
 };
 
 int launch_rms_norm(const NormParams &p, cudaStream_t st);
-int router_configure();
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st);
 size_t linear_weight_bytes(int fmt, int rows, int cols);
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, int cols, int n_sm, cudaStream_t st);

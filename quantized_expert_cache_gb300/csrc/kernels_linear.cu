@@ -1,16 +1,17 @@
 // y = W x of a dense layer with 4-bit weights and group scales, on the library's
-// int8 blocks: registration, and the kernel of one or two tokens (more:
+// int8 blocks: registration, and the kernel of few tokens (batches:
 // kernels_linear_gemm.cu).
 //
 //   y[t][r] = sum_b term(W block (r, b), x block (t, b)), block dots exact in
 //   int32, Q4_0: d_w d_a sum_i (q_w,i - 8) q_a,i
 //   Q4_K: d sc_j d_a sum_i q_w,i q_a,i - dmin m_j d_a sum_i q_a,i
 //
-// Bound: the weights' one read from HBM.  65536 x 2048 at one token (75.5 MB)
-// 14.6 us = 5.2 TB/s, 0.76 of a copy's rate.  At 8 tokens the dots (8 dp4a and 6
-// others to a block and a token) and the activations' shared-memory reads took
-// 53 us here, 39 with two rows a lane; the tensor cores' path takes 45, and
-// 8.6 us against 13.5 for 2880 x 2880.
+// Bound: at one token the weights' one read from HBM: 65536 x 2048 (75.5 MB)
+// 14.6 us = 5.2 TB/s, 0.76 of a copy's rate; 512 x 2048 2.3 us (latency).  With
+// more tokens the dots (8 dp4a and 6 others to a block and a token) and the
+// activations' shared-memory reads (4 cycles for 16 bytes that half a warp
+// shares): 2 tokens 18.8 us, 4 27, 8 53 (39 with two rows a lane), where the
+// tensor cores' path takes 44.
 //
 // Weight layout (made at registration): per 16 rows, per group of up to 8
 // blocks: the codes [block][row] x 16 bytes in Q4 order, then the scales: Q4_0

@@ -10,13 +10,13 @@
 //   y = 2^e (sum w_h x_h  +  sum (w_l x_h + w_h x_l)),
 // dropping w_l x_l (below 2^-22 of the product; with what the accumulation loses
 // 6e-7 of the result measured at 4096 columns, 1.1e-6 for an fp32 library
-// product).  Three MMAs a K step replace a
-// scaled epilogue for every 32 columns: the exact-block-sum GEMM of the
-// experts has to read every block's sums back from TMEM and is bound by that;
-// exact block sums on mma.sync, scaled in registers, measured 88 us for
-// 4096 x 4096 at 512 tokens (its f16 rate is a quarter of tcgen05's).  Q4_K weights are
-// formed in binary32 (d sc q - dmin m), scaled by a power of two so that the
-// largest of the layer is below 2^15, and split the same way.
+// product).  Three MMAs a K step replace a scaled epilogue for every 32 columns:
+// the exact-block-sum GEMM of the experts has to read every block's sums back
+// from TMEM and is bound by that; exact block sums on mma.sync, scaled in
+// registers, measured 88 us for 4096 x 4096 at 512 tokens (its f16 rate is a
+// quarter of tcgen05's).  Q4_K weights are formed in binary32 (d sc q - dmin m),
+// scaled by a power of two so that the largest of the layer is below 2^15, and
+// split the same way.
 //
 // The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
 // on a growing sum; so the large products are accumulated for 512 columns
@@ -28,6 +28,15 @@
 // more (46 cycles at N = 32 against 26; the measured floor at N = 64 and 128 is
 // 36 and 64), and every stage needs a fence between the converters' stores and
 // the MMA that measured 600 cycles.
+//
+// Bound.  4096 x 4096 at 512 tokens: 48.6 us (51.5 TFLOP of MMAs at 0.55 of the
+// measured bf16 rate; 4 us are the split kernel), the tensor pipe active 58% of
+// the time: operand reads, the tokens' copies and the weights' take 90 of the
+// 98 KB that shared memory moves in a stage's 768 tensor cycles.  Tiles of up to
+// 64 tokens: the conversions (about 170 instructions a warp and block of 32 x 32
+// weights, four warps a scheduler): 65536 x 2048 at 3 to 32 tokens 45 us, 2880 x
+// 2880 at 8 tokens 8.9 (latency of two launches, one round of stages and the
+// join), Q4_K 8192 x 2048 at 33 tokens 15.9.
 #include <cuda.h>
 #include <cooperative_groups.h>
 

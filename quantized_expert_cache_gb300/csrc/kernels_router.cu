@@ -14,8 +14,13 @@
 // too, so the logits are read once and no E-wide sum over tokens is kept.
 // Counts are integers (their atomics commute exactly); the loss is summed
 // in an order that only the grid size sets: results do not vary from run to run.
-#include <cooperative_groups.h>
-
+//
+// Bound: 8 tokens (one launch, 3.4 us) by latency; 4096 x 512 with all three
+// gradients 10.3 us against 2.5 of HBM's rate, padded 12288 x 512 18.3 against
+// 7.5: two dependent launches, then a row's chain of loads and five warp
+// reductions with 32 warps a SM to hide it (DRAM at 15% of its rate, a third of
+// the stalls on loads).  Double accumulators took another 3 us: this part's
+// binary64 rate is 1/64.
 #include <algorithm>
 #include <type_traits>
 
@@ -79,28 +84,17 @@ __device__ __forceinline__ void count_picks(const RouterParams &p, int *hist, in
     __syncthreads();
 }
 
-// Picks per expert of a long batch: one cluster of kCountCtas CTAs, each with
-// the histogram of its share in shared memory; the CTAs then sum a share of
-// the experts each over the cluster's histograms.
-constexpr int kCountCtas = 16, kCountThreads = 1024;
-__global__ void __launch_bounds__(kCountThreads) router_count_kernel(RouterParams p) {
+// Picks per expert of a long batch: the histogram of each CTA's share, added to
+// ws_count, which is zero between calls (the loss kernel leaves it so).
+// (With one cluster of 16 CTAs that joined its histograms in shared memory the
+// padded 12288 x 512 case took 20.2 us in all, 18.3 with this.)
+__global__ void __launch_bounds__(kThreads) router_count_kernel(RouterParams p) {
     extern __shared__ int hist[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-    const int rank = (int)cluster.block_rank();
-    count_picks(p, hist, rank * kCountThreads + threadIdx.x, kCountCtas * kCountThreads);
-    cluster.sync();
-    for (int e = rank * kCountThreads + threadIdx.x; e <= p.E; e += kCountCtas * kCountThreads) {
-        int c = 0;
-#pragma unroll
-        for (int r = 0; r < kCountCtas; ++r) c += *cluster.map_shared_rank(hist + e, r);
-        if (e < p.E)
-            p.counts[e] = c;
-        else
-            *p.n_valid = c;
-    }
-    cluster.sync();  // no CTA leaves while its histogram is read
+    count_picks(p, hist, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
+    for (int e = threadIdx.x; e <= p.E; e += kThreads)
+        if (hist[e]) atomicAdd(&p.ws_count[e], hist[e]);
 }
 
 // One warp a row, ITEMS packs of VEC logits a lane.  COUNT: a short batch, every CTA counts all
@@ -190,9 +184,13 @@ __global__ void __launch_bounds__(kThreads, VEC * ITEMS <= 16 ? 4 : 1) router_lo
         start();
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;");
-        n_valid = __ldcg(p.n_valid);
+        n_valid = __ldcg(p.ws_count + E);
         const float inv_nk = n_valid > 0 ? 1.0f / ((float)n_valid * (float)k) : 0.0f;
-        for (int i = threadIdx.x; i < E; i += kThreads) f[i] = (float)__ldcg(&p.counts[i]) * inv_nk;
+        for (int i = threadIdx.x; i < E; i += kThreads) {
+            const int c = __ldcg(p.ws_count + i);
+            if (blockIdx.x == 0) p.counts[i] = c;
+            f[i] = (float)c * inv_nk;
+        }
     }
     __syncthreads();
     const float inv_n = n_valid > 0 ? 1.0f / (float)n_valid : 0.0f;
@@ -351,6 +349,9 @@ __global__ void __launch_bounds__(kThreads, VEC * ITEMS <= 16 ? 4 : 1) router_lo
         for (unsigned c = lane; c < gridDim.x; c += 32) sum += __ldcg(&p.ws_part[2 * c + warp]);
         sum = warp_sum_f(sum);
     }
+    // (every CTA has read the counts)
+    if (!COUNT && warp == 0)
+        for (int i = lane; i <= E; i += 32) p.ws_count[i] = 0;
     if (lane == 0) {
         const float n = n_valid > 0 ? (float)n_valid : 1.0f;
         p.loss[warp] = (warp ? p.zcoef : p.balance * (float)E) * sum / n;
@@ -359,20 +360,17 @@ __global__ void __launch_bounds__(kThreads, VEC * ITEMS <= 16 ? 4 : 1) router_lo
 }
 
 template <typename K>
-int launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, const RouterParams &p, cudaStream_t st,
-               unsigned cluster = 1) {
+int launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, const RouterParams &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {cluster, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     return (int)cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -400,15 +398,12 @@ int launch_loss(const RouterParams &p, int n_sm, cudaStream_t st) {
 
 }  // namespace
 
-// Once per device: a cluster of more than 8 CTAs has to be asked for.
-int router_configure() {
-    return (int)cudaFuncSetAttribute(router_count_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-}
-
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st) {
     // up to kCountInLoss picks every CTA of the loss kernel counts them all
     if ((size_t)p.T * p.k <= kCountInLoss) return launch_loss<true>(p, n_sm, st);
-    int rc = launch_pdl(router_count_kernel, kCountCtas, kCountThreads, (size_t)(p.E + 1) * 4, p, st, kCountCtas);
+    const size_t ids = (size_t)p.T * p.k;
+    const unsigned grid = (unsigned)std::min<size_t>((ids + 2 * kThreads - 1) / (2 * kThreads), (size_t)n_sm);
+    int rc = launch_pdl(router_count_kernel, grid, kThreads, (size_t)(p.E + 1) * 4, p, st);
     return rc ? rc : launch_loss<false>(p, n_sm, st);
 }
 

@@ -164,7 +164,7 @@ struct moe_ctx {
     // registered with (captured graphs hold its address)
     std::vector<uint8_t *> lin_ws;
     size_t lin_ws_bytes = 0;
-    // router loss workspace: loss parts, unmasked tokens, tickets
+    // router loss workspace: loss parts, tickets, counts
     uint8_t *router_ws = nullptr;
     moe_stats_t stats{};
     int last_T = -1;
@@ -227,9 +227,9 @@ void set_entry(moe_ctx *c, int tid, int e, uint64_t entry, int32_t slot) {
     push_upd(c, 1, (size_t)tid * c->Et + e, (uint64_t)(int64_t)stamp_index(c, tid, slot));
 }
 
-// Router loss workspace: [loss parts][unmasked tokens][tickets]
-constexpr size_t kRouterTailOff = sizeof(float) * 2 * moe::kRouterParts;
-constexpr size_t kRouterWsBytes = kRouterTailOff + 16;
+// Router loss workspace: [loss parts][tickets][picks per expert, unmasked tokens]
+constexpr size_t kRouterTicketOff = sizeof(float) * 2 * moe::kRouterParts, kRouterCountOff = kRouterTicketOff + 16;
+constexpr size_t kRouterWsBytes = kRouterCountOff + sizeof(int32_t) * (4096 + 1);
 
 constexpr size_t kStepKeys = 256;  // miss keys read back with the hit bitmap
 
@@ -653,7 +653,6 @@ int moe_layer_init(const moe_cfg *cfg, void *cuda_stream, moe_ctx **out) {
         }
     }
 
-    CKI((cudaError_t)moe::router_configure());
     CKI(cudaMalloc(&ctx->router_ws, kRouterWsBytes));
     CKI(cudaMemset(ctx->router_ws, 0, kRouterWsBytes));
     CKI(cudaHostAlloc(&ctx->h_stamps, sizeof(uint32_t) * (size_t)nt * std::max(1, ctx->spt), cudaHostAllocDefault));
@@ -1987,8 +1986,8 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
     p.counts = d_counts;
     p.dlogits = d_dlogits;
     p.ws_part = (float *)ctx->router_ws;
-    p.n_valid = (int32_t *)(ctx->router_ws + kRouterTailOff);
-    p.ticket = (unsigned *)(ctx->router_ws + kRouterTailOff + 4);
+    p.ticket = (unsigned *)(ctx->router_ws + kRouterTicketOff);
+    p.ws_count = (int32_t *)(ctx->router_ws + kRouterCountOff);
     p.error = ctx->d_error;
     p.T = n_tokens;
     p.E = n_experts;
