@@ -8,10 +8,9 @@
 //
 // Bound: at one token the weights' one read from HBM: 65536 x 2048 (75.5 MB)
 // 14.6 us = 5.2 TB/s, 0.76 of a copy's rate; 512 x 2048 2.3 us (latency).  With
-// more tokens the dots (8 dp4a and 6 others to a block and a token) and the
-// activations' shared-memory reads (4 cycles for 16 bytes that half a warp
-// shares): 2 tokens 18.8 us, 4 27, 8 53 (39 with two rows a lane), where the
-// tensor cores' path takes 44.
+// more tokens the time grows with the dots and the activations' shared-memory
+// reads: 2 tokens 18.4 us, 3 27.2, 4 28.3 to 29.5, where the tensor cores' path
+// takes 44; an earlier form of this kernel took 53 at 8 tokens.
 //
 // Weight layout (made at registration): per 16 rows, per group of up to 8
 // blocks: the codes [block][row] x 16 bytes in Q4 order, then the scales: Q4_0

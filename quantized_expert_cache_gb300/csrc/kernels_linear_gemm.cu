@@ -14,7 +14,7 @@
 // the exact-block-sum GEMM of the experts has to read every block's sums back
 // from TMEM and is bound by that; exact block sums on mma.sync, scaled in
 // registers, measured 88 us for 4096 x 4096 at 512 tokens (its f16 rate is a
-// quarter of tcgen05's).  Q4_K weights are formed in binary32 (d sc q - dmin m),
+// third of tcgen05's).  Q4_K weights are formed in binary32 (d sc q - dmin m),
 // scaled by a power of two so that the largest of the layer is below 2^15, and
 // split the same way.
 //
@@ -25,16 +25,14 @@
 //
 // The weight halves go from the converters' registers to TMEM (tcgen05.st) and
 // the MMA takes its A operand there: with A in shared memory an MMA reads 4 KB
-// more (46 cycles at N = 32 against 26; the measured floor at N = 64 and 128 is
-// 36 and 64), and every stage needs a fence between the converters' stores and
-// the MMA that measured 600 cycles.
+// more (46 cycles at N = 32 against 26, 52 at N = 64 against 36; 64 at N = 128).
 //
-// Bound.  4096 x 4096 at 512 tokens: 48.6 us (51.5 TFLOP of MMAs at 0.55 of the
-// measured bf16 rate; 4 us are the split kernel), the tensor pipe active 58% of
-// the time: operand reads, the tokens' copies and the weights' take 90 of the
-// 98 KB that shared memory moves in a stage's 768 tensor cycles.  Tiles of up to
-// 64 tokens: the conversions (about 170 instructions a warp and block of 32 x 32
-// weights, four warps a scheduler): 65536 x 2048 at 3 to 32 tokens 45 us, 2880 x
+// Bound.  4096 x 4096 at 512 tokens: 48.6 us (51.5 GFLOP of MMAs, both
+// kernels' time: 0.55 of the measured bf16 rate), the tensor pipe active 58% of
+// the GEMM's time.  By count, not measured: operand reads, the tokens' copies and
+// the weights' move about 90 KB through shared memory in a stage's 768 tensor
+// cycles, near 128 bytes a cycle.  Tiles of up to 64 tokens: the conversions, on
+// four warps a scheduler: 65536 x 2048 at 5 to 16 tokens 44 to 45 us, 2880 x
 // 2880 at 8 tokens 8.9 (latency of two launches, one round of stages and the
 // join), Q4_K 8192 x 2048 at 33 tokens 15.9.
 #include <cuda.h>

@@ -17,10 +17,9 @@
 //
 // Bound: 8 tokens (one launch, 3.4 us) by latency; 4096 x 512 with all three
 // gradients 10.3 us against 2.5 of HBM's rate, padded 12288 x 512 18.3 against
-// 7.5: two dependent launches, then a row's chain of loads and five warp
-// reductions with 32 warps a SM to hide it (DRAM at 15% of its rate, a third of
-// the stalls on loads).  Double accumulators took another 3 us: this part's
-// binary64 rate is 1/64.
+// 7.5: two dependent launches, then a row's chain of loads and warp reductions
+// with 32 warps a SM to hide it.  (Profiled with a cold cache, the loss kernel
+// alone keeps DRAM at 15% of its rate and waits most often for loads.)
 #include <algorithm>
 #include <type_traits>
 

@@ -127,7 +127,7 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
 // The same with A in TMEM (lane = row, two K elements a 32-bit column), called
 // by a whole warp: one elected lane issues it.  With the warp converged the
 // operands stay in uniform registers; a single-lane branch moves them there
-// one by one for every MMA (80 cycles an MMA against 52).
+// one by one for every MMA.
 __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
