@@ -484,9 +484,12 @@ int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, co
  * experts' block formats).  host_w: canonical blocks [rows][cols/32][18 B]
  * (MOE_FMT_Q4_0) or super-blocks [rows][cols/256][144 B] (MOE_FMT_Q4_K), any
  * host memory, copied.  cols: a multiple of 32 (Q4_K: of 256), at most 65536;
- * rows: at most 2^26.  The context keeps rows x cols x 18 / 32 bytes of device memory
- * until moe_destroy (twice that while the call runs).  *linear_id receives the
- * layer's id.  Synchronous.
+ * rows: at most 2^26.  The context keeps, until moe_destroy, a device copy of
+ * 18 bytes (Q4_K: 18.5) to 32 weights, rows rounded up to 16; while the call
+ * runs also the blocks as given.  A context whose batches take the tensor cores
+ * also keeps a workspace of R x cols x 4 + R x 4 bytes, R = max_tokens rounded up
+ * to 32, shared by its layers (a layer that needs a larger one allocates it;
+ * the earlier ones stay).  *linear_id receives the layer's id.  Synchronous.
  * Errors: MOE_ERR_ARG, MOE_ERR_OOM, MOE_ERR_CUDA.
  */
 int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int rows, int cols, int *linear_id);
@@ -495,8 +498,15 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
  * y = W x of a registered dense layer (no counterpart on the source pages;
  * the block dots and scales of the pointer-table mat-vec of
  * Zapdev-labs/a6000-custom-kernels): y[t][r] = the sum over blocks of 32 of
- * the exact int32 block dot times the weight block's and the activation
- * block's scales, in fp32, as the expert forwards compute it.  The
+ * the block dot times the weight block's and the activation block's scales.
+ * Up to two tokens, and three or four of at most 2048 columns: exact int32
+ * block dots, scaled and summed in fp32, as the expert forwards compute them.
+ * Other batches multiply scaled weights and activations in two binary16 parts
+ * each with fp32 sums on the tensor cores: about 6e-7 of the result (2-norm) at
+ * 4096 columns.  So the bits of a token's result depend on the batch's size.
+ * Layers with weights outside binary16's range (Q4_K: above 1e30) take the
+ * first form for every batch.  A bounded wait of the second form that expires
+ * is reported by the next cache_step or miss_drain (MOE_ERR_FAULT).  The
  * activations are either d_x, fp32 [n_tokens][cols], quantized in the call as
  * the forwards quantize theirs, or d_q and d_d, the codes and scales
  * moe_rms_norm writes; the other pointers are NULL.  d_x and d_q 16-byte
