@@ -1900,7 +1900,9 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
     uint8_t *src = nullptr, *w = nullptr;
     cudaError_t e = cudaMalloc(&w, moe::linear_weight_bytes(fmt, rows, cols));
     if (e == cudaSuccess) e = cudaMalloc(&src, bytes);
-    if (e == cudaSuccess) e = cudaMemcpy(src, host_w, bytes, cudaMemcpyHostToDevice);
+    // on the stream of the kernel that reads it: a copy of pageable memory on the
+    // legacy stream may return before its last bytes have landed
+    if (e == cudaSuccess) e = cudaMemcpyAsync(src, host_w, bytes, cudaMemcpyHostToDevice, ctx->stream);
     if (e == cudaSuccess) e = (cudaError_t)moe::launch_linear_repack(src, w, fmt, rows, cols, ctx->n_sm, ctx->stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->stream);
     cudaFree(src);

@@ -1,0 +1,43 @@
+"""GPU tests of the operators around the routed experts where they can go
+wrong: registration beside other streams, weights and activations over the whole
+range of their formats, batches that leave the tensor cores, layers registered
+between a graph's capture and its replay.
+
+Tolerances, with u = 2^-24 (unit roundoff of binary32):
+- linear: as in the operators' own tests, |err| <= (6 nb + 16) 2^-23 sum |w x|
+  of nb blocks of 32 columns (operands to 2^-22, at most 6 accumulations a block).
+"""
+import numpy as np
+import pytest
+
+import quantized_expert_cache_gb300 as qec
+from test_gpu_operators import check_linear, check_norm, decode, make_weights, run_norm
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def context(max_tokens=64, experts=8, k=2, stream=None):
+    st = torch.cuda.current_stream() if stream is None else stream
+    return qec.moe_layer_init(64, 32, experts, k, 1, 0, max_tokens, stream=st.cuda_stream)
+
+
+def test_registration_on_a_side_stream():
+    # the same blocks registered on a stream of their own and on the default one: the same bits
+    rows, cols = 8192, 8192
+    w = make_weights(rows, cols, qec.FMT_Q4_0, 11)
+    x = torch.randn(40, cols, device="cuda")
+    out = []
+    for st in (torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()):
+        ctx = context(stream=st)
+        lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, rows, cols)
+        torch.cuda.synchronize()
+        for n in (1, 40):
+            y = torch.full((n, rows), 7.0, device="cuda")
+            torch.cuda.synchronize()
+            qec.moe_linear_forward(ctx, lid, x, n, y)
+            torch.cuda.synchronize()
+            out.append(y)
+        qec.moe_destroy(ctx)
+    for y in out[2:]:
+        assert torch.equal(y, out[0 if y.shape[0] == 1 else 1])
