@@ -358,14 +358,14 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
             for (int t = tile0; t < total; t += stride, ++n_tile) {
                 const uint32_t idesc = idesc_f16(kBM, (columns(t % ntt) + 15) & ~15), cross = tmem + C::CROSS;
                 // the cross sums of the tile before are read
-                if (!mbar_wait_spin(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
+                if (!mbar_wait_warp(crosse, ((uint32_t)n_tile & 1u) ^ 1u, abort_flag, p.error, 8)) goto mma_done;
                 for (int kt = kt0; kt < kt1; ++kt, ++it) {
                     const int slot = it % STAGES, in_chunk = (kt - kt0) % C::CHUNK, buf = chunk % C::MAINS;
                     if (in_chunk == 0) {
-                        if (!mbar_wait_spin(acce0 + 8 * buf, ((uint32_t)(chunk / C::MAINS) & 1u) ^ 1u, abort_flag, p.error, 8))
+                        if (!mbar_wait_warp(acce0 + 8 * buf, ((uint32_t)(chunk / C::MAINS) & 1u) ^ 1u, abort_flag, p.error, 8))
                             goto mma_done;
                     }
-                    if (!mbar_wait_spin(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
+                    if (!mbar_wait_warp(full0 + 8 * slot, (uint32_t)(it / STAGES) & 1u, abort_flag, p.error, 4))
                         goto mma_done;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + slot * C::SLOT), main = tmem + (uint32_t)(buf * BN);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
                 const int it = it0 + (set + 4 * j) / C::BPS, prev = it - AST;
                 if (prev >= 0) {
                     const uint32_t bar = done0 + 8 * (prev % STAGES), parity = (uint32_t)(prev / STAGES) & 1u;
-                    if (!mbar_test(bar, parity)) {
+                    if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
                         if (lane == 0) ok = mbar_wait(bar, parity, abort_flag, p.error, 16);
                         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                         if (!ok) break;

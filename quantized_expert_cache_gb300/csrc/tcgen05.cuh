@@ -81,6 +81,14 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, vo
     return mbar_wait(bar, parity, abort_flag, err, code);
 }
 
+// The same by a whole warp, with one outcome for all its lanes: a wait may
+// expire for some lanes and not for others, and lanes that part here would not
+// meet again at the next instruction that takes the converged warp.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
+                                               int code) {
+    return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, err, code));
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
