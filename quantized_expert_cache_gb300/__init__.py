@@ -254,29 +254,66 @@ def moe_pool_snapshot(ctx, n_slots):
     return dict(owner=owner[:n_slots], stamps=stamps[:n_slots])
 
 
+# Element types an argument may have, by name; the type objects met so far are
+# added, so that a later check is one look-up.
+_FP32 = {"float32"}
+_SCALES = {"float16", "int16", "uint16"}
+_CODES = {"int8", "uint8"}
+_IDS = {"int32", "uint32"}
+_FLAGS = {"uint8", "int8", "bool"}
+_DTYPES = {"float32": F32, "float16": F16, "bfloat16": BF16}
+
+
+def _type_name(dtype) -> str:
+    return str(dtype).rpartition(".")[2]
+
+
+def _elem(x, types) -> int | None:
+    """_dev() of a tensor whose elements must have one of the types: one of
+    another size would be read past its end.  An address is taken as it is."""
+    if x is None or x.__class__ is int:
+        return x
+    try:
+        if x.dtype in types and x.is_cuda and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _dev(x)
+    name = _type_name(x.dtype)
+    if name not in types:
+        raise ValueError(f"expected {' or '.join(sorted(t for t in types if isinstance(t, str)))}, got {name}")
+    types.add(x.dtype)
+    return _dev(x)
+
+
 def _dtype(x) -> int:
     """MOE_F32 / MOE_F16 / MOE_BF16 of a torch tensor (fp32 for an address)."""
     if isinstance(x, int) or x is None:
         return F32
-    name = str(x.dtype)
-    if name not in _DTYPES:
-        raise ValueError(f"expected float32, float16 or bfloat16, got {name}")
-    return _DTYPES[name]
-
-
-_DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        name = _type_name(x.dtype)
+        if name not in _DTYPES:
+            raise ValueError(f"expected float32, float16 or bfloat16, got {name}")
+        code = _DTYPES[x.dtype] = _DTYPES[name]
+    return code
 
 
 def moe_rms_norm(ctx, x, res, weight, n_tokens, width, eps, sum, y, q=None, d=None, dtype=None, stream=None):
     """sum = x + res; y = RMS norm of it times weight; q, d = y's int8 codes and
-    scales.  res, sum, y, (q, d) may be None.  dtype: x's by default."""
+    scales.  res, sum, y, (q, d) may be None.  dtype: x's by default; if given,
+    x, res and sum must have elements of its size."""
     if dtype is None:
         dtype = _dtype(x)
         for o in (res, sum):
             if o is not None and not isinstance(o, int) and _dtype(o) != dtype:
                 raise ValueError("x, res and sum must have one dtype")
-    return _check(ctx, load().moe_rms_norm(ctx, _dev(x), _dev(res), dtype, _dev(weight), n_tokens, width, eps,
-                                           _dev(sum), _dev(y), _dev(q), _dev(d), _stream(stream)))
+    elif dtype in (F32, F16, BF16):
+        for o in (x, res, sum):
+            if o is not None and not isinstance(o, int) and o.element_size() != (4 if dtype == F32 else 2):
+                raise ValueError("x, res and sum must have elements of dtype's size")
+    return _check(ctx, load().moe_rms_norm(ctx, _dev(x), _dev(res), dtype, _elem(weight, _FP32), n_tokens, width, eps,
+                                           _dev(sum), _elem(y, _FP32), _elem(q, _CODES), _elem(d, _SCALES),
+                                           _stream(stream)))
 
 
 def moe_linear_register(ctx, host_w: np.ndarray, weight_format, rows, cols) -> int:
@@ -287,16 +324,17 @@ def moe_linear_register(ctx, host_w: np.ndarray, weight_format, rows, cols) -> i
 
 def moe_linear_forward(ctx, linear_id, x, n_tokens, y, q=None, d=None, stream=None):
     """y = W x from fp32 x, or (x None) from the codes q and scales d."""
-    return _check(ctx, load().moe_linear_forward(ctx, linear_id, _dev(x), _dev(q), _dev(d), n_tokens, _dev(y),
-                                                 _stream(stream)))
+    return _check(ctx, load().moe_linear_forward(ctx, linear_id, _elem(x, _FP32), _elem(q, _CODES), _elem(d, _SCALES),
+                                                 n_tokens, _elem(y, _FP32), _stream(stream)))
 
 
 def moe_router_loss(ctx, logits, idx, mask, gw, n_tokens, n_experts, k, balance_coef, z_coef, loss, counts,
                     dlogits=None, stream=None):
     """Balance and z loss, picks per expert and the logits' gradient; mask, gw
-    and dlogits may be None."""
-    return _check(ctx, load().moe_router_loss(ctx, _dev(logits), _dev(idx), _dev(mask), _dev(gw), n_tokens, n_experts,
-                                              k, balance_coef, z_coef, _dev(loss), _dev(counts), _dev(dlogits),
+    and dlogits may be None.  fp32, but int32 idx and counts, 8-bit mask."""
+    return _check(ctx, load().moe_router_loss(ctx, _elem(logits, _FP32), _elem(idx, _IDS), _elem(mask, _FLAGS),
+                                              _elem(gw, _FP32), n_tokens, n_experts, k, balance_coef, z_coef,
+                                              _elem(loss, _FP32), _elem(counts, _IDS), _elem(dlogits, _FP32),
                                               _stream(stream)))
 
 
