@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormParams p) {
     const T *x = (const T *)p.x + base, *res = p.res ? (const T *)p.res + base : nullptr;
     T *sum = p.sum ? (T *)p.sum + base : nullptr;
     float ss = 0.0f;
-    for (int v = threadIdx.x; v < p.width; v += blockDim.x) {
+    // (unsigned: the step past the last element of the widest row needs the 32nd bit)
+    const unsigned n = (unsigned)p.width;
+    for (unsigned v = threadIdx.x; v < n; v += blockDim.x) {
         const float s = to_f32<T>(x[v]) + (res ? to_f32<T>(res[v]) : 0.0f);
         ss = fmaf(s, s, ss);
     }
@@ -158,9 +160,9 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormParams p) {
     __syncthreads();
     ss = warp_sum_f(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f);
     const float r = 1.0f / sqrtf(ss / (float)p.width + p.eps);
-    for (int v0 = threadIdx.x - lane; v0 < p.width; v0 += blockDim.x) {
-        const int v = v0 + lane;
-        const bool on = v < p.width;
+    for (unsigned v0 = threadIdx.x - lane; v0 < n; v0 += blockDim.x) {
+        const unsigned v = v0 + lane;
+        const bool on = v < n;
         const float s = on ? to_f32<T>(x[v]) + (res ? to_f32<T>(res[v]) : 0.0f) : 0.0f;
         const float y = on ? s * r * p.weight[v] : 0.0f;
         if (on && sum) sum[v] = from_f32<T>(s);

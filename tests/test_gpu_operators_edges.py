@@ -41,3 +41,20 @@ def test_registration_on_a_side_stream():
         qec.moe_destroy(ctx)
     for y in out[2:]:
         assert torch.equal(y, out[0 if y.shape[0] == 1 else 1])
+
+
+def test_norm_of_the_widest_row():
+    # 2^31 - 1 elements: the index steps past the end need the 32nd bit
+    n = 2 ** 31 - 1
+    ctx = context()
+    at = torch.cat([torch.arange(0, n, n // 60, device="cuda"), torch.arange(n - 3, n, device="cuda")]).unique()
+    x = torch.zeros(1, n, dtype=torch.bfloat16, device="cuda")
+    x[0, at] = 1
+    y = torch.full((1, n), 7.0, device="cuda")
+    qec.moe_rms_norm(ctx, x, None, torch.full((n,), 0.5, device="cuda"), 1, n, 1e-9, None, y)
+    torch.cuda.synchronize()
+    r = 0.5 / np.sqrt(at.numel() / n + 1e-9)  # sums of ones are exact; the rest is 6 roundings
+    assert (abs(y[0, at].double() - r) <= 6 * 2.0 ** -24 * r).all()
+    y[0, at] = 0
+    assert int(torch.count_nonzero(y)) == 0
+    qec.moe_destroy(ctx)
