@@ -471,8 +471,9 @@ int moe_set_router(moe_ctx *ctx, int layer, const float *host_w, const float *ho
  * least one output.  Outputs may be the inputs' own buffers (d_sum = d_res, say).  Infinities and NaN spread as
  * in the formulas over their row (a block whose max|y| is not a number, or
  * beyond binary16, has a scale that says so).  Asynchronous on `stream` (NULL:
- * the context's), any stream; capturable.  Rows whose buffers are 16-byte
- * aligned and whose width is a multiple of 4 take wide loads.
+ * the context's), any stream; capturable.  Every pointer is aligned to its
+ * elements; rows whose buffers are 16-byte aligned and whose width is a multiple
+ * of 4 take wide loads.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
@@ -538,7 +539,8 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
  * nothing else adds nothing to the losses, its ids still count and its
  * gradient is zero.  NaN spreads.  The same inputs give the same bits.
  * E and k: the context's (of all shards).  `stream` must be the context's
- * stream (or NULL).  Asynchronous; capturable.
+ * stream (or NULL).  Every pointer is aligned to its elements.  Asynchronous;
+ * capturable.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, const uint8_t *d_mask,

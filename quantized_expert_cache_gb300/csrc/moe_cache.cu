@@ -20,6 +20,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 #include <thread>
 #include <vector>
@@ -1826,6 +1827,13 @@ void moe_destroy(moe_ctx *ctx) {
     delete ctx;
 }
 
+// Whether all addresses are multiples of an element's size (null is).
+static bool whole(std::initializer_list<const void *> ptrs, uintptr_t size) {
+    for (const void *p : ptrs)
+        if ((uintptr_t)p & (size - 1)) return false;
+    return true;
+}
+
 int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
                  int width, float eps, void *d_sum, float *d_y, int8_t *d_q, uint16_t *d_d, void *stream) {
     if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
@@ -1837,6 +1845,8 @@ int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, co
     if (d_q && width % 32) return fail(ctx, MOE_ERR_ARG, "rms_norm: codes need a width that is a multiple of 32");
     if (n_tokens == 0) return MOE_OK;
     if (!d_x || !d_weight || (!d_sum && !d_y && !d_q)) return fail(ctx, MOE_ERR_ARG, "rms_norm: null pointer");
+    if (!whole({d_x, d_res, d_sum}, dtype == MOE_F32 ? 4 : 2) || !whole({d_weight, d_y}, 4) || !whole({d_d}, 2))
+        return fail(ctx, MOE_ERR_ARG, "rms_norm: a pointer is not aligned to its elements");
     moe::NormParams p{};
     p.x = d_x;
     p.res = d_res;
@@ -1979,6 +1989,8 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
         return fail(ctx, MOE_ERR_ARG, "router_loss: stream must be the context stream");
     if (!d_loss || !d_counts || (n_tokens > 0 && (!d_logits || !d_idx)) || (d_dlogits && d_dlogits == d_logits))
         return fail(ctx, MOE_ERR_ARG, "router_loss: null pointer, or d_dlogits is d_logits");
+    if (!whole({d_logits, d_idx, d_gw, d_loss, d_counts, d_dlogits}, 4))
+        return fail(ctx, MOE_ERR_ARG, "router_loss: a pointer is not aligned to its elements");
     moe::RouterParams p{};
     p.logits = d_logits;
     p.idx = d_idx;

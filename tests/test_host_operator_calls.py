@@ -84,3 +84,84 @@ def test_registration_uploads_on_the_stream_that_reads(host, fmt, block, max_tok
     # and the call returns when the caller's memory has been read
     assert any(c[0] == "sync" for c in log[upload:])
     host.lib.moe_destroy(ctx)
+
+
+# ---- refusals before any launch: addresses stand for device buffers, which nothing here reads
+A = 1 << 32  # far from one another unless a test moves them
+
+
+def buffers(names, **change):
+    at = {n: (i + 1) * A for i, n in enumerate(names)}
+    return dict(at, **change)
+
+
+def norm(host, ctx, dtype=0, tokens=3, width=64, **change):
+    b = buffers(("x", "res", "weight", "sum", "y", "q", "d"), **change)
+    return host.lib.moe_rms_norm(ctx, b["x"], b["res"], dtype, b["weight"], tokens, width, 1e-6, b["sum"], b["y"],
+                                 b["q"], b["d"], None)
+
+
+def linear(host, ctx, lid, tokens=3, **change):
+    b = buffers(("x", "q", "d", "y"), **change)
+    return host.lib.moe_linear_forward(ctx, lid, b["x"], b["q"], b["d"], tokens, b["y"], None)
+
+
+def router(host, ctx, tokens=3, **change):
+    b = buffers(("logits", "idx", "mask", "gw", "loss", "counts", "dlogits"), **change)
+    return host.lib.moe_router_loss(ctx, b["logits"], b["idx"], b["mask"], b["gw"], tokens, 8, 2, 0.1, 0.1, b["loss"],
+                                    b["counts"], b["dlogits"], None)
+
+
+class Call:
+    """One operator of a context: whether a call is taken, and that a refused one launches nothing."""
+
+    def __init__(self, host, call, *args):
+        self.host, self.call, self.args = host, call, args
+
+    def takes(self, **change):
+        self.host.lib.host_clear()
+        assert self.call(self.host, *self.args, **change) == 0, change
+        assert len(self.host.log()) == 1
+
+    def refuses(self, **change):
+        self.host.lib.host_clear()
+        assert self.call(self.host, *self.args, **change) == -1, change
+        assert not self.host.log()
+
+
+@pytest.fixture()
+def calls(host):
+    ctx = host.context()
+    rc, lid = host.register(ctx, np.zeros((24, 2, 18), np.uint8), qec.FMT_Q4_0, 24, 64)
+    assert rc == 0
+    yield Call(host, norm, ctx), Call(host, linear, ctx, lid), Call(host, router, ctx)
+    host.lib.moe_destroy(ctx)
+
+
+def test_addresses_off_their_elements_are_refused(calls):
+    norms, linears, routers = calls
+    norms.takes()
+    for name, size in dict(x=4, res=4, sum=4, weight=4, y=4, d=2).items():
+        for off in range(1, size):
+            norms.refuses(**{name: 16 * A + off})
+        norms.takes(**{name: 16 * A + size})
+    for dtype in (1, 2):
+        for name in ("x", "res", "sum"):
+            norms.refuses(dtype=dtype, **{name: 16 * A + 1})
+            norms.takes(dtype=dtype, **{name: 16 * A + 2})
+    norms.takes(q=16 * A + 1)
+    codes = dict(x=None)
+    values = dict(q=None, d=None)
+    linears.takes(**codes)
+    linears.takes(**values)
+    linears.refuses(x=16 * A + 4, q=None, d=None)
+    linears.refuses(x=None, q=16 * A + 4)
+    linears.refuses(x=None, d=16 * A + 1)
+    linears.refuses(y=16 * A + 2, **values)
+    linears.takes(y=16 * A + 4, **values)
+    routers.takes()
+    for name in ("logits", "idx", "gw", "loss", "counts", "dlogits"):
+        for off in (1, 2, 3):
+            routers.refuses(**{name: 16 * A + off})
+        routers.takes(**{name: 16 * A + 4})
+    routers.takes(mask=16 * A + 1)
