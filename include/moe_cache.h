@@ -468,7 +468,9 @@ int moe_set_router(moe_ctx *ctx, int layer, const float *host_w, const float *ho
  * d_res and d_sum may be NULL.  d_weight: fp32 [width].  d_y: fp32
  * [n_tokens][width] or NULL.  d_q, d_d: int8 [n_tokens][width] and binary16
  * [n_tokens][width/32], both or neither (both need width % 32 == 0).  At
- * least one output.  Outputs may be the inputs' own buffers (d_sum = d_res, say).  Infinities and NaN spread as
+ * least one output.  d_sum may be d_x or d_res, and so may d_y of MOE_F32 rows,
+ * at the same address; no output meets another buffer otherwise
+ * (MOE_ERR_ARG).  Infinities and NaN spread as
  * in the formulas over their row (a block whose max|y| is not a number, or
  * beyond binary16, has a scale that says so).  Asynchronous on `stream` (NULL:
  * the context's), any stream; capturable.  Every pointer is aligned to its
@@ -511,7 +513,8 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
  * activations are either d_x, fp32 [n_tokens][cols], quantized in the call as
  * the forwards quantize theirs, or d_q and d_d, the codes and scales
  * moe_rms_norm writes; the other pointers are NULL.  d_x and d_q 16-byte
- * aligned.  d_y: fp32 [n_tokens][rows].  n_tokens <= cfg.max_tokens.
+ * aligned.  d_y: fp32 [n_tokens][rows], meeting no input.  n_tokens <=
+ * cfg.max_tokens.
  * `stream` must be the context's stream (or NULL).  Asynchronous; capturable.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
@@ -534,8 +537,8 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
  * token out of everything (its gradient row is zero); all out: losses, counts
  * and gradients are zero.  d_gw: fp32 [n_tokens][k] or NULL; the routing
  * weights are route_topk's for cfg.renorm_topk.  d_loss: fp32 [2].  d_counts:
- * int32 [E], written.  d_dlogits: fp32 [n_tokens][E] or NULL; may not be
- * d_logits.  A logit of -infinity is an expert the token cannot take; a row of
+ * int32 [E], written.  d_dlogits: fp32 [n_tokens][E] or NULL.  No output
+ * meets another buffer (MOE_ERR_ARG).  A logit of -infinity is an expert the token cannot take; a row of
  * nothing else adds nothing to the losses, its ids still count and its
  * gradient is zero.  NaN spreads.  The same inputs give the same bits.
  * E and k: the context's (of all shards).  `stream` must be the context's

@@ -1834,6 +1834,29 @@ static bool whole(std::initializer_list<const void *> ptrs, uintptr_t size) {
     return true;
 }
 
+// Bytes that an operator reads or writes (none without an address).
+struct Span {
+    const void *p;
+    size_t n;
+    bool meets(const Span &o) const {
+        const uintptr_t a = (uintptr_t)p, b = (uintptr_t)o.p;
+        return p && o.p && a < b + o.n && b < a + n;
+    }
+};
+
+// Whether no output meets an input or another output.  Rows are worked on by
+// independent warps and CTAs: what one writes over bytes that another has yet to
+// read is a race.
+static bool apart(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+    for (const Span *o = out.begin(); o != out.end(); ++o) {
+        for (const Span &i : in)
+            if (o->meets(i)) return false;
+        for (const Span *q = out.begin(); q != o; ++q)
+            if (o->meets(*q)) return false;
+    }
+    return true;
+}
+
 int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
                  int width, float eps, void *d_sum, float *d_y, int8_t *d_q, uint16_t *d_d, void *stream) {
     if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
@@ -1847,6 +1870,16 @@ int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, co
     if (!d_x || !d_weight || (!d_sum && !d_y && !d_q)) return fail(ctx, MOE_ERR_ARG, "rms_norm: null pointer");
     if (!whole({d_x, d_res, d_sum}, dtype == MOE_F32 ? 4 : 2) || !whole({d_weight, d_y}, 4) || !whole({d_d}, 2))
         return fail(ctx, MOE_ERR_ARG, "rms_norm: a pointer is not aligned to its elements");
+    const size_t n = (size_t)n_tokens * width, el = dtype == MOE_F32 ? 4 : 2;
+    // an output of an input's element size may be that input: every element is
+    // written by the thread that read it
+    const auto input = [&](const void *p) {
+        return Span{p == d_sum || (dtype == MOE_F32 && p == d_y) ? nullptr : p, n * el};
+    };
+    const Span sum{d_sum, n * el}, y{d_y, n * 4}, q{d_q, n}, d{d_d, n / 16}, weight{d_weight, (size_t)width * 4};
+    if (!apart({input(d_x), input(d_res), weight}, {sum, y, q, d}))
+        return fail(ctx, MOE_ERR_ARG,
+                    "rms_norm: an output meets another buffer (only d_sum, and d_y of MOE_F32 rows, may be d_x or d_res)");
     moe::NormParams p{};
     p.x = d_x;
     p.res = d_res;
@@ -1951,6 +1984,9 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
     if (((uintptr_t)d_x & 15) || ((uintptr_t)d_q & 15) || ((uintptr_t)d_d & 1) || ((uintptr_t)d_y & 3))
         return fail(ctx, MOE_ERR_ARG, "linear: d_x and d_q must be 16-byte aligned");
     const auto &l = ctx->linears[linear_id];
+    const size_t n = (size_t)n_tokens * l.cols;
+    if (!apart({{d_x, n * 4}, {d_q, n}, {d_d, n / 16}}, {{d_y, (size_t)n_tokens * l.rows * 4}}))
+        return fail(ctx, MOE_ERR_ARG, "linear: d_y meets an input");
     moe::LinearParams p{};
     p.w = l.w;
     p.x = d_x;
@@ -1991,6 +2027,10 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
         return fail(ctx, MOE_ERR_ARG, "router_loss: null pointer, or d_dlogits is d_logits");
     if (!whole({d_logits, d_idx, d_gw, d_loss, d_counts, d_dlogits}, 4))
         return fail(ctx, MOE_ERR_ARG, "router_loss: a pointer is not aligned to its elements");
+    const size_t tn = (size_t)n_tokens, te = tn * n_experts * 4, tk = tn * k * 4;
+    if (!apart({{d_logits, te}, {d_idx, tk}, {d_mask, tn}, {d_gw, tk}},
+               {{d_loss, 8}, {d_counts, (size_t)n_experts * 4}, {d_dlogits, te}}))
+        return fail(ctx, MOE_ERR_ARG, "router_loss: an output meets another buffer");
     moe::RouterParams p{};
     p.logits = d_logits;
     p.idx = d_idx;

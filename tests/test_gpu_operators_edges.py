@@ -43,6 +43,29 @@ def test_registration_on_a_side_stream():
         assert torch.equal(y, out[0 if y.shape[0] == 1 else 1])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens,width", [(1, 2048), (5, 96), (300, 2048), (700, 160), (3, 1001), (3, 40000)])
+def test_norm_sums_in_place(tokens, width, dtype):
+    ctx = context()
+    g = torch.Generator(device="cuda").manual_seed(width)
+    x, res = (torch.randn(tokens, width, generator=g, device="cuda").to(dtype) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(width, generator=g, device="cuda")
+    want = run_norm(ctx, x, res, w, codes=width % 32 == 0)
+    check_norm(x, res, w, want)
+    for into in (0, 1):
+        a = [x.clone(), res.clone()]
+        y = torch.empty(tokens, width, device="cuda")
+        qec.moe_rms_norm(ctx, a[0], a[1], w, tokens, width, 1e-5, a[into], y)
+        assert torch.equal(a[into], want[0]) and torch.equal(y, want[1])
+        assert torch.equal(a[1 - into], (x, res)[1 - into])
+    if dtype == torch.float32:
+        for into in (0, 1):
+            a = [x.clone(), res.clone()]
+            qec.moe_rms_norm(ctx, a[0], a[1], w, tokens, width, 1e-5, a[1 - into], a[into])
+            assert torch.equal(a[1 - into], want[0]) and torch.equal(a[into], want[1])
+    qec.moe_destroy(ctx)
+
+
 def test_norm_of_the_widest_row():
     # 2^31 - 1 elements: the index steps past the end need the 32nd bit
     n = 2 ** 31 - 1

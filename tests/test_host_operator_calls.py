@@ -165,3 +165,59 @@ def test_addresses_off_their_elements_are_refused(calls):
             routers.refuses(**{name: 16 * A + off})
         routers.takes(**{name: 16 * A + 4})
     routers.takes(mask=16 * A + 1)
+
+
+def sizes(call, dtype=0, n=3 * 64):
+    el = 2 if dtype else 4
+    return dict(norm=dict(x=n * el, res=n * el, weight=64 * 4, sum=n * el, y=n * 4, q=n, d=n // 32 * 2),
+                linear=dict(x=n * 4, q=n, d=n // 32 * 2, y=3 * 24 * 4),
+                router=dict(logits=3 * 8 * 4, idx=3 * 2 * 4, mask=3, gw=3 * 2 * 4, loss=8, counts=8 * 4,
+                            dlogits=3 * 8 * 4))[call]
+
+
+def check_overlaps(call, names, outs, size, same=(), **fixed):
+    """Every output against every other buffer of the call: side by side is taken; the first byte on the
+    last, the last on the first, and the same address (but for the pairs of `same`) are refused."""
+    base = 64 * A
+    gap = lambda n: (n + 15) // 16 * 16  # noqa: E731  (aligned for every type)
+    for o in outs:
+        for i in names:
+            if i == o:
+                continue
+            call.takes(**fixed, **{i: base, o: base + gap(size[i])})
+            call.takes(**fixed, **{i: base, o: base - gap(size[o])})
+            last = (size[i] - 1) // 16 * 16  # the last aligned address inside i
+            for at in (last, -((size[o] - 1) // 16 * 16)):
+                if at:
+                    call.refuses(**fixed, **{i: base, o: base + at})
+            (call.takes if (o, i) in same else call.refuses)(**fixed, **{i: base, o: base})
+
+
+def test_buffers_that_meet_are_refused(calls):
+    norms, linears, routers = calls
+    outs = ("sum", "y", "q", "d")
+    same = {("sum", "x"), ("sum", "res")}
+    names = ("x", "res", "weight") + outs
+    check_overlaps(norms, names, outs, sizes("norm"), same | {("y", "x"), ("y", "res")})
+    for dtype in (1, 2):
+        check_overlaps(norms, names, outs, sizes("norm", dtype), same, dtype=dtype)
+    norms.takes(x=A, res=A)                      # inputs may be one buffer
+    norms.takes(x=A, res=A, sum=A)
+    norms.takes(x=A, res=2 * A, sum=2 * A, y=A)
+    norms.refuses(x=A, sum=A, y=A)               # two outputs on it may not
+    norms.refuses(x=A, res=A + 16, sum=A)        # and not where the other input is read elsewhere
+    check_overlaps(linears, ("x", "y"), ("y",), sizes("linear"), q=None, d=None)
+    check_overlaps(linears, ("q", "y"), ("y",), sizes("linear"), x=None)
+    check_overlaps(linears, ("d", "y"), ("y",), sizes("linear"), x=None)
+    check_overlaps(routers, ("logits", "idx", "mask", "gw", "loss", "counts", "dlogits"),
+                   ("loss", "counts", "dlogits"), sizes("router"))
+
+
+def test_calls_without_tokens_meet_nothing(host, calls):
+    norms, linears, routers = calls
+    host.lib.host_clear()
+    assert norm(host, norms.args[0], tokens=0, x=A, y=A, sum=A) == 0
+    assert linear(host, *linears.args, tokens=0, x=A, y=A) == 0
+    assert not host.log()
+    routers.takes(tokens=0, logits=A, dlogits=A + 4)
+    routers.refuses(tokens=0, loss=A, counts=A)
