@@ -488,8 +488,8 @@ int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, co
  * (MOE_FMT_Q4_0) or super-blocks [rows][cols/256][144 B] (MOE_FMT_Q4_K), any
  * host memory, copied.  cols: a multiple of 32 (Q4_K: of 256), at most 65536;
  * rows: at most 2^26.  The context keeps, until moe_destroy, a device copy of
- * 18 bytes (Q4_K: 18.5) to 32 weights, rows rounded up to 16; while the call
- * runs also the blocks as given.  A context whose batches take the tensor cores
+ * 18 bytes (Q4_K: 18.5) to 32 weights, rows rounded up to 16 (Q4_K: and 4 bytes
+ * a row, rounded up to 128); while the call runs also the blocks as given.  A context whose batches take the tensor cores
  * also keeps a workspace of R x cols x 4 + R x 4 bytes, R = max_tokens rounded up
  * to 32, shared by its layers (a layer that needs a larger one allocates it;
  * the earlier ones stay).  *linear_id receives the layer's id.  Synchronous.
@@ -506,7 +506,8 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
  * block dots, scaled and summed in fp32, as the expert forwards compute them.
  * Other batches multiply scaled weights and activations in two binary16 parts
  * each with fp32 sums on the tensor cores: about 6e-7 of the result (2-norm) at
- * 4096 columns.  So the bits of a token's result depend on the batch's size.
+ * 4096 columns, a Q4_K weight kept to at least 2^-39 of the largest of its row.
+ * So the bits of a token's result depend on the batch's size.
  * Layers with weights outside binary16's range (Q4_K: above 1e30) take the
  * first form for every batch.  A bounded wait of the second form that expires
  * is reported by the next cache_step or miss_drain (MOE_ERR_FAULT).  The

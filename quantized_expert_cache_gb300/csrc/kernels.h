@@ -197,11 +197,10 @@ struct LinearParams {
     const __half *d;            // [n_tokens][cols / 32]
     float *y;                   // [n_tokens][rows]
     int fmt, rows, cols, n_tokens;
-    // batches: the activations' two binary16 halves [max_tokens][cols], their
-    // token scales, the weights' power-of-two scale and its inverse
+    // batches: the activations' two binary16 halves [max_tokens][cols] and their
+    // token scales
     __half *ws_hi, *ws_lo;
     float *ws_scale;
-    float w_scale, w_unscale;
     int *error;                 // a bit set when a bounded wait expires
 };
 struct LinearGemm {
@@ -213,7 +212,7 @@ int launch_rms_norm(const NormParams &p, cudaStream_t st);
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st);
 size_t linear_weight_bytes(int fmt, int rows, int cols);
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, int cols, int n_sm, cudaStream_t st);
-int launch_linear_max(const uint8_t *w, int fmt, int rows, int cols, unsigned *out, int n_sm, cudaStream_t st);
+int launch_linear_max(uint8_t *w, int fmt, int rows, int cols, unsigned *out, int n_sm, cudaStream_t st);
 int launch_linear(const LinearParams &p, int n_sm, cudaStream_t st);
 int linear_gemm_box();
 int linear_gemm_configure();

@@ -239,21 +239,34 @@ __global__ void __launch_bounds__(kVecWarps * 32, TN > 2 ? 3 : 4) linear_vec_ker
 }
 
 // Largest magnitude a block's weights can take, over the matrix, as binary32
-// bits (NaN above infinity above all): *out, zero before.
+// bits (NaN above infinity above all): *out, zero before.  Q4_K: also the rows'
+// powers of two, which bring a row's largest magnitude to [2^14, 2^15) (1 for a
+// row of zeros).  A warp a row.
 template <int FMT>
-__global__ void linear_max_kernel(const uint8_t *__restrict__ w, int rows, int nb, unsigned *out) {
-    const size_t n = (size_t)((rows + 15) / 16) * 16 * nb;
-    unsigned m = 0;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
-        const size_t row = i / nb;
-        VBlock<FMT> v;
-        v.load(w + (row >> 4) * tile_bytes(FMT, nb), nb, (int)(i % nb), (int)(row & 15));
-        const float2 s = v.scale();
-        m = max(m, FMT == kFmtQ4 ? __float_as_uint(fabsf(8.0f * s.x))
-                                 : max(__float_as_uint(fabsf(s.y)), __float_as_uint(fabsf(fmaf(15.0f, s.x, s.y)))));
+__global__ void linear_max_kernel(const uint8_t *w, int rows, int nb, float *row_scale, unsigned *out) {
+    const int lane = threadIdx.x & 31, rt_n = (rows + 15) / 16;
+    const size_t n = (size_t)(rows + kScaleRows - 1) / kScaleRows * kScaleRows;
+    unsigned top = 0;
+    for (size_t row = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < n;
+         row += (size_t)gridDim.x * blockDim.x >> 5) {
+        unsigned m = 0;
+        if (row >> 4 < (size_t)rt_n)
+            for (int b = lane; b < nb; b += 32) {
+                VBlock<FMT> v;
+                v.load(w + (row >> 4) * tile_bytes(FMT, nb), nb, b, (int)(row & 15));
+                const float2 s = v.scale();
+                m = max(m, FMT == kFmtQ4
+                               ? __float_as_uint(fabsf(8.0f * s.x))
+                               : max(__float_as_uint(fabsf(s.y)), __float_as_uint(fabsf(fmaf(15.0f, s.x, s.y)))));
+            }
+        m = __reduce_max_sync(0xffffffffu, m);
+        top = max(top, m);
+        // (magnitudes are multiples of 2^-24 and below 2^27: the exponents stay in range; a layer with
+        // infinities or NaN has no use for them)
+        if (FMT == kFmtQ4K && lane == 0)
+            row_scale[row] = m && m < 0x7f800000u ? __uint_as_float((127u + 127u + 14u - (m >> 23)) << 23) : 1.0f;
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) atomicMax(out, m);
+    if (lane == 0) atomicMax(out, top);
 }
 
 // ---- launch ---------------------------------------------------------------------
@@ -301,7 +314,8 @@ int launch_fmt(const LinearParams &p, int n_sm, cudaStream_t st) {
 }  // namespace
 
 size_t linear_weight_bytes(int fmt, int rows, int cols) {
-    return (size_t)((rows + 15) / 16) * tile_bytes(fmt, cols / kBlock);
+    const size_t scales = fmt == kFmtQ4K ? (size_t)(rows + kScaleRows - 1) / kScaleRows * kScaleRows * 4 : 0;
+    return row_scale_offset(fmt, rows, cols / kBlock) + scales;
 }
 
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, int cols, int n_sm, cudaStream_t st) {
@@ -311,13 +325,13 @@ int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, in
     return (int)cudaGetLastError();
 }
 
-int launch_linear_max(const uint8_t *w, int fmt, int rows, int cols, unsigned *out, int n_sm, cudaStream_t st) {
-    const size_t n = (size_t)((rows + 15) / 16) * 16 * (cols / kBlock);
-    const unsigned g = (unsigned)std::min<size_t>((n + 255) / 256, (size_t)n_sm * 8);
+int launch_linear_max(uint8_t *w, int fmt, int rows, int cols, unsigned *out, int n_sm, cudaStream_t st) {
+    const int nb = cols / kBlock;
+    const unsigned g = (unsigned)std::min(rows / 8 + kScaleRows / 8, n_sm * 8);  // 8 rows a CTA
     if (fmt == kFmtQ4K)
-        linear_max_kernel<kFmtQ4K><<<g, 256, 0, st>>>(w, rows, cols / kBlock, out);
+        linear_max_kernel<kFmtQ4K><<<g, 256, 0, st>>>(w, rows, nb, (float *)(w + row_scale_offset(fmt, rows, nb)), out);
     else
-        linear_max_kernel<kFmtQ4><<<g, 256, 0, st>>>(w, rows, cols / kBlock, out);
+        linear_max_kernel<kFmtQ4><<<g, 256, 0, st>>>(w, rows, nb, nullptr, out);
     return (int)cudaGetLastError();
 }
 

@@ -15,8 +15,10 @@
 // from TMEM and is bound by that; exact block sums on mma.sync, scaled in
 // registers, measured 88 us for 4096 x 4096 at 512 tokens (its f16 rate is a
 // third of tcgen05's).  Q4_K weights are formed in binary32 (d sc q - dmin m),
-// scaled by a power of two so that the largest of the layer is below 2^15, and
-// split the same way.
+// scaled by a power of two so that the largest of their row is below 2^15, and
+// split the same way: to 2^-39 of the row's largest.  (One power of two for the
+// layer left rows far below its largest block to binary16's subnormals: 1e-3 off
+// beside a block of d = 65504.)
 //
 // The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
 // on a growing sum; so the large products are accumulated for 512 columns
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
     if (FP) top = __half2float(__float2half_rn(top / 127.0f));
     const int e = top > 0.0f && top <= 65504.0f ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 : 0;
     const float up = __uint_as_float((unsigned)(127 + e) << 23), down = __uint_as_float((unsigned)(127 - e) << 23);
-    if (threadIdx.x == 0) p.ws_scale[t] = up * p.w_unscale;
+    if (threadIdx.x == 0) p.ws_scale[t] = up;
     // 8 lanes a block (whole warps run every round)
     auto emit = [&](int i, Four f) {
         if (FP) {
@@ -399,7 +401,6 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
         if (C::WIDE) set_regs<kRegsConv, false>();
         const int set = (warp - C::WCONV) >> 2, quarter = warp & 3, row = quarter * 32 + lane, r = row & 15;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + C::A_COL + 32 * (set % C::BPS);
-        const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
         const size_t rt_bytes = tile_bytes(FMT, nb);
         const int me = threadIdx.x - C::WCONV * 32;
         const uint32_t codes = smem_u32(smem + C::RAW_OFF) + me * 16,
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
         for (int i = 0; i < kAhead; ++i) fetch();
         int ce = 0;
         bool ok = true;
-        for (int it0 = 0; it0 < n_it && ok; it0 += C::SPG) {
+        auto group = [&](int it0, float scale) {
             fetch();
             cp_wait<kAhead>();
 #pragma unroll
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
                          scales + ce * C::RAW_BYTES + C::SCALES);
                 raw.up = r >> 3;
                 uint32_t h[16], l[16];
-                convert(raw, p.w_scale, h, l);
+                convert(raw, scale, h, l);
                 // block set + 4 j's stage; its place in TMEM was that of AST stages ago
                 const int it = it0 + (set + 4 * j) / C::BPS, prev = it - AST;
                 if (prev >= 0) {
@@ -465,6 +466,19 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
                 mbar_arrive_warp(full0 + 8 * (it % STAGES), lane);
             }
             ce = ce == kAhead ? 0 : ce + 1;
+        };
+        // Q4_K goes tile by tile, each with the power of two of this thread's row
+        // (switched inside one loop over all groups, as Q4_0 has it, 65536 x 2048
+        // at 16 tokens took 72 us instead of 69; Q4_0 by tiles 47.7 instead of 47.3)
+        if constexpr (FMT == kFmtQ4K) {
+            const float *row_scale = (const float *)(p.w + row_scale_offset(FMT, p.rows, nb)) + row;
+            for (int t = tile0, it0 = 0; t < total && ok; t += stride) {
+                const float scale = __ldg(row_scale + t / ntt * kBM);
+                for (const int end = it0 + (kt1 - kt0); it0 < end && ok; it0 += C::SPG) group(it0, scale);
+            }
+        } else {
+            const int n_it = tile0 < total ? ((total - 1 - tile0) / stride + 1) * (kt1 - kt0) : 0;
+            for (int it0 = 0; it0 < n_it && ok; it0 += C::SPG) group(it0, 1.0f);
         }
         cp_wait<0>();
     } else {
@@ -478,6 +492,9 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
         int chunk = 0;
         for (int t = tile0; t < total; t += stride) {
             const int tt = t % ntt, nc = columns(tt) - c0;  // this warp's valid columns
+            const int row = t / ntt * kBM + r;
+            uint32_t rs = 0;  // Q4_K: the row's power of two
+            if (FMT == kFmtQ4K) rs = __ldg((const uint32_t *)(p.w + row_scale_offset(FMT, p.rows, nb)) + row);
             float acc[HC];
 #pragma unroll
             for (int i = 0; i < HC; ++i) acc[i] = 0.0f;
@@ -515,12 +532,12 @@ __global__ void __launch_bounds__((LCfg<FMT, BN>::THREADS), 1)
                     mbar_arrive_warp(crosse, lane);
                 }
             }
-            const int row = t / ntt * kBM + r;
             float *red = (float *)smem;  // a split tile: its sums [column][row], over the stages it is done with
 #pragma unroll
             for (int i = 0; i < HC; ++i) {
                 if (i >= nc) break;  // warp-uniform
-                const float v = acc[i] * __shfl_sync(0xffffffffu, ts[i / 32], i % 32);
+                float v = acc[i] * __shfl_sync(0xffffffffu, ts[i / 32], i % 32);
+                if (FMT == kFmtQ4K) v *= __uint_as_float((254u << 23) - rs);  // its inverse
                 if (S > 1)
                     red[(c0 + i) * kBM + r] = v;
                 else if (row < p.rows)

@@ -14,4 +14,11 @@ __host__ __device__ inline size_t tile_bytes(int fmt, int nb) {
     return (size_t)nb * kARec + (fmt == kFmtQ4K ? (size_t)(nb / kKB) * 64 : 0);
 }
 
+// Q4_K: the rows' powers of two (kernels_linear_gemm.cu), fp32, whole tiles of
+// 128 rows, stand after the blocks.
+__host__ __device__ inline size_t row_scale_offset(int fmt, int rows, int nb) {
+    return (size_t)((rows + 15) / 16) * tile_bytes(fmt, nb);
+}
+constexpr int kScaleRows = 128;
+
 }  // namespace moe

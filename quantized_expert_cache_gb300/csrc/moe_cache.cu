@@ -17,7 +17,6 @@
 
 #include <algorithm>
 #include <chrono>
-#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
@@ -153,10 +152,9 @@ struct moe_ctx {
     struct Linear {
         int fmt, rows, cols;
         uint8_t *w;
-        // batches: power-of-two scale of the weights, the split activations'
-        // workspace and its tensor maps (gemm: the tensor cores can take them)
+        // batches: the split activations' workspace and its tensor maps (gemm:
+        // the tensor cores can take them)
         bool gemm;
-        float w_scale;
         uint8_t *ws;
         CUtensorMap tm_hi, tm_lo;
     };
@@ -1917,11 +1915,9 @@ static int linear_batch_setup(moe_ctx *ctx, moe_ctx::Linear &l) {
     CK(cudaStreamSynchronize(ctx->stream));
     float top;
     memcpy(&top, &bits, sizeof top);
-    // Q4_0 weights are split as they are; Q4_K ones scaled to below 2^15.
-    // Weights out of binary16's range (or infinite, or NaN) stay with dp4a.
+    // Q4_0 weights are split as they are; Q4_K ones scaled to below 2^15, row by
+    // row.  Weights out of binary16's range (or infinite, or NaN) stay with dp4a.
     l.gemm = top <= (l.fmt == moe::kFmtQ4K ? 1e30f : 65504.0f);
-    l.w_scale = 1.0f;
-    if (l.fmt == moe::kFmtQ4K && l.gemm && top > 0.0f) l.w_scale = std::ldexp(1.0f, std::min(14 - std::ilogb(top), 100));
     if (make_tmap(ctx, &l.tm_hi, l.ws, rows, l.cols, (uint32_t)moe::linear_gemm_box()) ||
         make_tmap(ctx, &l.tm_lo, l.ws + half, rows, l.cols, (uint32_t)moe::linear_gemm_box()))
         return MOE_ERR_CUDA;
@@ -2004,8 +2000,6 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
         p.ws_hi = (__half *)l.ws;
         p.ws_lo = p.ws_hi + rows * l.cols;
         p.ws_scale = (float *)(p.ws_lo + rows * l.cols);
-        p.w_scale = l.w_scale;
-        p.w_unscale = 1.0f / l.w_scale;
         const moe::LinearGemm g{l.tm_hi, l.tm_lo, p};
         rc = moe::launch_linear_gemm(g, ctx->n_sm, ctx->stream);
     } else {

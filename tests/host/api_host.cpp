@@ -141,7 +141,7 @@ size_t linear_weight_bytes(int fmt, int rows, int cols) {
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int, int, int, int, cudaStream_t st) {
     return launch("linear_repack", st, src, dst);
 }
-int launch_linear_max(const uint8_t *w, int, int, int, unsigned *out, int, cudaStream_t st) {
+int launch_linear_max(uint8_t *w, int, int, int, unsigned *out, int, cudaStream_t st) {
     return launch("linear_max", st, w, out);
 }
 int launch_linear(const LinearParams &p, int, cudaStream_t st) { return launch("linear", st, p.x, p.y, p.n_tokens); }

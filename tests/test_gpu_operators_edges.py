@@ -22,6 +22,19 @@ def context(max_tokens=64, experts=8, k=2, stream=None):
     return qec.moe_layer_init(64, 32, experts, k, 1, 0, max_tokens, stream=st.cuda_stream)
 
 
+def elementwise(w, fmt, q, d, y):
+    """Every |err| against the bound, where the reference is finite; the reference."""
+    x = (q.astype(np.float64).reshape(q.shape[0], -1, 32) * d.astype(np.float64)[..., None]).reshape(q.shape)
+    wf = decode(w, fmt)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, mag = x @ wf.T, np.abs(x) @ np.abs(wf).T
+        err = np.abs(y.cpu().numpy().astype(np.float64) - ref)
+    tol = (6 * (x.shape[1] // 32) + 16) * 2.0 ** -23 * mag
+    on = np.isfinite(ref)
+    assert (err[on] <= tol[on]).all(), float((err[on] / tol[on].clip(1e-300)).max())
+    return ref
+
+
 def test_registration_on_a_side_stream():
     # the same blocks registered on a stream of their own and on the default one: the same bits
     rows, cols = 8192, 8192
@@ -41,6 +54,26 @@ def test_registration_on_a_side_stream():
         qec.moe_destroy(ctx)
     for y in out[2:]:
         assert torch.equal(y, out[0 if y.shape[0] == 1 else 1])
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 40, 130])
+def test_linear_q4k_rows_over_the_whole_scale_range(tokens):
+    # every row has its own magnitude, from the smallest to the largest binary16 scales
+    rows, cols = 300, 512
+    ctx = context(max_tokens=130)
+    w = make_weights(rows, cols, qec.FMT_Q4_K, 21)
+    top = np.geomspace(1e-6, 60000, rows)[np.random.default_rng(5).permutation(rows)][:, None]
+    f = np.random.default_rng(4).uniform(0.25, 1.0, (2, rows, cols // 256))
+    w[:, :, 0:2] = (top * f[0]).astype(np.float16)[..., None].view(np.uint8)
+    w[:, :, 2:4] = (top * f[1]).astype(np.float16)[..., None].view(np.uint8)
+    lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_K, rows, cols)
+    rng = np.random.default_rng(tokens)
+    q = rng.integers(-127, 128, (tokens, cols)).astype(np.int8)
+    d = rng.uniform(0.001, 0.01, (tokens, cols // 32)).astype(np.float16)
+    y = torch.empty(tokens, rows, device="cuda")
+    qec.moe_linear_forward(ctx, lid, None, tokens, y, q=torch.from_numpy(q).cuda(), d=torch.from_numpy(d).cuda())
+    elementwise(w, qec.FMT_Q4_K, q, d, y)
+    qec.moe_destroy(ctx)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
