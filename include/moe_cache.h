@@ -506,7 +506,9 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
  * block dots, scaled and summed in fp32, as the expert forwards compute them.
  * Other batches multiply scaled weights and activations in two binary16 parts
  * each with fp32 sums on the tensor cores: about 6e-7 of the result (2-norm) at
- * 4096 columns, a Q4_K weight kept to at least 2^-39 of the largest of its row.
+ * 4096 columns.  The parts hold a Q4_K weight to 2^-22 of itself or 2^-38 of the
+ * largest of its row, an activation exactly or to 2^-38 of 127 times the token's
+ * largest scale (a NaN or an infinity in a token makes its results NaN or infinite).
  * So the bits of a token's result depend on the batch's size.
  * Layers with weights outside binary16's range (Q4_K: above 1e30) take the
  * first form for every batch.  A bounded wait of the second form that expires

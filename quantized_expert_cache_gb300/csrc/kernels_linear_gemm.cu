@@ -4,9 +4,10 @@
 //
 // Arithmetic.  A Q4_0 weight d (q - 8) has at most 15 significant bits and an
 // activation d_a q_a at most 18, so neither fits one binary16; two do:
-//   w = w_h + w_l,  x 2^-e = x_h + x_l   (w exactly, w_l below 2^-11 of it; x to
-// 2^-24 of its token's largest value, each part the binary16 rounding of what
-// is left, e the exponent of the token's largest scale) and
+//   w = w_h + w_l,  x 2^-e = x_h + x_l   (each part the binary16 rounding of what
+// is left, w_l below 2^-11 of w; exact, but for parts below binary16's smallest
+// normal number, which are rounded to 2^-25: 2^e brings 127 times the token's
+// largest scale to [2^13.9, 2^15), so that is 2^-38 of it) and
 //   y = 2^e (sum w_h x_h  +  sum (w_l x_h + w_h x_l)),
 // dropping w_l x_l (below 2^-22 of the product; with what the accumulation loses
 // 6e-7 of the result measured at 4096 columns, 1.1e-6 for an fp32 library
@@ -16,9 +17,9 @@
 // registers, measured 88 us for 4096 x 4096 at 512 tokens (its f16 rate is a
 // third of tcgen05's).  Q4_K weights are formed in binary32 (d sc q - dmin m),
 // scaled by a power of two so that the largest of their row is below 2^15, and
-// split the same way: to 2^-39 of the row's largest.  (One power of two for the
-// layer left rows far below its largest block to binary16's subnormals: 1e-3 off
-// beside a block of d = 65504.)
+// split the same way: to 2^-22 of themselves or 2^-38 of the row's largest.  (One
+// power of two for the layer left rows far below its largest block to
+// binary16's subnormals: 1e-3 off beside a block of d = 65504.)
 //
 // The tensor core's fp32 accumulation truncates, a bias of about 2^-24 a step
 // on a growing sum; so the large products are accumulated for 512 columns
@@ -148,11 +149,12 @@ __global__ void __launch_bounds__(256) linear_split_kernel(LinearParams p) {
     if (lane == 0) part[warp] = m;
     __syncthreads();
     m = __reduce_max_sync(0xffffffffu, part[lane & 7]);
-    // the token's largest scale; the scales times 2^-e, its exponent (e = 0
-    // for a token of zeros, infinities or NaN)
+    // the token's largest scale; the scales times 2^-e, which brings them below
+    // 2^8 and the values (127 of them) below 2^15 (e = -7 for a token of zeros,
+    // infinities or NaN)
     float top = __uint_as_float(m);
     if (FP) top = __half2float(__float2half_rn(top / 127.0f));
-    const int e = top > 0.0f && top <= 65504.0f ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 : 0;
+    const int e = (top > 0.0f && top <= 65504.0f ? (int)((__float_as_uint(top) >> 23) & 255u) - 127 : 0) - 7;
     const float up = __uint_as_float((unsigned)(127 + e) << 23), down = __uint_as_float((unsigned)(127 - e) << 23);
     if (threadIdx.x == 0) p.ws_scale[t] = up;
     // 8 lanes a block (whole warps run every round)

@@ -76,6 +76,26 @@ def test_linear_q4k_rows_over_the_whole_scale_range(tokens):
     qec.moe_destroy(ctx)
 
 
+@pytest.mark.parametrize("fmt", [qec.FMT_Q4_0, qec.FMT_Q4_K])
+@pytest.mark.parametrize("tokens", [1, 5, 40, 130])
+def test_linear_small_activations_beside_a_block_that_the_weights_ignore(tokens, fmt):
+    # the first block is 2^22 times the others, and its weights are zero
+    rows, cols = 140, 512
+    ctx = context(max_tokens=130)
+    w = make_weights(rows, cols, fmt, 22)
+    first = 1  # blocks of the weights' format that hold the first 32 (256) columns
+    w[:, :first, :4 if fmt == qec.FMT_Q4_K else 2] = 0
+    lid = qec.moe_linear_register(ctx, w, fmt, rows, cols)
+    rng = np.random.default_rng(tokens)
+    q = rng.integers(-127, 128, (tokens, cols)).astype(np.int8)
+    d = (rng.uniform(1, 2, (tokens, cols // 32)) * 2.0 ** -14).astype(np.float16)
+    d[:, 0] = 256.0
+    y = torch.empty(tokens, rows, device="cuda")
+    qec.moe_linear_forward(ctx, lid, None, tokens, y, q=torch.from_numpy(q).cuda(), d=torch.from_numpy(d).cuda())
+    elementwise(w, fmt, q, d, y)
+    qec.moe_destroy(ctx)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("tokens,width", [(1, 2048), (5, 96), (300, 2048), (700, 160), (3, 1001), (3, 40000)])
 def test_norm_sums_in_place(tokens, width, dtype):
