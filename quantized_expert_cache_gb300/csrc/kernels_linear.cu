@@ -284,7 +284,6 @@ int launch_batch(const LinearParams &p, int n_sm, cudaStream_t st) {
     const size_t smem = (size_t)TN * (p.cols / kBlock) * (32 + sizeof(BlockScale));
     const int fit = (int)std::max<size_t>(1, std::min<size_t>(TN > 2 ? 3 : 4, 220 * 1024 / (smem + 10 * 1024)));
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)std::min((p.rows + 15) / 16, n_sm * fit), (unsigned)((p.n_tokens + TN - 1) / TN));
     cfg.blockDim = dim3(kVecWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -293,7 +292,19 @@ int launch_batch(const LinearParams &p, int n_sm, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, kernel, p);
+    // a grid has at most 65535 groups of tokens
+    const size_t total = p.n_tokens, most = 65535 * TN;
+    for (size_t t = 0; t < total; t += most) {
+        LinearParams part = p;
+        part.n_tokens = (int)std::min(total - t, most);
+        if (p.x) part.x += t * p.cols;
+        if (p.q) part.q += t * p.cols, part.d += t * (p.cols / kBlock);
+        part.y += t * p.rows;
+        cfg.gridDim = dim3((unsigned)std::min((p.rows + 15) / 16, n_sm * fit), (unsigned)((part.n_tokens + TN - 1) / TN));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, part);
+        if (e != cudaSuccess) return (int)e;
+    }
+    return 0;
 }
 
 template <int FMT, int TN>

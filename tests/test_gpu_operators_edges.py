@@ -96,6 +96,39 @@ def test_linear_small_activations_beside_a_block_that_the_weights_ignore(tokens,
     qec.moe_destroy(ctx)
 
 
+@pytest.mark.parametrize("tokens", [1, 5, 40, 130])
+def test_linear_weights_beyond_binary16(tokens):
+    # 8 d above 65504, infinite and NaN scales: batches too take the exact block dots
+    rows, cols = 70, 2080
+    ctx = context(max_tokens=130)
+    w = make_weights(rows, cols, qec.FMT_Q4_0, 23)
+    dd = np.geomspace(1e-6, 60000, rows * cols // 32).astype(np.float16).reshape(rows, cols // 32, 1)
+    w[:, :, :2] = dd.view(np.uint8)
+    rng = np.random.default_rng(tokens)
+    x = torch.from_numpy(rng.standard_normal((tokens, cols)).astype(np.float32)).cuda()
+    q, d = (a.cpu().numpy() for a in codes_of(ctx, x))
+    y = torch.empty(tokens, rows, device="cuda")
+    lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, rows, cols)
+    qec.moe_linear_forward(ctx, lid, x, tokens, y)
+    elementwise(w, qec.FMT_Q4_0, q, d, y)
+    w[3, 5, :2] = np.array([np.inf], np.float16).view(np.uint8)
+    w[9, 0, :2] = np.array([np.nan], np.float16).view(np.uint8)
+    lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, rows, cols)
+    y2 = torch.empty(tokens, rows, device="cuda")
+    qec.moe_linear_forward(ctx, lid, x, tokens, y2)
+    assert not torch.isfinite(y2[:, 3]).any() and torch.isnan(y2[:, 9]).all()
+    keep = [r for r in range(rows) if r not in (3, 9)]
+    assert torch.equal(y2[:, keep], y[:, keep])
+    qec.moe_destroy(ctx)
+
+
+def codes_of(ctx, x):
+    """int8 codes and binary16 scales of fp32 rows, each step in binary32."""
+    from test_gpu_operators import quantize32
+    q, d = quantize32(x.cpu().numpy())
+    return torch.from_numpy(q), torch.from_numpy(d)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("tokens,width", [(1, 2048), (5, 96), (300, 2048), (700, 160), (3, 1001), (3, 40000)])
 def test_norm_sums_in_place(tokens, width, dtype):
@@ -133,4 +166,21 @@ def test_norm_of_the_widest_row():
     assert (abs(y[0, at].double() - r) <= 6 * 2.0 ** -24 * r).all()
     y[0, at] = 0
     assert int(torch.count_nonzero(y)) == 0
+    qec.moe_destroy(ctx)
+
+
+def test_linear_more_token_groups_than_a_grid_has_rows():
+    # four tokens a pass: more than 65535 passes
+    tokens = 4 * 65535 + 5
+    ctx = context(max_tokens=tokens)
+    w = make_weights(3, 32, qec.FMT_Q4_0, 24)
+    w[:, :, :2] = np.full((3, 1, 1), 10000.0, np.float16).view(np.uint8)
+    lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, 3, 32)
+    rng = np.random.default_rng(3)
+    q = rng.integers(-127, 128, (tokens, 32)).astype(np.int8)
+    d = rng.uniform(0.001, 0.01, (tokens, 1)).astype(np.float16)
+    y = torch.full((tokens + 1, 3), 7.0, device="cuda")
+    qec.moe_linear_forward(ctx, lid, None, tokens, y, q=torch.from_numpy(q).cuda(), d=torch.from_numpy(d).cuda())
+    elementwise(w, qec.FMT_Q4_0, q, d, y[:tokens])
+    assert (y[tokens:] == 7).all()
     qec.moe_destroy(ctx)
