@@ -179,6 +179,9 @@ struct moe_ctx {
 namespace {
 
 int fail(moe_ctx *c, int code, const std::string &msg) {
+    // a failure of the runtime's is reported once: it also stands as the
+    // runtime's last error, which the next launch would answer with
+    if (code == MOE_ERR_CUDA || code == MOE_ERR_OOM) cudaGetLastError();
     if (c)
         c->err = msg;
     else
@@ -518,6 +521,7 @@ int moe_layer_init(const moe_cfg *cfg, void *cuda_stream, moe_ctx **out) {
     ctx->stride = (ctx->blob + 255) / 256 * 256;
     auto cleanup_fail = [&](int rc) {
         std::string m = ctx->err;
+        cudaGetLastError();  // as in fail()
         moe_destroy(ctx);
         g_init_error = m;
         return rc;

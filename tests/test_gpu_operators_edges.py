@@ -184,3 +184,17 @@ def test_linear_more_token_groups_than_a_grid_has_rows():
     elementwise(w, qec.FMT_Q4_0, q, d, y[:tokens])
     assert (y[tokens:] == 7).all()
     qec.moe_destroy(ctx)
+
+
+def test_linear_registration_without_memory_leaves_no_error():
+    # an allocation that cannot be had is reported once: the next calls do not meet it again
+    ctx = context()
+    w = make_weights(40, 256, qec.FMT_Q4_0, 25)
+    with pytest.raises(qec.MoeError) as e:
+        qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, 1 << 26, 65536)  # 2.4 TB: refused before w is read
+    assert e.value.code == -2
+    lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, 40, 256)
+    y = torch.empty(1, 40, device="cuda")
+    qec.moe_linear_forward(ctx, lid, torch.randn(1, 256, device="cuda"), 1, y)
+    torch.cuda.synchronize()
+    qec.moe_destroy(ctx)

@@ -221,3 +221,28 @@ def test_calls_without_tokens_meet_nothing(host, calls):
     assert not host.log()
     routers.takes(tokens=0, logits=A, dlogits=A + 4)
     routers.refuses(tokens=0, loss=A, counts=A)
+
+
+def test_a_failure_is_reported_once(host, calls):
+    # the runtime keeps a call's error as its last one; left there, the next launch, the library's or the
+    # caller's own, would answer with it
+    ctx = calls[0].args[0]
+    assert host.lib.host_last_error() == 0
+    rc, _ = host.register(ctx, np.zeros((24, 2, 18), np.uint8), qec.FMT_Q4_0, 1 << 26, 65536)  # no memory for it
+    assert rc == -2 and host.lib.host_last_error() == 0
+    cfg = qec.moe_cfg(64, 32, 8, 2, 1, 0, 1 << 30, 64, 0, 1, 10000, 0, qec.FMT_Q4_0, 0)
+    out = ctypes.c_void_p()
+    assert host.lib.moe_layer_init(ctypes.byref(cfg), STREAM, ctypes.byref(out)) == -2
+    assert host.lib.host_last_error() == 0
+    codes = dict(x=None)
+    for call, launch, change in ((calls[0], b"rms_norm", {}), (calls[1], b"linear", codes),
+                                 (calls[1], b"linear_gemm", dict(codes, tokens=40)), (calls[2], b"router_loss", {})):
+        host.lib.host_fail_launch(launch)
+        assert call.call(host, *call.args, **change) == -3
+        assert host.lib.host_last_error() == 0, launch
+        host.lib.host_fail_launch(b"")
+    for launch in (b"linear_repack", b"linear_max"):
+        host.lib.host_fail_launch(launch)
+        rc, _ = host.register(ctx, np.zeros((24, 2, 18), np.uint8), qec.FMT_Q4_0, 24, 64)
+        assert rc == -3 and host.lib.host_last_error() == 0, launch
+        host.lib.host_fail_launch(b"")
