@@ -2048,7 +2048,11 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
     p.balance = balance_coef;
     p.zcoef = z_coef;
     const int rc = moe::launch_router_loss(p, ctx->n_sm, ctx->stream);
-    if (rc) return fail(ctx, MOE_ERR_CUDA, std::string("router_loss launch: ") + cudaGetErrorString((cudaError_t)rc));
+    if (rc) {
+        // the picks may have been counted without the kernel that sets the counts back
+        cudaMemsetAsync(p.ticket, 0, kRouterWsBytes - kRouterTicketOff, ctx->stream);
+        return fail(ctx, MOE_ERR_CUDA, std::string("router_loss launch: ") + cudaGetErrorString((cudaError_t)rc));
+    }
     return MOE_OK;
 }
 

@@ -246,3 +246,18 @@ def test_a_failure_is_reported_once(host, calls):
         rc, _ = host.register(ctx, np.zeros((24, 2, 18), np.uint8), qec.FMT_Q4_0, 24, 64)
         assert rc == -3 and host.lib.host_last_error() == 0, launch
         host.lib.host_fail_launch(b"")
+
+
+def test_router_counts_start_from_zero_after_a_failed_launch(host, calls):
+    # the picks are counted by a launch before the one that uses them and sets them back
+    routers = calls[2]
+    host.lib.host_fail_launch(b"router_loss")
+    host.lib.host_clear()
+    assert routers.call(host, *routers.args, tokens=5000) == -3
+    host.lib.host_fail_launch(b"")
+    log = host.log()
+    counts = log[0][3]
+    assert [c[0] for c in log] == ["router_loss", "set"]
+    what, stream, start, _, size = log[1]
+    assert stream == STREAM and start <= counts and start + size >= counts + 4 * (4096 + 1)
+    routers.takes(tokens=5000)
