@@ -193,22 +193,26 @@ int launch_pdl(K kernel, unsigned grid, unsigned block, const NormParams &p, cud
     return (int)cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// (if constexpr: only the kernels that a call can reach are compiled)
 template <typename T, int VEC>
 int launch_typed(const NormParams &p, cudaStream_t st) {
     const int nv = p.width / VEC;
     const unsigned T_ = (unsigned)p.n_tokens;
+    const bool few = p.n_tokens <= 256;
     // one warp a row: no barrier, and short rows share a CTA
     if (nv <= 32) return launch_pdl(rms_norm_kernel<T, VEC, 1, true>, (T_ + 7) / 8, 256, p, st);
     if (nv <= 64) return launch_pdl(rms_norm_kernel<T, VEC, 2, true>, (T_ + 7) / 8, 256, p, st);
     if (nv <= 128) return launch_pdl(rms_norm_kernel<T, VEC, 4, true>, (T_ + 7) / 8, 256, p, st);
-    if (nv <= 256 && p.n_tokens > 256) return launch_pdl(rms_norm_kernel<T, VEC, 8, true>, (T_ + 7) / 8, 256, p, st);
-    if (VEC == 1 && nv <= 512 && p.n_tokens > 256)
-        return launch_pdl(rms_norm_kernel<T, VEC, 16, true>, (T_ + 7) / 8, 256, p, st);
+    if (nv <= 256 && !few) return launch_pdl(rms_norm_kernel<T, VEC, 8, true>, (T_ + 7) / 8, 256, p, st);
     // one CTA a row
     auto threads = [&](int items) { return (unsigned)(((nv + items - 1) / items + 31) / 32 * 32); };
-    if (p.n_tokens <= 256 && nv <= 1024) return launch_pdl(rms_norm_kernel<T, VEC, 1, false>, T_, threads(1), p, st);
-    if (nv <= 256) return launch_pdl(rms_norm_kernel<T, VEC, 1, false>, T_, threads(1), p, st);
-    if (nv <= 512) return launch_pdl(rms_norm_kernel<T, VEC, 2, false>, T_, threads(2), p, st);
+    if constexpr (VEC < 8)  // (packs of 8 are for many rows)
+        if (nv <= 1024 && few) return launch_pdl(rms_norm_kernel<T, VEC, 1, false>, T_, threads(1), p, st);
+    if constexpr (VEC == 1) {
+        if (nv <= 512) return launch_pdl(rms_norm_kernel<T, VEC, 16, true>, (T_ + 7) / 8, 256, p, st);
+    } else {
+        if (nv <= 512) return launch_pdl(rms_norm_kernel<T, VEC, 2, false>, T_, threads(2), p, st);
+    }
     if (nv <= 2048) return launch_pdl(rms_norm_kernel<T, VEC, 4, false>, T_, threads(4), p, st);
     if (nv <= 8192) return launch_pdl(rms_norm_kernel<T, VEC, 8, false>, T_, threads(8), p, st);
     return launch_pdl(rms_norm_wide_kernel<T>, T_, 1024, p, st);
@@ -217,9 +221,10 @@ int launch_typed(const NormParams &p, cudaStream_t st) {
 template <typename T>
 int launch_rows(const NormParams &p, cudaStream_t st) {
     const auto aligned = [](const void *q, size_t a) { return ((uintptr_t)q & (a - 1)) == 0; };
-    if (sizeof(T) == 2 && p.width % 8 == 0 && p.n_tokens > 256 && aligned(p.x, 16) && aligned(p.res, 16) &&
-        aligned(p.sum, 16) && aligned(p.weight, 16) && aligned(p.y, 16) && aligned(p.q, 8))
-        return launch_typed<T, 8>(p, st);
+    if constexpr (sizeof(T) == 2)
+        if (p.width % 8 == 0 && p.n_tokens > 256 && aligned(p.x, 16) && aligned(p.res, 16) && aligned(p.sum, 16) &&
+            aligned(p.weight, 16) && aligned(p.y, 16) && aligned(p.q, 8))
+            return launch_typed<T, 8>(p, st);
     const size_t e = 4 * sizeof(T);
     const bool vec = p.width % 4 == 0 && aligned(p.x, e) && aligned(p.res, e) && aligned(p.sum, e) &&
                      aligned(p.weight, 16) && aligned(p.y, 16) && aligned(p.q, 4);
