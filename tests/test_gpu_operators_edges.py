@@ -106,7 +106,7 @@ def test_linear_weights_beyond_binary16(tokens):
     w[:, :, :2] = dd.view(np.uint8)
     rng = np.random.default_rng(tokens)
     x = torch.from_numpy(rng.standard_normal((tokens, cols)).astype(np.float32)).cuda()
-    q, d = (a.cpu().numpy() for a in codes_of(ctx, x))
+    q, d = (a.numpy() for a in codes_of(x))
     y = torch.empty(tokens, rows, device="cuda")
     lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, rows, cols)
     qec.moe_linear_forward(ctx, lid, x, tokens, y)
@@ -122,7 +122,7 @@ def test_linear_weights_beyond_binary16(tokens):
     qec.moe_destroy(ctx)
 
 
-def codes_of(ctx, x):
+def codes_of(x):
     """int8 codes and binary16 scales of fp32 rows, each step in binary32."""
     from test_gpu_operators import quantize32
     q, d = quantize32(x.cpu().numpy())
@@ -169,6 +169,22 @@ def test_norm_of_the_widest_row():
     qec.moe_destroy(ctx)
 
 
+@pytest.mark.parametrize("fmt", [qec.FMT_Q4_0, qec.FMT_Q4_K])
+@pytest.mark.parametrize("tokens,rows,cols", [(1030, 130, 1280), (4096, 200, 512), (12289, 33, 256)])
+def test_linear_prompts(tokens, rows, cols, fmt):
+    # prompts of the workloads' lengths: many token tiles, the last one ragged
+    ctx = context(max_tokens=tokens)
+    w = make_weights(rows, cols, fmt, tokens)
+    lid = qec.moe_linear_register(ctx, w, fmt, rows, cols)
+    x = torch.randn(tokens, cols, generator=torch.Generator(device="cuda").manual_seed(tokens), device="cuda")
+    q, d = (a.numpy() for a in codes_of(x))
+    y = torch.full((tokens + 1, rows), 7.0, device="cuda")
+    qec.moe_linear_forward(ctx, lid, x, tokens, y)
+    check_linear(w, fmt, q, d, y[:tokens])
+    assert (y[tokens:] == 7).all()
+    qec.moe_destroy(ctx)
+
+
 def test_linear_more_token_groups_than_a_grid_has_rows():
     # four tokens a pass: more than 65535 passes
     tokens = 4 * 65535 + 5
@@ -183,6 +199,42 @@ def test_linear_more_token_groups_than_a_grid_has_rows():
     qec.moe_linear_forward(ctx, lid, None, tokens, y, q=torch.from_numpy(q).cuda(), d=torch.from_numpy(d).cuda())
     elementwise(w, qec.FMT_Q4_0, q, d, y[:tokens])
     assert (y[tokens:] == 7).all()
+    qec.moe_destroy(ctx)
+
+
+def test_linear_layer_keeps_its_workspace():
+    # a wider layer is registered after a batch of the first was captured: the graph and direct calls
+    # of both layers still give the bits of a context that holds one layer
+    st = torch.cuda.Stream()
+    shapes = ((200, 512), (130, 4096))
+    ws = [make_weights(r, c, qec.FMT_Q4_0, c) for r, c in shapes]
+    xs = [torch.randn(40, c, device="cuda") for _, c in shapes]
+    want = []
+    for w, x, (r, c) in zip(ws, xs, shapes):
+        ctx = context(stream=st)
+        lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, r, c)
+        y = torch.empty(40, r, device="cuda")
+        torch.cuda.synchronize()
+        qec.moe_linear_forward(ctx, lid, x, 40, y)
+        torch.cuda.synchronize()
+        want.append(y)
+        qec.moe_destroy(ctx)
+    ctx = context(stream=st)
+    ids = [qec.moe_linear_register(ctx, ws[0], qec.FMT_Q4_0, *shapes[0])]
+    yg = torch.zeros(40, shapes[0][0], device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        qec.moe_linear_forward(ctx, ids[0], xs[0], 40, yg)
+    ids.append(qec.moe_linear_register(ctx, ws[1], qec.FMT_Q4_0, *shapes[1]))
+    ys = [torch.zeros(40, r, device="cuda") for r, _ in shapes]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for i in (1, 0):
+            qec.moe_linear_forward(ctx, ids[i], xs[i], 40, ys[i])
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], want[0]) and torch.equal(ys[1], want[1]) and torch.equal(yg, want[0])
     qec.moe_destroy(ctx)
 
 
