@@ -469,10 +469,9 @@ int moe_set_router(moe_ctx *ctx, int layer, const float *host_w, const float *ho
  * [n_tokens][width] or NULL.  d_q, d_d: int8 [n_tokens][width] and binary16
  * [n_tokens][width/32], both or neither (both need width % 32 == 0).  At
  * least one output.  d_sum may be d_x or d_res, and so may d_y of MOE_F32 rows,
- * at the same address; no output meets another buffer otherwise
- * (MOE_ERR_ARG).  Infinities and NaN spread as
- * in the formulas over their row (a block whose max|y| is not a number, or
- * beyond binary16, has a scale that says so).  Asynchronous on `stream` (NULL:
+ * at the same address; no output meets another buffer otherwise (MOE_ERR_ARG).
+ * Infinities and NaN spread as in the formulas over their row (a block whose
+ * max|y| is not a number, or beyond binary16, has a scale that says so).  Asynchronous on `stream` (NULL:
  * the context's), any stream; capturable.  Every pointer is aligned to its
  * elements; rows whose buffers are 16-byte aligned and whose width is a multiple
  * of 4 take wide loads.
@@ -489,8 +488,8 @@ int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, co
  * host memory, copied.  cols: a multiple of 32 (Q4_K: of 256), at most 65536;
  * rows: at most 2^26.  The context keeps, until moe_destroy, a device copy of
  * 18 bytes (Q4_K: 18.5) to 32 weights, rows rounded up to 16 (Q4_K: and 4 bytes
- * a row, rounded up to 128); while the call runs also the blocks as given.  A context whose batches take the tensor cores
- * also keeps a workspace of R x cols x 4 + R x 4 bytes, R = max_tokens rounded up
+ * a row, rounded up to 128); while the call runs also the blocks as given.  A
+ * context whose batches take the tensor cores also keeps a workspace of R x cols x 4 + R x 4 bytes, R = max_tokens rounded up
  * to 32, shared by its layers (a layer that needs a larger one allocates it;
  * the earlier ones stay).  *linear_id receives the layer's id.  Synchronous.
  * Errors: MOE_ERR_ARG, MOE_ERR_OOM, MOE_ERR_CUDA.
@@ -519,6 +518,8 @@ int moe_linear_register(moe_ctx *ctx, const void *host_w, int weight_format, int
  * aligned.  d_y: fp32 [n_tokens][rows], meeting no input.  n_tokens <=
  * cfg.max_tokens.
  * `stream` must be the context's stream (or NULL).  Asynchronous; capturable.
+ * Batches use a workspace of the context's: a captured graph is replayed on the
+ * context's stream, or in order with it.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8_t *d_q, const uint16_t *d_d,
@@ -540,13 +541,16 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
  * token out of everything (its gradient row is zero); all out: losses, counts
  * and gradients are zero.  d_gw: fp32 [n_tokens][k] or NULL; the routing
  * weights are route_topk's for cfg.renorm_topk.  d_loss: fp32 [2].  d_counts:
- * int32 [E], written.  d_dlogits: fp32 [n_tokens][E] or NULL.  No output
- * meets another buffer (MOE_ERR_ARG).  A logit of -infinity is an expert the token cannot take; a row of
- * nothing else adds nothing to the losses, its ids still count and its
- * gradient is zero.  NaN spreads.  The same inputs give the same bits.
- * E and k: the context's (of all shards).  `stream` must be the context's
- * stream (or NULL).  Every pointer is aligned to its elements.  Asynchronous;
- * capturable.
+ * int32 [E], written.  d_dlogits: fp32 [n_tokens][E] or NULL.  No output meets
+ * another buffer (MOE_ERR_ARG).  A logit of -infinity is an expert the token
+ * cannot take; a row of nothing else adds nothing to the losses, its ids still
+ * count and its gradient is zero.  NaN spreads.  The same inputs give the same bits.
+ * Sums are in fp32, exponentials to (4 + |logit - the row's largest|) 2^-24 of
+ * themselves: about 1e-7 of the gradient (2-norm).  E and k: the context's (of all
+ * shards).  `stream` must be the context's stream (or NULL).  Every pointer is
+ * aligned to its elements.  Asynchronous; capturable; a captured graph is replayed
+ * on the context's stream, or in order with it (the picks are counted in a
+ * workspace of the context's).
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, const uint8_t *d_mask,

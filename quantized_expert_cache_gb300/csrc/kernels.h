@@ -187,8 +187,10 @@ constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
 constexpr int kLinearSmem = 200 * 1024;        // dynamic shared memory of a CTA
 // Whether a batch goes to the tensor cores: from 5 tokens on, and 3 or 4 of more
 // than 2048 columns (what the dp4a kernel's CTAs all stage and read from shared
-// memory; 3 tokens: 65536 x 2048 27 us there, 44 on the tensor cores, 8192 x
-// 8192 35 and 25).
+// memory).  3 tokens, us there and on the tensor cores: 512 x 512 2.4 and 6.6, 512
+// x 2048 5.5 and 6.7, 8192 x 2048 8.7 and 10.4, 65536 x 2048 26.3 and 45.0, 2880 x
+// 2880 9.7 and 8.0, 8192 x 8192 32.9 and 26.8.  Columns alone misjudge many rows
+// of a few more columns: 65536 x 4096 50.6 and 82.8.
 inline bool linear_takes_gemm(int n_tokens, int cols) { return n_tokens > 4 || (n_tokens > 2 && cols > 2048); }
 struct LinearParams {
     const uint8_t *w;           // the weights, layout of linear.cuh

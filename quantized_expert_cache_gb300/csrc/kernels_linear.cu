@@ -7,10 +7,11 @@
 //   Q4_K: d sc_j d_a sum_i q_w,i q_a,i - dmin m_j d_a sum_i q_a,i
 //
 // Bound: at one token the weights' one read from HBM: 65536 x 2048 (75.5 MB)
-// 14.6 us = 5.2 TB/s, 0.76 of a copy's rate; 512 x 2048 2.3 us (latency).  With
-// more tokens the time grows with the dots and the activations' shared-memory
-// reads: 2 tokens 18.4 us, 3 27.2, 4 28.3 to 29.5, where the tensor cores' path
-// takes 44; an earlier form of this kernel took 53 at 8 tokens.
+// 14.6 us = 5.2 TB/s, 0.76 of a copy's rate (Q4_K 15.5 us); 512 x 2048 2.3 us
+// (latency).  With more tokens the time grows with the dots and the activations'
+// shared-memory reads: 2 tokens 18.7 us, 3 26.3, 4 26.8 (Q4_K 29.5), where the
+// tensor cores' path takes 45 (67); an earlier form of this kernel took 53 at 8
+// tokens.
 //
 // Weight layout (made at registration): per 16 rows, per group of up to 8
 // blocks: the codes [block][row] x 16 bytes in Q4 order, then the scales: Q4_0

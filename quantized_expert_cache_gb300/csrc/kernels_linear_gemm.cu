@@ -30,14 +30,15 @@
 // the MMA takes its A operand there: with A in shared memory an MMA reads 4 KB
 // more (46 cycles at N = 32 against 26, 52 at N = 64 against 36; 64 at N = 128).
 //
-// Bound.  4096 x 4096 at 512 tokens: 48.6 us (51.5 GFLOP of MMAs, both
-// kernels' time: 0.55 of the measured bf16 rate), the tensor pipe active 58% of
-// the GEMM's time.  By count, not measured: operand reads, the tokens' copies and
-// the weights' move about 90 KB through shared memory in a stage's 768 tensor
-// cycles, near 128 bytes a cycle.  Tiles of up to 64 tokens: the conversions, on
-// four warps a scheduler: 65536 x 2048 at 5 to 16 tokens 44 to 45 us, 2880 x
-// 2880 at 8 tokens 8.9 (latency of two launches, one round of stages and the
-// join), Q4_K 8192 x 2048 at 33 tokens 15.9.
+// Bound.  4096 x 4096 at 512 tokens: 48.8 us (51.5 GFLOP of MMAs, both
+// kernels' time: 0.54 of the measured bf16 rate; Q4_K 56.0), the tensor pipe
+// active 57% of the GEMM's time; 2880 x 2880 at 12288 tokens 559 us.  By count, not
+// measured: operand reads, the tokens' copies and the weights' move about 90 KB
+// through shared memory in a stage's 768 tensor cycles, near 128 bytes a cycle.
+// Tiles of up to 64 tokens: the conversions, on four warps a scheduler: 65536 x
+// 2048 at 5, 16 and 64 tokens 45, 47 and 54 us (Q4_K at 16 tokens 69), 2880 x 2880
+// at 8 tokens 8.7 (latency of two launches, one round of stages and the join), Q4_K
+// 8192 x 2048 at 33 tokens 15.7.
 #include <cuda.h>
 #include <cooperative_groups.h>
 
@@ -644,10 +645,12 @@ long clocks_of(const LinearParams &p, int bn, int n_sm, long group) {
     return (tiles * S + n_sm - 1L) / n_sm * ((groups_of(p) + S - 1) / S) * group + (S > 1 ? 3000 : 0);
 }
 
-// Up to 128 tokens one tile holds them all: weights are converted once (80 x
-// 1000 x 2048 13.0 us against 15.2 in tiles of 64, 128 x 8192 x 8192 47.8
-// against 49.1); above, the shorter schedule (512 x 4096 x 4096 48.6 in tiles of
-// 128 against 53.4, 512 x 16384 x 1024 57.0 against 51.6).
+// Up to 128 tokens one tile holds them all and weights are converted once; above,
+// the shorter schedule.  us in tiles of 128 and of 64: Q4_0 80 x 1000 x 2048 (tokens,
+// rows, columns) 12.9 and 15.4, 128 x 8192 x 8192 53.2 and 53.0, 128 x 2880 x 2880
+// 18.8 and 17.0 (the rule's loss), 512 x 4096 x 4096 49.0 and 52.7, 512 x 16384 x
+// 1024 57.2 and 51.9, 4096 x 2048 x 2048 102.9 and 97.3; Q4_K 100 x 1000 x 2048 14.5
+// and 19.3, 128 x 8192 x 8192 59.7 and 75.5, 512 x 4096 x 4096 56.5 and 76.1.
 template <int FMT>
 int launch_fmt(const LinearGemm &g, int n_sm, cudaStream_t st) {
     if (g.p.n_tokens <= 32) return launch_tile<FMT, 32>(g, n_sm, st);

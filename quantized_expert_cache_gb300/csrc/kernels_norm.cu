@@ -9,12 +9,16 @@
 // to 16 bits is only what a 16-bit residual stream stores.
 //
 // Bound: HBM.  Every input is read once and every output written once; a row
-// stays in registers between the sum of squares and its outputs.  Measured:
-// 12288 x 2880 fp32 with codes 90.5 us = 0.98 of a copy's rate, 4096 x 2048
-// without 21.0 us = 0.94, 8192 x 4096 bf16 61 us = 0.89; one row of 2048 2.1 us,
-// 32 rows of 2880 bf16 2.4 us (latency; one pack a thread, 4.1 us with four).
-// Widths that are no multiple of 4 take single elements: 8192 x 4097 fp32 0.87,
-// bf16 0.72.
+// stays in registers between the sum of squares and its outputs (of widths above
+// 8192 packs it is read twice).  Measured: 12288 x 2880 fp32 with codes 90.6 us =
+// 0.98 of a copy's rate, 4096 x 2048 without 21.0 us = 0.94; 16-bit rows with codes
+// 8192 x 4096 61.5 us = 0.89, 12288 x 2880 68.9 = 0.84; one row of 2048 2.1 us, 32
+// rows of 2880 bf16 2.4 us (latency; one pack a thread, 4.1 us with four).
+// 16-bit rows of 1025 to 2048 elements at more than 256 tokens hold eight packs of
+// 8 a lane, which do not fit the 64 registers that blocks of 1024 threads leave:
+// 242 to 256 bytes a thread spill, 12288 x 2048 bf16 60.2 us = 0.68 (and rows of
+// 16385 to 65536 spill 306 to 332).  Widths that are no multiple of 4 take single
+// elements: 8192 x 4097 fp32 0.86, bf16 0.72.
 #include <cuda_bf16.h>
 
 #include <algorithm>

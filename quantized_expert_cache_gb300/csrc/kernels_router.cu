@@ -15,11 +15,13 @@
 // Counts are integers (their atomics commute exactly); the loss is summed
 // in an order that only the grid size sets: results do not vary from run to run.
 //
-// Bound: 8 tokens (one launch, 3.4 us) by latency; 4096 x 512 with all three
-// gradients 10.3 us against 2.5 of HBM's rate, padded 12288 x 512 18.3 against
-// 7.5: two dependent launches, then a row's chain of loads and warp reductions
-// with 32 warps a SM to hide it.  (Profiled with a cold cache, the loss kernel
-// alone keeps DRAM at 15% of its rate and waits most often for loads.)
+// Bound: 8 tokens (one launch, 3.3 us) by latency; 4096 x 512 with all three
+// gradients 10.3 to 10.7 us against 2.5 of HBM's rate, padded 12288 x 512 18.3 to
+// 18.6 against 7.5: two dependent launches, then a row's chain of loads and warp
+// reductions with 32 warps a SM to hide it.  (Profiled with a cold cache, the
+// padded case's counting kernel takes 6 us, the loss kernel 20; it keeps DRAM at 14%
+// of its rate and waits most often for loads.  What does not need the counts is not
+// yet done before their wait.)
 #include <algorithm>
 #include <type_traits>
 
