@@ -766,10 +766,14 @@ int register_shared_expert(moe_ctx *ctx, int layer, int kind, const void *host_w
     repack((const uint8_t *)host_w, blob.data(), ctx->fmt, 1, rows, cols / 32, ctx->blob);
     uint8_t *d = nullptr;
     CK(cudaMalloc(&d, ctx->stride));
-    cudaError_t e = cudaMemcpy(d, blob.data(), ctx->blob, cudaMemcpyHostToDevice);
+    // on the forwards' stream: copies of pageable memory on the legacy stream may
+    // return before they have landed
+    cudaError_t e = cudaMemcpyAsync(d, blob.data(), ctx->blob, cudaMemcpyHostToDevice, ctx->stream);
     const uint64_t entry = (uint64_t)(uintptr_t)d;
     if (e == cudaSuccess)
-        e = cudaMemcpy(ctx->d_tbl + (size_t)tid * ctx->Et + ctx->E, &entry, sizeof(entry), cudaMemcpyHostToDevice);
+        e = cudaMemcpyAsync(ctx->d_tbl + (size_t)tid * ctx->Et + ctx->E, &entry, sizeof(entry), cudaMemcpyHostToDevice,
+                            ctx->stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->stream);
     if (e != cudaSuccess) {
         cudaFree(d);
         return fail(ctx, MOE_ERR_CUDA, std::string("shared expert upload: ") + cudaGetErrorString(e));
@@ -1392,7 +1396,7 @@ int moe_pool_return(moe_ctx *ctx) {
     if (ctx->preheat && ctx->d_use) {
         use.resize((size_t)ctx->cfg.n_layers * E);
         CK(cudaMemcpy(use.data(), ctx->d_use, sizeof(uint32_t) * use.size(), cudaMemcpyDeviceToHost));
-        CK(cudaMemset(ctx->d_use, 0, sizeof(uint32_t) * use.size()));
+        CK(cudaMemsetAsync(ctx->d_use, 0, sizeof(uint32_t) * use.size(), ctx->stream));
     }
     // candidate order: prompt use count (desc), seed rank (asc), tensor (asc)
     auto better = [&](int ta, int ea, int tb, int eb) {
@@ -1680,19 +1684,20 @@ int moe_set_router(moe_ctx *ctx, int layer, const float *host_w, const float *ho
             ctx->d_prstats = nullptr;
             return fail(ctx, MOE_ERR_OOM, "set_router: device allocation failed");
         }
-        CK(cudaMemset(ctx->d_prcount, 0, sizeof(unsigned) * 2));
-        CK(cudaMemset(ctx->d_prset, 0xff, sizeof(int32_t) * (size_t)L * ctx->k));
-        CK(cudaMemset(ctx->d_prstats, 0, sizeof(unsigned long long) * 2));
+        CK(cudaMemsetAsync(ctx->d_prcount, 0, sizeof(unsigned) * 2, ctx->stream));
+        CK(cudaMemsetAsync(ctx->d_prset, 0xff, sizeof(int32_t) * (size_t)L * ctx->k, ctx->stream));
+        CK(cudaMemsetAsync(ctx->d_prstats, 0, sizeof(unsigned long long) * 2, ctx->stream));
         ctx->has_router.assign(L, 0);
     }
     std::vector<__nv_bfloat16> w((size_t)E * H);
     for (size_t i = 0; i < w.size(); ++i) w[i] = __float2bfloat16_rn(host_w[i]);
     std::vector<float> b(E, 0.0f);
     if (host_b) memcpy(b.data(), host_b, sizeof(float) * E);
+    CK(cudaMemcpyAsync(ctx->d_router + (size_t)layer * E * H, w.data(), sizeof(__nv_bfloat16) * w.size(),
+                       cudaMemcpyHostToDevice, ctx->stream));
+    CK(cudaMemcpyAsync(ctx->d_rbias + (size_t)layer * E, b.data(), sizeof(float) * E, cudaMemcpyHostToDevice,
+                       ctx->stream));
     CK(cudaStreamSynchronize(ctx->stream));
-    CK(cudaMemcpy(ctx->d_router + (size_t)layer * E * H, w.data(), sizeof(__nv_bfloat16) * w.size(),
-                  cudaMemcpyHostToDevice));
-    CK(cudaMemcpy(ctx->d_rbias + (size_t)layer * E, b.data(), sizeof(float) * E, cudaMemcpyHostToDevice));
     ctx->has_router[layer] = 1;
     return MOE_OK;
 }

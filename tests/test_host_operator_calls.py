@@ -25,14 +25,15 @@ class Host:
     def __init__(self, path):
         self.lib = ctypes.CDLL(path)
         for name in ("moe_layer_init", "moe_destroy", "moe_last_error", "moe_rms_norm", "moe_linear_register",
-                     "moe_linear_forward", "moe_router_loss"):
+                     "moe_linear_forward", "moe_router_loss", "register_shared_expert", "moe_set_router",
+                     "register_expert_tensor", "moe_set_preheat", "moe_pool_borrow", "moe_pool_return"):
             f = getattr(self.lib, name)
             f.restype, f.argtypes = qec.SIGNATURES[name]
         self.lib.host_log.restype = ctypes.c_char_p
         self.lib.host_fail_launch.argtypes = [ctypes.c_char_p]
 
-    def context(self, max_tokens=64, experts=8, k=2, stream=STREAM):
-        cfg = qec.moe_cfg(64, 32, experts, k, 1, 0, max_tokens, 64, 0, 1, 10000, 0, qec.FMT_Q4_0, 0)
+    def context(self, max_tokens=64, experts=8, k=2, stream=STREAM, slots=0, shared=0):
+        cfg = qec.moe_cfg(64, 32, experts, k, 1, slots, max_tokens, 64, 0, 1, 10000, 0, qec.FMT_Q4_0, shared)
         out = ctypes.c_void_p()
         assert self.lib.moe_layer_init(ctypes.byref(cfg), stream, ctypes.byref(out)) == 0
         self.lib.host_clear()
@@ -84,6 +85,34 @@ def test_registration_uploads_on_the_stream_that_reads(host, fmt, block, max_tok
     # and the call returns when the caller's memory has been read
     assert any(c[0] == "sync" for c in log[upload:])
     host.lib.moe_destroy(ctx)
+
+
+def test_later_uploads_and_sets_are_on_the_stream_that_reads(host):
+    # the same for a shared expert, a router for lookahead, and the use counts that a returned pool clears
+    lib, ctx = host.lib, host.context(slots=4, shared=1)
+    gate, down = np.zeros((32, 2, 18), np.uint8), np.zeros((64, 1, 18), np.uint8)
+    for kind in range(3):
+        w = down if kind == 2 else gate
+        assert lib.register_shared_expert(ctx, 0, kind, w.ctypes.data, w.shape[0], w.shape[1] * 32) == 0
+    router = np.zeros((8, 64), np.float32)
+    for _ in range(2):
+        assert lib.moe_set_router(ctx, 0, router.ctypes.data, None) == 0
+    log = host.log()
+    moved = [c for c in log if c[0] in ("copy", "set")]
+    assert len(moved) == 2 * 3 + 3 + 2 * 2 and all(c[1] == STREAM for c in moved), moved
+    assert log[-1][:2] == ("sync", STREAM)
+    for kind in range(3):
+        w = np.concatenate([down if kind == 2 else gate] * 8)
+        assert lib.register_expert_tensor(ctx, 0, kind, w.ctypes.data, w.shape[0] // 8, w.shape[1] * 32, 4, None, 4,
+                                          None) == 0
+    assert lib.moe_set_preheat(ctx, 1) == 0
+    ws, size = ctypes.c_void_p(), ctypes.c_size_t()
+    assert lib.moe_pool_borrow(ctx, 3, ctypes.byref(ws), ctypes.byref(size)) == 0
+    host.lib.host_clear()
+    assert lib.moe_pool_return(ctx) == 0
+    sets = [c for c in host.log() if c[0] == "set"]
+    assert sets and all(c[1] == STREAM for c in sets), sets
+    lib.moe_destroy(ctx)
 
 
 # ---- refusals before any launch: addresses stand for device buffers, which nothing here reads
