@@ -250,3 +250,83 @@ def test_linear_registration_without_memory_leaves_no_error():
     qec.moe_linear_forward(ctx, lid, torch.randn(1, 256, device="cuda"), 1, y)
     torch.cuda.synchronize()
     qec.moe_destroy(ctx)
+
+
+# ---- offsets that pass 32 bits: the first and the last rows of results of more than 2^31 elements
+def test_norm_offsets_beyond_32_bits():
+    tokens, width = 540000, 4096
+    ctx = context()
+    w = 1 + 0.3 * torch.randn(width, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    x = torch.zeros(tokens, width, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 262143, 524287, 524288, 524289, tokens - 1], device="cuda")
+    x[at] = torch.randn(len(at), width, generator=torch.Generator(device="cuda").manual_seed(2),
+                        device="cuda").bfloat16()
+    y = torch.full((tokens, width), 7.0, device="cuda")
+    q = torch.full((tokens, width), 7, dtype=torch.int8, device="cuda")
+    d = torch.full((tokens, width // 32), 7.0, dtype=torch.float16, device="cuda")
+    qec.moe_rms_norm(ctx, x, None, w, tokens, width, 1e-5, None, y, q, d)
+    torch.cuda.synchronize()
+    check_norm(x[at], None, w, (None, y[at], q[at], d[at]))
+    y[at], q[at], d[at] = 0, 0, 0
+    assert not y.any() and not q.any() and not d.any()
+    qec.moe_destroy(ctx)
+
+
+@pytest.mark.parametrize("large", [False, True])  # weights within binary16 and beyond: tensor cores, dp4a
+def test_linear_offsets_beyond_32_bits(large):
+    tokens, rows, cols = 33000, 65537, 32
+    ctx = context(max_tokens=tokens)
+    w = make_weights(rows, cols, qec.FMT_Q4_0, 31)
+    if large:
+        w[0, 0, :2] = np.array([10000.0], np.float16).view(np.uint8)
+    lid = qec.moe_linear_register(ctx, w, qec.FMT_Q4_0, rows, cols)
+    rng = np.random.default_rng(1)
+    q = rng.integers(-127, 128, (tokens, cols)).astype(np.int8)
+    d = rng.uniform(0.001, 0.01, (tokens, 1)).astype(np.float16)
+    y = torch.full((tokens, rows), float("inf"), device="cuda")
+    qec.moe_linear_forward(ctx, lid, None, tokens, y, q=torch.from_numpy(q).cuda(), d=torch.from_numpy(d).cuda())
+    torch.cuda.synchronize()
+    at = np.array([0, 1, 16383, 32766, 32767, 32768, tokens - 1])
+    elementwise(w, qec.FMT_Q4_0, q[at], d[at], y[torch.from_numpy(at).cuda()])
+    assert torch.isfinite(y.amax()) and torch.isfinite(y.amin())  # every element was written
+    qec.moe_destroy(ctx)
+
+
+def test_router_offsets_beyond_32_bits():
+    T, E, k, a, b = 530000, 4096, 2, 0.01, 0.001
+    ctx = context(max_tokens=1, experts=E, k=k)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.randn(T, E, generator=g, device="cuda")
+    idx = torch.randint(0, E // 2, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    idx[:, 1] += E // 2
+    gw = torch.randn(T, k, generator=g, device="cuda")
+    loss, counts = torch.empty(2, device="cuda"), torch.empty(E, dtype=torch.int32, device="cuda")
+    dz = torch.full((T, E), float("inf"), device="cuda")
+    qec.moe_router_loss(ctx, z, idx, None, gw, T, E, k, a, b, loss, counts, dz)
+    torch.cuda.synchronize()
+    ref_counts = torch.bincount(idx.reshape(-1).long(), minlength=E)
+    assert torch.equal(counts.long(), ref_counts)
+    f = ref_counts.double() / (T * k)
+    at = torch.tensor([0, 1, 262144, 524287, 524288, T - 1], device="cuda")
+    zz = z[at].double()
+    p, lse = torch.softmax(zz, 1), torch.logsumexp(zz, 1, keepdim=True)
+    dot = (p * f).sum(1, keepdim=True)
+    ref = p * (a * E * (f - dot) + 2 * b * lse) / T
+    mag = p * (a * E * (f + dot) + 2 * b * lse.abs()) / T
+    ids, gd = idx[at].long(), gw[at].double()
+    pw = torch.softmax(zz.gather(1, ids), 1)
+    mean = (pw * gd).sum(1, keepdim=True)
+    ref.scatter_add_(1, ids, pw * (gd - mean))
+    mag.scatter_add_(1, ids, pw * (gd.abs() + (pw * gd).abs().sum(1, keepdim=True)))
+    spread = float(zz.max() - zz.min())
+    assert ((dz[at].double() - ref).abs() <= (spread + E / 32 + 64) * 2.0 ** -24 * mag + 1e-37).all()
+    assert torch.isfinite(dz.amax()) and torch.isfinite(dz.amin())
+    # the losses, against the mean over all rows in 64 bits
+    total = torch.zeros(2, dtype=torch.float64, device="cuda")
+    for r in range(0, T, 20000):
+        zz = z[r:r + 20000].double()
+        total[0] += (torch.softmax(zz, 1) @ f).sum() * a * E / T
+        total[1] += torch.logsumexp(zz, 1).square().sum() * b / T
+    rel = (12 + E / 32 + 64 + T / (608 * 8)) * 2.0 ** -24  # a warp adds up its rows one by one
+    assert ((loss.double() - total).abs() <= rel * total).all()
+    qec.moe_destroy(ctx)
