@@ -471,10 +471,11 @@ int moe_set_router(moe_ctx *ctx, int layer, const float *host_w, const float *ho
  * least one output.  d_sum may be d_x or d_res, and so may d_y of MOE_F32 rows,
  * at the same address; no output meets another buffer otherwise (MOE_ERR_ARG).
  * Infinities and NaN spread as in the formulas over their row (a block whose
- * max|y| is not a number, or beyond binary16, has a scale that says so).  Asynchronous on `stream` (NULL:
- * the context's), any stream; capturable.  Every pointer is aligned to its
- * elements; rows whose buffers are 16-byte aligned and whose width is a multiple
- * of 4 take wide loads.
+ * max|y| is not a number, or beyond binary16, has a scale that says so); all steps
+ * are in fp32, so a row whose sum of squares passes its range gives zeros.
+ * Asynchronous on `stream` (NULL: the context's), any stream; capturable.  Every
+ * pointer is aligned to its elements; rows whose buffers are 16-byte aligned and
+ * whose width is a multiple of 4 take wide loads.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
