@@ -3,9 +3,9 @@ wrong: registration beside other streams, weights and activations over the whole
 range of their formats, batches that leave the tensor cores, layers registered
 between a graph's capture and its replay.
 
-Tolerances, with u = 2^-24 (unit roundoff of binary32):
-- linear: as in the operators' own tests, |err| <= (6 nb + 16) 2^-23 sum |w x|
-  of nb blocks of 32 columns (operands to 2^-22, at most 6 accumulations a block).
+Tolerances are those of the operators' own tests.  Linear, element by element:
+|err| <= (6 nb + 16) 2^-23 sum |w x| of nb blocks of 32 columns (operands to 2^-22,
+at most 6 accumulations a block).
 """
 import numpy as np
 import pytest
