@@ -291,7 +291,8 @@ int moe_ffn_forward_rows(moe_ctx *ctx, int layer, const float *d_x, int n_rows, 
  * cleared.  Errors: MOE_ERR_TIMEOUT (nothing changed; retry), MOE_ERR_CUDA,
  * MOE_ERR_FAULT: an injected upload failure (moe_debug_fail_upload), or a
  * kernel reported a device error since the last step or drain (bit 0: an
- * expert id outside [0, n_experts) was read as expert 0; other bits: a
+ * expert id outside [0, n_experts) was read as expert 0; bit 7: a target id past
+ * the vocabulary was read as none; other bits: a
  * bounded wait expired and its work item was skipped) -- the step's cache
  * update is done, the affected forwards' outputs are not valid, and the
  * error word is cleared (moe_last_error names the bits).
@@ -557,6 +558,54 @@ int moe_linear_forward(moe_ctx *ctx, int linear_id, const float *d_x, const int8
 int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, const uint8_t *d_mask,
                     const float *d_gw, int n_tokens, int n_experts, int k, float balance_coef, float z_coef,
                     float *d_loss, int32_t *d_counts, float *d_dlogits, void *stream);
+
+/*
+ * Log probabilities of given tokens, the entropy of each row and its largest
+ * logits (no counterpart on the source pages, which end at the experts: what a
+ * server answers with, and a tuner's loss, from the output head's logits).  With
+ * u_j = scale * (x_j - max x) and S = sum_j exp(u_j) over a row x of d_logits:
+ *   d_logp[t] = u_target - log S;  0 for a target below 0 (padding)
+ *   d_entropy[t] = log S - sum_j exp(u_j) u_j / S
+ *   d_top_idx[t][0..n_top): the largest logits, ordered by (logit desc, id asc),
+ *     and d_top_logp[t][..] their log probabilities
+ *   d_stats[t] = (max x, log S), which moe_token_logprobs_grad reads
+ * d_logits: [n_tokens][vocab] of dtype (MOE_F32, MOE_F16, MOE_BF16).  scale: one
+ * over the temperature, positive.  d_targets: int32 [n_tokens], or NULL without
+ * d_logp; a target past the vocabulary is read as none and reported by the next
+ * cache_step or miss_drain (MOE_ERR_FAULT).  Outputs are fp32 (d_top_idx int32),
+ * any of them NULL, at least one wanted; n_top <= min(32, vocab), 0: no
+ * alternatives.  A logit of -infinity is a token that cannot be taken (its log
+ * probability is -infinity, as one of the alternatives too); in a row of nothing
+ * else every log probability is -infinity, the entropy 0 and the stats
+ * (-infinity, 0).  NaN and +infinity give NaN in their row; which alternatives a
+ * row with a NaN has is unspecified.  Sums in fp32, without the largest terms,
+ * which are counted: log probabilities near 0 keep their digits (terms below 2^-126
+ * of the largest are left out).  The same inputs give the same bits.  Asynchronous on `stream` (NULL: the context's), any stream;
+ * capturable; no workspace.  vocab <= 2^30; rows of any alignment take wide loads.
+ * No output meets another buffer (MOE_ERR_ARG).  Every pointer is aligned to its
+ * elements.  Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
+ */
+int moe_token_logprobs(moe_ctx *ctx, const void *d_logits, int dtype, const int32_t *d_targets, int n_tokens,
+                       int vocab, float scale, int n_top, float *d_logp, float *d_entropy, int32_t *d_top_idx,
+                       float *d_top_logp, float *d_stats, void *stream);
+
+/*
+ * Gradient of the log probabilities and entropies to the logits (no counterpart on
+ * the source pages): with p = exp(logp) over a row, H its entropy,
+ *   d_dlogits[t][j] = scale * (g_t ([j = target] - p_j) - gH_t p_j (log p_j + H)),
+ * rounded once to dtype.  d_logits, dtype, d_targets, vocab and scale as given to
+ * moe_token_logprobs; d_stats and d_entropy as it wrote them (d_entropy only with
+ * d_g_entropy).  d_g_logp, d_g_entropy: fp32 [n_tokens], the gradients of d_logp and
+ * d_entropy; one of them may be NULL (zero).  A row without a target has the
+ * entropy's part only; a row of nothing but -infinity has a zero gradient.
+ * d_dlogits: [n_tokens][vocab] of dtype; it may be d_logits, and meets no buffer
+ * otherwise (MOE_ERR_ARG).  Asynchronous on `stream` (NULL: the context's), any
+ * stream; capturable.  Every pointer is aligned to its elements.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
+ */
+int moe_token_logprobs_grad(moe_ctx *ctx, const void *d_logits, int dtype, const int32_t *d_targets, int n_tokens,
+                            int vocab, float scale, const float *d_stats, const float *d_entropy,
+                            const float *d_g_logp, const float *d_g_entropy, void *d_dlogits, void *stream);
 
 /*
  * Snapshot of one tensor's cache state (inspection for tests: the table,

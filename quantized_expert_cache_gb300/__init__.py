@@ -71,6 +71,8 @@ SIGNATURES = {
     "moe_linear_register": (_i32, [_vp, _vp, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
     "moe_linear_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
     "moe_router_loss": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _f32, _vp, _vp, _vp, _vp]),
+    "moe_token_logprobs": (_i32, [_vp, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_token_logprobs_grad": (_i32, [_vp, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_cache_snapshot": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp]),
     "moe_cache_layout": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp]),
     "moe_stats": (_i32, [_vp, ctypes.POINTER(moe_stats_t)]),
@@ -336,6 +338,37 @@ def moe_router_loss(ctx, logits, idx, mask, gw, n_tokens, n_experts, k, balance_
                                               _elem(gw, _FP32), n_tokens, n_experts, k, balance_coef, z_coef,
                                               _elem(loss, _FP32), _elem(counts, _IDS), _elem(dlogits, _FP32),
                                               _stream(stream)))
+
+
+def _elem16(x, dtype) -> int | None:
+    """_dev() of a tensor of `dtype` (an MOE_ code); an address is taken as it is."""
+    if x is not None and not isinstance(x, int) and _dtype(x) != dtype:
+        raise ValueError("a tensor has another dtype than the call's")
+    return _dev(x)
+
+
+def moe_token_logprobs(ctx, logits, targets, n_tokens, vocab, logp, entropy=None, n_top=0, top_idx=None,
+                       top_logp=None, stats=None, scale=1.0, dtype=None, stream=None):
+    """Log probabilities of targets (int32, below 0: none) under softmax(scale *
+    logits), entropies, the n_top largest logits with theirs, and the stats the
+    gradient reads; outputs may be None.  dtype: logits' by default."""
+    dtype = _dtype(logits) if dtype is None else dtype
+    return _check(ctx, load().moe_token_logprobs(ctx, _elem16(logits, dtype), dtype, _elem(targets, _IDS), n_tokens,
+                                                 vocab, scale, n_top, _elem(logp, _FP32), _elem(entropy, _FP32),
+                                                 _elem(top_idx, _IDS), _elem(top_logp, _FP32), _elem(stats, _FP32),
+                                                 _stream(stream)))
+
+
+def moe_token_logprobs_grad(ctx, logits, targets, n_tokens, vocab, stats, entropy, g_logp, g_entropy, dlogits,
+                            scale=1.0, dtype=None, stream=None):
+    """dlogits (of logits' dtype, may be logits) from the gradients of the log
+    probabilities and of the entropies; one of these may be None."""
+    dtype = _dtype(logits) if dtype is None else dtype
+    return _check(ctx, load().moe_token_logprobs_grad(ctx, _elem16(logits, dtype), dtype, _elem(targets, _IDS),
+                                                      n_tokens, vocab, scale, _elem(stats, _FP32),
+                                                      _elem(entropy, _FP32), _elem(g_logp, _FP32),
+                                                      _elem(g_entropy, _FP32), _elem16(dlogits, dtype),
+                                                      _stream(stream)))
 
 
 def moe_cache_snapshot(ctx, tensor_id, n_experts, slots_per_tensor):

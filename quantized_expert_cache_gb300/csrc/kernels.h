@@ -182,6 +182,32 @@ struct RouterParams {
     float balance, zcoef;
 };
 
+// Log probabilities of tokens and their gradient (kernels_token.cu).
+constexpr int kTokenMaxTop = 32, kTokenMaxVocab = 1 << 30;
+constexpr int kErrorToken = 128;    // error bit: a target id past the vocabulary
+struct TokenParams {
+    const void *logits;         // [T][vocab] of dtype
+    const int32_t *targets;     // [T] or null; below 0: none
+    float *logp, *entropy;      // [T] or null
+    int32_t *top_idx;           // [T][n_top]
+    float *top_logp;            // [T][n_top]
+    float *stats;               // [T][2] or null: largest logit, log of the sum relative to it
+    int *error;                 // kErrorToken
+    int dtype, n_tokens, vocab, n_top;
+    float scale;
+};
+struct TokenGradParams {
+    const void *logits;         // [T][vocab] of dtype
+    const int32_t *targets;     // [T] or null
+    const float *stats;         // [T][2]
+    const float *entropy;       // [T] with g_entropy
+    const float *g_logp, *g_entropy;  // [T] or null
+    void *dlogits;              // [T][vocab] of dtype, may be logits
+    int *error;
+    int dtype, n_tokens, vocab;
+    float scale;
+};
+
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
 constexpr int kLinearSmem = 200 * 1024;        // dynamic shared memory of a CTA
@@ -212,6 +238,8 @@ struct LinearGemm {
 
 int launch_rms_norm(const NormParams &p, cudaStream_t st);
 int launch_router_loss(const RouterParams &p, int n_sm, cudaStream_t st);
+int launch_token_logprobs(const TokenParams &p, int n_sm, cudaStream_t st);
+int launch_token_grad(const TokenGradParams &p, cudaStream_t st);
 size_t linear_weight_bytes(int fmt, int rows, int cols);
 int launch_linear_repack(const uint8_t *src, uint8_t *dst, int fmt, int rows, int cols, int n_sm, cudaStream_t st);
 int launch_linear_max(uint8_t *w, int fmt, int rows, int cols, unsigned *out, int n_sm, cudaStream_t st);

@@ -11,6 +11,7 @@
 // pass borrows expert blocks and gives them back refilled with hot experts).
 #include "../../include/moe_cache.h"
 #include "kernels.h"
+#include "operands.h"
 #include "repack.h"
 
 #include <cudaTypedefs.h>
@@ -24,8 +25,11 @@
 #include <thread>
 #include <vector>
 
+using moe::apart;
 using moe::BlockScale;
+using moe::Span;
 using moe::Update;
+using moe::whole;
 
 namespace {
 
@@ -257,7 +261,9 @@ int device_fault(moe_ctx *ctx) {
     CK(cudaMemsetAsync(ctx->d_error, 0, sizeof(int), ctx->stream));
     char msg[160];
     snprintf(msg, sizeof msg, "device error bits 0x%x: %s", bits,
-             (bits & 1) ? "an expert id outside [0, n_experts) (read as expert 0)" : "a bounded wait expired");
+             (bits & 1) ? "an expert id outside [0, n_experts) (read as expert 0)"
+            : (bits & ~moe::kErrorToken) ? "a bounded wait expired"
+                                         : "a target id past the vocabulary (read as none)");
     return fail(ctx, MOE_ERR_FAULT, msg);
 }
 
@@ -1834,36 +1840,6 @@ void moe_destroy(moe_ctx *ctx) {
     delete ctx;
 }
 
-// Whether all addresses are multiples of an element's size (null is).
-static bool whole(std::initializer_list<const void *> ptrs, uintptr_t size) {
-    for (const void *p : ptrs)
-        if ((uintptr_t)p & (size - 1)) return false;
-    return true;
-}
-
-// Bytes that an operator reads or writes (none without an address).
-struct Span {
-    const void *p;
-    size_t n;
-    bool meets(const Span &o) const {
-        const uintptr_t a = (uintptr_t)p, b = (uintptr_t)o.p;
-        return p && o.p && a < b + o.n && b < a + n;
-    }
-};
-
-// Whether no output meets an input or another output.  Rows are worked on by
-// independent warps and CTAs: what one writes over bytes that another has yet to
-// read is a race.
-static bool apart(std::initializer_list<Span> in, std::initializer_list<Span> out) {
-    for (const Span *o = out.begin(); o != out.end(); ++o) {
-        for (const Span &i : in)
-            if (o->meets(i)) return false;
-        for (const Span *q = out.begin(); q != o; ++q)
-            if (o->meets(*q)) return false;
-    }
-    return true;
-}
-
 int moe_rms_norm(moe_ctx *ctx, const void *d_x, const void *d_res, int dtype, const float *d_weight, int n_tokens,
                  int width, float eps, void *d_sum, float *d_y, int8_t *d_q, uint16_t *d_d, void *stream) {
     if (!ctx) return fail(nullptr, MOE_ERR_ARG, "null ctx");
@@ -2208,3 +2184,10 @@ int moe_debug_busy(moe_ctx *ctx, int microseconds) {
 }
 
 }  // extern "C"
+
+namespace moe {
+
+OpContext op_context(const moe_ctx *ctx) { return {ctx->stream, ctx->dev, ctx->n_sm, ctx->d_error}; }
+int op_fail(moe_ctx *ctx, int code, const std::string &msg) { return fail(ctx, code, msg); }
+
+}  // namespace moe
