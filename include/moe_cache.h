@@ -607,6 +607,62 @@ int moe_token_logprobs_grad(moe_ctx *ctx, const void *d_logits, int dtype, const
                             int vocab, float scale, const float *d_stats, const float *d_entropy,
                             const float *d_g_logp, const float *d_g_entropy, void *d_dlogits, void *stream);
 
+/* Activations of a dense layer: none, z / (1 + exp(-z)), z Phi(z) (erf). */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1
+#define MOE_ACT_GELU 2
+
+/*
+ * A dense layer of 16-bit weights, the router and the projections that stay out of
+ * the 4-bit formats, with its epilogue (no counterpart on the source pages):
+ *   z = x W^T + bias,  d_pre = z,  d_y = act(z) + res
+ * in fp32, d_pre and d_y rounded once.  d_x: [n_tokens][cols] of x_dtype, d_w:
+ * [rows][cols] of w_dtype (MOE_F16, MOE_BF16), the caller's own device memory.
+ * x_dtype is w_dtype, or MOE_F32 with MOE_BF16 weights (the rows of moe_rms_norm).
+ * d_bias: fp32 [rows] or NULL.  d_res: [n_tokens][rows] of y_dtype or NULL; d_y may
+ * be d_res.  d_y, d_pre (what moe_dense_backward needs of an activation, or NULL):
+ * [n_tokens][rows] of y_dtype, which is MOE_F32 or w_dtype.  cols: a multiple of 8.
+ * d_x, d_w and d_ws are 16-byte aligned, the others to their elements.  Sums in fp32;
+ * fp32 rows enter with all their 24 bits (16 for a 16-bit result) but for what lies
+ * below 2^-133.  Up to 4 tokens a plain fp32 sum, above on the tensor cores: the bits
+ * of a token's result depend on the batch's size.  NaN and infinities spread as in the
+ * formulas.  A bounded wait that expires is reported by the next cache_step or
+ * miss_drain (MOE_ERR_FAULT).  d_ws: moe_dense_workspace's forward_bytes, the call's
+ * own while it runs (0 bytes: NULL).  Asynchronous on `stream` (NULL: the context's),
+ * any stream; capturable (a captured graph holds its buffers' addresses).  No output
+ * and no workspace meets another buffer (MOE_ERR_ARG).  Errors: MOE_ERR_ARG,
+ * MOE_ERR_CUDA.
+ */
+int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_w, int w_dtype, const float *d_bias,
+                      int act, const void *d_res, int n_tokens, int rows, int cols, void *d_y, int y_dtype,
+                      void *d_pre, void *d_ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of such a layer (no counterpart on the source pages: they continue the
+ * logits' gradient of moe_router_loss and moe_token_logprobs_grad): with dz = dy
+ * act'(pre),
+ *   d_dx = dz W,  d_dw = dz^T x,  d_db = the sum of dz over the tokens
+ * (the residual's gradient is dy).  d_dy, d_pre: [n_tokens][rows] of y_dtype, d_pre as
+ * moe_dense_forward wrote it (not read without an activation).  d_dx: [n_tokens][cols]
+ * of x_dtype; d_dw: [rows][cols] of dw_dtype, MOE_F32 or w_dtype; d_db: fp32 [rows];
+ * any of them NULL, at least one wanted; d_x is read for d_dw only, d_w for d_dx only.
+ * y_dtype MOE_F32 goes with MOE_BF16 weights.  Without tokens d_dw and d_db are zero.
+ * dz is held in fp32 and enters the products with 16 bits for a 16-bit result, 24 for
+ * an fp32 one (binary16 layers: 22, or 2^-25); without an activation a 16-bit dy
+ * enters as it is.  The same call on the same inputs gives the same bits (those of
+ * d_dx and d_dw depend on whether both are asked for).  d_ws:
+ * moe_dense_workspace's backward_bytes.  Everything else as moe_dense_forward.
+ */
+int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_w, int w_dtype, const void *d_dy,
+                       int y_dtype, const void *d_pre, int act, int n_tokens, int rows, int cols, void *d_dx,
+                       void *d_dw, int dw_dtype, float *d_db, void *d_ws, size_t ws_bytes, void *stream);
+
+/* Bytes that the two calls above need as their workspace (no counterpart on the source
+ * pages); either output may be NULL.  A workspace of a larger n_tokens serves fewer.
+ * Errors: MOE_ERR_ARG. */
+int moe_dense_workspace(moe_ctx *ctx, int x_dtype, int w_dtype, int y_dtype, int act, int n_tokens, int rows,
+                        int cols, size_t *forward_bytes, size_t *backward_bytes);
+
 /*
  * Snapshot of one tensor's cache state (inspection for tests: the table,
  * slots and stamps of Zapdev-labs/a6000-custom-kernels' pointer-table cache;

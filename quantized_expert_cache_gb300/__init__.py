@@ -24,6 +24,7 @@ ERRORS = {-1: "MOE_ERR_ARG", -2: "MOE_ERR_OOM", -3: "MOE_ERR_CUDA", -4: "MOE_ERR
           -5: "MOE_ERR_TIMEOUT", -6: "MOE_ERR_CAPACITY", -7: "MOE_ERR_STATE", -8: "MOE_ERR_FAULT"}
 KIND_GATE, KIND_UP, KIND_DOWN = 0, 1, 2
 F32, F16, BF16 = 0, 1, 2
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 FMT_Q4_0, FMT_Q8_0, FMT_Q5_0, FMT_Q4_K, FMT_Q6_K, FMT_Q5_K = 0, 1, 2, 3, 4, 5
 
 
@@ -73,6 +74,12 @@ SIGNATURES = {
     "moe_router_loss": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _f32, _vp, _vp, _vp, _vp]),
     "moe_token_logprobs": (_i32, [_vp, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_token_logprobs_grad": (_i32, [_vp, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_dense_forward": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
+                                 _sz, _vp]),
+    "moe_dense_backward": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32,
+                                  _vp, _vp, _sz, _vp]),
+    "moe_dense_workspace": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz),
+                                   ctypes.POINTER(_sz)]),
     "moe_cache_snapshot": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp]),
     "moe_cache_layout": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp]),
     "moe_stats": (_i32, [_vp, ctypes.POINTER(moe_stats_t)]),
@@ -340,8 +347,8 @@ def moe_router_loss(ctx, logits, idx, mask, gw, n_tokens, n_experts, k, balance_
                                               _stream(stream)))
 
 
-def _elem16(x, dtype) -> int | None:
-    """_dev() of a tensor of `dtype` (an MOE_ code); an address is taken as it is."""
+def _of_dtype(x, dtype) -> int | None:
+    """_dev() of a tensor that must be of `dtype` (an MOE_ code)."""
     if x is not None and not isinstance(x, int) and _dtype(x) != dtype:
         raise ValueError("a tensor has another dtype than the call's")
     return _dev(x)
@@ -353,7 +360,7 @@ def moe_token_logprobs(ctx, logits, targets, n_tokens, vocab, logp, entropy=None
     logits), entropies, the n_top largest logits with theirs, and the stats the
     gradient reads; outputs may be None.  dtype: logits' by default."""
     dtype = _dtype(logits) if dtype is None else dtype
-    return _check(ctx, load().moe_token_logprobs(ctx, _elem16(logits, dtype), dtype, _elem(targets, _IDS), n_tokens,
+    return _check(ctx, load().moe_token_logprobs(ctx, _of_dtype(logits, dtype), dtype, _elem(targets, _IDS), n_tokens,
                                                  vocab, scale, n_top, _elem(logp, _FP32), _elem(entropy, _FP32),
                                                  _elem(top_idx, _IDS), _elem(top_logp, _FP32), _elem(stats, _FP32),
                                                  _stream(stream)))
@@ -364,11 +371,57 @@ def moe_token_logprobs_grad(ctx, logits, targets, n_tokens, vocab, stats, entrop
     """dlogits (of logits' dtype, may be logits) from the gradients of the log
     probabilities and of the entropies; one of these may be None."""
     dtype = _dtype(logits) if dtype is None else dtype
-    return _check(ctx, load().moe_token_logprobs_grad(ctx, _elem16(logits, dtype), dtype, _elem(targets, _IDS),
+    return _check(ctx, load().moe_token_logprobs_grad(ctx, _of_dtype(logits, dtype), dtype, _elem(targets, _IDS),
                                                       n_tokens, vocab, scale, _elem(stats, _FP32),
                                                       _elem(entropy, _FP32), _elem(g_logp, _FP32),
-                                                      _elem(g_entropy, _FP32), _elem16(dlogits, dtype),
+                                                      _elem(g_entropy, _FP32), _of_dtype(dlogits, dtype),
                                                       _stream(stream)))
+
+
+def _dtype_of(x) -> int:
+    """MOE_ code of a tensor, of a dtype itself, or a code."""
+    if isinstance(x, int):
+        return x
+    return _dtype(x) if hasattr(x, "dtype") else _DTYPES[_type_name(x)]
+
+
+def _space(ws) -> tuple:
+    return (None, 0) if ws is None else (_dev(ws), ws.numel() * ws.element_size())
+
+
+def moe_dense_workspace(ctx, x, w, y, act, n_tokens, rows, cols) -> tuple:
+    """Workspace bytes (forward, backward) of a dense layer; x, w, y: tensors,
+    dtypes or MOE_ codes."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(ctx, load().moe_dense_workspace(ctx, _dtype_of(x), _dtype_of(w), _dtype_of(y), act, n_tokens, rows, cols,
+                                           ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def moe_dense_forward(ctx, x, w, n_tokens, rows, cols, y, bias=None, act=ACT_NONE, res=None, pre=None, ws=None,
+                      x_dtype=None, w_dtype=None, y_dtype=None, stream=None):
+    """y = act(x W^T + bias) + res, pre = the sums before the activation; fp32
+    bias; ws: a tensor of moe_dense_workspace's bytes.  The dtypes: those of x, w
+    and y by default (an address has none: give its own)."""
+    xd, wd, yd = (_dtype(t) if d is None else d for t, d in ((x, x_dtype), (w, w_dtype), (y, y_dtype)))
+    at, size = _space(ws)
+    return _check(ctx, load().moe_dense_forward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _elem(bias, _FP32), act,
+                                                _of_dtype(res, yd), n_tokens, rows, cols, _of_dtype(y, yd), yd,
+                                                _of_dtype(pre, yd), at, size, _stream(stream)))
+
+
+def moe_dense_backward(ctx, x, w, dy, n_tokens, rows, cols, dx=None, dw=None, db=None, act=ACT_NONE, pre=None,
+                       ws=None, x_dtype=None, w_dtype=None, y_dtype=None, dw_dtype=None, stream=None):
+    """dx (of x's dtype), dw (fp32 or w's dtype) and db (fp32) of a dense layer,
+    any of them None; x is read for dw only, w for dx only: the other may be None
+    with its dtype given.  ws: a tensor of moe_dense_workspace's bytes."""
+    xd, wd, yd, dwd = (_dtype(t) if d is None else d
+                       for t, d in ((x, x_dtype), (w, w_dtype), (dy, y_dtype), (dw, dw_dtype)))
+    at, size = _space(ws)
+    return _check(ctx, load().moe_dense_backward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _of_dtype(dy, yd), yd,
+                                                 _of_dtype(pre, yd), act, n_tokens, rows, cols, _of_dtype(dx, xd),
+                                                 _of_dtype(dw, dwd), dwd, _elem(db, _FP32), at, size,
+                                                 _stream(stream)))
 
 
 def moe_cache_snapshot(ctx, tensor_id, n_experts, slots_per_tensor):

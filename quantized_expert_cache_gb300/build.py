@@ -11,9 +11,10 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmoecache.so")
 SOURCES = ["moe_cache.cu", "kernels_decode.cu", "kernels_gemm.cu", "no_alloc.cu", "kernels_norm.cu",
-           "kernels_linear.cu", "kernels_linear_gemm.cu", "kernels_router.cu", "kernels_token.cu", "operators.cu"]
+           "kernels_linear.cu", "kernels_linear_gemm.cu", "kernels_router.cu", "kernels_token.cu", "kernels_dense.cu", "kernels_dense_gemm.cu",
+           "operators.cu"]
 HEADERS = ["common.cuh", "kernels.h", "repack.h", "tcgen05.cuh",
-           "linear.cuh", "operands.h"]
+           "linear.cuh", "dense.cuh", "operands.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]

@@ -208,6 +208,60 @@ struct TokenGradParams {
     float scale;
 };
 
+// 16-bit dense layers (kernels_dense.cu, kernels_dense_gemm.cu).
+constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
+constexpr int kErrorDense = 256;    // error bit: a bounded wait expired
+// Output [columns][ld], element (m, n) at n * ld + m, of dtype (0 fp32, 1 binary16, 2 bfloat16).
+struct DenseOut {
+    void *out;
+    const float *bias;          // [ld] by m, or null
+    const void *res;            // as out, added at the end, or null
+    void *pre;                  // as out, the sums before the activation, or null
+    int dtype, act, ld;
+};
+// Few tokens: y = act(x W^T + bias) + res, a warp to some rows of W.
+constexpr int kDenseFew = 4;
+struct DenseFew {
+    const void *x, *w;          // [n_tokens][cols], [rows][cols]
+    int x_dtype, w_dtype, n_tokens, rows, cols;
+    DenseOut o;                 // ld = rows
+};
+// An operand in 16-bit parts whose sum it is, and the sums of its columns.
+struct DenseSplit {
+    const void *src;            // [n_tokens][cols] of dtype
+    const void *pre;            // as src: multiplied by the activation's slope there, or null
+    int dtype, act, n_tokens, cols;
+    void *parts;                // [n_parts][n_tokens][ld] of part_dtype, or null
+    int part_dtype, n_parts, ld;
+    float *sums;                // [cols] or null, through
+    float *ws_sums;             // [dense_sum_blocks(n_tokens)][cols]
+};
+int dense_sum_blocks(int n_tokens);
+// One product D[m][n] = sum over pairs of parts and over k of A[m][k] B[n][k].
+struct DenseProduct {
+    CUtensorMap tm_a, tm_b;     // [part][outer][inner], boxes of 64 x 64 (x 128 rows, x tile columns: k inner)
+    int M, N, K;
+    int a_mn, b_mn;             // 1: stored [k][m] or [k][n]; 0: [m][k], [n][k]
+    int bf16;                   // operands: 1 bfloat16, 0 binary16
+    int n_pairs;
+    unsigned pairs;             // 4 bits each, the first lowest: part of A | part of B << 2
+    int m_tiles, n_tiles;
+    DenseOut o;                 // ld = M
+};
+struct DenseGemm {
+    DenseProduct p[2];
+    int n_products, splits;
+    int *error;
+};
+// Tile columns and K splits of a launch.
+struct DensePlan {
+    int bn, splits;
+};
+DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm);
+int launch_dense_few(const DenseFew &p, int n_sm, cudaStream_t st);
+int launch_dense_split(const DenseSplit &p, cudaStream_t st);
+int launch_dense_gemm(DenseGemm &g, int bn, int device, int n_sm, cudaStream_t st);
+
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;
 constexpr int kLinearSmem = 200 * 1024;        // dynamic shared memory of a CTA

@@ -1,0 +1,258 @@
+// 16-bit dense layers: products of few tokens, and the preparation of operands for
+// the tensor cores (kernels_dense_gemm.cu).
+//
+// Few tokens.  y = act(x W^T + bias) + res is bound by the read of W: a warp takes
+// some rows of W and all tokens, its lanes neighbouring packs of 8 columns; products
+// and sums in fp32.
+//
+// Parts.  An fp32 operand goes to the tensor cores as three bfloat16 numbers, each the
+// rounding of what the ones before leave: 24 bits, all of them (what lies below
+// 2^-133 is lost); dz = dy act'(z) of a binary16 layer as two binary16 numbers (22
+// bits, or 2^-25).  A gradient that is 16-bit itself goes as it is.  Products of
+// parts are further steps of the same sum.
+#include <algorithm>
+#include <type_traits>
+
+#include "dense.cuh"
+
+namespace moe {
+namespace {
+
+using namespace dense;
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack {
+    T v[N];
+};
+
+// ---- few tokens ---------------------------------------------------------------
+// ROWS rows of W a warp, T tokens, DEPTH packs of 8 columns in flight a row.
+template <typename TX, typename TW, int T, int ROWS>
+__global__ void __launch_bounds__(256) dense_few_kernel(DenseFew p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    constexpr int DEPTH = 8 / ROWS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, packs = p.cols / 8;
+    const size_t r0 = ((size_t)blockIdx.x * 8 + warp) * ROWS;
+    if (r0 >= (size_t)p.rows) return;
+    const TX *x = (const TX *)p.x;
+    const TW *w[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)  // (the last warp's rows past the end are its last one)
+        w[r] = (const TW *)p.w + min(r0 + r, (size_t)p.rows - 1) * p.cols;
+    float acc[ROWS][T];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[r][t] = 0.0f;
+    for (int c0 = lane; c0 < packs; c0 += 32 * DEPTH) {
+        Pack<TW, 8> v[DEPTH][ROWS];
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                v[d][r] = Pack<TW, 8>{};
+                if (c0 + 32 * d < packs) *(uint4 *)&v[d][r] = __ldcs((const uint4 *)w[r] + c0 + 32 * d);
+            }
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            if (c0 + 32 * d >= packs) break;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const Pack<TX, 8> a = *((const Pack<TX, 8> *)(x + (size_t)t * p.cols) + c0 + 32 * d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+                        acc[r][t] = fmaf(value<TX>(a.v[j]), value<TW>(v[d][r].v[j]), acc[r][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const float s = warp_sum_f(acc[r][t]);
+            if (lane == (r * T + t) % 32) acc[0][0] = s;
+        }
+    if (lane < ROWS * T) {
+        const size_t m = r0 + lane / T;
+        if (m < (size_t)p.rows) finish(p.o, m, lane % T, p.o.bias ? p.o.bias[m] : 0.0f, acc[0][0]);
+    }
+}
+
+// ---- parts and column sums ------------------------------------------------------
+// A CTA takes 256 columns (8 a lane) of some tokens, a warp every eighth of them.
+// WIDE: rows of 16-byte packs; else neighbouring lanes take neighbouring columns.
+constexpr int kSplitCols = 256;
+
+template <typename T, typename P, int PARTS, bool WIDE>
+__global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int block_tokens) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ float part_sum[8][kSplitCols];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int strips = (p.cols + kSplitCols - 1) / kSplitCols, strip = blockIdx.x % strips;
+    const int block = blockIdx.x / strips;
+    const int c0 = strip * kSplitCols;
+    const auto col = [&](int j) { return c0 + (WIDE ? lane * 8 + j : j * 32 + lane); };
+    const size_t t0 = (size_t)block * block_tokens, t1 = min(t0 + block_tokens, (size_t)p.n_tokens);
+    float sum[8] = {};
+    for (size_t t = t0 + warp; t < t1; t += 8) {
+        float v[8], z[8];
+        const T *src = (const T *)p.src + t * p.cols, *pre = (const T *)p.pre + t * p.cols;
+        if (WIDE) {
+            Pack<T, 8> a{}, b{};
+            if (col(0) < p.cols) {
+                a = *(const Pack<T, 8> *)(src + col(0));
+                if (p.pre) b = *(const Pack<T, 8> *)(pre + col(0));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = value<T>(a.v[j]), z[j] = value<T>(b.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = col(j) < p.cols ? value<T>(src[col(j)]) : 0.0f;
+                z[j] = p.pre && col(j) < p.cols ? value<T>(pre[col(j)]) : 0.0f;
+            }
+        }
+        if (p.pre)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], slope_of(z[j], p.act));  // (not fused into the sum)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        if (PARTS) {
+            unsigned cut = 0;
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                Pack<P, 8> o;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    o.v[j] = rounded<P>(v[j]);
+                    if constexpr (std::is_same<P, __nv_bfloat16>::value) {
+                        // values that round past bfloat16's range are cut, all their parts: no
+                        // sum of the first ones is larger than the value
+                        if (q == 0) cut |= isinf(value<P>(o.v[j])) && !isinf(v[j]) ? 1u << j : 0;
+                        if (cut >> j & 1) o.v[j] = __ushort_as_bfloat16((unsigned short)(__float_as_uint(v[j]) >> 16));
+                    }
+                    const float left = v[j] - value<P>(o.v[j]);
+                    // infinities and NaN are their first part
+                    v[j] = isfinite(value<P>(o.v[j])) ? left : 0.0f;
+                }
+                P *dst = (P *)p.parts + ((size_t)q * p.n_tokens + t) * p.ld;
+                if (WIDE) {
+                    if (col(0) < p.cols) *(Pack<P, 8> *)(dst + col(0)) = o;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (col(j) < p.cols) dst[col(j)] = o.v[j];
+                }
+            }
+        }
+    }
+    if (!p.sums) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part_sum[warp][col(j) - c0] = sum[j];
+    __syncthreads();
+    const int c = c0 + threadIdx.x;
+    if (c < p.cols) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += part_sum[w][threadIdx.x];
+        p.ws_sums[(size_t)block * p.cols + c] = s;
+    }
+}
+
+// The blocks' sums of a column, in order: the same bits every time.
+__global__ void __launch_bounds__(128) dense_sums_kernel(const float *part, float *sums, int blocks, int cols) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    // 4 threads a column, each every fourth block
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
+    __shared__ float four[4][32];
+    float s = 0.0f;
+    if (c < cols)
+        for (int b = q; b < blocks; b += 4) s += part[(size_t)b * cols + c];
+    four[q][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (q == 0 && c < cols) sums[c] = (four[0][threadIdx.x] + four[1][threadIdx.x]) + (four[2][threadIdx.x] + four[3][threadIdx.x]);
+}
+
+int block_tokens(int n_tokens) { return std::max(32, (n_tokens + 255) / 256); }
+
+template <typename K, typename... A>
+int launch(K kernel, size_t grid, int threads, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, typename P, int PARTS>
+int launch_split(const DenseSplit &p, cudaStream_t st) {
+    const int bt = block_tokens(p.n_tokens), strips = (p.cols + kSplitCols - 1) / kSplitCols;
+    const size_t grid = (size_t)strips * ((p.n_tokens + bt - 1) / bt);
+    const bool wide = p.cols % 8 == 0 && (((uintptr_t)p.src | (uintptr_t)p.pre | (uintptr_t)p.parts) & 15) == 0;
+    const int rc = wide ? launch(dense_split_kernel<T, P, PARTS, true>, grid, 256, st, p, bt)
+                        : launch(dense_split_kernel<T, P, PARTS, false>, grid, 256, st, p, bt);
+    if (rc || !p.sums) return rc;
+    return launch(dense_sums_kernel, (p.cols + 31) / 32, 128, st, (const float *)p.ws_sums, p.sums,
+                  dense_sum_blocks(p.n_tokens), p.cols);
+}
+
+template <typename TX, typename TW, int ROWS>
+int launch_few_rows(const DenseFew &p, cudaStream_t st) {
+    const size_t grid = ((size_t)p.rows + 8 * ROWS - 1) / (8 * ROWS);
+    switch (p.n_tokens) {
+        case 1: return launch(dense_few_kernel<TX, TW, 1, ROWS>, grid, 256, st, p);
+        case 2: return launch(dense_few_kernel<TX, TW, 2, ROWS>, grid, 256, st, p);
+        case 3: return launch(dense_few_kernel<TX, TW, 3, ROWS>, grid, 256, st, p);
+        default: return launch(dense_few_kernel<TX, TW, 4, ROWS>, grid, 256, st, p);
+    }
+}
+
+template <typename TX, typename TW>
+int launch_few(const DenseFew &p, int n_sm, cudaStream_t st) {
+    // a row a warp while that leaves warps to spare: more of them, shorter
+    return p.rows <= n_sm * 32 ? launch_few_rows<TX, TW, 1>(p, st) : launch_few_rows<TX, TW, 2>(p, st);
+}
+
+}  // namespace
+
+int dense_sum_blocks(int n_tokens) {
+    const int bt = block_tokens(n_tokens);
+    return (n_tokens + bt - 1) / bt;
+}
+
+// (a context's calls ask for 3 parts of fp32 or bfloat16 for an fp32 result, 2 for a
+// 16-bit one; a binary16 gradient's slope takes 2; 1 is a copy with aligned rows, 0 sums alone)
+int launch_dense_split(const DenseSplit &p, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    switch (p.dtype * 4 + p.n_parts) {
+        case 0: return launch_split<float, bf, 0>(p, st);
+        case 2: return launch_split<float, bf, 2>(p, st);
+        case 3: return launch_split<float, bf, 3>(p, st);
+        case 4: return launch_split<__half, __half, 0>(p, st);
+        case 5: return launch_split<__half, __half, 1>(p, st);
+        case 6: return launch_split<__half, __half, 2>(p, st);
+        case 8: return launch_split<bf, bf, 0>(p, st);
+        case 9: return launch_split<bf, bf, 1>(p, st);
+        case 10: return launch_split<bf, bf, 2>(p, st);
+        case 11: return launch_split<bf, bf, 3>(p, st);
+        default: return (int)cudaErrorInvalidValue;
+    }
+}
+
+int launch_dense_few(const DenseFew &p, int n_sm, cudaStream_t st) {
+    if (p.w_dtype == 1) return launch_few<__half, __half>(p, n_sm, st);
+    return p.x_dtype == 0 ? launch_few<float, __nv_bfloat16>(p, n_sm, st)
+                          : launch_few<__nv_bfloat16, __nv_bfloat16>(p, n_sm, st);
+}
+
+}  // namespace moe

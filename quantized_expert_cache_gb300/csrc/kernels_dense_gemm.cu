@@ -1,0 +1,376 @@
+// The products of a 16-bit dense layer on the 5th-generation tensor cores: the layer
+// itself, the gradient of its input and the gradient of its weights.
+//
+//   D[m][n] = sum_k A[m][k] B[n][k], m the contiguous direction of the result:
+//   layer:    m = rows of W, n = tokens, k = columns:  A = W [m][k],  B = x [n][k]
+//   input:    m = columns, n = tokens, k = rows of W:  A = W [k][m],  B = dz [n][k]
+//   weights:  m = columns, n = rows of W, k = tokens:  A = x [k][m],  B = dz [k][n]
+//
+// An operand is read as it lies in memory: one whose k is contiguous as rows of 64 k,
+// the other kind as rows of 64 m (or n), both in the 128-byte swizzle that the MMA's
+// descriptors name; nothing is transposed.  A thread of the epilogue has one m and
+// many n, so a warp writes 32 neighbours of the result at a time.
+//
+// The accumulators are drained every kChunk steps (512 of k) and added up in
+// registers, rounded to nearest: the tensor core's own fp32 accumulation truncates, a
+// bias of about 2^-24 a step on a growing sum.  Two accumulators in TMEM in turn hide
+// the drain, and the epilogue of a tile behind the next one's products.
+//
+// Where there are fewer tiles than SMs, a tile's steps are shared out over a cluster
+// of CTAs and their sums joined through distributed shared memory, in order.
+#include <cuda.h>
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "dense.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+using namespace gemm;
+
+constexpr int kBM = 128, kBK = 64;    // tile rows, k of a step
+constexpr int kChunk = 8;             // steps between drains
+constexpr int kEpi = 8, kThreads = (2 + kEpi) * 32;
+constexpr int kWTma = 0, kWMma = 1, kWEpi = 2;
+constexpr int kMaxSplits = 8;
+
+template <int BN>
+struct Cfg {
+    static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BN * kBK * 2, SLOT = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 8 : 10;
+    static constexpr int BAR_OFF = STAGES * SLOT;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
+    static constexpr int SMEM = MISC_OFF + 16 + 1024;  // (the first 1024: alignment)
+    static constexpr int COLS = 2 * BN;                // TMEM: two accumulators
+    static_assert(BN * kBM * 4 <= BAR_OFF, "a split tile's sums");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Descriptor of a 128-byte swizzled operand.  k contiguous: 8-row groups 1024 bytes
+// apart.  m (n) contiguous: chunks of 64 of it `chunk` bytes apart, groups of 8 k 1024.
+__device__ __forceinline__ uint64_t descriptor(uint32_t addr, bool mn, uint32_t chunk) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(mn ? chunk >> 4 : 1) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// One MMA by the converged warp's elected lane.
+__device__ __forceinline__ void mma_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+struct Tile {
+    const DenseProduct *p;
+    int m0, n0, kb, first, last;  // kb: steps of one pair of parts; [first, last): this CTA's
+};
+
+// Tiles of the products one after the other; in one, bands of 8 tiles of m run through
+// all n, so that the CTAs at work share rows of both operands in L2.
+template <int BN>
+__device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int rank) {
+    Tile r;
+    const int n0 = g.p[0].m_tiles * g.p[0].n_tiles;
+    r.p = &g.p[t < n0 ? 0 : 1];
+    if (t >= n0) t -= n0;
+    constexpr int BAND = 8;
+    const int band = t / (BAND * r.p->n_tiles), first = band * BAND, size = min(BAND, r.p->m_tiles - first);
+    t -= band * BAND * r.p->n_tiles;
+    r.m0 = (first + t % size) * kBM;
+    r.n0 = t / size * BN;
+    r.kb = (r.p->K + kBK - 1) / kBK;
+    const long long steps = (long long)r.kb * r.p->n_pairs;
+    r.first = (int)(steps * rank / g.splits);
+    r.last = (int)(steps * (rank + 1) / g.splits);
+    return r;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_constant__ DenseGemm g) {
+    using C = Cfg<BN>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int S = g.splits, rank = S > 1 ? (int)cluster.block_rank() : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t slots = smem_u32(smem), bars = smem_u32(smem + C::BAR_OFF);
+    const auto full = [&](int s) { return bars + 8 * s; };
+    const auto empty = [&](int s) { return bars + 8 * (C::STAGES + s); };
+    const auto acc_full = [&](int b) { return bars + 8 * (2 * C::STAGES + b); };
+    const auto acc_empty = [&](int b) { return bars + 8 * (2 * C::STAGES + 2 + b); };
+    volatile int *abort_flag = (volatile int *)(smem + C::MISC_OFF);
+    uint32_t *tmem_slot = (uint32_t *)(smem + C::MISC_OFF + 4);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), kEpi);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == kWMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "n"(C::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = g.p[0].m_tiles * g.p[0].n_tiles + (g.n_products > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
+    const int first_tile = (int)blockIdx.x / S, tile_step = (int)gridDim.x / S;
+
+    if (warp == kWTma) {
+        if (lane == 0) {
+            // (parts that the kernel before wrote are read by the copies' proxy)
+            asm volatile("fence.proxy.async;" ::: "memory");
+            uint32_t it = 0;
+            for (int t = first_tile; t < tiles; t += tile_step) {
+                const Tile w = tile_of<BN>(g, t, rank);
+                int pair = w.first / w.kb, kb = w.first % w.kb;
+                for (int i = w.first; i < w.last; ++i, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!mbar_wait(empty(s), (it / C::STAGES & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto loaded;
+                    const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
+                    const int parts = (int)(w.p->pairs >> (4 * pair)) & 15, k = kb * kBK;
+                    mbar_arrive_tx(full(s), C::SLOT);
+                    if (w.p->a_mn) {
+#pragma unroll
+                        for (int c = 0; c < kBM / 64; ++c)
+                            tma_load_3d(a + c * 8192, &w.p->tm_a, w.m0 + 64 * c, k, parts & 3, full(s));
+                    } else {
+                        tma_load_3d(a, &w.p->tm_a, k, w.m0, parts & 3, full(s));
+                    }
+                    if (BN >= 64 && w.p->b_mn) {
+#pragma unroll
+                        for (int c = 0; c < BN / 64; ++c)
+                            tma_load_3d(b + c * 8192, &w.p->tm_b, w.n0 + 64 * c, k, parts >> 2, full(s));
+                    } else {
+                        tma_load_3d(b, &w.p->tm_b, k, w.n0, parts >> 2, full(s));
+                    }
+                    if (++kb == w.kb) {
+                        kb = 0;
+                        ++pair;
+                    }
+                }
+            }
+        loaded:;
+        }
+        __syncwarp();
+    } else if (warp == kWMma) {
+        uint32_t it = 0, chunk = 0;
+        for (int t = first_tile; t < tiles; t += tile_step) {
+            const Tile w = tile_of<BN>(g, t, rank);
+            const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
+            // fp32 sums, both operands binary16 (0) or bfloat16 (1), their directions, N, M
+            const uint32_t type = w.p->bf16 ? 1u : 0u;
+            const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) |
+                                   (uint32_t)(BN >> 3) << 17 | (uint32_t)(kBM >> 4) << 24;
+            // 16 of k: 32 bytes in a row of 64 k, 16 rows of 128 bytes in the other kind
+            const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+            for (int i = w.first; i < w.last; ++chunk) {
+                const int buf = chunk & 1, end = min(w.last, i + kChunk);
+                if (!mbar_wait_warp(acc_empty(buf), (chunk >> 1 & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto multiplied;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * BN;
+                for (int j = i; j < end; ++j, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!mbar_wait_warp(full(s), it / C::STAGES & 1, abort_flag, g.error, kErrorDense)) goto multiplied;
+                    tc_fence_after();
+                    const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
+#pragma unroll
+                    for (int q = 0; q < kBK / 16; ++q)
+                        mma_warp(d, descriptor(a + q * a_step, a_mn, 8192), descriptor(b + q * b_step, b_mn, 8192),
+                                 idesc, j > i || q > 0);
+                    mma_commit_warp(empty(s));
+                }
+                mma_commit_warp(acc_full(buf));
+                i = end;
+            }
+        }
+    multiplied:;
+        __syncwarp();
+    } else {
+        // lanes of TMEM: a warp reaches the quarter of its number
+        const int quarter = warp & 3, half = (warp - kWEpi) >> 2;
+        constexpr int NC = BN / 2;      // columns of a thread
+        uint32_t chunk = 0;
+        for (int t = first_tile; t < tiles; t += tile_step) {
+            const Tile w = tile_of<BN>(g, t, rank);
+            float acc[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
+            for (int i = w.first; i < w.last; i += kChunk, ++chunk) {
+                const int buf = chunk & 1;
+                if (!mbar_wait_warp(acc_full(buf), chunk >> 1 & 1, abort_flag, g.error, kErrorDense)) goto finished;
+                tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * NC;
+#pragma unroll
+                for (int c = 0; c < NC; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16u(at + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(v[j]);
+                }
+                tc_fence_before();
+                mbar_arrive_warp(acc_empty(buf), lane);
+            }
+            const int ml = quarter * 32 + lane, m = w.m0 + ml, n0 = w.n0 + half * NC;
+            if (S > 1) {
+                // (all products of the CTA are done: its stages are free)
+                float *red = (float *)smem;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) red[(half * NC + c) * kBM + ml] = acc[c];
+            } else if (m < w.p->M) {
+                const float bias = w.p->o.bias ? w.p->o.bias[m] : 0.0f;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (n0 + c < w.p->N) dense::finish(w.p->o, m, n0 + c, bias, acc[c]);
+            }
+        }
+    finished:;
+        __syncwarp();
+    }
+    __syncthreads();
+    if (S > 1) {
+        cluster.sync();
+        if (!*abort_flag) {
+            const Tile w = tile_of<BN>(g, first_tile, rank);
+            const float *red = (const float *)smem;
+            const int cols = min(BN, w.p->N - w.n0);
+            for (int i = threadIdx.x + rank * kThreads; i < cols * kBM; i += S * kThreads) {
+                float v[kMaxSplits];
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s)
+                    if (s < S) v[s] = *cluster.map_shared_rank(red + i, s);
+                float sum = v[0];
+#pragma unroll
+                for (int s = 1; s < kMaxSplits; ++s)
+                    if (s < S) sum += v[s];
+                const int m = w.m0 + i % kBM;
+                if (m < w.p->M)
+                    dense::finish(w.p->o, m, w.n0 + i / kBM, w.p->o.bias ? w.p->o.bias[m] : 0.0f, sum);
+            }
+        }
+        __syncwarp();
+        cluster.sync();  // no CTA leaves while its sums are read
+    }
+    // after an abort, give the copies and MMAs of this CTA a bounded time (about 10 ms)
+    // to land, then free TMEM
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 20000000ll) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+}
+
+long long steps_of(const DenseProduct &p) { return (long long)((p.K + kBK - 1) / kBK) * p.n_pairs; }
+int tiles_of(const DenseProduct &p, int bn) { return (p.M + kBM - 1) / kBM * ((p.N + bn - 1) / bn); }
+
+template <int BN>
+int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
+    auto kernel = dense_gemm_kernel<BN>;
+    static std::atomic<unsigned long long> configured{0};  // a bit a device
+    if (!(configured.load() >> (device & 63) & 1)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
+        if (e != cudaSuccess) return (int)e;
+        configured.fetch_or(1ull << (device & 63));
+    }
+    int tiles = 0;
+    for (int i = 0; i < g.n_products; ++i) {
+        DenseProduct &p = g.p[i];
+        p.m_tiles = (p.M + kBM - 1) / kBM;
+        p.n_tiles = (p.N + BN - 1) / BN;
+        tiles += p.m_tiles * p.n_tiles;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(g.splits > 1 ? tiles * g.splits : std::min(tiles, n_sm)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<BN>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)g.splits, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return (int)cudaLaunchKernelEx(&cfg, kernel, g);
+}
+
+}  // namespace
+
+DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm) {
+    DensePlan best{256, 1};
+    double least = 1e30;
+    for (int bn : {256, 128, 64, 32}) {
+        // clocks of a step: the MMAs' operand reads and products (46 at N = 32 to 128 a
+        // 16 of k); a step's tile of A from HBM takes longer than either
+        const double clocks = bn == 256 ? 520 : bn == 128 ? 290 : bn == 64 ? 230 : 210;
+        bool fits = true;
+        long long tiles = 0, work = 0, longest = 0, fewest = 1ll << 40;
+        for (int i = 0; i < n_products; ++i) {
+            if (p[i].b_mn && bn < 64) fits = false;  // (columns of B come 64 at a time)
+            const long long t = tiles_of(p[i], bn), s = steps_of(p[i]);
+            tiles += t;
+            work += t * s;
+            longest = std::max(longest, s);
+            fewest = std::min(fewest, s);
+        }
+        if (!fits) continue;
+        for (int s = 1; s <= kMaxSplits; ++s) {
+            if (s > 1 && (tiles * s > n_sm || s > fewest)) break;
+            const double rounds = s > 1 ? (double)((longest + s - 1) / s)
+                                        : std::max((double)((work + n_sm - 1) / n_sm), (double)longest *
+                                              (n_products > 1 ? 1.0 : (double)((tiles + n_sm - 1) / n_sm)));
+            const double c = rounds * clocks + (s > 1 ? 2500 + 12 * bn : 12 * bn);
+            if (c < least) {
+                least = c;
+                best = {bn, s};
+            }
+        }
+    }
+    return best;
+}
+
+int launch_dense_gemm(DenseGemm &g, int bn, int device, int n_sm, cudaStream_t st) {
+    switch (bn) {
+        case 32: return launch_tile<32>(g, device, n_sm, st);
+        case 64: return launch_tile<64>(g, device, n_sm, st);
+        case 128: return launch_tile<128>(g, device, n_sm, st);
+        default: return launch_tile<256>(g, device, n_sm, st);
+    }
+}
+
+}  // namespace moe
