@@ -67,5 +67,80 @@ __device__ __forceinline__ void finish(const DenseOut &o, size_t m, size_t n, fl
     store_as(o.out, o.dtype, i, v);
 }
 
+// Four elements from i, at once if the array allows it.
+__device__ __forceinline__ void load4_as(const void *p, int dtype, size_t i, float *v) {
+    if (dtype == 0) {
+        const float4 f = *(const float4 *)((const float *)p + i);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+        const ushort4 u = *(const ushort4 *)((const unsigned short *)p + i);
+        const unsigned short h[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = dtype == 1 ? __half2float(__ushort_as_half(h[j])) : __uint_as_float((unsigned)h[j] << 16);
+    }
+}
+__device__ __forceinline__ void store4_as(void *p, int dtype, size_t i, const float *v) {
+    if (dtype == 0) {
+        *(float4 *)((float *)p + i) = float4{v[0], v[1], v[2], v[3]};
+    } else {
+        unsigned short h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            h[j] = dtype == 1 ? __half_as_ushort(__float2half_rn(v[j])) : __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+        *(ushort4 *)((unsigned short *)p + i) = ushort4{h[0], h[1], h[2], h[3]};
+    }
+}
+
+// The epilogue of a warp's 32 rows m: blocks of finished sums go through shared memory
+// so that a lane holds four neighbours of the result (8 lanes a column, 4 columns at a
+// time): fewer, wider stores, in a short loop.
+struct Epilogue {
+    DenseOut o;    // (a copy: stores through its pointers could alias the original)
+    float bias[4];
+    int m, left;   // the lane's first row, rows from it to the end
+    bool wide;
+    __device__ __forceinline__ Epilogue(const DenseOut &out, int M, int m_warp, int lane) : o(out) {
+        m = m_warp + (lane & 7) * 4;
+        left = M - m;
+        const uintptr_t at = (uintptr_t)o.out | (uintptr_t)o.res | (uintptr_t)o.pre;
+        wide = left >= 4 && o.ld % 4 == 0 && (at & (o.dtype == 0 ? 15 : 7)) == 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bias[j] = o.bias && j < left ? o.bias[m + j] : 0.0f;
+    }
+    // sums[column][32], `cols` columns from n of N
+    __device__ __forceinline__ void store(const float *sums, int cols, int n, int N, int lane) const {
+        if (left <= 0) return;
+#pragma unroll 1
+        for (int c = lane >> 3; c < cols && n + c < N; c += 4) {
+            const float4 f = *(const float4 *)(sums + c * 32 + (lane & 7) * 4);
+            float v[4] = {f.x + bias[0], f.y + bias[1], f.z + bias[2], f.w + bias[3]};
+            const size_t i = (size_t)(n + c) * (size_t)o.ld + m;
+            if (wide) {
+                if (o.pre) store4_as(o.pre, o.dtype, i, v);
+                if (o.act != kActNone)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = act_of(v[j], o.act);
+                if (o.res) {
+                    float r[4];
+                    load4_as(o.res, o.dtype, i, r);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] += r[j];
+                }
+                store4_as(o.out, o.dtype, i, v);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < 4 && j < left; ++j) {
+                    float z = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+                    if (o.pre) store_as(o.pre, o.dtype, i + j, z);
+                    z = act_of(z, o.act);
+                    if (o.res) z += load_as(o.res, o.dtype, i + j);
+                    store_as(o.out, o.dtype, i + j, z);
+                }
+            }
+        }
+    }
+};
+
 }  // namespace dense
 }  // namespace moe

@@ -253,14 +253,14 @@ struct DenseGemm {
     int n_products, splits;
     int *error;
 };
-// Tile columns and K splits of a launch.
+// Tile columns, rows of B in one box, whether two CTAs share a tile, K splits.
 struct DensePlan {
-    int bn, splits;
+    int bn, box, pair, splits;
 };
 DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm);
 int launch_dense_few(const DenseFew &p, int n_sm, cudaStream_t st);
 int launch_dense_split(const DenseSplit &p, cudaStream_t st);
-int launch_dense_gemm(DenseGemm &g, int bn, int device, int n_sm, cudaStream_t st);
+int launch_dense_gemm(DenseGemm &g, const DensePlan &plan, int device, int n_sm, cudaStream_t st);
 
 // Dense layer with 4-bit weights (kernels_linear.cu).
 constexpr int kLinearMaxCols = 65536, kLinearMaxRows = 1 << 26;

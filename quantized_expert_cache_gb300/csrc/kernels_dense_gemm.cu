@@ -38,15 +38,20 @@ constexpr int kEpi = 8, kThreads = (2 + kEpi) * 32;
 constexpr int kWTma = 0, kWMma = 1, kWEpi = 2;
 constexpr int kMaxSplits = 8;
 
-template <int BN>
+// Tiles of 128 x BN to a CTA, or (PAIR) of 256 x BN to the two CTAs of a cluster: each
+// has half of A's rows, half of B's and half of the result's, and the leader (rank 0)
+// issues the products of both.
+template <int BN, bool PAIR>
 struct Cfg {
-    static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BN * kBK * 2, SLOT = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 8 : 10;
-    static constexpr int BAR_OFF = STAGES * SLOT;
+    static constexpr int TM = PAIR ? 2 * kBM : kBM, BR = PAIR ? BN / 2 : BN;  // tile rows; rows of B to a CTA
+    static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BR * kBK * 2, SLOT = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BR == 128 ? 6 : 8;
+    static constexpr int STAGING = STAGES * SLOT;      // the epilogue's: 32 x 32 sums a warp
+    static constexpr int BAR_OFF = STAGING + kEpi * 4096;
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
     static constexpr int SMEM = MISC_OFF + 16 + 1024;  // (the first 1024: alignment)
     static constexpr int COLS = 2 * BN;                // TMEM: two accumulators
-    static_assert(BN * kBM * 4 <= BAR_OFF, "a split tile's sums");
+    static_assert(PAIR || BN * kBM * 4 <= STAGING, "a split tile's sums");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -65,13 +70,58 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t addr, bool mn, uint32_t 
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// One MMA by the converged warp's elected lane.
-__device__ __forceinline__ void mma_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The same into this CTA of a pair, its bytes counted by a barrier of either CTA.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *tm, int x, int y, int z,
+                                                 uint32_t bar) {
     asm volatile(
-        "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+// A shared address of this CTA as that of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t mapped(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// Arrival of a warp, by its lane 0, at a barrier of the cluster.
+__device__ __forceinline__ void arrive_cluster_warp(uint32_t bar, int lane) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.eq.s32 p, %1, 0;\n"
+        "@p mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(bar),
+        "r"(lane)
+        : "memory");
+}
+
+// One MMA by the converged warp's elected lane.
+template <bool PAIR>
+__device__ __forceinline__ void mma_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if (PAIR)
+        asm volatile(
+            "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// Arrival at a barrier (of both CTAs of a pair) when the lane's products are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit_warp(uint32_t bar) {
+    if (PAIR)
+        asm volatile(
+            "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::
+                "r"(bar),
+            "h"((unsigned short)3)
+            : "memory");
+    else
+        mma_commit_warp(bar);
 }
 
 struct Tile {
@@ -81,7 +131,7 @@ struct Tile {
 
 // Tiles of the products one after the other; in one, bands of 8 tiles of m run through
 // all n, so that the CTAs at work share rows of both operands in L2.
-template <int BN>
+template <int BN, bool PAIR>
 __device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int rank) {
     Tile r;
     const int n0 = g.p[0].m_tiles * g.p[0].n_tiles;
@@ -90,23 +140,24 @@ __device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int rank) {
     constexpr int BAND = 8;
     const int band = t / (BAND * r.p->n_tiles), first = band * BAND, size = min(BAND, r.p->m_tiles - first);
     t -= band * BAND * r.p->n_tiles;
-    r.m0 = (first + t % size) * kBM;
+    r.m0 = (first + t % size) * Cfg<BN, PAIR>::TM;
     r.n0 = t / size * BN;
     r.kb = (r.p->K + kBK - 1) / kBK;
     const long long steps = (long long)r.kb * r.p->n_pairs;
-    r.first = (int)(steps * rank / g.splits);
-    r.last = (int)(steps * (rank + 1) / g.splits);
+    r.first = PAIR ? 0 : (int)(steps * rank / g.splits);
+    r.last = PAIR ? (int)steps : (int)(steps * (rank + 1) / g.splits);
     return r;
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_constant__ DenseGemm g) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, PAIR>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    const int S = g.splits, rank = S > 1 ? (int)cluster.block_rank() : 0;
+    // CTAs of a tile; S of them share out its steps, the two of a pair its rows
+    const int S = PAIR ? 1 : g.splits, CTAS = PAIR ? 2 : S, rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t slots = smem_u32(smem), bars = smem_u32(smem + C::BAR_OFF);
     const auto full = [&](int s) { return bars + 8 * s; };
@@ -123,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), kEpi);
+            mbar_init(acc_empty(b), PAIR ? 2 * kEpi : kEpi);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -132,17 +183,29 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (warp == kWMma) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "n"(C::COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)),
+                         "n"(C::COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)),
+                         "n"(C::COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster.sync();  // (both CTAs' barriers are ready before either is signalled)
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int tiles = g.p[0].m_tiles * g.p[0].n_tiles + (g.n_products > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
-    const int first_tile = (int)blockIdx.x / S, tile_step = (int)gridDim.x / S;
+    const int first_tile = (int)blockIdx.x / CTAS, tile_step = (int)gridDim.x / CTAS;
 
     if (warp == kWTma) {
         if (lane == 0) {
@@ -150,27 +213,36 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
             asm volatile("fence.proxy.async;" ::: "memory");
             uint32_t it = 0;
             for (int t = first_tile; t < tiles; t += tile_step) {
-                const Tile w = tile_of<BN>(g, t, rank);
+                const Tile w = tile_of<BN, PAIR>(g, t, rank);
                 int pair = w.first / w.kb, kb = w.first % w.kb;
                 for (int i = w.first; i < w.last; ++i, ++it) {
                     const int s = it % C::STAGES;
                     if (!mbar_wait(empty(s), (it / C::STAGES & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto loaded;
                     const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
                     const int parts = (int)(w.p->pairs >> (4 * pair)) & 15, k = kb * kBK;
-                    mbar_arrive_tx(full(s), C::SLOT);
+                    const int m0 = w.m0 + (PAIR ? rank * kBM : 0), n0 = w.n0 + (PAIR ? rank * C::BR : 0);
+                    // the leader's barrier counts both CTAs' bytes
+                    const uint32_t bar = PAIR ? mapped(full(s), 0) : full(s);
+                    if (!PAIR || rank == 0) mbar_arrive_tx(full(s), PAIR ? 2 * C::SLOT : C::SLOT);
+                    const auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y, int z) {
+                        if (PAIR)
+                            tma_load_3d_pair(dst, tm, x, y, z, bar);
+                        else
+                            tma_load_3d(dst, tm, x, y, z, bar);
+                    };
                     if (w.p->a_mn) {
 #pragma unroll
                         for (int c = 0; c < kBM / 64; ++c)
-                            tma_load_3d(a + c * 8192, &w.p->tm_a, w.m0 + 64 * c, k, parts & 3, full(s));
+                            load(a + c * 8192, &w.p->tm_a, m0 + 64 * c, k, parts & 3);
                     } else {
-                        tma_load_3d(a, &w.p->tm_a, k, w.m0, parts & 3, full(s));
+                        load(a, &w.p->tm_a, k, m0, parts & 3);
                     }
-                    if (BN >= 64 && w.p->b_mn) {
+                    if (C::BR >= 64 && w.p->b_mn) {
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c)
-                            tma_load_3d(b + c * 8192, &w.p->tm_b, w.n0 + 64 * c, k, parts >> 2, full(s));
+                        for (int c = 0; c < C::BR / 64; ++c)
+                            load(b + c * 8192, &w.p->tm_b, n0 + 64 * c, k, parts >> 2);
                     } else {
-                        tma_load_3d(b, &w.p->tm_b, k, w.n0, parts >> 2, full(s));
+                        load(b, &w.p->tm_b, k, n0, parts >> 2);
                     }
                     if (++kb == w.kb) {
                         kb = 0;
@@ -178,18 +250,21 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
                     }
                 }
             }
+            // no CTA ends before the arrivals at its last stages have come
+            for (uint32_t i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+                if (!mbar_wait(empty(i % C::STAGES), i / C::STAGES & 1, abort_flag, g.error, kErrorDense)) break;
         loaded:;
         }
         __syncwarp();
     } else if (warp == kWMma) {
         uint32_t it = 0, chunk = 0;
-        for (int t = first_tile; t < tiles; t += tile_step) {
-            const Tile w = tile_of<BN>(g, t, rank);
+        for (int t = first_tile; t < tiles && (!PAIR || rank == 0); t += tile_step) {
+            const Tile w = tile_of<BN, PAIR>(g, t, rank);
             const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
             // fp32 sums, both operands binary16 (0) or bfloat16 (1), their directions, N, M
             const uint32_t type = w.p->bf16 ? 1u : 0u;
             const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) |
-                                   (uint32_t)(BN >> 3) << 17 | (uint32_t)(kBM >> 4) << 24;
+                                   (uint32_t)(BN >> 3) << 17 | (uint32_t)(C::TM >> 4) << 24;
             // 16 of k: 32 bytes in a row of 64 k, 16 rows of 128 bytes in the other kind
             const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
             for (int i = w.first; i < w.last; ++chunk) {
@@ -204,11 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
                     const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
 #pragma unroll
                     for (int q = 0; q < kBK / 16; ++q)
-                        mma_warp(d, descriptor(a + q * a_step, a_mn, 8192), descriptor(b + q * b_step, b_mn, 8192),
+                        mma_warp<PAIR>(d, descriptor(a + q * a_step, a_mn, 8192), descriptor(b + q * b_step, b_mn, 8192),
                                  idesc, j > i || q > 0);
-                    mma_commit_warp(empty(s));
+                    commit_warp<PAIR>(empty(s));
                 }
-                mma_commit_warp(acc_full(buf));
+                commit_warp<PAIR>(acc_full(buf));
                 i = end;
             }
         }
@@ -220,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         constexpr int NC = BN / 2;      // columns of a thread
         uint32_t chunk = 0;
         for (int t = first_tile; t < tiles; t += tile_step) {
-            const Tile w = tile_of<BN>(g, t, rank);
+            const Tile w = tile_of<BN, PAIR>(g, t, rank);
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
@@ -238,30 +313,42 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
                     for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(v[j]);
                 }
                 tc_fence_before();
-                mbar_arrive_warp(acc_empty(buf), lane);
+                if (PAIR)
+                    arrive_cluster_warp(mapped(acc_empty(buf), 0), lane);
+                else
+                    mbar_arrive_warp(acc_empty(buf), lane);
             }
-            const int ml = quarter * 32 + lane, m = w.m0 + ml, n0 = w.n0 + half * NC;
-            if (S > 1) {
+            const int ml = quarter * 32 + lane, n0 = w.n0 + half * NC;
+            if (!PAIR && S > 1) {
                 // (all products of the CTA are done: its stages are free)
                 float *red = (float *)smem;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) red[(half * NC + c) * kBM + ml] = acc[c];
-            } else if (m < w.p->M) {
-                const float bias = w.p->o.bias ? w.p->o.bias[m] : 0.0f;
+            } else {
+                const dense::Epilogue e(w.p->o, w.p->M, w.m0 + (PAIR ? rank * kBM : 0) + quarter * 32, lane);
+                float *mine = (float *)(smem + C::STAGING) + (warp - kWEpi) * 1024;
+                constexpr int GROUP = NC < 32 ? NC : 32;
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    if (n0 + c < w.p->N) dense::finish(w.p->o, m, n0 + c, bias, acc[c]);
+                for (int c = 0; c < NC; c += GROUP) {
+#pragma unroll
+                    for (int j = 0; j < GROUP; ++j) mine[j * 32 + lane] = acc[c + j];
+                    __syncwarp();
+                    e.store(mine, GROUP, n0 + c, w.p->N, lane);
+                    __syncwarp();
+                }
             }
         }
     finished:;
         __syncwarp();
     }
     __syncthreads();
-    if (S > 1) {
+    if (!PAIR && S > 1) {
         cluster.sync();
         if (!*abort_flag) {
-            const Tile w = tile_of<BN>(g, first_tile, rank);
+            const Tile w = tile_of<BN, PAIR>(g, first_tile, rank);
             const float *red = (const float *)smem;
+            const DenseOut o = w.p->o;
+            const int M = w.p->M;
             const int cols = min(BN, w.p->N - w.n0);
             for (int i = threadIdx.x + rank * kThreads; i < cols * kBM; i += S * kThreads) {
                 float v[kMaxSplits];
@@ -273,8 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
                 for (int s = 1; s < kMaxSplits; ++s)
                     if (s < S) sum += v[s];
                 const int m = w.m0 + i % kBM;
-                if (m < w.p->M)
-                    dense::finish(w.p->o, m, w.n0 + i / kBM, w.p->o.bias ? w.p->o.bias[m] : 0.0f, sum);
+                if (m < M) dense::finish(o, m, w.n0 + i / kBM, o.bias ? o.bias[m] : 0.0f, sum);
             }
         }
         __syncwarp();
@@ -288,42 +374,59 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster.sync();  // no CTA leaves while the other's products read it or its arrivals come
+    else
+        __syncthreads();
     tc_fence_after();
-    if (warp == kWMma)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+    if (warp == kWMma) {
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+    }
 }
 
 long long steps_of(const DenseProduct &p) { return (long long)((p.K + kBK - 1) / kBK) * p.n_pairs; }
-int tiles_of(const DenseProduct &p, int bn) { return (p.M + kBM - 1) / kBM * ((p.N + bn - 1) / bn); }
 
-template <int BN>
+// The tiles that are compiled, and what one costs.  Clocks of a step: measured, but
+// for the pairs' near what 128 bytes a clock of shared memory allow (a step's operands
+// are written there once and read once; a pair's B is read by halves).
+struct Shape {
+    int bn;
+    bool pair;
+    double clocks;
+};
+constexpr Shape kShapes[] = {{256, true, 560}, {128, true, 420}, {128, false, 640}, {64, false, 480}, {32, false, 420}};
+
+template <int BN, bool PAIR>
 int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
-    auto kernel = dense_gemm_kernel<BN>;
+    using C = Cfg<BN, PAIR>;
+    auto kernel = dense_gemm_kernel<BN, PAIR>;
     static std::atomic<unsigned long long> configured{0};  // a bit a device
     if (!(configured.load() >> (device & 63) & 1)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return (int)e;
         configured.fetch_or(1ull << (device & 63));
     }
     int tiles = 0;
     for (int i = 0; i < g.n_products; ++i) {
         DenseProduct &p = g.p[i];
-        p.m_tiles = (p.M + kBM - 1) / kBM;
+        p.m_tiles = (p.M + C::TM - 1) / C::TM;
         p.n_tiles = (p.N + BN - 1) / BN;
         tiles += p.m_tiles * p.n_tiles;
     }
+    const int ctas = PAIR ? 2 : g.splits;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(g.splits > 1 ? tiles * g.splits : std::min(tiles, n_sm)));
+    cfg.gridDim = dim3((unsigned)(g.splits > 1 ? tiles * ctas : std::min(tiles, n_sm / ctas) * ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<BN>::SMEM;
+    cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {(unsigned)g.splits, 1, 1};
+    attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return (int)cudaLaunchKernelEx(&cfg, kernel, g);
@@ -331,45 +434,47 @@ int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
 
 }  // namespace
 
+// The cheapest of the tiles and K splits, by the clocks of the longest CTA (for two
+// products the larger of the longest tile and an even share of all).
 DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm) {
-    DensePlan best{256, 1};
+    DensePlan best{};
     double least = 1e30;
-    for (int bn : {256, 128, 64, 32}) {
-        // clocks of a step: the MMAs' operand reads and products (46 at N = 32 to 128 a
-        // 16 of k); a step's tile of A from HBM takes longer than either
-        const double clocks = bn == 256 ? 520 : bn == 128 ? 290 : bn == 64 ? 230 : 210;
+    for (const Shape &f : kShapes) {
+        const int tm = f.pair ? 2 * kBM : kBM, workers = f.pair ? n_sm / 2 : n_sm;
         bool fits = true;
         long long tiles = 0, work = 0, longest = 0, fewest = 1ll << 40;
         for (int i = 0; i < n_products; ++i) {
-            if (p[i].b_mn && bn < 64) fits = false;  // (columns of B come 64 at a time)
-            const long long t = tiles_of(p[i], bn), s = steps_of(p[i]);
+            if (p[i].b_mn && (f.pair ? f.bn / 2 : f.bn) < 64) fits = false;  // (columns of B come 64 at a time)
+            const long long t = (long long)((p[i].M + tm - 1) / tm) * ((p[i].N + f.bn - 1) / f.bn), s = steps_of(p[i]);
             tiles += t;
             work += t * s;
             longest = std::max(longest, s);
             fewest = std::min(fewest, s);
         }
         if (!fits) continue;
-        for (int s = 1; s <= kMaxSplits; ++s) {
-            if (s > 1 && (tiles * s > n_sm || s > fewest)) break;
-            const double rounds = s > 1 ? (double)((longest + s - 1) / s)
-                                        : std::max((double)((work + n_sm - 1) / n_sm), (double)longest *
-                                              (n_products > 1 ? 1.0 : (double)((tiles + n_sm - 1) / n_sm)));
-            const double c = rounds * clocks + (s > 1 ? 2500 + 12 * bn : 12 * bn);
+        for (int s = 1; s <= (f.pair ? 1 : kMaxSplits); ++s) {
+            if (s > 1 && (tiles * s > workers || s > fewest)) break;
+            const long long rounds = (tiles + workers - 1) / workers;
+            const double steps = s > 1            ? (double)((longest + s - 1) / s)
+                                 : n_products == 1 ? (double)(rounds * longest)
+                                                   : std::max((double)longest, (double)((work + workers - 1) / workers));
+            const double c = steps * f.clocks + (s > 1 ? 2500 + 12 * f.bn : 12 * f.bn);
             if (c < least) {
                 least = c;
-                best = {bn, s};
+                best = {f.bn, f.pair ? f.bn / 2 : f.bn, f.pair, s};
             }
         }
     }
     return best;
 }
 
-int launch_dense_gemm(DenseGemm &g, int bn, int device, int n_sm, cudaStream_t st) {
-    switch (bn) {
-        case 32: return launch_tile<32>(g, device, n_sm, st);
-        case 64: return launch_tile<64>(g, device, n_sm, st);
-        case 128: return launch_tile<128>(g, device, n_sm, st);
-        default: return launch_tile<256>(g, device, n_sm, st);
+int launch_dense_gemm(DenseGemm &g, const DensePlan &plan, int device, int n_sm, cudaStream_t st) {
+    if (plan.pair)
+        return plan.bn == 256 ? launch_tile<256, true>(g, device, n_sm, st) : launch_tile<128, true>(g, device, n_sm, st);
+    switch (plan.bn) {
+        case 32: return launch_tile<32, false>(g, device, n_sm, st);
+        case 64: return launch_tile<64, false>(g, device, n_sm, st);
+        default: return launch_tile<128, false>(g, device, n_sm, st);
     }
 }
 

@@ -150,10 +150,10 @@ int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const De
                                   p.a_mn ? 64 : 128);
         if (rc) return rc;
         const int rd = encode_map(ctx, &p.tm_b, b[i].base, p.bf16, b[i].inner, b[i].outer, b[i].ld, b[i].parts,
-                                  p.b_mn ? 64 : (uint32_t)plan.bn);
+                                  p.b_mn ? 64 : (uint32_t)plan.box);
         if (rd) return rd;
     }
-    return launched(ctx, what, moe::launch_dense_gemm(g, plan.bn, c.device, c.n_sm, st));
+    return launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
 }
 
 }  // namespace
