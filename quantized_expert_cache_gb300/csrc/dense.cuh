@@ -41,9 +41,10 @@ __device__ __forceinline__ void store_as(void *p, int dtype, size_t i, float v) 
 }
 
 // act(z) and its slope: silu z s, s = 1 / (1 + exp(-z)); gelu z Phi(z), Phi the
-// normal distribution's.  (Phi by erf: to 2^-24 or so of 1, not of itself.)
+// normal distribution's.  (Phi by erf: to 2^-24 or so of 1, not of itself; exp by the
+// special-function unit: |z| 2^-24 of itself more.)
 __device__ __forceinline__ float act_of(float z, int act) {
-    if (act == kActSilu) return z / (1.0f + expf(-z));
+    if (act == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
     if (act == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
     return z;
 }
@@ -92,52 +93,56 @@ __device__ __forceinline__ void store4_as(void *p, int dtype, size_t i, const fl
     }
 }
 
-// The epilogue of a warp's 32 rows m: blocks of finished sums go through shared memory
-// so that a lane holds four neighbours of the result (8 lanes a column, 4 columns at a
-// time): fewer, wider stores, in a short loop.
+// The epilogue of four neighbours m of the result in a lane.
 struct Epilogue {
     DenseOut o;    // (a copy: stores through its pointers could alias the original)
     float bias[4];
     int m, left;   // the lane's first row, rows from it to the end
     bool wide;
-    __device__ __forceinline__ Epilogue(const DenseOut &out, int M, int m_warp, int lane) : o(out) {
-        m = m_warp + (lane & 7) * 4;
-        left = M - m;
+    __device__ __forceinline__ Epilogue(const DenseOut &out, int M, int m_) : o(out), m(m_), left(M - m_) {
         const uintptr_t at = (uintptr_t)o.out | (uintptr_t)o.res | (uintptr_t)o.pre;
         wide = left >= 4 && o.ld % 4 == 0 && (at & (o.dtype == 0 ? 15 : 7)) == 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) bias[j] = o.bias && j < left ? o.bias[m + j] : 0.0f;
     }
-    // sums[column][32], `cols` columns from n of N
+    // column n's finished sums
+    __device__ __forceinline__ void column(const float *sums, int n) const {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = sums[j] + bias[j];
+        const size_t i = (size_t)n * (size_t)o.ld + m;
+        if (wide) {
+            if (o.pre) store4_as(o.pre, o.dtype, i, v);
+            if (o.act != kActNone)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = act_of(v[j], o.act);
+            if (o.res) {
+                float r[4];
+                load4_as(o.res, o.dtype, i, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += r[j];
+            }
+            store4_as(o.out, o.dtype, i, v);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < 4 && j < left; ++j) {
+                float z = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+                if (o.pre) store_as(o.pre, o.dtype, i + j, z);
+                z = act_of(z, o.act);
+                if (o.res) z += load_as(o.res, o.dtype, i + j);
+                store_as(o.out, o.dtype, i + j, z);
+            }
+        }
+    }
+    // A warp's 32 rows (8 lanes, from 4 (lane & 7) on) of `cols` columns from n of N:
+    // sums[column][32] in shared memory, four columns at a time.
     __device__ __forceinline__ void store(const float *sums, int cols, int n, int N, int lane) const {
         if (left <= 0) return;
 #pragma unroll 1
         for (int c = lane >> 3; c < cols && n + c < N; c += 4) {
             const float4 f = *(const float4 *)(sums + c * 32 + (lane & 7) * 4);
-            float v[4] = {f.x + bias[0], f.y + bias[1], f.z + bias[2], f.w + bias[3]};
-            const size_t i = (size_t)(n + c) * (size_t)o.ld + m;
-            if (wide) {
-                if (o.pre) store4_as(o.pre, o.dtype, i, v);
-                if (o.act != kActNone)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = act_of(v[j], o.act);
-                if (o.res) {
-                    float r[4];
-                    load4_as(o.res, o.dtype, i, r);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] += r[j];
-                }
-                store4_as(o.out, o.dtype, i, v);
-            } else {
-#pragma unroll 1
-                for (int j = 0; j < 4 && j < left; ++j) {
-                    float z = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
-                    if (o.pre) store_as(o.pre, o.dtype, i + j, z);
-                    z = act_of(z, o.act);
-                    if (o.res) z += load_as(o.res, o.dtype, i + j);
-                    store_as(o.out, o.dtype, i + j, z);
-                }
-            }
+            const float v[4] = {f.x, f.y, f.z, f.w};
+            column(v, n + c);
         }
     }
 };

@@ -253,11 +253,13 @@ struct DenseGemm {
     int n_products, splits;
     int *error;
 };
-// Tile columns, rows of B in one box, whether two CTAs share a tile, K splits.
+// Tile columns, rows of B in one box, whether two CTAs share a tile, K splits, an
+// estimate of its clocks.
 struct DensePlan {
     int bn, box, pair, splits;
+    double clocks;
 };
-DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm);
+DensePlan dense_plan(const DenseProduct *p, int n_products, int device, int n_sm);
 int launch_dense_few(const DenseFew &p, int n_sm, cudaStream_t st);
 int launch_dense_split(const DenseSplit &p, cudaStream_t st);
 int launch_dense_gemm(DenseGemm &g, const DensePlan &plan, int device, int n_sm, cudaStream_t st);

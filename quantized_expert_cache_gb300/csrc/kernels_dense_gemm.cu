@@ -11,10 +11,13 @@
 // descriptors name; nothing is transposed.  A thread of the epilogue has one m and
 // many n, so a warp writes 32 neighbours of the result at a time.
 //
-// The accumulators are drained every kChunk steps (512 of k) and added up in
+// The accumulators are drained every kChunk32 steps (512 of k) and added up in
 // registers, rounded to nearest: the tensor core's own fp32 accumulation truncates, a
-// bias of about 2^-24 a step on a growing sum.  Two accumulators in TMEM in turn hide
-// the drain, and the epilogue of a tile behind the next one's products.
+// bias of about 2^-24 a step on a growing sum.  For 16-bit results, whose own rounding
+// is 2^-12 and more, every kChunk16 (2048 of k): the drains' reads of TMEM hold the
+// products up (8192^3 697 us at every 8 steps, 658 at 32; 4096 x 8192 x 2048 115 and
+// 103).  Two accumulators in turn hide most of it, and the epilogue of a tile behind
+// the next one's products.
 //
 // Where there are fewer tiles than SMs, a tile's steps are shared out over a cluster
 // of CTAs and their sums joined through distributed shared memory, in order.
@@ -33,8 +36,7 @@ namespace {
 using namespace gemm;
 
 constexpr int kBM = 128, kBK = 64;    // tile rows, k of a step
-constexpr int kChunk = 8;             // steps between drains
-constexpr int kEpi = 8, kThreads = (2 + kEpi) * 32;
+constexpr int kChunk32 = 8, kChunk16 = 32;  // steps between drains
 constexpr int kWTma = 0, kWMma = 1, kWEpi = 2;
 constexpr int kMaxSplits = 8;
 
@@ -44,14 +46,16 @@ constexpr int kMaxSplits = 8;
 template <int BN, bool PAIR>
 struct Cfg {
     static constexpr int TM = PAIR ? 2 * kBM : kBM, BR = PAIR ? BN / 2 : BN;  // tile rows; rows of B to a CTA
+    static constexpr int EPI = BN >= 128 ? 16 : 8, THREADS = (2 + EPI) * 32;  // epilogue warps
+    static constexpr int NC = BN * 4 / EPI, GROUP = NC < 16 ? NC : 16;        // columns of a thread, staged at a time
     static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BR * kBK * 2, SLOT = A_BYTES + B_BYTES;
     static constexpr int STAGES = BR == 128 ? 6 : 8;
-    static constexpr int STAGING = STAGES * SLOT;      // the epilogue's: 32 x 32 sums a warp
-    static constexpr int BAR_OFF = STAGING + kEpi * 4096;
+    static constexpr int STAGING = STAGES * SLOT;      // the epilogue's: GROUP x 32 sums a warp
+    static constexpr int BAR_OFF = STAGING + EPI * GROUP * 128;
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
     static constexpr int SMEM = MISC_OFF + 16 + 1024;  // (the first 1024: alignment)
     static constexpr int COLS = 2 * BN;                // TMEM: two accumulators
-    static_assert(PAIR || BN * kBM * 4 <= STAGING, "a split tile's sums");
+    static_assert(BN * kBM * 4 <= STAGING, "a split tile's sums");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -112,13 +116,13 @@ __device__ __forceinline__ void mma_warp(uint32_t d, uint64_t a, uint64_t b, uin
 }
 // Arrival at a barrier (of both CTAs of a pair) when the lane's products are done.
 template <bool PAIR>
-__device__ __forceinline__ void commit_warp(uint32_t bar) {
+__device__ __forceinline__ void commit_warp(uint32_t bar, int ctas) {
     if (PAIR)
         asm volatile(
             "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
             "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::
                 "r"(bar),
-            "h"((unsigned short)3)
+            "h"((unsigned short)ctas)
             : "memory");
     else
         mma_commit_warp(bar);
@@ -127,12 +131,13 @@ __device__ __forceinline__ void commit_warp(uint32_t bar) {
 struct Tile {
     const DenseProduct *p;
     int m0, n0, kb, first, last;  // kb: steps of one pair of parts; [first, last): this CTA's
+    int chunk;
 };
 
 // Tiles of the products one after the other; in one, bands of 8 tiles of m run through
 // all n, so that the CTAs at work share rows of both operands in L2.
 template <int BN, bool PAIR>
-__device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int rank) {
+__device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int split) {
     Tile r;
     const int n0 = g.p[0].m_tiles * g.p[0].n_tiles;
     r.p = &g.p[t < n0 ? 0 : 1];
@@ -144,20 +149,22 @@ __device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int rank) {
     r.n0 = t / size * BN;
     r.kb = (r.p->K + kBK - 1) / kBK;
     const long long steps = (long long)r.kb * r.p->n_pairs;
-    r.first = PAIR ? 0 : (int)(steps * rank / g.splits);
-    r.last = PAIR ? (int)steps : (int)(steps * (rank + 1) / g.splits);
+    r.first = (int)(steps * split / g.splits);
+    r.last = (int)(steps * (split + 1) / g.splits);
+    r.chunk = r.p->o.dtype == 0 ? kChunk32 : kChunk16;
     return r;
 }
 
 template <int BN, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_constant__ DenseGemm g) {
+__global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel(const __grid_constant__ DenseGemm g) {
     using C = Cfg<BN, PAIR>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    // CTAs of a tile; S of them share out its steps, the two of a pair its rows
-    const int S = PAIR ? 1 : g.splits, CTAS = PAIR ? 2 : S, rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
+    // CTAs of a tile: S (pairs) share out its steps, the two of a pair its rows
+    const int S = g.splits, CTAS = PAIR ? 2 * S : S, rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
+    const int split = PAIR ? rank >> 1 : rank, side = PAIR ? rank & 1 : 0, leader = rank - side;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t slots = smem_u32(smem), bars = smem_u32(smem + C::BAR_OFF);
     const auto full = [&](int s) { return bars + 8 * s; };
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), PAIR ? 2 * kEpi : kEpi);
+            mbar_init(acc_empty(b), PAIR ? 2 * C::EPI : C::EPI);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -213,17 +220,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
             asm volatile("fence.proxy.async;" ::: "memory");
             uint32_t it = 0;
             for (int t = first_tile; t < tiles; t += tile_step) {
-                const Tile w = tile_of<BN, PAIR>(g, t, rank);
+                const Tile w = tile_of<BN, PAIR>(g, t, split);
                 int pair = w.first / w.kb, kb = w.first % w.kb;
                 for (int i = w.first; i < w.last; ++i, ++it) {
                     const int s = it % C::STAGES;
                     if (!mbar_wait(empty(s), (it / C::STAGES & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto loaded;
                     const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
                     const int parts = (int)(w.p->pairs >> (4 * pair)) & 15, k = kb * kBK;
-                    const int m0 = w.m0 + (PAIR ? rank * kBM : 0), n0 = w.n0 + (PAIR ? rank * C::BR : 0);
+                    const int m0 = w.m0 + side * kBM, n0 = w.n0 + side * C::BR;
                     // the leader's barrier counts both CTAs' bytes
-                    const uint32_t bar = PAIR ? mapped(full(s), 0) : full(s);
-                    if (!PAIR || rank == 0) mbar_arrive_tx(full(s), PAIR ? 2 * C::SLOT : C::SLOT);
+                    const uint32_t bar = PAIR ? mapped(full(s), leader) : full(s);
+                    if (side == 0) mbar_arrive_tx(full(s), PAIR ? 2 * C::SLOT : C::SLOT);
                     const auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y, int z) {
                         if (PAIR)
                             tma_load_3d_pair(dst, tm, x, y, z, bar);
@@ -258,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         __syncwarp();
     } else if (warp == kWMma) {
         uint32_t it = 0, chunk = 0;
-        for (int t = first_tile; t < tiles && (!PAIR || rank == 0); t += tile_step) {
-            const Tile w = tile_of<BN, PAIR>(g, t, rank);
+        for (int t = first_tile; t < tiles && side == 0; t += tile_step) {
+            const Tile w = tile_of<BN, PAIR>(g, t, split);
             const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
             // fp32 sums, both operands binary16 (0) or bfloat16 (1), their directions, N, M
             const uint32_t type = w.p->bf16 ? 1u : 0u;
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
             // 16 of k: 32 bytes in a row of 64 k, 16 rows of 128 bytes in the other kind
             const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
             for (int i = w.first; i < w.last; ++chunk) {
-                const int buf = chunk & 1, end = min(w.last, i + kChunk);
+                const int buf = chunk & 1, end = min(w.last, i + w.chunk);
                 if (!mbar_wait_warp(acc_empty(buf), (chunk >> 1 & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto multiplied;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
@@ -281,9 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
                     for (int q = 0; q < kBK / 16; ++q)
                         mma_warp<PAIR>(d, descriptor(a + q * a_step, a_mn, 8192), descriptor(b + q * b_step, b_mn, 8192),
                                  idesc, j > i || q > 0);
-                    commit_warp<PAIR>(empty(s));
+                    commit_warp<PAIR>(empty(s), 3 << leader);
                 }
-                commit_warp<PAIR>(acc_full(buf));
+                commit_warp<PAIR>(acc_full(buf), 3 << leader);
                 i = end;
             }
         }
@@ -291,19 +298,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         __syncwarp();
     } else {
         // lanes of TMEM: a warp reaches the quarter of its number
-        const int quarter = warp & 3, half = (warp - kWEpi) >> 2;
-        constexpr int NC = BN / 2;      // columns of a thread
+        const int quarter = warp & 3, share = (warp - kWEpi) >> 2;
+        constexpr int NC = C::NC, GROUP = C::GROUP;
         uint32_t chunk = 0;
         for (int t = first_tile; t < tiles; t += tile_step) {
-            const Tile w = tile_of<BN, PAIR>(g, t, rank);
+            const Tile w = tile_of<BN, PAIR>(g, t, split);
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-            for (int i = w.first; i < w.last; i += kChunk, ++chunk) {
+            for (int i = w.first; i < w.last; i += w.chunk, ++chunk) {
                 const int buf = chunk & 1;
                 if (!mbar_wait_warp(acc_full(buf), chunk >> 1 & 1, abort_flag, g.error, kErrorDense)) goto finished;
                 tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * NC;
+                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + share * NC;
 #pragma unroll
                 for (int c = 0; c < NC; c += 16) {
                     uint32_t v[16];
@@ -314,20 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
                 }
                 tc_fence_before();
                 if (PAIR)
-                    arrive_cluster_warp(mapped(acc_empty(buf), 0), lane);
+                    arrive_cluster_warp(mapped(acc_empty(buf), leader), lane);
                 else
                     mbar_arrive_warp(acc_empty(buf), lane);
             }
-            const int ml = quarter * 32 + lane, n0 = w.n0 + half * NC;
-            if (!PAIR && S > 1) {
+            const int ml = quarter * 32 + lane, n0 = w.n0 + share * NC;
+            if (S > 1) {
                 // (all products of the CTA are done: its stages are free)
                 float *red = (float *)smem;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) red[(half * NC + c) * kBM + ml] = acc[c];
+                for (int c = 0; c < NC; ++c) red[(share * NC + c) * kBM + ml] = acc[c];
             } else {
-                const dense::Epilogue e(w.p->o, w.p->M, w.m0 + (PAIR ? rank * kBM : 0) + quarter * 32, lane);
-                float *mine = (float *)(smem + C::STAGING) + (warp - kWEpi) * 1024;
-                constexpr int GROUP = NC < 32 ? NC : 32;
+                const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + quarter * 32 + (lane & 7) * 4);
+                float *mine = (float *)(smem + C::STAGING) + (warp - kWEpi) * GROUP * 32;
 #pragma unroll
                 for (int c = 0; c < NC; c += GROUP) {
 #pragma unroll
@@ -342,25 +348,24 @@ __global__ void __launch_bounds__(kThreads, 1) dense_gemm_kernel(const __grid_co
         __syncwarp();
     }
     __syncthreads();
-    if (!PAIR && S > 1) {
+    if (S > 1) {
         cluster.sync();
         if (!*abort_flag) {
-            const Tile w = tile_of<BN, PAIR>(g, first_tile, rank);
-            const float *red = (const float *)smem;
-            const DenseOut o = w.p->o;
-            const int M = w.p->M;
+            // a lane: four rows; a warp: a column; the CTAs of the same rows: every S-th warp
+            const Tile w = tile_of<BN, PAIR>(g, first_tile, split);
+            const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + lane * 4);
+            const float4 *red = (const float4 *)smem + lane;
             const int cols = min(BN, w.p->N - w.n0);
-            for (int i = threadIdx.x + rank * kThreads; i < cols * kBM; i += S * kThreads) {
-                float v[kMaxSplits];
+            for (int c = split * (C::THREADS / 32) + warp; c < cols; c += S * (C::THREADS / 32)) {
+                float4 v[kMaxSplits];
 #pragma unroll
                 for (int s = 0; s < kMaxSplits; ++s)
-                    if (s < S) v[s] = *cluster.map_shared_rank(red + i, s);
-                float sum = v[0];
+                    if (s < S) v[s] = *cluster.map_shared_rank(red + c * (kBM / 4), PAIR ? 2 * s + side : s);
+                float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
                 for (int s = 1; s < kMaxSplits; ++s)
-                    if (s < S) sum += v[s];
-                const int m = w.m0 + i % kBM;
-                if (m < M) dense::finish(o, m, w.n0 + i / kBM, o.bias ? o.bias[m] : 0.0f, sum);
+                    if (s < S) sum[0] += v[s].x, sum[1] += v[s].y, sum[2] += v[s].z, sum[3] += v[s].w;
+                if (e.left > 0) e.column(sum, w.n0 + c);
             }
         }
         __syncwarp();
@@ -416,10 +421,10 @@ int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
         p.n_tiles = (p.N + BN - 1) / BN;
         tiles += p.m_tiles * p.n_tiles;
     }
-    const int ctas = PAIR ? 2 : g.splits;
+    const int ctas = PAIR ? 2 * g.splits : g.splits;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(g.splits > 1 ? tiles * ctas : std::min(tiles, n_sm / ctas) * ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -432,15 +437,43 @@ int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
     return (int)cudaLaunchKernelEx(&cfg, kernel, g);
 }
 
+// Clusters of `ctas` CTAs that run at a time (a GPC's SMs that make up no whole cluster
+// stay idle: 76 of 2, 46 of 3, 36 of 4, 23 of 6 and 15 of 8 on 152 SMs).
+int clusters_at_once(int ctas, int device, int n_sm) {
+    if (ctas == 1) return n_sm;
+    static std::atomic<int> known[64][kMaxSplits + 1];  // 0: not asked yet
+    std::atomic<int> &n = known[device & 63][ctas];
+    if (n.load() == 0) {
+        using C = Cfg<256, true>;  // (one CTA of any tile fills an SM)
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int most = 0;
+        if (cudaFuncSetAttribute(dense_gemm_kernel<256, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&most, dense_gemm_kernel<256, true>, &cfg) != cudaSuccess || most < 1) {
+            cudaGetLastError();
+            most = std::max(1, n_sm / ctas / 2);
+        }
+        n.store(most);
+    }
+    return n.load();
+}
+
 }  // namespace
 
 // The cheapest of the tiles and K splits, by the clocks of the longest CTA (for two
-// products the larger of the longest tile and an even share of all).
-DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm) {
+// products at once the larger of the longest tile and an even share of all).
+DensePlan dense_plan(const DenseProduct *p, int n_products, int device, int n_sm) {
     DensePlan best{};
-    double least = 1e30;
     for (const Shape &f : kShapes) {
-        const int tm = f.pair ? 2 * kBM : kBM, workers = f.pair ? n_sm / 2 : n_sm;
+        const int tm = f.pair ? 2 * kBM : kBM;
         bool fits = true;
         long long tiles = 0, work = 0, longest = 0, fewest = 1ll << 40;
         for (int i = 0; i < n_products; ++i) {
@@ -452,17 +485,16 @@ DensePlan dense_plan(const DenseProduct *p, int n_products, int n_sm) {
             fewest = std::min(fewest, s);
         }
         if (!fits) continue;
-        for (int s = 1; s <= (f.pair ? 1 : kMaxSplits); ++s) {
-            if (s > 1 && (tiles * s > workers || s > fewest)) break;
+        for (int s = 1; s <= (f.pair ? kMaxSplits / 2 : kMaxSplits); ++s) {
+            if (s > 1 && (n_products > 1 || s > fewest)) break;
+            const int workers = clusters_at_once(f.pair ? 2 * s : s, device, n_sm);
             const long long rounds = (tiles + workers - 1) / workers;
-            const double steps = s > 1            ? (double)((longest + s - 1) / s)
-                                 : n_products == 1 ? (double)(rounds * longest)
-                                                   : std::max((double)longest, (double)((work + workers - 1) / workers));
-            const double c = steps * f.clocks + (s > 1 ? 2500 + 12 * f.bn : 12 * f.bn);
-            if (c < least) {
-                least = c;
-                best = {f.bn, f.pair ? f.bn / 2 : f.bn, f.pair, s};
-            }
+            if (s > 1 && rounds > 1) break;
+            const double steps = n_products == 1
+                                     ? (double)(rounds * ((longest + s - 1) / s))
+                                     : std::max((double)longest, (double)((work + workers - 1) / workers));
+            const double c = steps * f.clocks + (s > 1 ? 2500 + 20 * f.bn : 12 * f.bn);
+            if (best.splits == 0 || c < best.clocks) best = {f.bn, f.pair ? f.bn / 2 : f.bn, f.pair, s, c};
         }
     }
     return best;

@@ -138,10 +138,8 @@ void dense_pairs(moe::DenseProduct &p, int a_parts, int b_parts) {
                 p.pairs |= (unsigned)(a | (sum - a) << 2) << (4 * p.n_pairs++);
 }
 
-int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b, const moe::OpContext &c,
-                 cudaStream_t st, const char *what) {
-    for (int i = 0; i < g.n_products; ++i) dense_pairs(g.p[i], a[i].parts, b[i].parts);
-    const moe::DensePlan plan = moe::dense_plan(g.p, g.n_products, c.n_sm);
+int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b,
+                 const moe::DensePlan &plan, const moe::OpContext &c, cudaStream_t st, const char *what) {
     g.splits = plan.splits;
     g.error = c.error;
     for (int i = 0; i < g.n_products; ++i) {
@@ -154,6 +152,24 @@ int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const De
         if (rd) return rd;
     }
     return launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
+}
+
+// The products of a call, two of them in one launch (their tiles fill the SMs
+// together) or in two (each with its own tiles and K splits), as the plans have it.
+int dense_products(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b,
+                   const moe::OpContext &c, cudaStream_t st, const char *what) {
+    for (int i = 0; i < g.n_products; ++i) dense_pairs(g.p[i], a[i].parts, b[i].parts);
+    const moe::DensePlan all = moe::dense_plan(g.p, g.n_products, c.device, c.n_sm);
+    if (g.n_products == 1) return dense_launch(ctx, g, a, b, all, c, st, what);
+    const moe::DensePlan one = moe::dense_plan(g.p, 1, c.device, c.n_sm),
+                         two = moe::dense_plan(g.p + 1, 1, c.device, c.n_sm);
+    constexpr double kLaunch = 5000;  // clocks
+    if (all.clocks <= one.clocks + two.clocks + kLaunch) return dense_launch(ctx, g, a, b, all, c, st, what);
+    g.n_products = 1;
+    const int rc = dense_launch(ctx, g, a, b, one, c, st, what);
+    if (rc) return rc;
+    g.p[0] = g.p[1];
+    return dense_launch(ctx, g, a + 1, b + 1, two, c, st, what);
 }
 
 }  // namespace
@@ -297,7 +313,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
     g.p[0].K = cols;
     g.p[0].bf16 = w_dtype == MOE_BF16;
     g.p[0].o = out;
-    return dense_launch(ctx, g, &w, &x, c, st, "dense");
+    return dense_products(ctx, g, &w, &x, c, st, "dense");
 }
 
 int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_w, int w_dtype, const void *d_dy,
@@ -408,7 +424,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         g.p[i].bf16 = w_dtype == MOE_BF16;
         g.p[i].o.ld = cols;
     }
-    return dense_launch(ctx, g, a, b, c, st, "dense_backward");
+    return dense_products(ctx, g, a, b, c, st, "dense_backward");
 }
 
 }  // extern "C"
