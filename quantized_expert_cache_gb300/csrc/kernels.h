@@ -239,7 +239,7 @@ struct DenseSplit {
 int dense_sum_blocks(int n_tokens);
 // One product D[m][n] = sum over pairs of parts and over k of A[m][k] B[n][k].
 struct DenseProduct {
-    CUtensorMap tm_a, tm_b;     // [part][outer][inner], boxes of 64 x 64 (x 128 rows, x tile columns: k inner)
+    CUtensorMap tm_a, tm_b;     // [part][outer][inner], boxes of 64 x 128 (B with k inner: x box rows)
     int M, N, K;
     int a_mn, b_mn;             // 1: stored [k][m] or [k][n]; 0: [m][k], [n][k]
     int bf16;                   // operands: 1 bfloat16, 0 binary16

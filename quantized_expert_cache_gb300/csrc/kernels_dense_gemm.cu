@@ -6,17 +6,16 @@
 //   input:    m = columns, n = tokens, k = rows of W:  A = W [k][m],  B = dz [n][k]
 //   weights:  m = columns, n = rows of W, k = tokens:  A = x [k][m],  B = dz [k][n]
 //
-// An operand is read as it lies in memory: one whose k is contiguous as rows of 64 k,
-// the other kind as rows of 64 m (or n), both in the 128-byte swizzle that the MMA's
-// descriptors name; nothing is transposed.  A thread of the epilogue has one m and
+// An operand is read as it lies in memory: one whose k is contiguous as rows of 64 k
+// (two blocks to a step), the other kind as rows of 64 m (or n), both in the 128-byte
+// swizzle that the MMA's descriptors name; nothing is transposed.  A thread of the epilogue has one m and
 // many n, so a warp writes 32 neighbours of the result at a time.
 //
-// The accumulators are drained every kChunk32 steps (512 of k) and added up in
+// The accumulators are drained every 512 of k (kChunk32) and added up in
 // registers, rounded to nearest: the tensor core's own fp32 accumulation truncates, a
 // bias of about 2^-24 a step on a growing sum.  For 16-bit results, whose own rounding
-// is 2^-12 and more, every kChunk16 (2048 of k): the drains' reads of TMEM hold the
-// products up (8192^3 697 us at every 8 steps, 658 at 32; 4096 x 8192 x 2048 115 and
-// 103).  Two accumulators in turn hide most of it, and the epilogue of a tile behind
+// is 2^-12 and more, every 2048 (kChunk16): the drains' reads of TMEM hold the
+// products up (8192^3 697 us and 658, 4096 x 8192 x 2048 115 and 103).  Two accumulators in turn hide most of it, and the epilogue of a tile behind
 // the next one's products.
 //
 // Where there are fewer tiles than SMs, a tile's steps are shared out over a cluster
@@ -35,10 +34,14 @@ namespace {
 
 using namespace gemm;
 
-constexpr int kBM = 128, kBK = 64;    // tile rows, k of a step
-constexpr int kChunk32 = 8, kChunk16 = 32;  // steps between drains
+// Tile rows of a CTA, k of a step.  (A step's barriers, copies and commit cost the
+// issuing threads about 500 clocks: with 64 of k, whose products take 512, 8192^3 took
+// 638 us.)
+constexpr int kBM = 128, kBK = 128;
+constexpr int kChunk32 = 4, kChunk16 = 16;  // steps between drains
 constexpr int kWTma = 0, kWMma = 1, kWEpi = 2;
 constexpr int kMaxSplits = 8;
+constexpr int kChunkMn = kBK * 128;   // bytes of a step's rows of 64 m (n)
 
 // Tiles of 128 x BN to a CTA, or (PAIR) of 256 x BN to the two CTAs of a cluster: each
 // has half of A's rows, half of B's and half of the result's, and the leader (rank 0)
@@ -49,7 +52,7 @@ struct Cfg {
     static constexpr int EPI = BN >= 128 ? 16 : 8, THREADS = (2 + EPI) * 32;  // epilogue warps
     static constexpr int NC = BN * 4 / EPI, GROUP = NC < 16 ? NC : 16;        // columns of a thread, staged at a time
     static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BR * kBK * 2, SLOT = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BR == 128 ? 6 : 8;
+    static constexpr int STAGES = BR == 128 ? 3 : BR == 64 ? 4 : 5;
     static constexpr int STAGING = STAGES * SLOT;      // the epilogue's: GROUP x 32 sums a warp
     static constexpr int BAR_OFF = STAGING + EPI * GROUP * 128;
     static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 4) * 8;
@@ -218,42 +221,51 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
         if (lane == 0) {
             // (parts that the kernel before wrote are read by the copies' proxy)
             asm volatile("fence.proxy.async;" ::: "memory");
-            uint32_t it = 0;
+            // the leader's barriers count both CTAs' bytes
+            const uint32_t full_at = PAIR ? mapped(full(0), leader) : full(0);
+            uint32_t it = 0, slot = 0, phase = 0;
             for (int t = first_tile; t < tiles; t += tile_step) {
                 const Tile w = tile_of<BN, PAIR>(g, t, split);
-                int pair = w.first / w.kb, kb = w.first % w.kb;
+                // (what a step needs in registers: a load of the parameters costs each step more
+                // than its copies' issue)
+                const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
+                const CUtensorMap *tm_a = &w.p->tm_a, *tm_b = &w.p->tm_b;
+                const int m0 = w.m0 + side * kBM, n0 = w.n0 + side * C::BR, k_end = w.kb * kBK;
+                int k = w.first % w.kb * kBK;
+                unsigned pairs = w.p->pairs >> (4 * (w.first / w.kb));
                 for (int i = w.first; i < w.last; ++i, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!mbar_wait(empty(s), (it / C::STAGES & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto loaded;
-                    const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
-                    const int parts = (int)(w.p->pairs >> (4 * pair)) & 15, k = kb * kBK;
-                    const int m0 = w.m0 + side * kBM, n0 = w.n0 + side * C::BR;
-                    // the leader's barrier counts both CTAs' bytes
-                    const uint32_t bar = PAIR ? mapped(full(s), leader) : full(s);
-                    if (side == 0) mbar_arrive_tx(full(s), PAIR ? 2 * C::SLOT : C::SLOT);
+                    if (!mbar_wait(empty(slot), phase ^ 1, abort_flag, g.error, kErrorDense)) goto loaded;
+                    const uint32_t a = slots + slot * C::SLOT, b = a + C::A_BYTES, bar = full_at + 8 * slot;
+                    const int part_a = pairs & 3, part_b = pairs >> 2 & 3;
+                    if (side == 0) mbar_arrive_tx(full(slot), PAIR ? 2 * C::SLOT : C::SLOT);
                     const auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y, int z) {
                         if (PAIR)
                             tma_load_3d_pair(dst, tm, x, y, z, bar);
                         else
                             tma_load_3d(dst, tm, x, y, z, bar);
                     };
-                    if (w.p->a_mn) {
-#pragma unroll
-                        for (int c = 0; c < kBM / 64; ++c)
-                            load(a + c * 8192, &w.p->tm_a, m0 + 64 * c, k, parts & 3);
+                    if (a_mn) {
+                        load(a, tm_a, m0, k, part_a);
+                        load(a + C::A_BYTES / 2, tm_a, m0 + 64, k, part_a);
                     } else {
-                        load(a, &w.p->tm_a, k, m0, parts & 3);
+                        load(a, tm_a, k, m0, part_a);
+                        load(a + C::A_BYTES / 2, tm_a, k + 64, m0, part_a);
                     }
-                    if (C::BR >= 64 && w.p->b_mn) {
+                    if (C::BR >= 64 && b_mn) {
 #pragma unroll
-                        for (int c = 0; c < C::BR / 64; ++c)
-                            load(b + c * 8192, &w.p->tm_b, n0 + 64 * c, k, parts >> 2);
+                        for (int c = 0; c < C::BR / 64; ++c) load(b + c * kChunkMn, tm_b, n0 + 64 * c, k, part_b);
                     } else {
-                        load(b, &w.p->tm_b, k, n0, parts >> 2);
+                        load(b, tm_b, k, n0, part_b);
+                        load(b + C::B_BYTES / 2, tm_b, k + 64, n0, part_b);
                     }
-                    if (++kb == w.kb) {
-                        kb = 0;
-                        ++pair;
+                    k += kBK;
+                    if (k == k_end) {
+                        k = 0;
+                        pairs >>= 4;
+                    }
+                    if (++slot == C::STAGES) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
             }
@@ -264,7 +276,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
         }
         __syncwarp();
     } else if (warp == kWMma) {
-        uint32_t it = 0, chunk = 0;
+        uint32_t slot = 0, phase = 0, chunk = 0;
         for (int t = first_tile; t < tiles && side == 0; t += tile_step) {
             const Tile w = tile_of<BN, PAIR>(g, t, split);
             const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
@@ -272,26 +284,34 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             const uint32_t type = w.p->bf16 ? 1u : 0u;
             const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) |
                                    (uint32_t)(BN >> 3) << 17 | (uint32_t)(C::TM >> 4) << 24;
-            // 16 of k: 32 bytes in a row of 64 k, 16 rows of 128 bytes in the other kind
-            const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+            const uint64_t a0 = descriptor(slots, a_mn, kChunkMn), b0 = descriptor(slots + C::A_BYTES, b_mn, kChunkMn);
+            // 16 of k: 32 bytes in a row of 64 k (and the second block), 16 rows of 128 bytes
+            // in the other kind
+            const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, a_half = (a_mn ? 8192 : C::A_BYTES / 2) >> 4;
+            const uint32_t b_step = (b_mn ? 2048 : 32) >> 4, b_half = (b_mn ? 8192 : C::B_BYTES / 2) >> 4;
             for (int i = w.first; i < w.last; ++chunk) {
                 const int buf = chunk & 1, end = min(w.last, i + w.chunk);
                 if (!mbar_wait_warp(acc_empty(buf), (chunk >> 1 & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto multiplied;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
-                for (int j = i; j < end; ++j, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!mbar_wait_warp(full(s), it / C::STAGES & 1, abort_flag, g.error, kErrorDense)) goto multiplied;
+                uint32_t more = 0;
+                for (; i < end; ++i) {
+                    if (!mbar_wait_warp(full(slot), phase, abort_flag, g.error, kErrorDense)) goto multiplied;
                     tc_fence_after();
-                    const uint32_t a = slots + s * C::SLOT, b = a + C::A_BYTES;
+                    const uint32_t at = slot * (C::SLOT >> 4);
 #pragma unroll
-                    for (int q = 0; q < kBK / 16; ++q)
-                        mma_warp<PAIR>(d, descriptor(a + q * a_step, a_mn, 8192), descriptor(b + q * b_step, b_mn, 8192),
-                                 idesc, j > i || q > 0);
-                    commit_warp<PAIR>(empty(s), 3 << leader);
+                    for (int q = 0; q < kBK / 16; ++q) {
+                        mma_warp<PAIR>(d, a0 + at + q % 4 * a_step + q / 4 * a_half,
+                                       b0 + at + q % 4 * b_step + q / 4 * b_half, idesc, more);
+                        more = 1;
+                    }
+                    commit_warp<PAIR>(empty(slot), 3 << leader);
+                    if (++slot == C::STAGES) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
                 commit_warp<PAIR>(acc_full(buf), 3 << leader);
-                i = end;
             }
         }
     multiplied:;
@@ -402,7 +422,8 @@ struct Shape {
     bool pair;
     double clocks;
 };
-constexpr Shape kShapes[] = {{256, true, 560}, {128, true, 420}, {128, false, 640}, {64, false, 480}, {32, false, 420}};
+constexpr Shape kShapes[] = {
+    {256, true, 1120}, {128, true, 840}, {128, false, 1280}, {64, false, 960}, {32, false, 840}};
 
 template <int BN, bool PAIR>
 int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {

@@ -145,10 +145,10 @@ int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const De
     for (int i = 0; i < g.n_products; ++i) {
         moe::DenseProduct &p = g.p[i];
         const int rc = encode_map(ctx, &p.tm_a, a[i].base, p.bf16, a[i].inner, a[i].outer, a[i].ld, a[i].parts,
-                                  p.a_mn ? 64 : 128);
+                                  128);
         if (rc) return rc;
         const int rd = encode_map(ctx, &p.tm_b, b[i].base, p.bf16, b[i].inner, b[i].outer, b[i].ld, b[i].parts,
-                                  p.b_mn ? 64 : (uint32_t)plan.box);
+                                  p.b_mn ? 128 : (uint32_t)plan.box);
         if (rd) return rd;
     }
     return launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
