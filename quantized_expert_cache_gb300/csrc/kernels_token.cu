@@ -65,6 +65,22 @@ struct alignas(16) Pack16 {
     T v[N];
 };
 
+// 16-bit values rounded in pairs: one by one, the conversions share the special-function
+// unit with the exponentials.
+__device__ __forceinline__ Pack16<float> packed(const float *v, float) { return Pack16<float>{v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ Pack16<__half> packed(const float *v, __half) {
+    Pack16<__half> o;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) *(__half2 *)&o.v[j] = __floats2half2_rn(v[j], v[j + 1]);
+    return o;
+}
+__device__ __forceinline__ Pack16<__nv_bfloat16> packed(const float *v, __nv_bfloat16) {
+    Pack16<__nv_bfloat16> o;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) *(__nv_bfloat162 *)&o.v[j] = __floats2bfloat162_rn(v[j], v[j + 1]);
+    return o;
+}
+
 // 2^x for x <= 0 by the special-function unit; NaN stays.
 __device__ __forceinline__ float exp2_neg(float x) {
     float r;
@@ -109,25 +125,22 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b, float c) {
     return Sums{m, a.s + b.s, a.n + b.n, a.t + b.t};
 }
 
-// A row as packs of 16 bytes from the boundary at or below its first element:
-// element j of pack i is the row's element i N + j - head.
+// A row: `head` elements up to the first 16-byte boundary, `packs` packs of 16 bytes,
+// the rest.  Elements outside the packs (fewer than 32) are a lane each.
 template <typename T>
 struct Row {
+    static constexpr int N = 16 / (int)sizeof(T);
     const T *x;
-    int head, vocab;
-    __device__ __forceinline__ Row(const void *logits, size_t row, int vocab_)
-        : x((const T *)logits + row * (size_t)vocab_), vocab(vocab_) {
-        head = (int)(((uintptr_t)x & 15) / sizeof(T));
+    int head, packs, edge;
+    __device__ __forceinline__ Row(const void *logits, size_t row, int vocab)
+        : x((const T *)logits + row * (size_t)vocab) {
+        head = min(vocab, (int)((16 - ((uintptr_t)x & 15)) % 16 / sizeof(T)));
+        packs = (vocab - head) / N;
+        edge = vocab - packs * N;
     }
-    __device__ __forceinline__ Pack16<T> load(int pack) const {
-        constexpr int N = Pack16<T>::N;
-        const int e = pack * N - head;
-        if (e >= 0 && e + N <= vocab) return *(const Pack16<T> *)(x + e);
-        Pack16<T> p;
-#pragma unroll
-        for (int j = 0; j < N; ++j) p.v[j] = e + j >= 0 && e + j < vocab ? x[e + j] : rounded<T>(-kInf);
-        return p;
-    }
+    __device__ __forceinline__ Pack16<T> load(int pack) const { return *(const Pack16<T> *)(x + head + pack * N); }
+    // the index of edge element i
+    __device__ __forceinline__ int edge_at(int i) const { return i < head ? i : i + packs * N; }
 };
 
 // Two sorted lists (largest in lane 0) -> the 32 largest of both, sorted.
@@ -167,11 +180,33 @@ __device__ __forceinline__ unsigned long long merge_warps(unsigned long long (*l
     return list;
 }
 
+// A list of 32 keys over the lanes, largest in lane 0; only the first n_top are wanted.
+struct List {
+    unsigned long long mine = 0, last = 0;  // last: the n_top-th
+    // one candidate a lane (0: none)
+    __device__ __forceinline__ void insert(unsigned long long cand, int n_top, int lane) {
+        unsigned who = __ballot_sync(0xffffffffu, cand > last);
+        while (who) {
+            const unsigned long long one = __shfl_sync(0xffffffffu, cand, __ffs(who) - 1);
+            who &= who - 1;
+            if (one > last) {
+                const int at = __popc(__ballot_sync(0xffffffffu, mine > one));
+                const unsigned long long up = __shfl_up_sync(0xffffffffu, mine, 1);
+                mine = lane < at ? mine : lane == at ? one : up;
+                last = __shfl_sync(0xffffffffu, mine, n_top - 1);
+            }
+        }
+    }
+};
+__device__ __forceinline__ unsigned long long candidate(float x, int index) {
+    return (unsigned long long)order_of(x) << 32 | (0xffffffffu - (unsigned)index);
+}
+
 struct TokenShared {
     Sums part[kTokenWarps];           // of the warps
     Sums cta;
     unsigned unit[kUnits];            // the maxima of this CTA's units
-    unsigned all[kUnits];             // of all CTAs'
+    alignas(16) unsigned all[kUnits];  // of all CTAs'
     unsigned long long list[kTokenWarps][kList], joint[kTokenWarps][kList];
     int flagged[kUnits];
     int n_flagged;
@@ -190,8 +225,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t row = blockIdx.x / C;
     const Row<T> r(p.logits, row, p.vocab);
-    const int packs = (r.head + p.vocab + N - 1) / N;
-    const int units = (packs + (TILE << shift) - 1) / (TILE << shift);
+    const int units = (r.packs + (TILE << shift) - 1) / (TILE << shift);
     const int u0 = min(units, rank * units_cta), u1 = min(units, u0 + units_cta);
     const float c = p.scale * kLog2e;
 
@@ -209,16 +243,55 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
 
     // ---- the pass: tiles in turn, the next one's loads in flight
     Sums a{-kInf, 0.0f, 0.0f, 0.0f};
+    // Sums of K elements a lane, `high` the largest of the warp's.
+    const auto add = [&](const float *x, int K, float high) {
+        if (high > a.m) {
+            if (a.m != -kInf) lower(a, c * (a.m - high));
+            a.m = high;
+        }
+        // (all -infinity so far: relative to 0 they stay it)
+        const float m = a.m == -kInf ? 0.0f : a.m;
+        if (high < a.m) {
+#pragma unroll
+            for (int e = 0; e < K; ++e) {
+                const float u = bounded((x[e] - m) * c), f = exp2_neg(u);
+                a.s += f;
+                a.t = fmaf(f, u, a.t);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < K; ++e) {
+                const float u = bounded((x[e] - m) * c), f = exp2_neg(u);
+                const bool is_max = u == 0.0f;
+                a.n += is_max ? 1.0f : 0.0f;
+                a.s += is_max ? 0.0f : f;
+                a.t = fmaf(f, u, a.t);
+            }
+        }
+    };
+    const bool edges = rank == 0 && warp == 0 && r.edge > 0;
+    if (edges) {
+        const float x = lane < r.edge ? value<T>(r.x[r.edge_at(lane)]) : -kInf;
+        add(&x, 1, of_order(__reduce_max_sync(0xffffffffu, order_of(fmaxf(x, -kInf)))));
+    }
     const int mine = u0 + warp < u1 ? (u1 - u0 - warp + kTokenWarps - 1) / kTokenWarps : 0;
     const int tiles = mine << shift;
-    auto tile_pack = [&](int i) {
+    const auto tile_pack = [&](int i) {
         const int unit = u0 + warp + (i >> shift) * kTokenWarps;
         return ((unit << shift) + (i & ((1 << shift) - 1))) * TILE + lane;
     };
-    Pack16<T> next[U];
-    if (tiles > 0)
+    Pack16<T> none16;
 #pragma unroll
-        for (int k = 0; k < U; ++k) next[k] = r.load(tile_pack(0) + 32 * k);
+    for (int j = 0; j < N; ++j) none16.v[j] = rounded<T>(-kInf);
+    const auto tile_load = [&](Pack16<T> *v, int at) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            v[k] = none16;
+            if (at + 32 * k < r.packs) v[k] = r.load(at + 32 * k);
+        }
+    };
+    Pack16<T> next[U];
+    if (tiles > 0) tile_load(next, tile_pack(0));
     unsigned top = 0;
     for (int i = 0; i < tiles; ++i) {
         float x[U * N];
@@ -230,41 +303,14 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
                 x[k * N + j] = value<T>(next[k].v[j]);
                 high = fmaxf(high, x[k * N + j]);
             }
-        if (i + 1 < tiles) {
-            const int at = tile_pack(i + 1);
-#pragma unroll
-            for (int k = 0; k < U; ++k) next[k] = r.load(at + 32 * k);
-        }
+        if (i + 1 < tiles) tile_load(next, tile_pack(i + 1));
         const unsigned key = __reduce_max_sync(0xffffffffu, order_of(high));
-        const float tm = of_order(key);
         top = max(top, key);
         if ((i & ((1 << shift) - 1)) == (1 << shift) - 1) {
             if (lane == 0) sh.unit[warp + (i >> shift) * kTokenWarps] = top;
             top = 0;
         }
-        if (tm > a.m) {
-            if (a.m != -kInf) lower(a, c * (a.m - tm));
-            a.m = tm;
-        }
-        // (all -infinity so far: relative to 0 they stay it)
-        const float m = a.m == -kInf ? 0.0f : a.m;
-        if (tm < a.m) {
-#pragma unroll
-            for (int e = 0; e < U * N; ++e) {
-                const float u = bounded((x[e] - m) * c), f = exp2_neg(u);
-                a.s += f;
-                a.t = fmaf(f, u, a.t);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < U * N; ++e) {
-                const float u = bounded((x[e] - m) * c), f = exp2_neg(u);
-                const bool is_max = u == 0.0f;
-                a.n += is_max ? 1.0f : 0.0f;
-                a.s += is_max ? 0.0f : f;
-                a.t = fmaf(f, u, a.t);
-            }
-        }
+        add(x, U * N, of_order(key));
     }
     a.s = warp_sum_f(a.s);
     a.n = warp_sum_f(a.n);
@@ -293,9 +339,13 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
         if (units > p.n_top) {
             // the maximum with n_top - 1 before it bounds the n largest from below
             int before = 0;
-            for (int j = 0; j < units; ++j) {
-                const unsigned k = sh.all[j];
-                before += k > mine_key || (k == mine_key && j < t) ? 1 : 0;
+            for (int j = 0; j < units; j += 4) {
+                // (units past the last are 0, before none)
+                const uint4 k = *(const uint4 *)(sh.all + j);
+                before += (k.x > mine_key || (k.x == mine_key && j < t) ? 1 : 0) +
+                          (k.y > mine_key || (k.y == mine_key && j + 1 < t) ? 1 : 0) +
+                          (k.z > mine_key || (k.z == mine_key && j + 2 < t) ? 1 : 0) +
+                          (k.w > mine_key || (k.w == mine_key && j + 3 < t) ? 1 : 0);
             }
             if (t < units && before == p.n_top - 1) sh.bound = mine_key;
             __syncthreads();
@@ -303,56 +353,44 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
         const unsigned bound = sh.bound;
         if (t >= u0 && t < u1 && mine_key >= bound) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = t;
         __syncthreads();
-        unsigned long long list = 0, last = 0;  // last: the n_top-th entry
+        List list;
+        if (edges) {
+            const int e = r.edge_at(lane);
+            list.insert(lane < r.edge ? candidate(value<T>(r.x[e]), e) : 0, p.n_top, lane);
+        }
         const int n_flagged = sh.n_flagged;
         for (int f = warp; f < n_flagged; f += kTokenWarps) {
             const int first = (sh.flagged[f] << shift) * TILE;
             for (int i = first; i < first + (TILE << shift); i += TILE) {
                 Pack16<T> v[U];
-#pragma unroll
-                for (int k = 0; k < U; ++k) v[k] = r.load(i + 32 * k + lane);
+                tile_load(v, i + lane);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const int e0 = (i + 32 * k + lane) * N - r.head;
-                    float high = value<T>(v[k].v[0]);
-                    bool nan = high != high;
+                    // (a NaN's key is above all others; one past the packs is no candidate)
+                    unsigned high = 0;
 #pragma unroll
-                    for (int j = 1; j < N; ++j) {
-                        const float y = value<T>(v[k].v[j]);
-                        high = fmaxf(high, y);
-                        nan |= y != y;
-                    }
-                    if (!__any_sync(0xffffffffu, nan || order_of(high) >= bound)) continue;
-#pragma unroll
+                    for (int j = 0; j < N; ++j) high = max(high, order_of(value<T>(v[k].v[j])));
+                    const int at = i + 32 * k + lane;
+                    const bool any = at < r.packs && high >= bound;
+                    if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll 1
                     for (int j = 0; j < N; ++j) {
-                        const int e = e0 + j;
-                        const unsigned key = order_of(value<T>(v[k].v[j]));
-                        unsigned long long cand = 0;
-                        if (e >= 0 && e < p.vocab && key >= bound)
-                            cand = (unsigned long long)key << 32 | (0xffffffffu - (unsigned)e);
-                        unsigned who = __ballot_sync(0xffffffffu, cand > last);
-                        while (who) {
-                            const unsigned long long one = __shfl_sync(0xffffffffu, cand, __ffs(who) - 1);
-                            who &= who - 1;
-                            if (one > last) {
-                                const int at = __popc(__ballot_sync(0xffffffffu, list > one));
-                                const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
-                                list = lane < at ? list : lane == at ? one : up;
-                                last = __shfl_sync(0xffffffffu, list, p.n_top - 1);
-                            }
-                        }
+                        float y = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < N; ++q)
+                            if (q == j) y = value<T>(v[k].v[q]);
+                        list.insert(any && order_of(y) >= bound ? candidate(y, r.head + at * N + j) : 0, p.n_top, lane);
                     }
                 }
             }
         }
-        list = merge_warps(sh.list, list, warp, lane);
+        best = merge_warps(sh.list, list.mine, warp, lane);
         if (C > 1) {
             cluster.sync();
             if (rank == 0)  // (C <= kTokenWarps: a warp takes a CTA's list)
-                list = merge_warps(sh.joint, warp < C ? cluster.map_shared_rank(sh.list[0], warp)[lane] : 0, warp,
+                best = merge_warps(sh.joint, warp < C ? cluster.map_shared_rank(sh.list[0], warp)[lane] : 0, warp,
                                    lane);
         }
-        best = list;
     }
     // ---- results
     if (rank == 0 && warp == 0) {
@@ -386,52 +424,83 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
 }
 
 // ---- gradient: one read, one write, a row's scalars in every thread --------------
-// CTAs take `step` packs of a row each.  Results go where the logits were, to the
-// same thread, when the two buffers are one.
+struct GradRow {
+    float top, log_sum, scale, by_log, by_one;
+    bool none;  // nothing but -infinity: zero
+    // -p (by_log log p + by_one): all of a logit's gradient but a target's own term.
+    __device__ __forceinline__ float of(float x) const {
+        const float lp = fmaf(x - top, scale, -log_sum);
+        // (where p is 0 the clamped factor stays finite)
+        const float d = -exp2_neg(lp * kLog2e) * fmaf(by_log, fmaxf(lp, -150.0f), by_one);
+        return none ? 0.0f : d;
+    }
+};
+
+// A CTA takes kThreads x kTokenGradPacks packs of a row, all loads of a thread in flight
+// together.  Results go where the logits were, to the same thread, when the two buffers
+// are one.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenGradParams p, int chunks, bool same_align) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int N = Pack16<T>::N;
+    constexpr int N = Pack16<T>::N, PACKS = kTokenGradPacks, SPAN = kThreads * PACKS;
     const size_t row = blockIdx.x / chunks;
     const Row<T> r(p.logits, row, p.vocab);
     T *dx = (T *)p.dlogits + row * (size_t)p.vocab;
-    const int first = (int)(blockIdx.x % chunks) * (kThreads * kTokenGradPacks) + threadIdx.x;
-    Pack16<T> v[kTokenGradPacks];
+    // packs from the boundary at or below the row's first element
+    const int before = (int)(((uintptr_t)r.x & 15) / sizeof(T));
+    const int pack0 = (int)(blockIdx.x % chunks) * SPAN, e0 = (pack0 + (int)threadIdx.x) * N - before;
+    const auto whole = [&](int e) { return same_align && e >= 0 && e + N <= p.vocab; };
+    Pack16<T> v[PACKS];
 #pragma unroll
-    for (int k = 0; k < kTokenGradPacks; ++k) v[k] = r.load(first + kThreads * k);
+    for (int k = 0; k < PACKS; ++k)
+        if (whole(e0 + k * kThreads * N)) v[k] = *(const Pack16<T> *)(r.x + e0 + k * kThreads * N);
     int target = p.targets ? p.targets[row] : -1;
     if (target >= p.vocab) {
         if (threadIdx.x == 0) atomicOr(p.error, kErrorToken);
         target = -1;
     }
-    const float top = p.stats[2 * row], log_sum = p.stats[2 * row + 1];
+    GradRow w;
+    w.top = p.stats[2 * row];
+    w.log_sum = p.stats[2 * row + 1];
+    w.scale = p.scale;
+    w.none = w.top == -kInf && w.log_sum == 0.0f;
     const float g = p.g_logp && target >= 0 ? p.g_logp[row] : 0.0f;
     const float gh = p.g_entropy ? p.g_entropy[row] : 0.0f, h = p.g_entropy ? p.entropy[row] : 0.0f;
-    const bool none = top == -kInf && log_sum == 0.0f;
+    w.by_log = gh * p.scale;
+    w.by_one = fmaf(gh, h, g) * p.scale;
+    // the thread that has the target's pack: g (1 - p) by expm1, so that a likely target's
+    // keeps its digits (read before the pack is stored over it)
+    const int at = target < 0 ? -1 : (target + before) / N - pack0;
+    const bool mine = at >= 0 && at < SPAN && at % kThreads == (int)threadIdx.x;
+    float d_target = 0.0f;
+    if (mine) {
+        const float lp = fmaf(value<T>(r.x[target]) - w.top, p.scale, -w.log_sum);
+        d_target = -p.scale * fmaf(exp2_neg(lp * kLog2e) * gh, fmaxf(lp, -150.0f) + h, g * expm1f(lp));
+    }
+    bool edge = false;
 #pragma unroll
-    for (int k = 0; k < kTokenGradPacks; ++k) {
-        const int e = (first + kThreads * k) * N - r.head;
-        if (e + N <= 0 || e >= p.vocab) continue;
-        Pack16<T> o;
+    for (int k = 0; k < PACKS; ++k) {
+        const int e = e0 + k * kThreads * N;
+        if (whole(e)) {
+            float d[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float lp = (value<T>(v[k].v[j]) - top) * p.scale - log_sum;
-            const float q = exp2_neg(bounded(lp * kLog2e));
-            // (where q is 0 the clamped factor stays finite)
-            float d = -q * gh * (fmaxf(lp, -150.0f) + h);
-            // g (1 - p): a likely target's keeps its digits
-            d += e + j == target ? -g * expm1f(lp) : -q * g;
-            o.v[j] = rounded<T>(none ? 0.0f : d * p.scale);
-        }
-        if (same_align && e >= 0 && e + N <= p.vocab) {
-            *(Pack16<T> *)(dx + e) = o;
+            for (int j = 0; j < N; ++j) d[j] = w.of(value<T>(v[k].v[j]));
+            *(Pack16<T> *)(dx + e) = packed(d, T());
         } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (e + j >= 0 && e + j < p.vocab) dx[e + j] = o.v[j];
+            edge |= e + N > 0 && e < p.vocab;
         }
     }
+    // a row's first and last pack, and rows whose gradients lie otherwise than the logits
+    if (edge)
+#pragma unroll 1
+        for (int k = 0; k < PACKS; ++k) {
+            const int e = e0 + k * kThreads * N;
+            if (!whole(e))
+#pragma unroll 1
+                for (int i = max(e, 0); i < min(e + N, p.vocab); ++i) dx[i] = rounded<T>(w.of(value<T>(r.x[i])));
+        }
+    if (mine && !w.none) dx[target] = rounded<T>(d_target);
 }
 
 template <typename K, typename... A>
@@ -453,10 +522,10 @@ int launch(K kernel, size_t grid, int cluster, cudaStream_t st, const A &...args
 template <typename T, int U>
 int launch_logprobs(const TokenParams &p, int n_sm, cudaStream_t st) {
     constexpr int N = 16 / (int)sizeof(T), TILE = 32 * U;
-    const int packs = (p.vocab + N - 1) / N + 1;  // with any head
+    const int packs = p.vocab / N;  // or one less, by the head
     int shift = 0;
     while ((packs + (TILE << shift) - 1) / (TILE << shift) > kUnits) ++shift;
-    const int units = (packs + (TILE << shift) - 1) / (TILE << shift);
+    const int units = std::max(1, (packs + (TILE << shift) - 1) / (TILE << shift));
     // CTAs of a row: as many as keep every warp at a unit, up to four CTAs a SM
     int C = 1;
     while (C < kTokenCluster && (long long)p.n_tokens * C * 2 <= 4ll * n_sm && units >= 2 * C * kTokenWarps) C *= 2;
@@ -466,17 +535,19 @@ int launch_logprobs(const TokenParams &p, int n_sm, cudaStream_t st) {
 
 template <typename T>
 int launch_rows(const TokenParams &p, int n_sm, cudaStream_t st) {
-    // tiles of one pack a lane where that makes no more than kUnits units, else of 16
-    // elements a lane
+    // tiles of one pack a lane where 16 elements a lane would make few units to choose
+    // from; else 16 (a tile's own work, 60 instructions, to twice the elements: 4096 x
+    // 65536 bf16 207 us in tiles of 8)
     constexpr int N = 16 / (int)sizeof(T);
-    return p.vocab + 16 <= 32 * kUnits * N ? launch_logprobs<T, 1>(p, n_sm, st)
+    return p.vocab <= 32 * 64 * N ? launch_logprobs<T, 1>(p, n_sm, st)
                                            : launch_logprobs<T, 16 / N>(p, n_sm, st);
 }
 
 template <typename T>
 int launch_grad(const TokenGradParams &p, cudaStream_t st) {
-    constexpr int N = 16 / (int)sizeof(T);
-    const int packs = (p.vocab + N - 1) / N + 1, chunks = (packs + kThreads * kTokenGradPacks - 1) / (kThreads * kTokenGradPacks);
+    // (64 bytes a thread: 4096 x 65536 bf16 166 us; 32 bytes 269, 128 173)
+    constexpr int N = 16 / (int)sizeof(T), PACKS = kTokenGradPacks;
+    const int packs = (p.vocab + N - 1) / N + 1, chunks = (packs + kThreads * PACKS - 1) / (kThreads * PACKS);
     return launch(token_grad_kernel<T>, (size_t)p.n_tokens * chunks, 1, st, p, chunks,
                   (((uintptr_t)p.logits ^ (uintptr_t)p.dlogits) & 15) == 0);
 }
