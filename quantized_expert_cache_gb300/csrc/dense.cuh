@@ -68,6 +68,35 @@ __device__ __forceinline__ void finish(const DenseOut &o, size_t m, size_t n, fl
     store_as(o.out, o.dtype, i, v);
 }
 
+// The blocks' sums of a column, in a fixed order: the same bits every time.  Warp `first`
+// of `step` takes 32 columns at a time.
+__device__ __forceinline__ void finish_sums(const float *parts, float *sums, int blocks, int cols, int first, int step,
+                                            int lane) {
+    for (long long c = (long long)first * 32 + lane; c < cols; c += 32ll * step) {
+        float s[4] = {};
+        int b = 0;
+        for (; b + 8 <= blocks; b += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = parts[(size_t)(b + i) * cols + c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i & 3] += v[i];
+        }
+        for (; b < blocks; ++b) {
+            const float v = parts[(size_t)b * cols + c];
+            if ((b & 3) == 0)
+                s[0] += v;
+            else if ((b & 3) == 1)
+                s[1] += v;
+            else if ((b & 3) == 2)
+                s[2] += v;
+            else
+                s[3] += v;
+        }
+        sums[c] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+}
+
 // Four elements from i, at once if the array allows it.
 __device__ __forceinline__ void load4_as(const void *p, int dtype, size_t i, float *v) {
     if (dtype == 0) {

@@ -235,6 +235,8 @@ struct DenseSplit {
     int part_dtype, n_parts, ld;
     float *sums;                // [cols] or null, through
     float *ws_sums;             // [dense_sum_blocks(n_tokens)][cols]
+    int finish;                 // 1: sums are finished too; 0: the products' launch does
+    int beside;                 // 1: runs beside the call's other split, which goes before
 };
 int dense_sum_blocks(int n_tokens);
 // One product D[m][n] = sum over pairs of parts and over k of A[m][k] B[n][k].
@@ -249,10 +251,16 @@ struct DenseProduct {
     DenseOut o;                 // ld = M
 };
 struct DenseGemm {
-    DenseProduct p[2];
+    DenseProduct p[2];          // two: the one of more steps a tile first
     int n_products, splits;
+    int second[2];              // tiles of the second product for workers with one more of the first, and for the others
     int *error;
+    // column sums to finish on the side (sums null: none): [sum_blocks][sum_cols]
+    const float *sum_parts;
+    float *sums;
+    int sum_blocks, sum_cols;
 };
+int dense_steps(const DenseProduct &p);  // of a tile
 // Tile columns, rows of B in one box, whether two CTAs share a tile, K splits, an
 // estimate of its clocks.
 struct DensePlan {

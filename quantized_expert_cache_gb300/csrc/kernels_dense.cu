@@ -5,11 +5,16 @@
 // some rows of W and all tokens, its lanes neighbouring packs of 8 columns; products
 // and sums in fp32.
 //
-// Parts.  An fp32 operand goes to the tensor cores as three bfloat16 numbers, each the
-// rounding of what the ones before leave: 24 bits, all of them (what lies below
-// 2^-133 is lost); dz = dy act'(z) of a binary16 layer as two binary16 numbers (22
-// bits, or 2^-25).  A gradient that is 16-bit itself goes as it is.  Products of
-// parts are further steps of the same sum.
+// Parts.  An fp32 operand goes to the tensor cores as bfloat16 numbers, each the rounding
+// of what the ones before leave; products of parts are further steps of the same sum.
+//   the layer, fp32 result: three, all 24 bits (what lies below 2^-133 is lost): a
+//     router's logits order its experts;  16-bit result: two
+//   gradients, fp32 result: two parts of x and of dz and three products, to 2^-16 of
+//     each term (about 3e-6 of a result's norm; three parts took twice the products);
+//     dz of a binary16 layer in two binary16 parts (22 bits, or 2^-25)
+//   gradients, 16-bit result: one, dz rounded as a 16-bit gradient is where layers
+//     store them: 2^-9 (2^-12) of each term, next to the result's own rounding
+// A gradient that is 16-bit itself, without a slope, goes as it is.
 #include <algorithm>
 #include <type_traits>
 
@@ -88,7 +93,9 @@ constexpr int kSplitCols = 256;
 
 template <typename T, typename P, int PARTS, bool WIDE>
 __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int block_tokens) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (beside another split, which started after all work before the call was done and
+    // whose end is waited for below: this one's end then stands for both)
+    if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ float part_sum[8][kSplitCols];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -150,6 +157,7 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
             }
         }
     }
+    if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!p.sums) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) part_sum[warp][col(j) - c0] = sum[j];
@@ -163,19 +171,10 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
     }
 }
 
-// The blocks' sums of a column, in order: the same bits every time.
-__global__ void __launch_bounds__(128) dense_sums_kernel(const float *part, float *sums, int blocks, int cols) {
+__global__ void __launch_bounds__(32) dense_sums_kernel(const float *part, float *sums, int blocks, int cols) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    // 4 threads a column, each every fourth block
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
-    __shared__ float four[4][32];
-    float s = 0.0f;
-    if (c < cols)
-        for (int b = q; b < blocks; b += 4) s += part[(size_t)b * cols + c];
-    four[q][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (q == 0 && c < cols) sums[c] = (four[0][threadIdx.x] + four[1][threadIdx.x]) + (four[2][threadIdx.x] + four[3][threadIdx.x]);
+    finish_sums(part, sums, blocks, cols, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
 int block_tokens(int n_tokens) { return std::max(32, (n_tokens + 255) / 256); }
@@ -201,8 +200,8 @@ int launch_split(const DenseSplit &p, cudaStream_t st) {
     const bool wide = p.cols % 8 == 0 && (((uintptr_t)p.src | (uintptr_t)p.pre | (uintptr_t)p.parts) & 15) == 0;
     const int rc = wide ? launch(dense_split_kernel<T, P, PARTS, true>, grid, 256, st, p, bt)
                         : launch(dense_split_kernel<T, P, PARTS, false>, grid, 256, st, p, bt);
-    if (rc || !p.sums) return rc;
-    return launch(dense_sums_kernel, (p.cols + 31) / 32, 128, st, (const float *)p.ws_sums, p.sums,
+    if (rc || !p.sums || !p.finish) return rc;
+    return launch(dense_sums_kernel, (p.cols + 31) / 32, 32, st, (const float *)p.ws_sums, p.sums,
                   dense_sum_blocks(p.n_tokens), p.cols);
 }
 
@@ -230,12 +229,13 @@ int dense_sum_blocks(int n_tokens) {
     return (n_tokens + bt - 1) / bt;
 }
 
-// (a context's calls ask for 3 parts of fp32 or bfloat16 for an fp32 result, 2 for a
-// 16-bit one; a binary16 gradient's slope takes 2; 1 is a copy with aligned rows, 0 sums alone)
+// (3 parts: the layer's fp32 rows for an fp32 result; 1 of a 16-bit type: rounded
+// slopes, or a copy with aligned rows; 0: sums alone)
 int launch_dense_split(const DenseSplit &p, cudaStream_t st) {
     using bf = __nv_bfloat16;
     switch (p.dtype * 4 + p.n_parts) {
         case 0: return launch_split<float, bf, 0>(p, st);
+        case 1: return launch_split<float, bf, 1>(p, st);
         case 2: return launch_split<float, bf, 2>(p, st);
         case 3: return launch_split<float, bf, 3>(p, st);
         case 4: return launch_split<__half, __half, 0>(p, st);
@@ -244,7 +244,6 @@ int launch_dense_split(const DenseSplit &p, cudaStream_t st) {
         case 8: return launch_split<bf, bf, 0>(p, st);
         case 9: return launch_split<bf, bf, 1>(p, st);
         case 10: return launch_split<bf, bf, 2>(p, st);
-        case 11: return launch_split<bf, bf, 3>(p, st);
         default: return (int)cudaErrorInvalidValue;
     }
 }

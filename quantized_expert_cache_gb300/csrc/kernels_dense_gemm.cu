@@ -137,14 +137,26 @@ struct Tile {
     int chunk;
 };
 
-// Tiles of the products one after the other; in one, bands of 8 tiles of m run through
-// all n, so that the CTAs at work share rows of both operands in L2.
+// The j-th tile of worker w (a cluster), or false.  Workers take the first product's
+// tiles in turn, then the second's (shorter ones) in turn too, but each as many as
+// the plan has it: those with fewer of the first take more.  Neighbouring workers are
+// at neighbouring tiles; in a product, bands of 8 tiles of m run through all n, so that
+// the CTAs at work share rows of both operands in L2.
 template <int BN, bool PAIR>
-__device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int split) {
-    Tile r;
+__device__ __forceinline__ bool tile_of(const DenseGemm &g, int worker, int workers, int j, int split, Tile &r) {
     const int n0 = g.p[0].m_tiles * g.p[0].n_tiles;
-    r.p = &g.p[t < n0 ? 0 : 1];
-    if (t >= n0) t -= n0;
+    int t = j * workers + worker;
+    r.p = &g.p[0];
+    if (t >= n0) {
+        if (g.n_products == 1) return false;
+        const int more = n0 % workers, group = worker < more ? 0 : 1, mine = n0 / workers + (group == 0 ? 1 : 0);
+        const int k = j - mine, both = min(g.second[0], g.second[1]);
+        if (k >= g.second[group]) return false;
+        const int members = group == 0 ? more : workers - more, i = group == 0 ? worker : worker - more;
+        t = k < both ? k * workers + worker : both * workers + (k - both) * members + i;
+        r.p = &g.p[1];
+        if (t >= r.p->m_tiles * r.p->n_tiles) return false;
+    }
     constexpr int BAND = 8;
     const int band = t / (BAND * r.p->n_tiles), first = band * BAND, size = min(BAND, r.p->m_tiles - first);
     t -= band * BAND * r.p->n_tiles;
@@ -155,7 +167,7 @@ __device__ __forceinline__ Tile tile_of(const DenseGemm &g, int t, int split) {
     r.first = (int)(steps * split / g.splits);
     r.last = (int)(steps * (split + 1) / g.splits);
     r.chunk = r.p->o.dtype == 0 ? kChunk32 : kChunk16;
-    return r;
+    return true;
 }
 
 template <int BN, bool PAIR>
@@ -214,8 +226,10 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int tiles = g.p[0].m_tiles * g.p[0].n_tiles + (g.n_products > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
-    const int first_tile = (int)blockIdx.x / CTAS, tile_step = (int)gridDim.x / CTAS;
+    // (worked out anew each time: the epilogue has no registers to keep it in)
+    const auto tile = [&](int j, Tile &w) {
+        return tile_of<BN, PAIR>(g, (int)blockIdx.x / CTAS, (int)gridDim.x / CTAS, j, split, w);
+    };
 
     if (warp == kWTma) {
         if (lane == 0) {
@@ -224,8 +238,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             // the leader's barriers count both CTAs' bytes
             const uint32_t full_at = PAIR ? mapped(full(0), leader) : full(0);
             uint32_t it = 0, slot = 0, phase = 0;
-            for (int t = first_tile; t < tiles; t += tile_step) {
-                const Tile w = tile_of<BN, PAIR>(g, t, split);
+            Tile w;
+            for (int j = 0; tile(j, w); ++j) {
                 // (what a step needs in registers: a load of the parameters costs each step more
                 // than its copies' issue)
                 const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
@@ -277,8 +291,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
         __syncwarp();
     } else if (warp == kWMma) {
         uint32_t slot = 0, phase = 0, chunk = 0;
-        for (int t = first_tile; t < tiles && side == 0; t += tile_step) {
-            const Tile w = tile_of<BN, PAIR>(g, t, split);
+        Tile w;
+        for (int j = 0; side == 0 && tile(j, w); ++j) {
             const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
             // fp32 sums, both operands binary16 (0) or bfloat16 (1), their directions, N, M
             const uint32_t type = w.p->bf16 ? 1u : 0u;
@@ -320,9 +334,13 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
         // lanes of TMEM: a warp reaches the quarter of its number
         const int quarter = warp & 3, share = (warp - kWEpi) >> 2;
         constexpr int NC = C::NC, GROUP = C::GROUP;
+        // (the first products are some time off)
+        if (g.sums)
+            dense::finish_sums(g.sum_parts, g.sums, g.sum_blocks, g.sum_cols,
+                               (int)blockIdx.x + (int)gridDim.x * (warp - kWEpi), (int)gridDim.x * C::EPI, lane);
         uint32_t chunk = 0;
-        for (int t = first_tile; t < tiles; t += tile_step) {
-            const Tile w = tile_of<BN, PAIR>(g, t, split);
+        Tile w;
+        for (int j = 0; tile(j, w); ++j) {
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
@@ -372,7 +390,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
         cluster.sync();
         if (!*abort_flag) {
             // a lane: four rows; a warp: a column; the CTAs of the same rows: every S-th warp
-            const Tile w = tile_of<BN, PAIR>(g, first_tile, split);
+            Tile w;
+            tile(0, w);
             const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + lane * 4);
             const float4 *red = (const float4 *)smem + lane;
             const int cols = min(BN, w.p->N - w.n0);
@@ -414,6 +433,29 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
 
 long long steps_of(const DenseProduct &p) { return (long long)((p.K + kBK - 1) / kBK) * p.n_pairs; }
 
+// Tiles of a second product (n1 of s1 steps) for the workers that have one tile more of
+// the first (n0 of s0) and for the others, so that the longest is as short as it can be:
+// its steps.
+long long share_out(long long n0, long long s0, long long n1, long long s1, long long workers, int *second) {
+    const long long more = n0 % workers, low = n0 / workers * s0, high = low + s0;
+    const auto fits = [&](long long level, long long load) { return level > load ? (level - load) / s1 : 0; };
+    const auto room = [&](long long level) { return more * fits(level, high) + (workers - more) * fits(level, low); };
+    long long from = 0, to = high + n1 * s1;
+    while (from < to) {
+        const long long level = (from + to) / 2;
+        if (room(level) >= n1)
+            to = level;
+        else
+            from = level + 1;
+    }
+    if (second) {
+        second[0] = (int)fits(to, high);
+        second[1] = (int)fits(to, low);
+    }
+    return std::max(to, more > 0 ? high : low);
+}
+
+
 // The tiles that are compiled, and what one costs.  Clocks of a step: measured, but
 // for the pairs' near what 128 bytes a clock of shared memory allow (a step's operands
 // are written there once and read once; a pair's B is read by halves).
@@ -435,16 +477,17 @@ int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
         if (e != cudaSuccess) return (int)e;
         configured.fetch_or(1ull << (device & 63));
     }
-    int tiles = 0;
     for (int i = 0; i < g.n_products; ++i) {
         DenseProduct &p = g.p[i];
         p.m_tiles = (p.M + C::TM - 1) / C::TM;
         p.n_tiles = (p.N + BN - 1) / BN;
-        tiles += p.m_tiles * p.n_tiles;
     }
-    const int ctas = PAIR ? 2 * g.splits : g.splits;
+    const int ctas = PAIR ? 2 * g.splits : g.splits, n0 = g.p[0].m_tiles * g.p[0].n_tiles;
+    const int n1 = g.n_products > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0;
+    const int workers = g.splits > 1 ? n0 : std::min(n0 + n1, n_sm / ctas);
+    if (n1 > 0) share_out(n0, steps_of(g.p[0]), n1, steps_of(g.p[1]), workers, g.second);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(g.splits > 1 ? tiles * ctas : std::min(tiles, n_sm / ctas) * ctas));
+    cfg.gridDim = dim3((unsigned)workers * ctas);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
@@ -489,37 +532,36 @@ int clusters_at_once(int ctas, int device, int n_sm) {
 
 }  // namespace
 
-// The cheapest of the tiles and K splits, by the clocks of the longest CTA (for two
-// products at once the larger of the longest tile and an even share of all).
+// The cheapest of the tiles and K splits, by the clocks of the longest CTA.
 DensePlan dense_plan(const DenseProduct *p, int n_products, int device, int n_sm) {
     DensePlan best{};
     for (const Shape &f : kShapes) {
         const int tm = f.pair ? 2 * kBM : kBM;
         bool fits = true;
-        long long tiles = 0, work = 0, longest = 0, fewest = 1ll << 40;
+        long long tiles[2] = {}, steps[2] = {};
         for (int i = 0; i < n_products; ++i) {
             if (p[i].b_mn && (f.pair ? f.bn / 2 : f.bn) < 64) fits = false;  // (columns of B come 64 at a time)
-            const long long t = (long long)((p[i].M + tm - 1) / tm) * ((p[i].N + f.bn - 1) / f.bn), s = steps_of(p[i]);
-            tiles += t;
-            work += t * s;
-            longest = std::max(longest, s);
-            fewest = std::min(fewest, s);
+            tiles[i] = (long long)((p[i].M + tm - 1) / tm) * ((p[i].N + f.bn - 1) / f.bn);
+            steps[i] = steps_of(p[i]);
         }
         if (!fits) continue;
         for (int s = 1; s <= (f.pair ? kMaxSplits / 2 : kMaxSplits); ++s) {
-            if (s > 1 && (n_products > 1 || s > fewest)) break;
+            if (s > 1 && (n_products > 1 || s > steps[0])) break;
             const int workers = clusters_at_once(f.pair ? 2 * s : s, device, n_sm);
-            const long long rounds = (tiles + workers - 1) / workers;
+            const long long rounds = (tiles[0] + workers - 1) / workers;
             if (s > 1 && rounds > 1) break;
-            const double steps = n_products == 1
-                                     ? (double)(rounds * ((longest + s - 1) / s))
-                                     : std::max((double)longest, (double)((work + workers - 1) / workers));
-            const double c = steps * f.clocks + (s > 1 ? 2500 + 20 * f.bn : 12 * f.bn);
+            const long long longest =
+                n_products == 1 ? rounds * ((steps[0] + s - 1) / s)
+                                : share_out(tiles[0], steps[0], tiles[1], steps[1],
+                                            std::min<long long>(tiles[0] + tiles[1], workers), nullptr);
+            const double c = (double)longest * f.clocks + (s > 1 ? 2500 + 20 * f.bn : 12 * f.bn);
             if (best.splits == 0 || c < best.clocks) best = {f.bn, f.pair ? f.bn / 2 : f.bn, f.pair, s, c};
         }
     }
     return best;
 }
+
+int dense_steps(const DenseProduct &p) { return (int)std::min(steps_of(p), 1ll << 30); }
 
 int launch_dense_gemm(DenseGemm &g, const DensePlan &plan, int device, int n_sm, cudaStream_t st) {
     if (plan.pair)

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 namespace {
 
@@ -71,13 +72,9 @@ int dense_sizes(moe_ctx *ctx, const char *what, int x_dtype, int w_dtype, int y_
     return MOE_OK;
 }
 
-// Parts of an operand of the tensor cores.  A 16-bit result asks for 16 bits of it, an
-// fp32 one for all 24.
-int dense_parts(int dtype, bool slope, bool f32_result) {
-    if (dtype == MOE_F32) return f32_result ? 3 : 2;
-    if (!slope) return 1;
-    return dtype == MOE_F16 ? 2 : f32_result ? 3 : 2;
-}
+// Parts of an operand of the tensor cores (kernels_dense.cu says why).
+int forward_parts(int x_dtype, int y_dtype) { return x_dtype != MOE_F32 ? 1 : y_dtype == MOE_F32 ? 3 : 2; }
+int gradient_parts(int dtype, bool slope, bool f32_result) { return f32_result && (dtype == MOE_F32 || slope) ? 2 : 1; }
 
 // Regions of a call's workspace.
 struct DenseSpace {
@@ -95,8 +92,8 @@ DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_t
         if (x_dtype == MOE_F32 && n_tokens > moe::kDenseFew) s.x_parts = take(t * cols * 3 * 2);
         return s;
     }
-    if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 3 * 2);
-    s.z_parts = take(t * round_up(rows, 8) * dense_parts(y_dtype, act != MOE_ACT_NONE, true) * 2);
+    if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 2 * 2);
+    s.z_parts = take(t * round_up(rows, 8) * gradient_parts(y_dtype, act != MOE_ACT_NONE, true) * 2);
     s.sums = take((size_t)moe::dense_sum_blocks(n_tokens) * rows * 4);
     return s;
 }
@@ -127,9 +124,8 @@ struct DenseMatrix {
     int parts;
 };
 
-// The pairs of parts a result takes: those above 2^-24 (fp32) or 2^-16 of the product.
-void dense_pairs(moe::DenseProduct &p, int a_parts, int b_parts) {
-    const int most = p.o.dtype == MOE_F32 ? 2 : 1;
+// The pairs of parts a product takes, those up to `most` of the places in all.
+void dense_pairs(moe::DenseProduct &p, int a_parts, int b_parts, int most) {
     p.n_pairs = 0;
     p.pairs = 0;
     for (int sum = 0; sum <= most; ++sum)
@@ -138,8 +134,8 @@ void dense_pairs(moe::DenseProduct &p, int a_parts, int b_parts) {
                 p.pairs |= (unsigned)(a | (sum - a) << 2) << (4 * p.n_pairs++);
 }
 
-int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b,
-                 const moe::DensePlan &plan, const moe::OpContext &c, cudaStream_t st, const char *what) {
+int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b, const moe::DensePlan &plan,
+                 const moe::OpContext &c, cudaStream_t st, const char *what) {
     g.splits = plan.splits;
     g.error = c.error;
     for (int i = 0; i < g.n_products; ++i) {
@@ -154,11 +150,16 @@ int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const De
     return launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
 }
 
-// The products of a call, two of them in one launch (their tiles fill the SMs
-// together) or in two (each with its own tiles and K splits), as the plans have it.
-int dense_products(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b,
-                   const moe::OpContext &c, cudaStream_t st, const char *what) {
-    for (int i = 0; i < g.n_products; ++i) dense_pairs(g.p[i], a[i].parts, b[i].parts);
+// The products of a call (their pairs of parts set), two of them in one launch (their
+// tiles fill the SMs together) or in two (each with its own tiles and K splits), as the
+// plans have it.
+int dense_products(moe_ctx *ctx, moe::DenseGemm &g, DenseMatrix *a, DenseMatrix *b, const moe::OpContext &c,
+                   cudaStream_t st, const char *what) {
+    if (g.n_products == 2 && moe::dense_steps(g.p[0]) < moe::dense_steps(g.p[1])) {
+        std::swap(g.p[0], g.p[1]);
+        std::swap(a[0], a[1]);
+        std::swap(b[0], b[1]);
+    }
     const moe::DensePlan all = moe::dense_plan(g.p, g.n_products, c.device, c.n_sm);
     if (g.n_products == 1) return dense_launch(ctx, g, a, b, all, c, st, what);
     const moe::DensePlan one = moe::dense_plan(g.p, 1, c.device, c.n_sm),
@@ -169,6 +170,7 @@ int dense_products(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const 
     const int rc = dense_launch(ctx, g, a, b, one, c, st, what);
     if (rc) return rc;
     g.p[0] = g.p[1];
+    g.sums = nullptr;
     return dense_launch(ctx, g, a + 1, b + 1, two, c, st, what);
 }
 
@@ -292,7 +294,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
         const moe::DenseFew f{d_x, d_w, x_dtype, w_dtype, n_tokens, rows, cols, out};
         return launched(ctx, "dense", moe::launch_dense_few(f, c.n_sm, st));
     }
-    DenseMatrix x{d_x, (size_t)cols, t, (size_t)cols, dense_parts(x_dtype, false, y_dtype == MOE_F32)};
+    DenseMatrix x{d_x, (size_t)cols, t, (size_t)cols, forward_parts(x_dtype, y_dtype)};
     if (x_dtype == MOE_F32) {
         moe::DenseSplit s{};
         s.src = d_x;
@@ -305,7 +307,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
         if (r) return r;
         x.base = s.parts;
     }
-    const DenseMatrix w{d_w, (size_t)cols, (size_t)rows, (size_t)cols, 1};
+    DenseMatrix w{d_w, (size_t)cols, (size_t)rows, (size_t)cols, 1};
     moe::DenseGemm g{};
     g.n_products = 1;
     g.p[0].M = rows;
@@ -313,6 +315,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
     g.p[0].K = cols;
     g.p[0].bf16 = w_dtype == MOE_BF16;
     g.p[0].o = out;
+    dense_pairs(g.p[0], 1, x.parts, x.parts - 1);
     return dense_products(ctx, g, &w, &x, c, st, "dense");
 }
 
@@ -360,9 +363,11 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     const bool f32_result = (d_dx && x_dtype == MOE_F32) || (d_dw && dw_dtype == MOE_F32);
     // dz, as it is if it is 16-bit and its rows are aligned
     const bool product = d_dx || d_dw;
-    DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, dense_parts(y_dtype, slope, f32_result)};
+    DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, gradient_parts(y_dtype, slope, f32_result)};
     const bool direct = !slope && y_dtype != MOE_F32 && rows % 8 == 0 && whole({d_dy}, 16);
-    if (d_db || (product && !direct)) {
+    moe::DenseGemm g{};
+    const bool first = d_db || (product && !direct);
+    if (first) {
         moe::DenseSplit s{};
         s.src = d_dy;
         s.pre = pre;
@@ -379,6 +384,13 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         }
         s.sums = d_db;
         s.ws_sums = (float *)(ws + space.sums);
+        s.finish = !product;
+        if (d_db && product) {
+            g.sum_parts = s.ws_sums;
+            g.sums = d_db;
+            g.sum_blocks = moe::dense_sum_blocks(n_tokens);
+            g.sum_cols = rows;
+        }
         const int r = launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
         if (r) return r;
     }
@@ -391,12 +403,12 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         s.n_tokens = n_tokens;
         s.cols = s.ld = cols;
         s.parts = ws + space.x_parts;
-        s.n_parts = xs.parts = dense_parts(x_dtype, false, dw_dtype == MOE_F32);
+        s.n_parts = xs.parts = gradient_parts(x_dtype, false, dw_dtype == MOE_F32);
+        s.beside = first;
         const int r = launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
         if (r) return r;
         xs.base = s.parts;
     }
-    moe::DenseGemm g{};
     DenseMatrix a[2], b[2];
     if (d_dw) {
         moe::DenseProduct &p = g.p[g.n_products];
@@ -423,6 +435,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     for (int i = 0; i < g.n_products; ++i) {
         g.p[i].bf16 = w_dtype == MOE_BF16;
         g.p[i].o.ld = cols;
+        dense_pairs(g.p[i], a[i].parts, b[i].parts, g.p[i].o.dtype == MOE_F32 ? 1 : 0);
     }
     return dense_products(ctx, g, a, b, c, st, "dense_backward");
 }

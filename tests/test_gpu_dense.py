@@ -11,9 +11,12 @@ of a result:
   pair of parts, K counting every pair's steps.  By norms (a partial sum of i of the 32
   terms has sqrt(i/32) of the whole's): 32 (2/3) 2^-23 = 42 u of the result's norm.  A
   16-bit result has 128 accumulations between two: 256 and 171 in place of 64 and 42.
-- operands in parts: fp32 ones whole for an fp32 result (the pairs left out are below
-  3 2^-24 A), to 2^-16 for a 16-bit one (pairs left out: 3 2^-16 A, a parts' cut 2^-16);
-  binary16 slopes to 2^-22 or 2^-25.
+- operands in parts, the layer: fp32 rows whole for an fp32 result (the pairs left out
+  are below 3 2^-24 A), to 2^-16 for a 16-bit one (pairs left out: 3 2^-16 A, a parts'
+  cut 2^-16).  Gradients: for an fp32 result each operand in two parts, off by at most
+  2^-17 of it (bfloat16; binary16 2^-22, or 2^-25), the pair left out 2^-16 A: 2^-15 A;
+  by norms, errors of different terms being independent, 2^-16.  For a 16-bit result dz
+  (and fp32 rows) rounded to the type: a half step of each, by A.
 - the epilogue: bias, activation and residual a few roundings (expf and erff 2 ulp):
   8 u of each term, |act'| <= 1.13; then half a step of the result's type.
 - slopes: 12 u (1 + |z|) of dy.
@@ -224,21 +227,23 @@ def check_backward(s, types, got, act, dw_dtype):
         edz = 12 * U * (1 + z.abs()) * dz.abs()
         dz = dz * slope_ref(s["pre"], act)
         if types[1] == F16:
-            edz = edz + dz.abs() * 2.0 ** -22 + 2.0 ** -25
-    z_parts = 3 if types[2] == F32 or act else 1
-    f32 = types[0] == F32
+            edz = edz + 2.0 ** -25
+    def product(ref, a, n_k, dtype, cut, spread):
+        """cut: operands that go in parts or rounded."""
+        tol = sums_tol(a, n_k, 1, False, dtype == F32) + spread
+        if cut:
+            tol = tol + a * (2.0 ** -15 + 2 * n_k / 512 * U if dtype == F32 else cut * torch.finfo(dtype).eps / 2)
+        return tol
+
+    z_cut = 1 if types[2] == F32 or act else 0
     if dx is not None:
-        a = dz.abs() @ w.abs()
-        close(dx, dz @ w, sums_tol(a, r, z_parts, False, f32) + edz @ w.abs(), types[0], "dx")
+        close(dx, dz @ w, product(dz @ w, dz.abs() @ w.abs(), r, types[0], z_cut, edz @ w.abs()), types[0], "dx")
     if dw is not None:
-        f32w = dw_dtype == F32
-        a = dz.abs().t() @ x.abs()
-        parts = z_parts * (2 if types[0] == F32 else 1) if z_parts > 1 or types[0] == F32 else 1
-        if types[0] == F32 and z_parts == 1:
-            parts = 3
-        close(dw, dz.t() @ x, sums_tol(a, t, parts, False, f32w) + edz.t() @ x.abs(), dw_dtype, "dw")
-        if f32w and types[1] == BF16 and not act and t >= 64:
-            close_norm(dw, dz.t() @ x, dw_dtype, "dw")
+        cut = z_cut + (1 if types[0] == F32 else 0)
+        ref = dz.t() @ x
+        close(dw, ref, product(ref, dz.abs().t() @ x.abs(), t, dw_dtype, cut, edz.t() @ x.abs()), dw_dtype, "dw")
+        if dw_dtype == F32 and types[1] == BF16 and not act and t >= 64:
+            close_norm(dw, ref, dw_dtype, "dw", 2.0 ** -16 / U if cut else 0)
     if db is not None:
         close(db, dz.sum(0), (t / 8 + 40) * U * dz.abs().sum(0) + edz.sum(0), F32, "db")
 
@@ -315,8 +320,11 @@ def test_gradients_against_differences(ctx):
             up, down = list(base), list(base)
             up[i], down[i] = base[i] + h * v, base[i] - h * v
             slope = float((f(*up) - f(*down)) / (2 * h))
-            # fp32 gradients of fp32-rounded sums: 200 u of the absolute parts
-            assert abs(slope - float((d * v).sum())) <= 1.3e-5 * float((d.abs() * v.abs()).sum())
+            # the gradients' operands are off by 2^-17 each at most: 2^-15 of the absolute terms,
+            # of which a direction adds up |v| in each; the slope's own error is far below
+            a = ((s["dy"].double().abs() * 1.13) @ base[1].abs(), (s["dy"].double().abs() * 1.13).t() @ base[0].abs(),
+                 s["dy"].double().abs().sum(0) * 1.13)[i]
+            assert abs(slope - float((d * v).sum())) <= 2.0 ** -15 * float((a * v.abs()).sum())
 
 
 # ------------------------------------------------------- streams, graphs, sizes
