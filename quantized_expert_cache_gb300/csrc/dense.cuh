@@ -68,32 +68,19 @@ __device__ __forceinline__ void finish(const DenseOut &o, size_t m, size_t n, fl
     store_as(o.out, o.dtype, i, v);
 }
 
-// The blocks' sums of a column, in a fixed order: the same bits every time.  Warp `first`
-// of `step` takes 32 columns at a time.
+// The blocks' sums of a column, in a fixed order: the same bits every time.  A warp takes
+// 8 columns at a time, every fourth block in a lane; `first` of `step` warps.
 __device__ __forceinline__ void finish_sums(const float *parts, float *sums, int blocks, int cols, int first, int step,
                                             int lane) {
-    for (long long c = (long long)first * 32 + lane; c < cols; c += 32ll * step) {
-        float s[4] = {};
-        int b = 0;
-        for (; b + 8 <= blocks; b += 8) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = parts[(size_t)(b + i) * cols + c];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i & 3] += v[i];
-        }
-        for (; b < blocks; ++b) {
-            const float v = parts[(size_t)b * cols + c];
-            if ((b & 3) == 0)
-                s[0] += v;
-            else if ((b & 3) == 1)
-                s[1] += v;
-            else if ((b & 3) == 2)
-                s[2] += v;
-            else
-                s[3] += v;
-        }
-        sums[c] = (s[0] + s[1]) + (s[2] + s[3]);
+    for (long long c0 = 8ll * first; c0 < cols; c0 += 8ll * step) {
+        const long long c = c0 + (lane & 7);
+        float s = 0.0f;
+        if (c < cols)
+#pragma unroll 8
+            for (int b = lane >> 3; b < blocks; b += 4) s += parts[(size_t)b * cols + c];
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+        if (lane < 8 && c < cols) sums[c] = s;
     }
 }
 
@@ -128,7 +115,8 @@ struct Epilogue {
     float bias[4];
     int m, left;   // the lane's first row, rows from it to the end
     bool wide;
-    __device__ __forceinline__ Epilogue(const DenseOut &out, int M, int m_) : o(out), m(m_), left(M - m_) {
+    __device__ __forceinline__ Epilogue(const DenseOut &out, int M, int m_, size_t offset) : o(out), m(m_), left(M - m_) {
+        if (offset) o.out = (float *)o.out + offset;  // (a K share's sums)
         const uintptr_t at = (uintptr_t)o.out | (uintptr_t)o.res | (uintptr_t)o.pre;
         wide = left >= 4 && o.ld % 4 == 0 && (at & (o.dtype == 0 ? 15 : 7)) == 0;
 #pragma unroll

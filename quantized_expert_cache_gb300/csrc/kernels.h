@@ -249,6 +249,9 @@ struct DenseProduct {
     unsigned pairs;             // 4 bits each, the first lowest: part of A | part of B << 2
     int m_tiles, n_tiles;
     DenseOut o;                 // ld = M
+    // K shares of a tile, each an own tile whose fp32 sums go to o.out + share * M * N
+    // (joined by launch_dense_join); up to most_shares of them
+    int shares, most_shares;
 };
 struct DenseGemm {
     DenseProduct p[2];          // two: the one of more steps a tile first
@@ -261,12 +264,14 @@ struct DenseGemm {
     int sum_blocks, sum_cols;
 };
 int dense_steps(const DenseProduct &p);  // of a tile
-// Tile columns, rows of B in one box, whether two CTAs share a tile, K splits, an
-// estimate of its clocks.
+// Tile columns, rows of B in one box, whether two CTAs share a tile, K splits over a
+// cluster, K shares of the first product, an estimate of its clocks.
 struct DensePlan {
-    int bn, box, pair, splits;
+    int bn, box, pair, splits, shares;
     double clocks;
 };
+// out[i] = the sum of `shares` arrays of n fp32 numbers, of dtype.
+int launch_dense_join(const float *parts, int shares, size_t n, void *out, int dtype, int n_sm, cudaStream_t st);
 DensePlan dense_plan(const DenseProduct *p, int n_products, int device, int n_sm);
 int launch_dense_few(const DenseFew &p, int n_sm, cudaStream_t st);
 int launch_dense_split(const DenseSplit &p, cudaStream_t st);

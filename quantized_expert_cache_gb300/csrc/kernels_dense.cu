@@ -5,15 +5,15 @@
 // some rows of W and all tokens, its lanes neighbouring packs of 8 columns; products
 // and sums in fp32.
 //
-// Parts.  An fp32 operand goes to the tensor cores as bfloat16 numbers, each the rounding
-// of what the ones before leave; products of parts are further steps of the same sum.
-//   the layer, fp32 result: three, all 24 bits (what lies below 2^-133 is lost): a
-//     router's logits order its experts;  16-bit result: two
-//   gradients, fp32 result: two parts of x and of dz and three products, to 2^-16 of
-//     each term (about 3e-6 of a result's norm; three parts took twice the products);
-//     dz of a binary16 layer in two binary16 parts (22 bits, or 2^-25)
-//   gradients, 16-bit result: one, dz rounded as a 16-bit gradient is where layers
-//     store them: 2^-9 (2^-12) of each term, next to the result's own rounding
+// Parts.  An fp32 operand (or one with a slope) goes to the tensor cores as 16-bit
+// numbers, each the rounding of what the ones before leave; products of parts are further
+// steps of the same sum.
+//   fp32 results: three bfloat16 parts, all 24 bits (what lies below 2^-133 is lost), and
+//     the products to 2^-24: 3 with a 16-bit operand, 6 of two fp32 ones.  (Two parts
+//     and three products leave 3e-6 to 4.5e-6 of a gradient's norm, a plain fp32 product
+//     about 1e-6.)  A slope of binary16: two binary16 parts (22 bits, or 2^-25).
+//   16-bit results: two parts; one for a large gradient's dz, which layers store in 16
+//     bits too: 2^-9 (2^-12) of each term next to the result's own rounding.
 // A gradient that is 16-bit itself, without a slope, goes as it is.
 #include <algorithm>
 #include <type_traits>
@@ -105,24 +105,34 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
     const auto col = [&](int j) { return c0 + (WIDE ? lane * 8 + j : j * 32 + lane); };
     const size_t t0 = (size_t)block * block_tokens, t1 = min(t0 + block_tokens, (size_t)p.n_tokens);
     float sum[8] = {};
-    for (size_t t = t0 + warp; t < t1; t += 8) {
-        float v[8], z[8];
+    // a token's 8 columns of a lane, the next one's loads in flight
+    struct Eight {
+        Pack<T, 8> src, pre;
+    };
+    const auto load = [&](size_t t) {
+        Eight e{};
         const T *src = (const T *)p.src + t * p.cols, *pre = (const T *)p.pre + t * p.cols;
         if (WIDE) {
-            Pack<T, 8> a{}, b{};
             if (col(0) < p.cols) {
-                a = *(const Pack<T, 8> *)(src + col(0));
-                if (p.pre) b = *(const Pack<T, 8> *)(pre + col(0));
+                e.src = *(const Pack<T, 8> *)(src + col(0));
+                if (p.pre) e.pre = *(const Pack<T, 8> *)(pre + col(0));
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = value<T>(a.v[j]), z[j] = value<T>(b.v[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] = col(j) < p.cols ? value<T>(src[col(j)]) : 0.0f;
-                z[j] = p.pre && col(j) < p.cols ? value<T>(pre[col(j)]) : 0.0f;
+                if (col(j) < p.cols) e.src.v[j] = src[col(j)];
+                if (p.pre && col(j) < p.cols) e.pre.v[j] = pre[col(j)];
             }
         }
+        return e;
+    };
+    Eight next{};
+    if (t0 + warp < t1) next = load(t0 + warp);
+    for (size_t t = t0 + warp; t < t1; t += 8) {
+        float v[8], z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = value<T>(next.src.v[j]), z[j] = value<T>(next.pre.v[j]);
+        if (t + 8 < t1) next = load(t + 8);
         if (p.pre)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], slope_of(z[j], p.act));  // (not fused into the sum)
@@ -177,7 +187,27 @@ __global__ void __launch_bounds__(32) dense_sums_kernel(const float *part, float
     finish_sums(part, sums, blocks, cols, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
-int block_tokens(int n_tokens) { return std::max(32, (n_tokens + 255) / 256); }
+// ---- K shares of a product -------------------------------------------------------
+template <int VEC>
+__global__ void __launch_bounds__(256) dense_join_kernel(const float *parts, int shares, size_t n, void *out, int dtype) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * VEC; i < n; i += (size_t)gridDim.x * 256 * VEC) {
+        float v[VEC] = {};
+#pragma unroll 4
+        for (int s = 0; s < shares; ++s) {
+            const Pack<float, VEC> p = *(const Pack<float, VEC> *)(parts + s * n + i);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[j] += p.v[j];
+        }
+        if (VEC == 4)
+            store4_as(out, dtype, i, v);
+        else
+            store_as(out, dtype, i, v[0]);
+    }
+}
+
+int block_tokens(int n_tokens) { return std::max(16, (n_tokens + 127) / 128 + 7 & ~7); }
 
 template <typename K, typename... A>
 int launch(K kernel, size_t grid, int threads, cudaStream_t st, const A &...args) {
@@ -201,7 +231,7 @@ int launch_split(const DenseSplit &p, cudaStream_t st) {
     const int rc = wide ? launch(dense_split_kernel<T, P, PARTS, true>, grid, 256, st, p, bt)
                         : launch(dense_split_kernel<T, P, PARTS, false>, grid, 256, st, p, bt);
     if (rc || !p.sums || !p.finish) return rc;
-    return launch(dense_sums_kernel, (p.cols + 31) / 32, 32, st, (const float *)p.ws_sums, p.sums,
+    return launch(dense_sums_kernel, (p.cols + 7) / 8, 32, st, (const float *)p.ws_sums, p.sums,
                   dense_sum_blocks(p.n_tokens), p.cols);
 }
 
@@ -229,8 +259,7 @@ int dense_sum_blocks(int n_tokens) {
     return (n_tokens + bt - 1) / bt;
 }
 
-// (3 parts: the layer's fp32 rows for an fp32 result; 1 of a 16-bit type: rounded
-// slopes, or a copy with aligned rows; 0: sums alone)
+// (1 part of a 16-bit type: rounded slopes, or a copy with aligned rows; 0: sums alone)
 int launch_dense_split(const DenseSplit &p, cudaStream_t st) {
     using bf = __nv_bfloat16;
     switch (p.dtype * 4 + p.n_parts) {
@@ -244,8 +273,17 @@ int launch_dense_split(const DenseSplit &p, cudaStream_t st) {
         case 8: return launch_split<bf, bf, 0>(p, st);
         case 9: return launch_split<bf, bf, 1>(p, st);
         case 10: return launch_split<bf, bf, 2>(p, st);
+        case 11: return launch_split<bf, bf, 3>(p, st);
         default: return (int)cudaErrorInvalidValue;
     }
+}
+
+int launch_dense_join(const float *parts, int shares, size_t n, void *out, int dtype, int n_sm, cudaStream_t st) {
+    const bool wide = n % 4 == 0 && ((uintptr_t)out & (dtype == 0 ? 15 : 7)) == 0;
+    const size_t blocks = (n / (wide ? 4 : 1) + 255) / 256;
+    const unsigned grid = (unsigned)std::max<size_t>(1, std::min<size_t>(blocks, (size_t)n_sm * 8));
+    return wide ? launch(dense_join_kernel<4>, grid, 256, st, parts, shares, n, out, dtype)
+                : launch(dense_join_kernel<1>, grid, 256, st, parts, shares, n, out, dtype);
 }
 
 int launch_dense_few(const DenseFew &p, int n_sm, cudaStream_t st) {

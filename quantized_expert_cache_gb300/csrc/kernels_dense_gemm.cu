@@ -134,7 +134,7 @@ __device__ __forceinline__ void commit_warp(uint32_t bar, int ctas) {
 struct Tile {
     const DenseProduct *p;
     int m0, n0, kb, first, last;  // kb: steps of one pair of parts; [first, last): this CTA's
-    int chunk;
+    int chunk, share;
 };
 
 // The j-th tile of worker w (a cluster), or false.  Workers take the first product's
@@ -144,10 +144,17 @@ struct Tile {
 // the CTAs at work share rows of both operands in L2.
 template <int BN, bool PAIR>
 __device__ __forceinline__ bool tile_of(const DenseGemm &g, int worker, int workers, int j, int split, Tile &r) {
-    const int n0 = g.p[0].m_tiles * g.p[0].n_tiles;
-    int t = j * workers + worker;
+    const int one = g.p[0].m_tiles * g.p[0].n_tiles, n0 = one * g.p[0].shares;
+    int t = j * workers + worker, of = g.splits;
     r.p = &g.p[0];
-    if (t >= n0) {
+    r.share = 0;
+    if (t < n0) {
+        if (g.p[0].shares > 1) {
+            r.share = split = t / one;
+            of = g.p[0].shares;
+            t -= split * one;
+        }
+    } else {
         if (g.n_products == 1) return false;
         const int more = n0 % workers, group = worker < more ? 0 : 1, mine = n0 / workers + (group == 0 ? 1 : 0);
         const int k = j - mine, both = min(g.second[0], g.second[1]);
@@ -164,8 +171,8 @@ __device__ __forceinline__ bool tile_of(const DenseGemm &g, int worker, int work
     r.n0 = t / size * BN;
     r.kb = (r.p->K + kBK - 1) / kBK;
     const long long steps = (long long)r.kb * r.p->n_pairs;
-    r.first = (int)(steps * split / g.splits);
-    r.last = (int)(steps * (split + 1) / g.splits);
+    r.first = (int)(steps * split / of);
+    r.last = (int)(steps * (split + 1) / of);
     r.chunk = r.p->o.dtype == 0 ? kChunk32 : kChunk16;
     return true;
 }
@@ -370,7 +377,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
 #pragma unroll
                 for (int c = 0; c < NC; ++c) red[(share * NC + c) * kBM + ml] = acc[c];
             } else {
-                const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + quarter * 32 + (lane & 7) * 4);
+                const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + quarter * 32 + (lane & 7) * 4,
+                                        (size_t)w.share * w.p->M * w.p->N);
                 float *mine = (float *)(smem + C::STAGING) + (warp - kWEpi) * GROUP * 32;
 #pragma unroll
                 for (int c = 0; c < NC; c += GROUP) {
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             // a lane: four rows; a warp: a column; the CTAs of the same rows: every S-th warp
             Tile w;
             tile(0, w);
-            const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + lane * 4);
+            const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + lane * 4, 0);
             const float4 *red = (const float4 *)smem + lane;
             const int cols = min(BN, w.p->N - w.n0);
             for (int c = split * (C::THREADS / 32) + warp; c < cols; c += S * (C::THREADS / 32)) {
@@ -482,10 +490,10 @@ int launch_tile(DenseGemm &g, int device, int n_sm, cudaStream_t st) {
         p.m_tiles = (p.M + C::TM - 1) / C::TM;
         p.n_tiles = (p.N + BN - 1) / BN;
     }
-    const int ctas = PAIR ? 2 * g.splits : g.splits, n0 = g.p[0].m_tiles * g.p[0].n_tiles;
+    const int ctas = PAIR ? 2 * g.splits : g.splits, n0 = g.p[0].m_tiles * g.p[0].n_tiles * g.p[0].shares;
     const int n1 = g.n_products > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0;
     const int workers = g.splits > 1 ? n0 : std::min(n0 + n1, n_sm / ctas);
-    if (n1 > 0) share_out(n0, steps_of(g.p[0]), n1, steps_of(g.p[1]), workers, g.second);
+    if (n1 > 0) share_out(n0, (steps_of(g.p[0]) + g.p[0].shares - 1) / g.p[0].shares, n1, steps_of(g.p[1]), workers, g.second);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)workers * ctas);
     cfg.blockDim = dim3(C::THREADS);
@@ -538,25 +546,30 @@ DensePlan dense_plan(const DenseProduct *p, int n_products, int device, int n_sm
     for (const Shape &f : kShapes) {
         const int tm = f.pair ? 2 * kBM : kBM;
         bool fits = true;
-        long long tiles[2] = {}, steps[2] = {};
+        long long tiles[2] = {}, steps[2] = {};  // (of a tile)
         for (int i = 0; i < n_products; ++i) {
             if (p[i].b_mn && (f.pair ? f.bn / 2 : f.bn) < 64) fits = false;  // (columns of B come 64 at a time)
             tiles[i] = (long long)((p[i].M + tm - 1) / tm) * ((p[i].N + f.bn - 1) / f.bn);
             steps[i] = steps_of(p[i]);
         }
         if (!fits) continue;
-        for (int s = 1; s <= (f.pair ? kMaxSplits / 2 : kMaxSplits); ++s) {
-            if (s > 1 && (n_products > 1 || s > steps[0])) break;
-            const int workers = clusters_at_once(f.pair ? 2 * s : s, device, n_sm);
-            const long long rounds = (tiles[0] + workers - 1) / workers;
-            if (s > 1 && rounds > 1) break;
+        const auto consider = [&](int splits, int shares) {
+            const int workers = clusters_at_once(f.pair ? 2 * splits : splits, device, n_sm);
+            const long long n0 = tiles[0] * shares, s0 = (steps[0] + splits * shares - 1) / (splits * shares);
+            const long long rounds = (n0 + workers - 1) / workers;
+            if (splits > 1 && rounds > 1) return;
             const long long longest =
-                n_products == 1 ? rounds * ((steps[0] + s - 1) / s)
-                                : share_out(tiles[0], steps[0], tiles[1], steps[1],
-                                            std::min<long long>(tiles[0] + tiles[1], workers), nullptr);
-            const double c = (double)longest * f.clocks + (s > 1 ? 2500 + 20 * f.bn : 12 * f.bn);
-            if (best.splits == 0 || c < best.clocks) best = {f.bn, f.pair ? f.bn / 2 : f.bn, f.pair, s, c};
-        }
+                n_products == 1 ? rounds * s0
+                                : share_out(n0, s0, tiles[1], steps[1], std::min<long long>(n0 + tiles[1], workers), nullptr);
+            // joins: through shared memory, or through HBM at its rate
+            const double c = (double)longest * f.clocks + (splits > 1 ? 2500 + 20 * f.bn : 12 * f.bn) +
+                             (shares > 1 ? 6000 + 1.5e-3 * p[0].M * p[0].N * shares : 0);
+            if (best.splits == 0 || c < best.clocks) best = {f.bn, f.pair ? f.bn / 2 : f.bn, f.pair, splits, shares, c};
+        };
+        if (n_products == 1)
+            for (int s = 1; s <= std::min<long long>(f.pair ? kMaxSplits / 2 : kMaxSplits, steps[0]); ++s) consider(s, 1);
+        for (int s = n_products == 1 ? 2 : 1; s <= std::min<long long>(std::max(1, p[0].most_shares), steps[0]); ++s)
+            consider(1, s);
     }
     return best;
 }

@@ -73,12 +73,21 @@ int dense_sizes(moe_ctx *ctx, const char *what, int x_dtype, int w_dtype, int y_
 }
 
 // Parts of an operand of the tensor cores (kernels_dense.cu says why).
-int forward_parts(int x_dtype, int y_dtype) { return x_dtype != MOE_F32 ? 1 : y_dtype == MOE_F32 ? 3 : 2; }
-int gradient_parts(int dtype, bool slope, bool f32_result) { return f32_result && (dtype == MOE_F32 || slope) ? 2 : 1; }
+int row_parts(int x_dtype, bool f32_result) { return x_dtype != MOE_F32 ? 1 : f32_result ? 3 : 2; }
+int gradient_parts(int dtype, bool slope, bool f32_result, bool large) {
+    if (dtype != MOE_F32 && !slope) return 1;
+    if (f32_result) return dtype == MOE_F16 ? 2 : 3;
+    return large ? 1 : 2;
+}
+// Where a gradient's products bound its call, not its launches: 2^33 of them (4.6 us of
+// the measured bf16 rate for a pair of parts).
+bool large_gradient(int n_tokens, int rows, int cols) { return (double)n_tokens * rows * cols >= 1ll << 32; }
+// K shares of the weights' gradient: what 32 MB of sums hold.
+int weight_shares(int rows, int cols) { return (int)std::min<size_t>(8, ((size_t)32 << 20) / ((size_t)rows * cols * 4)); }
 
 // Regions of a call's workspace.
 struct DenseSpace {
-    size_t x_parts = 0, z_parts = 0, sums = 0, bytes = 0;  // offsets
+    size_t x_parts = 0, z_parts = 0, sums = 0, shares = 0, bytes = 0;  // offsets
 };
 DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_tokens, int rows, int cols) {
     DenseSpace s;
@@ -92,9 +101,11 @@ DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_t
         if (x_dtype == MOE_F32 && n_tokens > moe::kDenseFew) s.x_parts = take(t * cols * 3 * 2);
         return s;
     }
-    if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 2 * 2);
-    s.z_parts = take(t * round_up(rows, 8) * gradient_parts(y_dtype, act != MOE_ACT_NONE, true) * 2);
+    if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 3 * 2);
+    s.z_parts = take(t * round_up(rows, 8) * std::max(gradient_parts(y_dtype, act != MOE_ACT_NONE, true, false),
+                                                    gradient_parts(y_dtype, act != MOE_ACT_NONE, false, false)) * 2);
     s.sums = take((size_t)moe::dense_sum_blocks(n_tokens) * rows * 4);
+    if (weight_shares(rows, cols) > 1) s.shares = take((size_t)weight_shares(rows, cols) * rows * cols * 4);
     return s;
 }
 
@@ -135,9 +146,16 @@ void dense_pairs(moe::DenseProduct &p, int a_parts, int b_parts, int most) {
 }
 
 int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const DenseMatrix *b, const moe::DensePlan &plan,
-                 const moe::OpContext &c, cudaStream_t st, const char *what) {
+                 float *sums, const moe::OpContext &c, cudaStream_t st, const char *what) {
     g.splits = plan.splits;
     g.error = c.error;
+    for (int i = 0; i < g.n_products; ++i) g.p[i].shares = 1;
+    const moe::DenseOut joined = g.p[0].o;
+    if (plan.shares > 1) {
+        g.p[0].shares = plan.shares;
+        g.p[0].o.out = sums;
+        g.p[0].o.dtype = MOE_F32;
+    }
     for (int i = 0; i < g.n_products; ++i) {
         moe::DenseProduct &p = g.p[i];
         const int rc = encode_map(ctx, &p.tm_a, a[i].base, p.bf16, a[i].inner, a[i].outer, a[i].ld, a[i].parts,
@@ -147,31 +165,34 @@ int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const De
                                   p.b_mn ? 128 : (uint32_t)plan.box);
         if (rd) return rd;
     }
-    return launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
+    const int rc = launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
+    if (rc || plan.shares == 1) return rc;
+    return launched(ctx, what, moe::launch_dense_join(sums, plan.shares, (size_t)g.p[0].M * g.p[0].N, joined.out,
+                                                      joined.dtype, c.n_sm, st));
 }
 
 // The products of a call (their pairs of parts set), two of them in one launch (their
 // tiles fill the SMs together) or in two (each with its own tiles and K splits), as the
 // plans have it.
-int dense_products(moe_ctx *ctx, moe::DenseGemm &g, DenseMatrix *a, DenseMatrix *b, const moe::OpContext &c,
-                   cudaStream_t st, const char *what) {
+int dense_products(moe_ctx *ctx, moe::DenseGemm &g, DenseMatrix *a, DenseMatrix *b, float *sums,
+                   const moe::OpContext &c, cudaStream_t st, const char *what) {
     if (g.n_products == 2 && moe::dense_steps(g.p[0]) < moe::dense_steps(g.p[1])) {
         std::swap(g.p[0], g.p[1]);
         std::swap(a[0], a[1]);
         std::swap(b[0], b[1]);
     }
     const moe::DensePlan all = moe::dense_plan(g.p, g.n_products, c.device, c.n_sm);
-    if (g.n_products == 1) return dense_launch(ctx, g, a, b, all, c, st, what);
+    if (g.n_products == 1) return dense_launch(ctx, g, a, b, all, sums, c, st, what);
     const moe::DensePlan one = moe::dense_plan(g.p, 1, c.device, c.n_sm),
                          two = moe::dense_plan(g.p + 1, 1, c.device, c.n_sm);
     constexpr double kLaunch = 5000;  // clocks
-    if (all.clocks <= one.clocks + two.clocks + kLaunch) return dense_launch(ctx, g, a, b, all, c, st, what);
+    if (all.clocks <= one.clocks + two.clocks + kLaunch) return dense_launch(ctx, g, a, b, all, sums, c, st, what);
     g.n_products = 1;
-    const int rc = dense_launch(ctx, g, a, b, one, c, st, what);
+    const int rc = dense_launch(ctx, g, a, b, one, sums, c, st, what);
     if (rc) return rc;
     g.p[0] = g.p[1];
     g.sums = nullptr;
-    return dense_launch(ctx, g, a + 1, b + 1, two, c, st, what);
+    return dense_launch(ctx, g, a + 1, b + 1, two, sums, c, st, what);
 }
 
 }  // namespace
@@ -294,7 +315,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
         const moe::DenseFew f{d_x, d_w, x_dtype, w_dtype, n_tokens, rows, cols, out};
         return launched(ctx, "dense", moe::launch_dense_few(f, c.n_sm, st));
     }
-    DenseMatrix x{d_x, (size_t)cols, t, (size_t)cols, forward_parts(x_dtype, y_dtype)};
+    DenseMatrix x{d_x, (size_t)cols, t, (size_t)cols, row_parts(x_dtype, y_dtype == MOE_F32)};
     if (x_dtype == MOE_F32) {
         moe::DenseSplit s{};
         s.src = d_x;
@@ -316,7 +337,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
     g.p[0].bf16 = w_dtype == MOE_BF16;
     g.p[0].o = out;
     dense_pairs(g.p[0], 1, x.parts, x.parts - 1);
-    return dense_products(ctx, g, &w, &x, c, st, "dense");
+    return dense_products(ctx, g, &w, &x, nullptr, c, st, "dense");
 }
 
 int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_w, int w_dtype, const void *d_dy,
@@ -363,7 +384,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     const bool f32_result = (d_dx && x_dtype == MOE_F32) || (d_dw && dw_dtype == MOE_F32);
     // dz, as it is if it is 16-bit and its rows are aligned
     const bool product = d_dx || d_dw;
-    DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, gradient_parts(y_dtype, slope, f32_result)};
+    DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, gradient_parts(y_dtype, slope, f32_result, large_gradient(n_tokens, rows, cols))};
     const bool direct = !slope && y_dtype != MOE_F32 && rows % 8 == 0 && whole({d_dy}, 16);
     moe::DenseGemm g{};
     const bool first = d_db || (product && !direct);
@@ -403,7 +424,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         s.n_tokens = n_tokens;
         s.cols = s.ld = cols;
         s.parts = ws + space.x_parts;
-        s.n_parts = xs.parts = gradient_parts(x_dtype, false, dw_dtype == MOE_F32);
+        s.n_parts = xs.parts = row_parts(x_dtype, dw_dtype == MOE_F32);
         s.beside = first;
         const int r = launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
         if (r) return r;
@@ -418,6 +439,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         p.a_mn = p.b_mn = 1;
         p.o.out = d_dw;
         p.o.dtype = dw_dtype;
+        p.most_shares = weight_shares(rows, cols);
         a[g.n_products] = xs;
         b[g.n_products++] = dz;
     }
@@ -435,9 +457,9 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     for (int i = 0; i < g.n_products; ++i) {
         g.p[i].bf16 = w_dtype == MOE_BF16;
         g.p[i].o.ld = cols;
-        dense_pairs(g.p[i], a[i].parts, b[i].parts, g.p[i].o.dtype == MOE_F32 ? 1 : 0);
+        dense_pairs(g.p[i], a[i].parts, b[i].parts, g.p[i].o.dtype == MOE_F32 ? 2 : 1);
     }
-    return dense_products(ctx, g, a, b, c, st, "dense_backward");
+    return dense_products(ctx, g, a, b, (float *)(ws + space.shares), c, st, "dense_backward");
 }
 
 }  // extern "C"
