@@ -349,7 +349,14 @@ def moe_router_loss(ctx, logits, idx, mask, gw, n_tokens, n_experts, k, balance_
 
 def _of_dtype(x, dtype) -> int | None:
     """_dev() of a tensor that must be of `dtype` (an MOE_ code)."""
-    if x is not None and not isinstance(x, int) and _dtype(x) != dtype:
+    if x is None or x.__class__ is int:
+        return x
+    try:
+        if _DTYPES[x.dtype] == dtype and x.is_cuda and x.is_contiguous():
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    if _dtype(x) != dtype:
         raise ValueError("a tensor has another dtype than the call's")
     return _dev(x)
 
@@ -386,7 +393,7 @@ def _dtype_of(x) -> int:
 
 
 def _space(ws) -> tuple:
-    return (None, 0) if ws is None else (_dev(ws), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (_dev(ws), ws.nbytes)
 
 
 def moe_dense_workspace(ctx, x, w, y, act, n_tokens, rows, cols) -> tuple:
@@ -403,10 +410,12 @@ def moe_dense_forward(ctx, x, w, n_tokens, rows, cols, y, bias=None, act=ACT_NON
     """y = act(x W^T + bias) + res, pre = the sums before the activation; fp32
     bias; ws: a tensor of moe_dense_workspace's bytes.  The dtypes: those of x, w
     and y by default (an address has none: give its own)."""
-    xd, wd, yd = (_dtype(t) if d is None else d for t, d in ((x, x_dtype), (w, w_dtype), (y, y_dtype)))
+    xd = _dtype(x) if x_dtype is None else x_dtype
+    wd = _dtype(w) if w_dtype is None else w_dtype
+    yd = _dtype(y) if y_dtype is None else y_dtype
     at, size = _space(ws)
-    return _check(ctx, load().moe_dense_forward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _elem(bias, _FP32), act,
-                                                _of_dtype(res, yd), n_tokens, rows, cols, _of_dtype(y, yd), yd,
+    return _check(ctx, load().moe_dense_forward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _elem(bias, _FP32),
+                                                act, _of_dtype(res, yd), n_tokens, rows, cols, _of_dtype(y, yd), yd,
                                                 _of_dtype(pre, yd), at, size, _stream(stream)))
 
 
@@ -415,8 +424,10 @@ def moe_dense_backward(ctx, x, w, dy, n_tokens, rows, cols, dx=None, dw=None, db
     """dx (of x's dtype), dw (fp32 or w's dtype) and db (fp32) of a dense layer,
     any of them None; x is read for dw only, w for dx only: the other may be None
     with its dtype given.  ws: a tensor of moe_dense_workspace's bytes."""
-    xd, wd, yd, dwd = (_dtype(t) if d is None else d
-                       for t, d in ((x, x_dtype), (w, w_dtype), (dy, y_dtype), (dw, dw_dtype)))
+    xd = _dtype(x) if x_dtype is None else x_dtype
+    wd = _dtype(w) if w_dtype is None else w_dtype
+    yd = _dtype(dy) if y_dtype is None else y_dtype
+    dwd = _dtype(dw) if dw_dtype is None else dw_dtype
     at, size = _space(ws)
     return _check(ctx, load().moe_dense_backward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _of_dtype(dy, yd), yd,
                                                  _of_dtype(pre, yd), act, n_tokens, rows, cols, _of_dtype(dx, xd),

@@ -13,14 +13,17 @@
 // are positive.
 //
 // The n largest: the row falls into at most 256 units, whose maxima the pass
-// keeps anyway.  The n-th largest of these is a bound below the n-th largest
-// element, and units below it hold none of the n; the others, about n of them, are
-// read again (from L2) into lists of 32 sorted over a warp's lanes, which are merged
-// pairwise.  Keys hold the value over the inverted index, so order and ties (the
-// lowest index) are one comparison of whole numbers, whatever the order of work.
+// keeps anyway.  A value that n of these reach is a bound below the n-th largest
+// element, and units below it hold none of the n; the others, little more than n of
+// them, are read again (from L2).  What reaches the bound there, seldom more than a few
+// dozen elements, is put in order by counting what comes before each; where it is more
+// than kCand (ties, masked rows), lists of 32 sorted over a warp's lanes take it in and
+// are merged pairwise.  Keys hold the value over the inverted index, so order and ties
+// (the lowest index) are one comparison of whole numbers, whatever the order of work.
 //
-// A row takes a cluster of 1 to 16 CTAs, joined through distributed shared memory:
-// no workspace, any stream, one launch.
+// A row takes a cluster of 1 to 8 CTAs.  They write their units' maxima into each other's
+// shared memory, their sums and candidates into the first one's: no workspace, any
+// stream, one launch.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -202,15 +205,20 @@ __device__ __forceinline__ unsigned long long candidate(float x, int index) {
     return (unsigned long long)order_of(x) << 32 | (0xffffffffu - (unsigned)index);
 }
 
+constexpr int kCand = 256;     // candidates that are ordered by counting, one a thread
+static_assert(kCand <= kThreads && kUnits <= kThreads, "one thread to a unit and to a candidate");
+
 struct TokenShared {
-    Sums part[kTokenWarps];           // of the warps
-    Sums cta;
-    unsigned unit[kUnits];            // the maxima of this CTA's units
-    alignas(16) unsigned all[kUnits];  // of all CTAs'
-    unsigned long long list[kTokenWarps][kList], joint[kTokenWarps][kList];
+    Sums part[kTokenWarps];        // of the warps
+    Sums ctas[kTokenCluster];      // of the CTAs (in the first)
+    unsigned unit[kUnits];         // the maxima of the row's units
+    unsigned low[kTokenWarps], high[kTokenWarps];  // of the warps' units
+    unsigned long long cand[kCand];  // (in the first CTA)
+    unsigned long long list[kTokenWarps][kList];
     int flagged[kUnits];
-    int n_flagged;
-    unsigned bound;  // 0: every unit may hold one
+    int n_flagged, n_cand;
+    float top, log_sum;            // the row's
+    bool none;
 };
 
 // U packs a lane and tile; a unit is 2^shift tiles of a warp.
@@ -270,10 +278,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
         }
     };
     const bool edges = rank == 0 && warp == 0 && r.edge > 0;
-    if (edges) {
-        const float x = lane < r.edge ? value<T>(r.x[r.edge_at(lane)]) : -kInf;
-        add(&x, 1, of_order(__reduce_max_sync(0xffffffffu, order_of(fmaxf(x, -kInf)))));
-    }
+    const float x_edge = edges && lane < r.edge ? value<T>(r.x[r.edge_at(lane)]) : -kInf;
+    if (edges) add(&x_edge, 1, of_order(__reduce_max_sync(0xffffffffu, order_of(fmaxf(x_edge, -kInf)))));
     const int mine = u0 + warp < u1 ? (u1 - u0 - warp + kTokenWarps - 1) / kTokenWarps : 0;
     const int tiles = mine << shift;
     const auto tile_pack = [&](int i) {
@@ -292,6 +298,9 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
     };
     Pack16<T> next[U];
     if (tiles > 0) tile_load(next, tile_pack(0));
+    if (threadIdx.x == 0) sh.n_flagged = 0, sh.n_cand = 0;
+    if (C > 1)
+        cluster.sync();  // (all CTAs have started: their shared memory may be written)
     unsigned top = 0;
     for (int i = 0; i < tiles; ++i) {
         float x[U * N];
@@ -307,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
         const unsigned key = __reduce_max_sync(0xffffffffu, order_of(high));
         top = max(top, key);
         if ((i & ((1 << shift) - 1)) == (1 << shift) - 1) {
-            if (lane == 0) sh.unit[warp + (i >> shift) * kTokenWarps] = top;
+            unsigned *unit = &sh.unit[u0 + warp + (i >> shift) * kTokenWarps];
+            if (lane < C) *(C > 1 ? cluster.map_shared_rank(unit, lane) : unit) = top;
             top = 0;
         }
         add(x, U * N, of_order(key));
@@ -316,48 +326,55 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
     a.n = warp_sum_f(a.n);
     a.t = warp_sum_f(a.t);
     if (lane == 0) sh.part[warp] = a;
-    if (threadIdx.x == 0) sh.n_flagged = 0, sh.bound = 0;
     __syncthreads();
     if (warp == 0) {
         a = joined_lanes<kTokenWarps>(sh.part[lane % kTokenWarps], c);
-        if (lane == 0) sh.cta = a;
+        if (lane == 0) *(C > 1 ? cluster.map_shared_rank(&sh.ctas[rank], 0) : &sh.ctas[0]) = a;
     }
     if (C > 1)
         cluster.sync();
     else
         __syncthreads();
 
-    // ---- the units that may hold one of the n largest
-    unsigned long long best = 0;  // rank 0, warp 0: lane i's is the i-th largest
+    // ---- elements that may be among the n largest
+    unsigned bound = 0;  // (0: every unit may hold one)
+    const unsigned mine_key = (int)threadIdx.x < units ? sh.unit[threadIdx.x] : 0;
     if (p.n_top > 0) {
-        unsigned mine_key = 0;
-        const int t = threadIdx.x;
-        if (t < units)
-            mine_key = C > 1 ? cluster.map_shared_rank(sh.unit, t / units_cta)[t % units_cta] : sh.unit[t];
-        sh.all[t] = mine_key;
-        __syncthreads();
         if (units > p.n_top) {
-            // the maximum with n_top - 1 before it bounds the n largest from below
-            int before = 0;
-            for (int j = 0; j < units; j += 4) {
-                // (units past the last are 0, before none)
-                const uint4 k = *(const uint4 *)(sh.all + j);
-                before += (k.x > mine_key || (k.x == mine_key && j < t) ? 1 : 0) +
-                          (k.y > mine_key || (k.y == mine_key && j + 1 < t) ? 1 : 0) +
-                          (k.z > mine_key || (k.z == mine_key && j + 2 < t) ? 1 : 0) +
-                          (k.w > mine_key || (k.w == mine_key && j + 3 < t) ? 1 : 0);
-            }
-            if (t < units && before == p.n_top - 1) sh.bound = mine_key;
+            const unsigned least = (int)threadIdx.x < units ? mine_key : 0xffffffffu;
+            const unsigned lo = __reduce_min_sync(0xffffffffu, least), hi = __reduce_max_sync(0xffffffffu, mine_key);
+            if (lane == 0) sh.low[warp] = lo, sh.high[warp] = hi;
             __syncthreads();
+            unsigned from = sh.low[0], to = sh.high[0];
+#pragma unroll
+            for (int w = 1; w < kTokenWarps; ++w) from = min(from, sh.low[w]), to = max(to, sh.high[w]);
+            // the largest value that n_top maxima reach lies in [from, to]; one that a few
+            // more reach will do
+            for (;;) {
+                bound = from;
+                if (from == to) break;
+                const unsigned middle = to - (to - from) / 2;
+                const int reach = __syncthreads_count(mine_key >= middle);
+                if (reach >= p.n_top) {
+                    bound = from = middle;
+                    if (reach <= p.n_top + p.n_top / 2 + 4) break;
+                } else {
+                    to = middle - 1;
+                }
+            }
         }
-        const unsigned bound = sh.bound;
-        if (t >= u0 && t < u1 && mine_key >= bound) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = t;
+        if ((int)threadIdx.x >= u0 && (int)threadIdx.x < u1 && mine_key >= bound)
+            sh.flagged[atomicAdd(&sh.n_flagged, 1)] = threadIdx.x;
         __syncthreads();
-        List list;
-        if (edges) {
-            const int e = r.edge_at(lane);
-            list.insert(lane < r.edge ? candidate(value<T>(r.x[e]), e) : 0, p.n_top, lane);
-        }
+        int *n_cand = C > 1 ? cluster.map_shared_rank(&sh.n_cand, 0) : &sh.n_cand;
+        unsigned long long *cands = C > 1 ? cluster.map_shared_rank(sh.cand, 0) : sh.cand;
+        const auto offer = [&](float x, int index) {
+            if (order_of(x) >= bound) {
+                const int at = atomicAdd(n_cand, 1);
+                if (at < kCand) cands[at] = candidate(x, index);
+            }
+        };
+        if (edges && lane < r.edge) offer(x_edge, r.edge_at(lane));
         const int n_flagged = sh.n_flagged;
         for (int f = warp; f < n_flagged; f += kTokenWarps) {
             const int first = (sh.flagged[f] << shift) * TILE;
@@ -366,41 +383,25 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
                 tile_load(v, i + lane);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    // (a NaN's key is above all others; one past the packs is no candidate)
-                    unsigned high = 0;
-#pragma unroll
-                    for (int j = 0; j < N; ++j) high = max(high, order_of(value<T>(v[k].v[j])));
                     const int at = i + 32 * k + lane;
-                    const bool any = at < r.packs && high >= bound;
-                    if (!__any_sync(0xffffffffu, any)) continue;
-#pragma unroll 1
-                    for (int j = 0; j < N; ++j) {
-                        float y = 0.0f;
+                    if (at < r.packs)
 #pragma unroll
-                        for (int q = 0; q < N; ++q)
-                            if (q == j) y = value<T>(v[k].v[q]);
-                        list.insert(any && order_of(y) >= bound ? candidate(y, r.head + at * N + j) : 0, p.n_top, lane);
-                    }
+                        for (int j = 0; j < N; ++j) offer(value<T>(v[k].v[j]), r.head + at * N + j);
                 }
             }
         }
-        best = merge_warps(sh.list, list.mine, warp, lane);
-        if (C > 1) {
+        if (C > 1)
             cluster.sync();
-            if (rank == 0)  // (C <= kTokenWarps: a warp takes a CTA's list)
-                best = merge_warps(sh.joint, warp < C ? cluster.map_shared_rank(sh.list[0], warp)[lane] : 0, warp,
-                                   lane);
-        }
+        else
+            __syncthreads();
     }
+    if (rank > 0) return;  // (nothing reads or writes the other CTAs' memory from here on)
+
     // ---- results
-    if (rank == 0 && warp == 0) {
-        static_assert(kTokenCluster <= kTokenWarps, "one lane and one warp to a CTA");
-        Sums q = sh.cta;
-        if (C > 1) {
-            q = lane % kTokenWarps < C ? *cluster.map_shared_rank(&sh.cta, lane % kTokenWarps)
-                                       : Sums{-kInf, 0.0f, 0.0f, 0.0f};
-            q = joined_lanes<kTokenWarps>(q, c);
-        }
+    if (warp == 0) {
+        static_assert(kTokenCluster <= kTokenWarps, "one lane to a CTA");
+        Sums q = lane % kTokenWarps < C ? sh.ctas[lane % kTokenWarps] : Sums{-kInf, 0.0f, 0.0f, 0.0f};
+        q = joined_lanes<kTokenWarps>(q, c);
         // nothing but -infinity: no distribution
         const bool none = q.m == -kInf && q.s == 0.0f;
         const float rest = q.s + (q.n - 1.0f);
@@ -413,14 +414,61 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
                 p.stats[2 * row] = q.m;
                 p.stats[2 * row + 1] = log_sum;
             }
-        }
-        if (lane < p.n_top) {
-            p.top_idx[row * p.n_top + lane] = (int32_t)(0xffffffffu - (unsigned)best);
-            const float x = of_order((unsigned)(best >> 32));
-            p.top_logp[row * p.n_top + lane] = none ? -kInf : (x - q.m) * p.scale - log_sum;
+            sh.top = q.m;
+            sh.log_sum = log_sum;
+            sh.none = none;
         }
     }
-    if (C > 1) cluster.sync();  // no CTA leaves while its shared memory is read
+    if (p.n_top == 0) return;
+    __syncthreads();
+    const auto write = [&](int place, unsigned long long key) {
+        p.top_idx[row * p.n_top + place] = (int32_t)(0xffffffffu - (unsigned)key);
+        p.top_logp[row * p.n_top + place] =
+            sh.none ? -kInf : (of_order((unsigned)(key >> 32)) - sh.top) * p.scale - sh.log_sum;
+    };
+    const int n = sh.n_cand;
+    if (n <= kCand) {
+        const unsigned long long key = (int)threadIdx.x < n ? sh.cand[threadIdx.x] : 0;
+        int before = 0;
+        for (int j = 0; j < n; ++j) before += sh.cand[j] > key ? 1 : 0;
+        if ((int)threadIdx.x < n && before < p.n_top) write(before, key);
+        return;
+    }
+    // more: all of the row's units that reach the bound, by the first CTA
+    if (threadIdx.x == 0) sh.n_flagged = 0;
+    __syncthreads();
+    if ((int)threadIdx.x < units && mine_key >= bound) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = threadIdx.x;
+    __syncthreads();
+    List list;
+    if (edges) list.insert(lane < r.edge ? candidate(x_edge, r.edge_at(lane)) : 0, p.n_top, lane);
+    const int n_flagged = sh.n_flagged;
+    for (int f = warp; f < n_flagged; f += kTokenWarps) {
+        const int first = (sh.flagged[f] << shift) * TILE;
+        for (int i = first; i < first + (TILE << shift); i += TILE) {
+            Pack16<T> v[U];
+            tile_load(v, i + lane);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                // (a NaN's key is above all others; one past the packs is no candidate)
+                unsigned high = 0;
+#pragma unroll
+                for (int j = 0; j < N; ++j) high = max(high, order_of(value<T>(v[k].v[j])));
+                const int at = i + 32 * k + lane;
+                const bool any = at < r.packs && high >= bound;
+                if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll 1
+                for (int j = 0; j < N; ++j) {
+                    float y = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < N; ++q)
+                        if (q == j) y = value<T>(v[k].v[q]);
+                    list.insert(any && order_of(y) >= bound ? candidate(y, r.head + at * N + j) : 0, p.n_top, lane);
+                }
+            }
+        }
+    }
+    const unsigned long long best = merge_warps(sh.list, list.mine, warp, lane);
+    if (warp == 0 && lane < p.n_top) write(lane, best);
 }
 
 // ---- gradient: one read, one write, a row's scalars in every thread --------------
