@@ -6,6 +6,8 @@ library's operators as a decoder uses them together.
                      on the codes, the routed experts
     at the end:      the last norm, the output head as a 4-bit linear layer,
                      the promotion pass of the expert cache
+    to answer:       the log probabilities of the tokens taken, the entropies and
+                     the likeliest alternatives
 
 and, for a router that is tuned on the way, the balance and z loss of every
 layer with the gradient of its logits, and the picks of every expert: the
@@ -86,6 +88,16 @@ class DecoderStack:
         qec.cache_step(self.ctx, n)
         return self.head_logits[:n]
 
+    def answer(self, tokens, n_top):
+        """Of the last step's logits, for int32 tokens [n]: (log probabilities [n], entropies [n], the n_top likeliest
+        tokens [n][n_top], their log probabilities)."""
+        n = tokens.shape[0]
+        made = [torch.empty(n, device="cuda"), torch.empty(n, device="cuda"),
+                torch.empty(n, n_top, dtype=torch.int32, device="cuda"), torch.empty(n, n_top, device="cuda")]
+        logp, entropy, idx, alternatives = made
+        qec.moe_token_logprobs(self.ctx, self.head_logits, tokens, n, self.V, logp, entropy, n_top, idx, alternatives)
+        return made
+
     def router_losses(self, n, mask=None, balance=0.01, z=0.001):
         """Of the last step: per layer (losses [2], picks [E], the logits' gradient [n][E])."""
         made = []
@@ -111,7 +123,9 @@ def main():
         for layer, (_, counts, _) in enumerate(made):
             picks[layer] += counts
         tokens = logits.argmax(1)
-        print(f"step {step}: tokens {tokens.tolist()}, balance loss "
+        logp, _, _, _ = stack.answer(tokens.to(torch.int32), 4)
+        print(f"step {step}: tokens {tokens.tolist()}, log probabilities "
+              + " ".join(f"{float(v):.3f}" for v in logp) + ", balance loss "
               + " ".join(f"{float(loss[0]):.5f}" for loss, _, _ in made))
     for layer in range(stack.L):
         order = np.argsort(-picks[layer].cpu().numpy(), kind="stable")

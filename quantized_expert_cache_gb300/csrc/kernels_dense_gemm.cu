@@ -92,11 +92,13 @@ __device__ __forceinline__ uint32_t mapped(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrival of a warp, by its lane 0, at a barrier of the cluster.
+// Arrival of a warp, by its lane 0, at a barrier of the cluster.  (Without a release to the
+// cluster, which would wait for the last tile's stores; what it orders, reads of TMEM, is
+// done.)
 __device__ __forceinline__ void arrive_cluster_warp(uint32_t bar, int lane) {
     asm volatile(
         "{\n.reg .pred p;\nsetp.eq.s32 p, %1, 0;\n"
-        "@p mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(bar),
+        "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}" ::"r"(bar),
         "r"(lane)
         : "memory");
 }
