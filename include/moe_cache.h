@@ -653,6 +653,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
  * it is.  The same call on the same inputs gives the same bits (those of
  * d_dx and d_dw depend on whether both are asked for).  d_ws:
  * moe_dense_workspace's backward_bytes.  Everything else as moe_dense_forward.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_w, int w_dtype, const void *d_dy,
                        int y_dtype, const void *d_pre, int act, int n_tokens, int rows, int cols, void *d_dx,

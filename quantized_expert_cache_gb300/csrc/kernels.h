@@ -238,7 +238,14 @@ struct DenseSplit {
     int finish;                 // 1: sums are finished too; 0: the products' launch does
     int beside;                 // 1: runs beside the call's other split, which goes before
 };
-int dense_sum_blocks(int n_tokens);
+// Tokens of a block of column sums, the blocks, and a bound of them that does not fall as
+// the tokens rise.
+inline int dense_block_tokens(int n_tokens) { return n_tokens <= 2048 ? 16 : ((n_tokens + 127) / 128 + 7) / 8 * 8; }
+inline int dense_sum_blocks(int n_tokens) {
+    const int t = dense_block_tokens(n_tokens);
+    return (n_tokens + t - 1) / t;
+}
+inline int dense_most_blocks(int n_tokens) { return n_tokens < 2048 ? (n_tokens + 15) / 16 : 128; }
 // One product D[m][n] = sum over pairs of parts and over k of A[m][k] B[n][k].
 struct DenseProduct {
     CUtensorMap tm_a, tm_b;     // [part][outer][inner], boxes of 64 x 128 (B with k inner: x box rows)

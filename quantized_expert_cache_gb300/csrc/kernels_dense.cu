@@ -207,8 +207,6 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const float *parts, int
     }
 }
 
-int block_tokens(int n_tokens) { return std::max(16, (n_tokens + 127) / 128 + 7 & ~7); }
-
 template <typename K, typename... A>
 int launch(K kernel, size_t grid, int threads, cudaStream_t st, const A &...args) {
     cudaLaunchConfig_t cfg{};
@@ -225,7 +223,7 @@ int launch(K kernel, size_t grid, int threads, cudaStream_t st, const A &...args
 
 template <typename T, typename P, int PARTS>
 int launch_split(const DenseSplit &p, cudaStream_t st) {
-    const int bt = block_tokens(p.n_tokens), strips = (p.cols + kSplitCols - 1) / kSplitCols;
+    const int bt = dense_block_tokens(p.n_tokens), strips = (p.cols + kSplitCols - 1) / kSplitCols;
     const size_t grid = (size_t)strips * ((p.n_tokens + bt - 1) / bt);
     const bool wide = p.cols % 8 == 0 && (((uintptr_t)p.src | (uintptr_t)p.pre | (uintptr_t)p.parts) & 15) == 0;
     const int rc = wide ? launch(dense_split_kernel<T, P, PARTS, true>, grid, 256, st, p, bt)
@@ -253,11 +251,6 @@ int launch_few(const DenseFew &p, int n_sm, cudaStream_t st) {
 }
 
 }  // namespace
-
-int dense_sum_blocks(int n_tokens) {
-    const int bt = block_tokens(n_tokens);
-    return (n_tokens + bt - 1) / bt;
-}
 
 // (1 part of a 16-bit type: rounded slopes, or a copy with aligned rows; 0: sums alone)
 int launch_dense_split(const DenseSplit &p, cudaStream_t st) {

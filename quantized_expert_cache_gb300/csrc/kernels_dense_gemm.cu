@@ -450,7 +450,8 @@ long long share_out(long long n0, long long s0, long long n1, long long s1, long
     const long long more = n0 % workers, low = n0 / workers * s0, high = low + s0;
     const auto fits = [&](long long level, long long load) { return level > load ? (level - load) / s1 : 0; };
     const auto room = [&](long long level) { return more * fits(level, high) + (workers - more) * fits(level, low); };
-    long long from = 0, to = high + n1 * s1;
+    // between an even share of all and what the last tiles may add to it
+    long long from = (n0 * s0 + n1 * s1) / workers, to = std::max(from, high) + s0 + s1;
     while (from < to) {
         const long long level = (from + to) / 2;
         if (room(level) >= n1)

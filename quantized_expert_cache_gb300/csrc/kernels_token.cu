@@ -368,25 +368,38 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
         __syncthreads();
         int *n_cand = C > 1 ? cluster.map_shared_rank(&sh.n_cand, 0) : &sh.n_cand;
         unsigned long long *cands = C > 1 ? cluster.map_shared_rank(sh.cand, 0) : sh.cand;
-        const auto offer = [&](float x, int index) {
-            if (order_of(x) >= bound) {
-                const int at = atomicAdd(n_cand, 1);
-                if (at < kCand) cands[at] = candidate(x, index);
-            }
+        // A candidate of every lane that has one; false once there are too many.
+        const auto offer = [&](bool on, float x, int index) {
+            const unsigned who = __ballot_sync(0xffffffffu, on);
+            if (!who) return true;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(n_cand, __popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0);
+            const int mine_at = at + __popc(who & ((1u << lane) - 1));
+            if (on && mine_at < kCand) cands[mine_at] = candidate(x, index);
+            return at < kCand;
         };
-        if (edges && lane < r.edge) offer(x_edge, r.edge_at(lane));
+        bool room = true;
+        if (edges)
+            room = offer(lane < r.edge && order_of(x_edge) >= bound, x_edge, r.edge_at(lane));
         const int n_flagged = sh.n_flagged;
-        for (int f = warp; f < n_flagged; f += kTokenWarps) {
+        for (int f = warp; f < n_flagged && room; f += kTokenWarps) {
             const int first = (sh.flagged[f] << shift) * TILE;
-            for (int i = first; i < first + (TILE << shift); i += TILE) {
+            for (int i = first; i < first + (TILE << shift) && room; i += TILE) {
                 Pack16<T> v[U];
                 tile_load(v, i + lane);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const int at = i + 32 * k + lane;
-                    if (at < r.packs)
+                    unsigned high = 0;
 #pragma unroll
-                        for (int j = 0; j < N; ++j) offer(value<T>(v[k].v[j]), r.head + at * N + j);
+                    for (int j = 0; j < N; ++j) high = max(high, order_of(value<T>(v[k].v[j])));
+                    if (!__any_sync(0xffffffffu, at < r.packs && high >= bound)) continue;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float x = value<T>(v[k].v[j]);
+                        room &= offer(at < r.packs && order_of(x) >= bound, x, r.head + at * N + j);
+                    }
                 }
             }
         }
@@ -453,8 +466,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
                 unsigned high = 0;
 #pragma unroll
                 for (int j = 0; j < N; ++j) high = max(high, order_of(value<T>(v[k].v[j])));
-                const int at = i + 32 * k + lane;
-                const bool any = at < r.packs && high >= bound;
+                const int at = i + 32 * k + lane, e0 = r.head + at * N;
+                // (the best that the pack can hold: a masked row's many equal elements end here)
+                const unsigned long long most = (unsigned long long)high << 32 | (0xffffffffu - (unsigned)e0);
+                const bool any = at < r.packs && high >= bound && most > list.last;
                 if (!__any_sync(0xffffffffu, any)) continue;
 #pragma unroll 1
                 for (int j = 0; j < N; ++j) {
@@ -462,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
 #pragma unroll
                     for (int q = 0; q < N; ++q)
                         if (q == j) y = value<T>(v[k].v[q]);
-                    list.insert(any && order_of(y) >= bound ? candidate(y, r.head + at * N + j) : 0, p.n_top, lane);
+                    list.insert(any && order_of(y) >= bound ? candidate(y, e0 + j) : 0, p.n_top, lane);
                 }
             }
         }

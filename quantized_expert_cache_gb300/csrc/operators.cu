@@ -104,7 +104,7 @@ DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_t
     if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 3 * 2);
     s.z_parts = take(t * round_up(rows, 8) * std::max(gradient_parts(y_dtype, act != MOE_ACT_NONE, true, false),
                                                     gradient_parts(y_dtype, act != MOE_ACT_NONE, false, false)) * 2);
-    s.sums = take((size_t)moe::dense_sum_blocks(n_tokens) * rows * 4);
+    s.sums = take((size_t)moe::dense_most_blocks(n_tokens) * rows * 4);
     if (weight_shares(rows, cols) > 1) s.shares = take((size_t)weight_shares(rows, cols) * rows * cols * 4);
     return s;
 }

@@ -14,7 +14,6 @@ int launch_token_logprobs(const TokenParams &p, int, cudaStream_t st) {
 int launch_token_grad(const TokenGradParams &p, cudaStream_t st) {
     return launch("token_grad", st, p.logits, p.dlogits, p.n_tokens);
 }
-int dense_sum_blocks(int n_tokens) { return (n_tokens + 15) / 16; }
 int dense_steps(const DenseProduct &p) { return (p.K + 127) / 128 * p.n_pairs; }
 DensePlan dense_plan(const DenseProduct *, int n, int, int) { return DensePlan{256, 128, 1, 1, 1, n * 100.0}; }
 int launch_dense_few(const DenseFew &p, int, cudaStream_t st) { return launch("dense_few", st, p.x, p.o.out, p.n_tokens); }

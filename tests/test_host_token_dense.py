@@ -276,8 +276,12 @@ def test_dense_workspaces(lib, ctx, xd, wd, yd, act):
                 c.refuses(ws_bytes=need - 1, **at)
                 c.refuses(ws=None, **at)
                 c.refuses(ws=99 * A + 8, **at)
-    small, large = ask(5), ask(4000)
-    assert all(s <= l for s, l in zip(small, large))
+    # a workspace of more tokens serves fewer
+    before = (0, 0)
+    for tokens in range(1, 5000):
+        now = ask(tokens)
+        assert all(s <= l for s, l in zip(before, now)), tokens
+        before = now
     assert lib.moe_dense_workspace(ctx, xd, wd, yd, act, 5, 33, 64, None, None) == 0
     assert lib.moe_dense_workspace(ctx, xd, wd, yd, act, 5, 33, 60, ctypes.byref(f), ctypes.byref(b)) == -1
 
