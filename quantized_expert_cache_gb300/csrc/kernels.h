@@ -236,7 +236,7 @@ struct DenseSplit {
     float *sums;                // [cols] or null, through
     float *ws_sums;             // [dense_sum_blocks(n_tokens)][cols]
     int finish;                 // 1: sums are finished too; 0: the products' launch does
-    int beside;                 // 1: runs beside the call's other split, which goes before
+    int beside;                 // 1: runs beside the launch before it (of the same call), and ends after it
 };
 // Tokens of a block of column sums, the blocks, and a bound of them that does not fall as
 // the tokens rise.

@@ -93,8 +93,8 @@ constexpr int kSplitCols = 256;
 
 template <typename T, typename P, int PARTS, bool WIDE>
 __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int block_tokens) {
-    // (beside another split, which started after all work before the call was done and
-    // whose end is waited for below: this one's end then stands for both)
+    // (beside another kernel of the call, which started after all work before the call was
+    // done and whose end is waited for below: this one's end then stands for both)
     if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ float part_sum[8][kSplitCols];

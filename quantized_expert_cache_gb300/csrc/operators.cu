@@ -387,9 +387,11 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, gradient_parts(y_dtype, slope, f32_result, large_gradient(n_tokens, rows, cols))};
     const bool direct = !slope && y_dtype != MOE_F32 && rows % 8 == 0 && whole({d_dy}, 16);
     moe::DenseGemm g{};
-    const bool first = d_db || (product && !direct);
-    if (first) {
-        moe::DenseSplit s{};
+    moe::DenseSplit s{};
+    // dz goes first where the products need it; else its sums alone go last, beside the
+    // products' tail (4096^3 bf16: 8 us less)
+    const bool first = product && !direct;
+    if (d_db || first) {
         s.src = d_dy;
         s.pre = pre;
         s.dtype = y_dtype;
@@ -405,30 +407,31 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         }
         s.sums = d_db;
         s.ws_sums = (float *)(ws + space.sums);
-        s.finish = !product;
-        if (d_db && product) {
+        s.finish = !first;
+        if (d_db && first) {
             g.sum_parts = s.ws_sums;
             g.sums = d_db;
             g.sum_blocks = moe::dense_sum_blocks(n_tokens);
             g.sum_cols = rows;
         }
-        const int r = launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
-        if (r) return r;
+        if (first || !product) {
+            const int r = launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
+            if (r || !product) return r;
+        }
     }
-    if (!product) return MOE_OK;
     DenseMatrix xs{d_x, (size_t)cols, t, (size_t)cols, 1};
     if (d_dw && x_dtype == MOE_F32) {
-        moe::DenseSplit s{};
-        s.src = d_x;
-        s.dtype = x_dtype;
-        s.n_tokens = n_tokens;
-        s.cols = s.ld = cols;
-        s.parts = ws + space.x_parts;
-        s.n_parts = xs.parts = row_parts(x_dtype, dw_dtype == MOE_F32);
-        s.beside = first;
-        const int r = launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
+        moe::DenseSplit q{};
+        q.src = d_x;
+        q.dtype = x_dtype;
+        q.n_tokens = n_tokens;
+        q.cols = q.ld = cols;
+        q.parts = ws + space.x_parts;
+        q.n_parts = xs.parts = row_parts(x_dtype, dw_dtype == MOE_F32);
+        q.beside = first;
+        const int r = launched(ctx, "dense_backward", moe::launch_dense_split(q, st));
         if (r) return r;
-        xs.base = s.parts;
+        xs.base = q.parts;
     }
     DenseMatrix a[2], b[2];
     if (d_dw) {
@@ -459,7 +462,10 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
         g.p[i].o.ld = cols;
         dense_pairs(g.p[i], a[i].parts, b[i].parts, g.p[i].o.dtype == MOE_F32 ? 2 : 1);
     }
-    return dense_products(ctx, g, a, b, (float *)(ws + space.shares), c, st, "dense_backward");
+    const int r = dense_products(ctx, g, a, b, (float *)(ws + space.shares), c, st, "dense_backward");
+    if (r || first || !d_db) return r;
+    s.beside = 1;
+    return launched(ctx, "dense_backward", moe::launch_dense_split(s, st));
 }
 
 }  // extern "C"

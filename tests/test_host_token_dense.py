@@ -237,7 +237,7 @@ def test_dense_backward_launches(lib, ctx):
     c = backward(lib, ctx)
     c.takes(["dense_split", "dense_gemm"])
     c.takes(["dense_split", "dense_gemm"], act=0)                       # rows that are no multiple of 8
-    c.takes(["dense_split", "dense_gemm"], act=0, rows=32)              # the sums of dz
+    c.takes(["dense_gemm", "dense_split"], act=0, rows=32)              # the sums of dz, last
     c.takes(["dense_gemm"], act=0, rows=32, db=None)
     c.takes(["dense_split", "dense_gemm"], act=0, rows=32, db=None, dy=9 * A + 2)
     c.takes(["dense_split", "dense_split", "dense_gemm"], xd=F32)
