@@ -181,6 +181,53 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
     }
 }
 
+// Column sums alone, of what has no slope: the split's order of summation (and bits) with
+// four tokens' loads of a warp in flight and no more registers than that.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) dense_columns_kernel(DenseSplit p, int block_tokens) {
+    if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ float part_sum[8][kSplitCols];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int strips = (p.cols + kSplitCols - 1) / kSplitCols, c0 = blockIdx.x % strips * kSplitCols;
+    const int block = blockIdx.x / strips;
+    const auto col = [&](int j) { return c0 + (WIDE ? lane * 8 + j : j * 32 + lane); };
+    const size_t t0 = (size_t)block * block_tokens, t1 = min(t0 + block_tokens, (size_t)p.n_tokens);
+    float sum[8] = {};
+    for (size_t t = t0 + warp; t < t1; t += 32) {
+        Pack<T, 8> v[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            v[d] = Pack<T, 8>{};
+            const T *src = (const T *)p.src + (t + 8 * d) * p.cols;
+            if (t + 8 * d >= t1) continue;
+            if (WIDE) {
+                if (col(0) < p.cols) v[d] = *(const Pack<T, 8> *)(src + col(0));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col(j) < p.cols) v[d].v[j] = src[col(j)];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            if (t + 8 * d < t1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += value<T>(v[d].v[j]);
+    }
+    if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part_sum[warp][col(j) - c0] = sum[j];
+    __syncthreads();
+    const int c = c0 + threadIdx.x;
+    if (c < p.cols) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += part_sum[w][threadIdx.x];
+        p.ws_sums[(size_t)block * p.cols + c] = s;
+    }
+}
+
 __global__ void __launch_bounds__(32) dense_sums_kernel(const float *part, float *sums, int blocks, int cols) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -226,8 +273,13 @@ int launch_split(const DenseSplit &p, cudaStream_t st) {
     const int bt = dense_block_tokens(p.n_tokens), strips = (p.cols + kSplitCols - 1) / kSplitCols;
     const size_t grid = (size_t)strips * ((p.n_tokens + bt - 1) / bt);
     const bool wide = p.cols % 8 == 0 && (((uintptr_t)p.src | (uintptr_t)p.pre | (uintptr_t)p.parts) & 15) == 0;
-    const int rc = wide ? launch(dense_split_kernel<T, P, PARTS, true>, grid, 256, st, p, bt)
-                        : launch(dense_split_kernel<T, P, PARTS, false>, grid, 256, st, p, bt);
+    int rc;
+    if (PARTS == 0 && !p.pre)
+        rc = wide ? launch(dense_columns_kernel<T, true>, grid, 256, st, p, bt)
+                  : launch(dense_columns_kernel<T, false>, grid, 256, st, p, bt);
+    else
+        rc = wide ? launch(dense_split_kernel<T, P, PARTS, true>, grid, 256, st, p, bt)
+                  : launch(dense_split_kernel<T, P, PARTS, false>, grid, 256, st, p, bt);
     if (rc || !p.sums || !p.finish) return rc;
     return launch(dense_sums_kernel, (p.cols + 7) / 8, 32, st, (const float *)p.ws_sums, p.sums,
                   dense_sum_blocks(p.n_tokens), p.cols);
