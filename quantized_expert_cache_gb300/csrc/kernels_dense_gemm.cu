@@ -11,15 +11,27 @@
 // swizzle that the MMA's descriptors name; nothing is transposed.  A thread of the epilogue has one m and
 // many n, so a warp writes 32 neighbours of the result at a time.
 //
-// The accumulators are drained every 512 of k (kChunk32) and added up in
-// registers, rounded to nearest: the tensor core's own fp32 accumulation truncates, a
-// bias of about 2^-24 a step on a growing sum.  For 16-bit results, whose own rounding
-// is 2^-12 and more, every 2048 (kChunk16): the drains' reads of TMEM hold the
-// products up (8192^3 697 us and 658, 4096 x 8192 x 2048 115 and 103).  Two accumulators in turn hide most of it, and the epilogue of a tile behind
-// the next one's products.
+// The accumulators are drained every 512 of k (kChunk32) and added up in registers,
+// rounded to nearest: the tensor core's own fp32 accumulation truncates, a bias of about
+// 2^-24 a step on a growing sum.  Every 2048 (kChunk16) for 16-bit results, whose own
+// rounding is 2^-12 and more, and for products of lower parts, which are small beside the
+// last pair's: the drains' reads of TMEM hold the products up (8192^3 697 us at 512,
+// 658 at 2048; 4096 x 8192 x 2048 115 and 103, in the forms of that time).  Two
+// accumulators in turn hide most of it, and the epilogue of a tile behind the next one's
+// products.
 //
 // Where there are fewer tiles than SMs, a tile's steps are shared out over a cluster
-// of CTAs and their sums joined through distributed shared memory, in order.
+// of CTAs and their sums joined through distributed shared memory, in order; or, in a
+// weights' gradient, over tiles of their own whose sums are joined in the workspace.
+//
+// Bound.  8192^3 bf16 609 us, 4096^3 99, 4096 x 8192 x 2048 89 (the library's product 545,
+// 80 and 74; all with a cold cache); both gradients of 4096^3 168 (1630 TFLOP/s, 0.85 of
+// the measured rate; tensor pipe active 76% of the time).  What a step takes in: by
+// count 64 KB for 1024 clocks of products, near what an SM draws from L2 (without
+// loads 8192^3 took 507 us, without products 564).  Activations and a second output add
+// their epilogue: 97 us with silu and pre-activations.  8 tokens on 65536 x 2048: HBM,
+// 45 us = 0.88 of a copy.  33 on 2887 x 2880 8.1 us: latency of the launch, one
+// round of steps and the join.
 #include <cuda.h>
 #include <cooperative_groups.h>
 
@@ -136,7 +148,11 @@ __device__ __forceinline__ void commit_warp(uint32_t bar, int ctas) {
 struct Tile {
     const DenseProduct *p;
     int m0, n0, kb, first, last;  // kb: steps of one pair of parts; [first, last): this CTA's
-    int chunk, share;
+    int low, chunk, share;        // low: steps of all pairs but the last, the largest products
+    // the step after the last one that is added up in TMEM from step i on
+    __device__ __forceinline__ int chunk_end(int i) const {
+        return i < low ? min(min(last, low), i + kChunk16) : min(last, i + chunk);
+    }
 };
 
 // The j-th tile of worker w (a cluster), or false.  Workers take the first product's
@@ -176,6 +192,7 @@ __device__ __forceinline__ bool tile_of(const DenseGemm &g, int worker, int work
     r.first = (int)(steps * split / of);
     r.last = (int)(steps * (split + 1) / of);
     r.chunk = r.p->o.dtype == 0 ? kChunk32 : kChunk16;
+    r.low = r.kb * (r.p->n_pairs - 1);
     return true;
 }
 
@@ -313,7 +330,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, a_half = (a_mn ? 8192 : C::A_BYTES / 2) >> 4;
             const uint32_t b_step = (b_mn ? 2048 : 32) >> 4, b_half = (b_mn ? 8192 : C::B_BYTES / 2) >> 4;
             for (int i = w.first; i < w.last; ++chunk) {
-                const int buf = chunk & 1, end = min(w.last, i + w.chunk);
+                const int buf = chunk & 1, end = w.chunk_end(i);
                 if (!mbar_wait_warp(acc_empty(buf), (chunk >> 1 & 1) ^ 1, abort_flag, g.error, kErrorDense)) goto multiplied;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-            for (int i = w.first; i < w.last; i += w.chunk, ++chunk) {
+            for (int i = w.first; i < w.last; i = w.chunk_end(i), ++chunk) {
                 const int buf = chunk & 1;
                 if (!mbar_wait_warp(acc_full(buf), chunk >> 1 & 1, abort_flag, g.error, kErrorDense)) goto finished;
                 tc_fence_after();

@@ -135,11 +135,12 @@ struct DenseMatrix {
     int parts;
 };
 
-// The pairs of parts a product takes, those up to `most` of the places in all.
+// The pairs of parts a product takes, those up to `most` of the places in all, the largest
+// products last.
 void dense_pairs(moe::DenseProduct &p, int a_parts, int b_parts, int most) {
     p.n_pairs = 0;
     p.pairs = 0;
-    for (int sum = 0; sum <= most; ++sum)
+    for (int sum = most; sum >= 0; --sum)
         for (int a = 0; a <= sum; ++a)
             if (a < a_parts && sum - a < b_parts)
                 p.pairs |= (unsigned)(a | (sum - a) << 2) << (4 * p.n_pairs++);
