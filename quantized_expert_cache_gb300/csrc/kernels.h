@@ -219,8 +219,16 @@ struct DenseOut {
     void *pre;                  // as out, the sums before the activation, or null
     int dtype, act, ld;
 };
-// Few tokens: y = act(x W^T + bias) + res, a warp to some rows of W.
-constexpr int kDenseFew = 4;
+// Few tokens: y = act(x W^T + bias) + res, warps to rows of W.  us there and on the tensor
+// cores at 2, 3 and 4 tokens (bf16 rows, fp32 result): 512 x 2048 3.0, 3.4, 3.5 and 5.5;
+// 2880 x 2880 7.2, 8.5, 8.3 and 7.9; 8192 x 2048 7.8, 10.4, 10.0 and 9.8; 8192 x 8192 25.6,
+// 35.4, 33.1 and 26.6, 26.1, 24.8; 65536 x 2048 44.3, 52.9, 56.1 and 43.4, 43.8, 44.1.
+inline bool dense_takes_few(int n_tokens, int rows, int cols) {
+    return n_tokens <= 2 || (n_tokens <= 4 && (long long)rows * cols <= 1 << 21);
+}
+// Up to so many tokens the parts of fp32 rows are columns of one product, which reads
+// the weights once; above they are further steps of it.
+constexpr int kDenseFold = 64;
 struct DenseFew {
     const void *x, *w;          // [n_tokens][cols], [rows][cols]
     int x_dtype, w_dtype, n_tokens, rows, cols;
@@ -231,8 +239,8 @@ struct DenseSplit {
     const void *src;            // [n_tokens][cols] of dtype
     const void *pre;            // as src: multiplied by the activation's slope there, or null
     int dtype, act, n_tokens, cols;
-    void *parts;                // [n_parts][n_tokens][ld] of part_dtype, or null
-    int part_dtype, n_parts, ld;
+    void *parts;                // [n_parts][n_tokens][ld], or by_row: [n_tokens][n_parts][ld]; or null
+    int n_parts, ld, by_row;
     float *sums;                // [cols] or null, through
     float *ws_sums;             // [dense_sum_blocks(n_tokens)][cols]
     int finish;                 // 1: sums are finished too; 0: the products' launch does
@@ -252,6 +260,7 @@ struct DenseProduct {
     int M, N, K;
     int a_mn, b_mn;             // 1: stored [k][m] or [k][n]; 0: [m][k], [n][k]
     int bf16;                   // operands: 1 bfloat16, 0 binary16
+    int fold;                   // 1: N counts columns of B, four to a token, whose sum is the token's
     int n_pairs;
     unsigned pairs;             // 4 bits each, the first lowest: part of A | part of B << 2
     int m_tiles, n_tiles;

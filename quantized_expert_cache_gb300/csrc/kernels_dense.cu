@@ -33,40 +33,42 @@ struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack {
 };
 
 // ---- few tokens ---------------------------------------------------------------
-// ROWS rows of W a warp, T tokens, DEPTH packs of 8 columns in flight a row.
-template <typename TX, typename TW, int T, int ROWS>
+// ROWS rows of W and T tokens to KW warps (of a row's packs every KW-th 32), DEPTH
+// packs of 8 columns in flight a row.
+template <typename TX, typename TW, int T, int ROWS, int KW>
 __global__ void __launch_bounds__(256) dense_few_kernel(DenseFew p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int DEPTH = 8 / ROWS;
+    constexpr int DEPTH = 8 / ROWS, STEP = 32 * KW;
+    static_assert(KW == 1 || ROWS == 1, "one row to several warps");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, packs = p.cols / 8;
-    const size_t r0 = ((size_t)blockIdx.x * 8 + warp) * ROWS;
-    if (r0 >= (size_t)p.rows) return;
+    const size_t r0 = ((size_t)blockIdx.x * (8 / KW) + warp / KW) * ROWS;
+    if (KW == 1 && r0 >= (size_t)p.rows) return;
     const TX *x = (const TX *)p.x;
     const TW *w[ROWS];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r)  // (the last warp's rows past the end are its last one)
+    for (int r = 0; r < ROWS; ++r)  // (rows past the end are the last one)
         w[r] = (const TW *)p.w + min(r0 + r, (size_t)p.rows - 1) * p.cols;
     float acc[ROWS][T];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[r][t] = 0.0f;
-    for (int c0 = lane; c0 < packs; c0 += 32 * DEPTH) {
+    for (int c0 = lane + 32 * (warp % KW); c0 < packs; c0 += STEP * DEPTH) {
         Pack<TW, 8> v[DEPTH][ROWS];
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 v[d][r] = Pack<TW, 8>{};
-                if (c0 + 32 * d < packs) *(uint4 *)&v[d][r] = __ldcs((const uint4 *)w[r] + c0 + 32 * d);
+                if (c0 + STEP * d < packs) *(uint4 *)&v[d][r] = __ldcs((const uint4 *)w[r] + c0 + STEP * d);
             }
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            if (c0 + 32 * d >= packs) break;
+            if (c0 + STEP * d >= packs) break;
 #pragma unroll
             for (int t = 0; t < T; ++t) {
-                const Pack<TX, 8> a = *((const Pack<TX, 8> *)(x + (size_t)t * p.cols) + c0 + 32 * d);
+                const Pack<TX, 8> a = *((const Pack<TX, 8> *)(x + (size_t)t * p.cols) + c0 + STEP * d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -75,16 +77,26 @@ __global__ void __launch_bounds__(256) dense_few_kernel(DenseFew p) {
             }
         }
     }
+    float mine = 0.0f;  // lane i: row i / T, token i % T
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             const float s = warp_sum_f(acc[r][t]);
-            if (lane == (r * T + t) % 32) acc[0][0] = s;
+            if (lane == r * T + t) mine = s;
         }
+    if (KW > 1) {
+        __shared__ float part[8][T];
+        if (lane < T) part[warp][lane] = mine;
+        __syncthreads();
+        if (warp % KW != 0) return;
+        if (lane < T)
+#pragma unroll
+            for (int k = 1; k < KW; ++k) mine += part[warp + k][lane];
+    }
     if (lane < ROWS * T) {
         const size_t m = r0 + lane / T;
-        if (m < (size_t)p.rows) finish(p.o, m, lane % T, p.o.bias ? p.o.bias[m] : 0.0f, acc[0][0]);
+        if (m < (size_t)p.rows) finish(p.o, m, lane % T, p.o.bias ? p.o.bias[m] : 0.0f, mine);
     }
 }
 
@@ -158,7 +170,7 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
                     // infinities and NaN are their first part
                     v[j] = isfinite(value<P>(o.v[j])) ? left : 0.0f;
                 }
-                P *dst = (P *)p.parts + ((size_t)q * p.n_tokens + t) * p.ld;
+                P *dst = (P *)p.parts + (p.by_row ? t * PARTS + q : (size_t)q * p.n_tokens + t) * p.ld;
                 if (WIDE) {
                     if (col(0) < p.cols) *(Pack<P, 8> *)(dst + col(0)) = o;
                 } else {
@@ -287,21 +299,24 @@ int launch_split(const DenseSplit &p, cudaStream_t st) {
                   dense_sum_blocks(p.n_tokens), p.cols);
 }
 
-template <typename TX, typename TW, int ROWS>
+template <typename TX, typename TW, int ROWS, int KW>
 int launch_few_rows(const DenseFew &p, cudaStream_t st) {
-    const size_t grid = ((size_t)p.rows + 8 * ROWS - 1) / (8 * ROWS);
+    const int rows = 8 / KW * ROWS;
+    const size_t grid = ((size_t)p.rows + rows - 1) / rows;
     switch (p.n_tokens) {
-        case 1: return launch(dense_few_kernel<TX, TW, 1, ROWS>, grid, 256, st, p);
-        case 2: return launch(dense_few_kernel<TX, TW, 2, ROWS>, grid, 256, st, p);
-        case 3: return launch(dense_few_kernel<TX, TW, 3, ROWS>, grid, 256, st, p);
-        default: return launch(dense_few_kernel<TX, TW, 4, ROWS>, grid, 256, st, p);
+        case 1: return launch(dense_few_kernel<TX, TW, 1, ROWS, KW>, grid, 256, st, p);
+        case 2: return launch(dense_few_kernel<TX, TW, 2, ROWS, KW>, grid, 256, st, p);
+        case 3: return launch(dense_few_kernel<TX, TW, 3, ROWS, KW>, grid, 256, st, p);
+        default: return launch(dense_few_kernel<TX, TW, 4, ROWS, KW>, grid, 256, st, p);
     }
 }
 
 template <typename TX, typename TW>
 int launch_few(const DenseFew &p, int n_sm, cudaStream_t st) {
-    // a row a warp while that leaves warps to spare: more of them, shorter
-    return p.rows <= n_sm * 32 ? launch_few_rows<TX, TW, 1>(p, st) : launch_few_rows<TX, TW, 2>(p, st);
+    // four warps a row where rows are few and long, a warp a row while that leaves warps to
+    // spare: more of them, shorter
+    if (p.rows <= n_sm * 8 && p.cols >= 1024) return launch_few_rows<TX, TW, 1, 4>(p, st);
+    return p.rows <= n_sm * 32 ? launch_few_rows<TX, TW, 1, 1>(p, st) : launch_few_rows<TX, TW, 2, 1>(p, st);
 }
 
 }  // namespace

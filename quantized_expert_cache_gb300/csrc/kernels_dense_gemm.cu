@@ -20,6 +20,10 @@
 // accumulators in turn hide most of it, and the epilogue of a tile behind the next one's
 // products.
 //
+// Few tokens of fp32 rows: their parts are columns of B, four to a token (the fourth
+// zero), and a token's four sums are added in the epilogue: the weights are read once
+// (8 tokens on 65536 x 2048: 91 us with a pass for each part).
+//
 // Where there are fewer tiles than SMs, a tile's steps are shared out over a cluster
 // of CTAs and their sums joined through distributed shared memory, in order; or, in a
 // weights' gradient, over tiles of their own whose sums are joined in the workspace.
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             for (int j = 0; tile(j, w); ++j) {
                 // (what a step needs in registers: a load of the parameters costs each step more
                 // than its copies' issue)
-                const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn;
+                const bool a_mn = w.p->a_mn, b_mn = w.p->b_mn, fold = w.p->fold;
                 const CUtensorMap *tm_a = &w.p->tm_a, *tm_b = &w.p->tm_b;
                 const int m0 = w.m0 + side * kBM, n0 = w.n0 + side * C::BR, k_end = w.kb * kBK;
                 int k = w.first % w.kb * kBK;
@@ -291,7 +295,10 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                         load(a, tm_a, k, m0, part_a);
                         load(a + C::A_BYTES / 2, tm_a, k + 64, m0, part_a);
                     }
-                    if (C::BR >= 64 && b_mn) {
+                    if (fold) {
+                        load(b, tm_b, k, 0, n0 / 4);
+                        load(b + C::B_BYTES / 2, tm_b, k + 64, 0, n0 / 4);
+                    } else if (C::BR >= 64 && b_mn) {
 #pragma unroll
                         for (int c = 0; c < C::BR / 64; ++c) load(b + c * kChunkMn, tm_b, n0 + 64 * c, k, part_b);
                     } else {
@@ -395,6 +402,20 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                 float *red = (float *)smem;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) red[(share * NC + c) * kBM + ml] = acc[c];
+            } else if (w.p->fold) {
+                const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + quarter * 32 + (lane & 7) * 4, 0);
+                float *mine = (float *)(smem + C::STAGING) + (warp - kWEpi) * GROUP * 32;
+                // (the lowest parts first)
+#pragma unroll
+                for (int c = 0; c < NC; c += 4 * GROUP) {
+                    constexpr int TOKENS = NC / 4 < GROUP ? NC / 4 : GROUP;
+#pragma unroll
+                    for (int j = 0; j < TOKENS; ++j)
+                        mine[j * 32 + lane] = (acc[c + 4 * j + 2] + acc[c + 4 * j + 1]) + acc[c + 4 * j];
+                    __syncwarp();
+                    e.store(mine, TOKENS, (n0 + c) / 4, w.p->N / 4, lane);
+                    __syncwarp();
+                }
             } else {
                 const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + quarter * 32 + (lane & 7) * 4,
                                         (size_t)w.share * w.p->M * w.p->N);
@@ -421,17 +442,20 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             tile(0, w);
             const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + lane * 4, 0);
             const float4 *red = (const float4 *)smem + lane;
-            const int cols = min(BN, w.p->N - w.n0);
+            const int fold = w.p->fold ? 4 : 1, cols = min(BN, w.p->N - w.n0) / fold;
             for (int c = split * (C::THREADS / 32) + warp; c < cols; c += S * (C::THREADS / 32)) {
-                float4 v[kMaxSplits];
+                float sum[4] = {};
+                for (int f = fold - 1; f >= 0; --f) {  // (the lowest parts first)
+                    float4 v[kMaxSplits];
 #pragma unroll
-                for (int s = 0; s < kMaxSplits; ++s)
-                    if (s < S) v[s] = *cluster.map_shared_rank(red + c * (kBM / 4), PAIR ? 2 * s + side : s);
-                float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                    for (int s = 0; s < kMaxSplits; ++s)
+                        if (s < S)
+                            v[s] = *cluster.map_shared_rank(red + (c * fold + f) * (kBM / 4), PAIR ? 2 * s + side : s);
 #pragma unroll
-                for (int s = 1; s < kMaxSplits; ++s)
-                    if (s < S) sum[0] += v[s].x, sum[1] += v[s].y, sum[2] += v[s].z, sum[3] += v[s].w;
-                if (e.left > 0) e.column(sum, w.n0 + c);
+                    for (int s = 0; s < kMaxSplits; ++s)
+                        if (s < S) sum[0] += v[s].x, sum[1] += v[s].y, sum[2] += v[s].z, sum[3] += v[s].w;
+                }
+                if (e.left > 0) e.column(sum, w.n0 / fold + c);
             }
         }
         __syncwarp();

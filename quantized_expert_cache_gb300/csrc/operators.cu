@@ -98,7 +98,7 @@ DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_t
     };
     const size_t t = (size_t)n_tokens;
     if (!backward) {
-        if (x_dtype == MOE_F32 && n_tokens > moe::kDenseFew) s.x_parts = take(t * cols * 3 * 2);
+        if (x_dtype == MOE_F32 && !moe::dense_takes_few(n_tokens, rows, cols)) s.x_parts = take(t * cols * 3 * 2);
         return s;
     }
     if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 3 * 2);
@@ -109,8 +109,10 @@ DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_t
     return s;
 }
 
+// [part][outer][inner] in boxes of 64 x box_outer; fold: [outer][part][inner], a box has four
+// parts (those past the last are zero) of a fourth as many rows.
 int encode_map(moe_ctx *ctx, CUtensorMap *tm, const void *base, bool bf16, size_t inner, size_t outer, size_t ld,
-               int parts, uint32_t box_outer) {
+               int parts, uint32_t box_outer, bool fold) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -119,8 +121,9 @@ int encode_map(moe_ctx *ctx, CUtensorMap *tm, const void *base, bool bf16, size_
         return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? (PFN_cuTensorMapEncodeTiled_v12000)fn : nullptr;
     }();
     if (!encode) return fail(ctx, MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
-    const cuuint64_t dims[3] = {inner, outer, (cuuint64_t)parts}, strides[2] = {ld * 2, outer * ld * 2};
-    const cuuint32_t box[3] = {64, box_outer, 1}, one[3] = {1, 1, 1};
+    const cuuint64_t n_parts = (cuuint64_t)parts, middle = fold ? n_parts : outer, last = fold ? outer : n_parts;
+    const cuuint64_t dims[3] = {inner, middle, last}, strides[2] = {ld * 2, middle * ld * 2};
+    const cuuint32_t box[3] = {64, fold ? 4 : box_outer, fold ? box_outer / 4 : 1}, one[3] = {1, 1, 1};
     const CUresult r = encode(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                               (void *)base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -160,10 +163,10 @@ int dense_launch(moe_ctx *ctx, moe::DenseGemm &g, const DenseMatrix *a, const De
     for (int i = 0; i < g.n_products; ++i) {
         moe::DenseProduct &p = g.p[i];
         const int rc = encode_map(ctx, &p.tm_a, a[i].base, p.bf16, a[i].inner, a[i].outer, a[i].ld, a[i].parts,
-                                  128);
+                                  128, false);
         if (rc) return rc;
         const int rd = encode_map(ctx, &p.tm_b, b[i].base, p.bf16, b[i].inner, b[i].outer, b[i].ld, b[i].parts,
-                                  p.b_mn ? 128 : (uint32_t)plan.box);
+                                  p.b_mn ? 128 : (uint32_t)plan.box, p.fold);
         if (rd) return rd;
     }
     const int rc = launched(ctx, what, moe::launch_dense_gemm(g, plan, c.device, c.n_sm, st));
@@ -312,7 +315,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
     const cudaStream_t st = stream ? (cudaStream_t)stream : c.stream;
     const OnDevice on(c.device);
     const moe::DenseOut out{d_y, d_bias, d_res, d_pre, y_dtype, act, rows};
-    if (n_tokens <= moe::kDenseFew) {
+    if (moe::dense_takes_few(n_tokens, rows, cols)) {
         const moe::DenseFew f{d_x, d_w, x_dtype, w_dtype, n_tokens, rows, cols, out};
         return launched(ctx, "dense", moe::launch_dense_few(f, c.n_sm, st));
     }
@@ -325,6 +328,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
         s.cols = s.ld = cols;
         s.parts = (uint8_t *)ws + space.x_parts;
         s.n_parts = x.parts;
+        s.by_row = n_tokens <= moe::kDenseFold;
         const int r = launched(ctx, "dense", moe::launch_dense_split(s, st));
         if (r) return r;
         x.base = s.parts;
@@ -337,7 +341,11 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
     g.p[0].K = cols;
     g.p[0].bf16 = w_dtype == MOE_BF16;
     g.p[0].o = out;
-    dense_pairs(g.p[0], 1, x.parts, x.parts - 1);
+    if (x.parts > 1 && n_tokens <= moe::kDenseFold) {
+        g.p[0].fold = 1;
+        g.p[0].N = 4 * n_tokens;
+    }
+    dense_pairs(g.p[0], 1, g.p[0].fold ? 1 : x.parts, x.parts - 1);
     return dense_products(ctx, g, &w, &x, nullptr, c, st, "dense");
 }
 
