@@ -624,10 +624,10 @@ int moe_token_logprobs_grad(moe_ctx *ctx, const void *d_logits, int dtype, const
  * [n_tokens][rows] of y_dtype, which is MOE_F32 or w_dtype.  cols: a multiple of 8.
  * d_x, d_w and d_ws are 16-byte aligned, the others to their elements.  Sums in fp32;
  * fp32 rows enter with all their 24 bits (16 for a 16-bit result) but for what lies
- * below 2^-133.  Up to 2 tokens, and 3 or 4 on up to
- * 2^21 weights, a plain fp32 sum, others on the tensor cores: the bits
- * of a token's result depend on the batch's size.  NaN and infinities spread as in the
- * formulas.  A bounded wait that expires is reported by the next cache_step or
+ * below 2^-133.  Up to 2 tokens, and 3 or 4 on up to 2^22 weights, a plain fp32 sum,
+ * others on the tensor cores: the bits of a token's result depend on the batch's size.
+ * NaN and infinities spread as in the formulas.  A bounded wait that expires is
+ * reported by the next cache_step or
  * miss_drain (MOE_ERR_FAULT).  d_ws: moe_dense_workspace's forward_bytes, the call's
  * own while it runs (0 bytes: NULL).  Asynchronous on `stream` (NULL: the context's),
  * any stream; capturable (a captured graph holds its buffers' addresses).  No output

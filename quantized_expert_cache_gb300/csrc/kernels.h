@@ -220,11 +220,12 @@ struct DenseOut {
     int dtype, act, ld;
 };
 // Few tokens: y = act(x W^T + bias) + res, warps to rows of W.  us there and on the tensor
-// cores at 2, 3 and 4 tokens (bf16 rows, fp32 result): 512 x 2048 3.0, 3.4, 3.5 and 5.5;
-// 2880 x 2880 7.2, 8.5, 8.3 and 7.9; 8192 x 2048 7.8, 10.4, 10.0 and 9.8; 8192 x 8192 25.6,
-// 35.4, 33.1 and 26.6, 26.1, 24.8; 65536 x 2048 44.3, 52.9, 56.1 and 43.4, 43.8, 44.1.
+// cores at 2, 3 and 4 tokens (bf16 rows, fp32 result): 512 x 2048 2.0, 2.3, 2.7 and 5.5;
+// 512 x 8192 4.0, 4.3, 5.1 and 7.7; 2048 x 2048 3.8, 4.1, 5.0 and 6.7; 1000 x 8192 5.9, 6.5,
+// 8.7 and 8.4; 2880 x 2880 7.2, 8.5, 8.3 and 8.2; 8192 x 2048 7.6, 10.4, 10.0 and 9.9; 8192 x
+// 8192 25.5, 35.4, 33.1 and 26.2; 65536 x 2048 44.3, 52.9, 56.1 and 43.8.
 inline bool dense_takes_few(int n_tokens, int rows, int cols) {
-    return n_tokens <= 2 || (n_tokens <= 4 && (long long)rows * cols <= 1 << 21);
+    return n_tokens <= 2 || (n_tokens <= 4 && (long long)rows * cols <= 1 << 22);
 }
 // Up to so many tokens the parts of fp32 rows are columns of one product, which reads
 // the weights once; above they are further steps of it.

@@ -112,7 +112,7 @@ def check_forward(s, types, got, act=qec.ACT_NONE, bias=False, res=False, norm=T
     t, c = x.shape
     a = x.abs() @ w.abs().t()
     ref = x @ w.t()
-    few = t <= 2 or (t <= 4 and s["w"].numel() <= 1 << 21)
+    few = t <= 2 or (t <= 4 and s["w"].numel() <= 1 << 22)
     tol = sums_tol(a, c, 1 if types[0] != F32 else 3, few, types[2] == F32)
     if norm and act == qec.ACT_NONE and not bias and not res:
         if not few and c >= 64:
