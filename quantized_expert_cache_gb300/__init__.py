@@ -347,6 +347,18 @@ def moe_router_loss(ctx, logits, idx, mask, gw, n_tokens, n_experts, k, balance_
                                               _stream(stream)))
 
 
+def _address(x) -> int | None:
+    """_dev(), the common case first."""
+    if x is None or x.__class__ is int:
+        return x
+    try:
+        if x.is_cuda and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    return _dev(x)
+
+
 def _of_dtype(x, dtype) -> int | None:
     """_dev() of a tensor that must be of `dtype` (an MOE_ code)."""
     if x is None or x.__class__ is int:
@@ -361,28 +373,37 @@ def _of_dtype(x, dtype) -> int | None:
     return _dev(x)
 
 
+def _typed(x, dtype) -> tuple:
+    """(address, MOE_ code) of a tensor of any type the operators take, or of `dtype`."""
+    if dtype is not None:
+        return _of_dtype(x, dtype), dtype
+    try:
+        return _address(x), _DTYPES[x.dtype]
+    except (AttributeError, KeyError):
+        return _dev(x), _dtype(x)
+
+
 def moe_token_logprobs(ctx, logits, targets, n_tokens, vocab, logp, entropy=None, n_top=0, top_idx=None,
                        top_logp=None, stats=None, scale=1.0, dtype=None, stream=None):
     """Log probabilities of targets (int32, below 0: none) under softmax(scale *
     logits), entropies, the n_top largest logits with theirs, and the stats the
     gradient reads; outputs may be None.  dtype: logits' by default."""
-    dtype = _dtype(logits) if dtype is None else dtype
-    return _check(ctx, load().moe_token_logprobs(ctx, _of_dtype(logits, dtype), dtype, _elem(targets, _IDS), n_tokens,
-                                                 vocab, scale, n_top, _elem(logp, _FP32), _elem(entropy, _FP32),
-                                                 _elem(top_idx, _IDS), _elem(top_logp, _FP32), _elem(stats, _FP32),
-                                                 _stream(stream)))
+    at, dtype = _typed(logits, dtype)
+    rc = (_lib or load()).moe_token_logprobs(
+        ctx, at, dtype, _elem(targets, _IDS), n_tokens, vocab, scale, n_top, _elem(logp, _FP32), _elem(entropy, _FP32),
+        _elem(top_idx, _IDS), _elem(top_logp, _FP32), _elem(stats, _FP32), _stream(stream))
+    return rc and _check(ctx, rc)
 
 
 def moe_token_logprobs_grad(ctx, logits, targets, n_tokens, vocab, stats, entropy, g_logp, g_entropy, dlogits,
                             scale=1.0, dtype=None, stream=None):
     """dlogits (of logits' dtype, may be logits) from the gradients of the log
     probabilities and of the entropies; one of these may be None."""
-    dtype = _dtype(logits) if dtype is None else dtype
-    return _check(ctx, load().moe_token_logprobs_grad(ctx, _of_dtype(logits, dtype), dtype, _elem(targets, _IDS),
-                                                      n_tokens, vocab, scale, _elem(stats, _FP32),
-                                                      _elem(entropy, _FP32), _elem(g_logp, _FP32),
-                                                      _elem(g_entropy, _FP32), _of_dtype(dlogits, dtype),
-                                                      _stream(stream)))
+    at, dtype = _typed(logits, dtype)
+    rc = (_lib or load()).moe_token_logprobs_grad(
+        ctx, at, dtype, _elem(targets, _IDS), n_tokens, vocab, scale, _elem(stats, _FP32), _elem(entropy, _FP32),
+        _elem(g_logp, _FP32), _elem(g_entropy, _FP32), _of_dtype(dlogits, dtype), _stream(stream))
+    return rc and _check(ctx, rc)
 
 
 def _dtype_of(x) -> int:
@@ -390,10 +411,6 @@ def _dtype_of(x) -> int:
     if isinstance(x, int):
         return x
     return _dtype(x) if hasattr(x, "dtype") else _DTYPES[_type_name(x)]
-
-
-def _space(ws) -> tuple:
-    return (None, 0) if ws is None else (_dev(ws), ws.nbytes)
 
 
 def moe_dense_workspace(ctx, x, w, y, act, n_tokens, rows, cols) -> tuple:
@@ -410,13 +427,13 @@ def moe_dense_forward(ctx, x, w, n_tokens, rows, cols, y, bias=None, act=ACT_NON
     """y = act(x W^T + bias) + res, pre = the sums before the activation; fp32
     bias; ws: a tensor of moe_dense_workspace's bytes.  The dtypes: those of x, w
     and y by default (an address has none: give its own)."""
-    xd = _dtype(x) if x_dtype is None else x_dtype
-    wd = _dtype(w) if w_dtype is None else w_dtype
-    yd = _dtype(y) if y_dtype is None else y_dtype
-    at, size = _space(ws)
-    return _check(ctx, load().moe_dense_forward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _elem(bias, _FP32),
-                                                act, _of_dtype(res, yd), n_tokens, rows, cols, _of_dtype(y, yd), yd,
-                                                _of_dtype(pre, yd), at, size, _stream(stream)))
+    x, xd = _typed(x, x_dtype)
+    w, wd = _typed(w, w_dtype)
+    y, yd = _typed(y, y_dtype)
+    rc = (_lib or load()).moe_dense_forward(
+        ctx, x, xd, w, wd, _elem(bias, _FP32), act, _of_dtype(res, yd), n_tokens, rows, cols, y, yd,
+        _of_dtype(pre, yd), _address(ws), 0 if ws is None else ws.nbytes, _stream(stream))
+    return rc and _check(ctx, rc)
 
 
 def moe_dense_backward(ctx, x, w, dy, n_tokens, rows, cols, dx=None, dw=None, db=None, act=ACT_NONE, pre=None,
@@ -424,15 +441,14 @@ def moe_dense_backward(ctx, x, w, dy, n_tokens, rows, cols, dx=None, dw=None, db
     """dx (of x's dtype), dw (fp32 or w's dtype) and db (fp32) of a dense layer,
     any of them None; x is read for dw only, w for dx only: the other may be None
     with its dtype given.  ws: a tensor of moe_dense_workspace's bytes."""
-    xd = _dtype(x) if x_dtype is None else x_dtype
-    wd = _dtype(w) if w_dtype is None else w_dtype
-    yd = _dtype(dy) if y_dtype is None else y_dtype
-    dwd = _dtype(dw) if dw_dtype is None else dw_dtype
-    at, size = _space(ws)
-    return _check(ctx, load().moe_dense_backward(ctx, _of_dtype(x, xd), xd, _of_dtype(w, wd), wd, _of_dtype(dy, yd), yd,
-                                                 _of_dtype(pre, yd), act, n_tokens, rows, cols, _of_dtype(dx, xd),
-                                                 _of_dtype(dw, dwd), dwd, _elem(db, _FP32), at, size,
-                                                 _stream(stream)))
+    x, xd = _typed(x, x_dtype)
+    w, wd = _typed(w, w_dtype)
+    dy, yd = _typed(dy, y_dtype)
+    dw, dwd = _typed(dw, dw_dtype)
+    rc = (_lib or load()).moe_dense_backward(
+        ctx, x, xd, w, wd, dy, yd, _of_dtype(pre, yd), act, n_tokens, rows, cols, _of_dtype(dx, xd), dw, dwd,
+        _elem(db, _FP32), _address(ws), 0 if ws is None else ws.nbytes, _stream(stream))
+    return rc and _check(ctx, rc)
 
 
 def moe_cache_snapshot(ctx, tensor_id, n_experts, slots_per_tensor):
