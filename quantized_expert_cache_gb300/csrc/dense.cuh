@@ -109,24 +109,34 @@ __device__ __forceinline__ void store4_as(void *p, int dtype, size_t i, const fl
     }
 }
 
+// Two values rounded to binary16 or bfloat16, the first in the low half.
+__device__ __forceinline__ unsigned pair16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *(const unsigned *)&h;
+}
+__device__ __forceinline__ unsigned pairb16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *(const unsigned *)&h;
+}
+
 // The epilogue of four neighbours m of the result in a lane.
 struct Epilogue {
     DenseOut o;    // (a copy: stores through its pointers could alias the original)
-    float bias[4];
     int m, left;   // the lane's first row, rows from it to the end
-    bool wide;
+    bool wide;     // the lane's four at once
+    bool plain;    // sums as they are, all lanes' rows at once
     __device__ __forceinline__ Epilogue(const DenseOut &out, int M, int m_, size_t offset) : o(out), m(m_), left(M - m_) {
         if (offset) o.out = (float *)o.out + offset;  // (a K share's sums)
         const uintptr_t at = (uintptr_t)o.out | (uintptr_t)o.res | (uintptr_t)o.pre;
         wide = left >= 4 && o.ld % 4 == 0 && (at & (o.dtype == 0 ? 15 : 7)) == 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) bias[j] = o.bias && j < left ? o.bias[m + j] : 0.0f;
+        plain = !o.pre && !o.res && o.act == kActNone && M == o.ld && M % (o.dtype == 0 ? 4 : 8) == 0 &&
+                ((uintptr_t)o.out & 15) == 0;
     }
-    // column n's finished sums
+    // column n's finished sums, the bias among them
     __device__ __forceinline__ void column(const float *sums, int n) const {
         float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = sums[j] + bias[j];
+        for (int j = 0; j < 4; ++j) v[j] = sums[j];
         const size_t i = (size_t)n * (size_t)o.ld + m;
         if (wide) {
             if (o.pre) store4_as(o.pre, o.dtype, i, v);
@@ -154,9 +164,31 @@ struct Epilogue {
     // A warp's 32 rows (8 lanes, from 4 (lane & 7) on) of `cols` columns from n of N:
     // sums[column][32] in shared memory, four columns at a time.
     __device__ __forceinline__ void store(const float *sums, int cols, int n, int N, int lane) const {
+        const int most = min(cols, N - n);
+        if (plain && o.dtype != 0) {
+            // rounded sums alone: eight neighbours a lane, eight columns at a time
+            const int at = (lane & 3) * 8, m8 = m - (lane & 7) * 4 + at;
+            if (left + m <= m8) return;
+            unsigned short *out = (unsigned short *)o.out + (size_t)n * (size_t)o.ld + m8;
+#pragma unroll 2
+            for (int c = lane >> 2; c < most; c += 8) {
+                const float4 f = *(const float4 *)(sums + c * 32 + at), g = *(const float4 *)(sums + c * 32 + at + 4);
+                const uint4 u = o.dtype == 1 ? uint4{pair16(f.x, f.y), pair16(f.z, f.w), pair16(g.x, g.y), pair16(g.z, g.w)}
+                                             : uint4{pairb16(f.x, f.y), pairb16(f.z, f.w), pairb16(g.x, g.y), pairb16(g.z, g.w)};
+                *(uint4 *)(out + (size_t)c * o.ld) = u;
+            }
+            return;
+        }
         if (left <= 0) return;
+        if (plain) {
+            float *out = (float *)o.out + (size_t)n * (size_t)o.ld + m;
+#pragma unroll 2
+            for (int c = lane >> 3; c < most; c += 4)
+                *(float4 *)(out + (size_t)c * o.ld) = *(const float4 *)(sums + c * 32 + (lane & 7) * 4);
+            return;
+        }
 #pragma unroll 1
-        for (int c = lane >> 3; c < cols && n + c < N; c += 4) {
+        for (int c = lane >> 3; c < most; c += 4) {
             const float4 f = *(const float4 *)(sums + c * 32 + (lane & 7) * 4);
             const float v[4] = {f.x, f.y, f.z, f.w};
             column(v, n + c);

@@ -396,7 +396,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                 else
                     mbar_arrive_warp(acc_empty(buf), lane);
             }
-            const int ml = quarter * 32 + lane, n0 = w.n0 + share * NC;
+            const int ml = quarter * 32 + lane, n0 = w.n0 + share * NC, m = w.m0 + side * kBM + ml;
+            const float bias = S == 1 && w.p->o.bias && m < w.p->M ? w.p->o.bias[m] : 0.0f;
             if (S > 1) {
                 // (all products of the CTA are done: its stages are free)
                 float *red = (float *)smem;
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                     constexpr int TOKENS = NC / 4 < GROUP ? NC / 4 : GROUP;
 #pragma unroll
                     for (int j = 0; j < TOKENS; ++j)
-                        mine[j * 32 + lane] = (acc[c + 4 * j + 2] + acc[c + 4 * j + 1]) + acc[c + 4 * j];
+                        mine[j * 32 + lane] = (acc[c + 4 * j + 2] + acc[c + 4 * j + 1]) + acc[c + 4 * j] + bias;
                     __syncwarp();
                     e.store(mine, TOKENS, (n0 + c) / 4, w.p->N / 4, lane);
                     __syncwarp();
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
 #pragma unroll
                 for (int c = 0; c < NC; c += GROUP) {
 #pragma unroll
-                    for (int j = 0; j < GROUP; ++j) mine[j * 32 + lane] = acc[c + j];
+                    for (int j = 0; j < GROUP; ++j) mine[j * 32 + lane] = acc[c + j] + bias;
                     __syncwarp();
                     e.store(mine, GROUP, n0 + c, w.p->N, lane);
                     __syncwarp();
@@ -442,6 +443,9 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             tile(0, w);
             const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + lane * 4, 0);
             const float4 *red = (const float4 *)smem + lane;
+            float bias[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bias[j] = e.o.bias && j < e.left ? e.o.bias[e.m + j] : 0.0f;
             const int fold = w.p->fold ? 4 : 1, cols = min(BN, w.p->N - w.n0) / fold;
             for (int c = split * (C::THREADS / 32) + warp; c < cols; c += S * (C::THREADS / 32)) {
                 float sum[4] = {};
@@ -455,6 +459,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                     for (int s = 0; s < kMaxSplits; ++s)
                         if (s < S) sum[0] += v[s].x, sum[1] += v[s].y, sum[2] += v[s].z, sum[3] += v[s].w;
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] += bias[j];
                 if (e.left > 0) e.column(sum, w.n0 / fold + c);
             }
         }
