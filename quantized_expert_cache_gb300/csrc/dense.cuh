@@ -50,11 +50,11 @@ __device__ __forceinline__ float act_of(float z, int act) {
 }
 __device__ __forceinline__ float slope_of(float z, int act) {
     if (act == kActSilu) {
-        const float s = 1.0f / (1.0f + expf(-z));
+        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
         return s * (1.0f + z * (1.0f - s));
     }
     if (act == kActGelu)
-        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
     return 1.0f;
 }
 

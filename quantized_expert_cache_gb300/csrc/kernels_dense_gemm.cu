@@ -8,8 +8,9 @@
 //
 // An operand is read as it lies in memory: one whose k is contiguous as rows of 64 k
 // (two blocks to a step), the other kind as rows of 64 m (or n), both in the 128-byte
-// swizzle that the MMA's descriptors name; nothing is transposed.  A thread of the epilogue has one m and
-// many n, so a warp writes 32 neighbours of the result at a time.
+// swizzle that the MMA's descriptors name; nothing is transposed.  A thread of the
+// epilogue has one m and many n; blocks of them turn in shared memory, so that a lane
+// stores four or eight neighbours of the result.
 //
 // The accumulators are drained every 512 of k (kChunk32) and added up in registers,
 // rounded to nearest: the tensor core's own fp32 accumulation truncates, a bias of about
@@ -28,13 +29,13 @@
 // of CTAs and their sums joined through distributed shared memory, in order; or, in a
 // weights' gradient, over tiles of their own whose sums are joined in the workspace.
 //
-// Bound.  8192^3 bf16 609 us, 4096^3 99, 4096 x 8192 x 2048 89 (the library's product 545,
+// Bound.  8192^3 bf16 605 us, 4096^3 99, 4096 x 8192 x 2048 87 (the library's product 545,
 // 80 and 74; all with a cold cache); both gradients of 4096^3 168 (1630 TFLOP/s, 0.85 of
 // the measured rate; tensor pipe active 76% of the time).  What a step takes in: by
 // count 64 KB for 1024 clocks of products, near what an SM draws from L2 (without
 // loads 8192^3 took 507 us, without products 564).  Activations and a second output add
-// their epilogue: 97 us with silu and pre-activations.  8 tokens on 65536 x 2048: HBM,
-// 45 us = 0.88 of a copy.  33 on 2887 x 2880 8.1 us: latency of the launch, one
+// their epilogue: 98 us with silu and pre-activations.  8 tokens on 65536 x 2048: HBM,
+// 45 us = 0.88 of a copy.  33 on 2887 x 2880 8.3 us: latency of the launch, one
 // round of steps and the join.
 #include <cuda.h>
 #include <cooperative_groups.h>

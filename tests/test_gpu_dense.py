@@ -403,3 +403,42 @@ def test_refusals(ctx):
         qec.moe_dense_backward(ctx, x, w, y, 5, 9, 16, x.clone())
     with pytest.raises(qec.MoeError):
         qec.moe_dense_forward(ctx, x, w, 5, 9, 16, y, act=3)
+
+
+def test_two_streams_at_once(ctx):
+    # calls in flight together, each with its own workspace: split tiles, pairs and parts
+    types = (F32, BF16, F32)
+    shapes = [(70, 700, 1032), (300, 520, 2048)]
+    layers = [layer(t, r, c, types, 20 + i) for i, (t, r, c) in enumerate(shapes)]
+
+    def run(s, stream):
+        t, c = s["x"].shape
+        r = s["w"].shape[0]
+        y, dx, dw, db = (torch.empty(n, device="cuda") for n in ((t, r), (t, c), (r, c), (r,)))
+        ws = [space(ctx, types, qec.ACT_NONE, t, r, c, i) for i in (0, 1)]
+
+        def go():
+            qec.moe_dense_forward(ctx, s["x"], s["w"], t, r, c, y, ws=ws[0], stream=stream)
+            qec.moe_dense_backward(ctx, s["x"], s["w"], s["dy"], t, r, c, dx, dw, db, ws=ws[1], stream=stream)
+        return go, (y, dx, dw, db)
+
+    streams = [torch.cuda.Stream() for _ in layers]
+    calls = [run(s, st) for s, st in zip(layers, streams)]
+    torch.cuda.synchronize()
+    want = []
+    for go, out in calls:
+        go()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in out])
+    for _ in range(20):
+        for _, out in calls:
+            for o in out:
+                o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for go, _ in calls:
+                go()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(calls, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+    qec.miss_drain(ctx)

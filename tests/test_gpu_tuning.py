@@ -137,3 +137,47 @@ def test_the_example_answers_with_log_probabilities(capsys):
     for got, ref in ((logp, want), (entropy, torch.special.entr(lp.exp()).sum(1)), (alternatives, lp.gather(1, top))):
         assert ((got.double() - ref).abs() <= 1e-4 * (ref.abs() + 1)).all()
     stack.close()
+
+
+FIRST = """
+import torch
+import quantized_expert_cache_gb300 as qec
+t, r, c = 100, 520, 264
+st = torch.cuda.Stream()
+ctx = qec.moe_layer_init(64, 32, 8, 2, 1, 0, 1, stream=st.cuda_stream)
+g = torch.Generator(device="cuda").manual_seed(1)
+x, w = torch.randn(t, c, generator=g, device="cuda"), (torch.randn(r, c, generator=g, device="cuda") / 16).bfloat16()
+y, dx, dw, db = (torch.empty(n, device="cuda") for n in ((t, r), (t, c), (r, c), (r,)))
+logp, stats = torch.empty(t, device="cuda"), torch.empty(t, 2, device="cuda")
+targets = torch.arange(t, dtype=torch.int32, device="cuda")
+ws = torch.empty(max(qec.moe_dense_workspace(ctx, x, w, y, 0, t, r, c)), dtype=torch.uint8, device="cuda")
+one = torch.ones(t, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.stream(st):
+    with torch.cuda.graph(graph, stream=st):
+        qec.moe_dense_forward(ctx, x, w, t, r, c, y, ws=ws, stream=st)
+        qec.moe_token_logprobs(ctx, y, targets, t, r, logp, None, 0, None, None, stats, stream=st)
+        qec.moe_token_logprobs_grad(ctx, y, targets, t, r, stats, None, one, None, y, stream=st)
+        qec.moe_dense_backward(ctx, x, w, y, t, r, c, dx, dw, db, ws=ws, stream=st)
+    graph.replay()
+torch.cuda.synchronize()
+xd, wd = x.double().requires_grad_(), w.double().requires_grad_()
+lp = torch.log_softmax(xd @ wd.t(), 1).gather(1, targets.long()[:, None]).squeeze(1)
+lp.sum().backward()
+for got, ref in ((logp, lp), (dx, xd.grad), (dw, wd.grad)):
+    assert float(torch.linalg.vector_norm(got.double() - ref) / torch.linalg.vector_norm(ref)) <= 8e-5
+qec.moe_destroy(ctx)
+print("first in a graph")
+"""
+
+
+def test_a_process_may_capture_its_first_calls():
+    # nothing that a call sets up on first use may break a capture
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "first in a graph" in done.stdout, done.stderr[-2000:]
