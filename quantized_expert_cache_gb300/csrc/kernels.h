@@ -230,6 +230,9 @@ inline bool dense_takes_few(int n_tokens, int rows, int cols) {
 // Up to so many tokens the parts of fp32 rows are columns of one product, which reads
 // the weights once; above they are further steps of it.
 constexpr int kDenseFold = 64;
+// A binary16 operand's second part is held this much larger: 2^-11 of the first and less,
+// it would sink into binary16's subnormal numbers.
+constexpr float kDenseLowScale = 2048.0f;
 struct DenseFew {
     const void *x, *w;          // [n_tokens][cols], [rows][cols]
     int x_dtype, w_dtype, n_tokens, rows, cols;
@@ -265,6 +268,7 @@ struct DenseProduct {
     int n_pairs;
     unsigned pairs;             // 4 bits each, the first lowest: part of A | part of B << 2
     int m_tiles, n_tiles;
+    float low_scale;            // of the sums of all pairs but the last
     DenseOut o;                 // ld = M
     // K shares of a tile, each an own tile whose fp32 sums go to o.out + share * M * N
     // (joined by launch_dense_join); up to most_shares of them

@@ -13,7 +13,8 @@
 //   fp32 results: three bfloat16 parts, all 24 bits (what lies below 2^-133 is lost), and
 //     the products to 2^-24: 3 with a 16-bit operand, 6 of two fp32 ones.  (Two parts
 //     and three products leave 3e-6 to 4.5e-6 of a gradient's norm, a plain fp32 product
-//     about 1e-6.)  A slope of binary16: two binary16 parts (22 bits, or 2^-25).
+//     about 1e-6.)  A slope of binary16: two binary16 parts, the second
+//     held 2^11 larger (22 bits, or 2^-36).
 //   16-bit results: two parts; one for a large gradient's dz, which layers store in 16
 //     bits too: 2^-9 (2^-12) of each term next to the result's own rounding.
 // A gradient that is 16-bit itself, without a slope, goes as it is.  Measured (cold):
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
                     const float left = v[j] - value<P>(o.v[j]);
                     // infinities and NaN are their first part
                     v[j] = isfinite(value<P>(o.v[j])) ? left : 0.0f;
+                    if constexpr (std::is_same<P, __half>::value) v[j] *= kDenseLowScale;
                 }
                 P *dst = (P *)p.parts + (p.by_row ? t * PARTS + q : (size_t)q * p.n_tokens + t) * p.ld;
                 if (WIDE) {

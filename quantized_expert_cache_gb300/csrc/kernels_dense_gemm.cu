@@ -378,8 +378,9 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-            for (int i = w.first; i < w.last; i = w.chunk_end(i), ++chunk) {
+            for (int i = w.first, end; i < w.last; i = end, ++chunk) {
                 const int buf = chunk & 1;
+                end = w.chunk_end(i);
                 if (!mbar_wait_warp(acc_full(buf), chunk >> 1 & 1, abort_flag, g.error, kErrorDense)) goto finished;
                 tc_fence_after();
                 const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + share * NC;
@@ -391,6 +392,10 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(v[j]);
                 }
+                // (the lower parts' products come first)
+                if (i < w.low && end == min(w.last, w.low) && w.p->low_scale != 1.0f)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) acc[c] *= w.p->low_scale;
                 tc_fence_before();
                 if (PAIR)
                     arrive_cluster_warp(mapped(acc_empty(buf), leader), lane);
