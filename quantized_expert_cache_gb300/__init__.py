@@ -410,7 +410,11 @@ def _dtype_of(x) -> int:
     """MOE_ code of a tensor, of a dtype itself, or a code."""
     if isinstance(x, int):
         return x
-    return _dtype(x) if hasattr(x, "dtype") else _DTYPES[_type_name(x)]
+    if hasattr(x, "dtype"):
+        return _dtype(x)
+    if _type_name(x) not in _DTYPES:
+        raise ValueError(f"expected float32, float16 or bfloat16, got {x}")
+    return _DTYPES[_type_name(x)]
 
 
 def moe_dense_workspace(ctx, x, w, y, act, n_tokens, rows, cols) -> tuple:

@@ -93,6 +93,16 @@ def test_codes_of_the_types(lib):
     assert sent[1:3] == (None, qec.BF16) and sent[13] is None
 
 
+def test_workspace_takes_tensors_types_and_codes(lib):
+    for x, w, y in ((F32, T("bfloat16"), T("float16")), (F32.dtype, T("bfloat16").dtype, T("float16").dtype),
+                    (qec.F32, qec.BF16, qec.F16)):
+        assert qec.moe_dense_workspace(1, x, w, y, 0, 2, 8, 16) == (0, 0)
+        assert lib.calls[-1][1][1:8] == (qec.F32, qec.BF16, qec.F16, 0, 2, 8, 16)
+    for bad in (T("float64"), T("float64").dtype):
+        with pytest.raises(ValueError):
+            qec.moe_dense_workspace(1, bad, qec.BF16, qec.F32, 0, 2, 8, 16)
+
+
 def test_an_error_raises(monkeypatch):
     class Refusing:
         def __getattr__(self, name):
