@@ -230,9 +230,12 @@ inline bool dense_takes_few(int n_tokens, int rows, int cols) {
 // Up to so many tokens the parts of fp32 rows are columns of one product, which reads
 // the weights once; above they are further steps of it.
 constexpr int kDenseFold = 64;
-// A binary16 operand's second part is held this much larger: 2^-11 of the first and less,
-// it would sink into binary16's subnormal numbers.
-constexpr float kDenseLowScale = 2048.0f;
+// A binary16 gradient times a slope (up to 1.13) passes binary16's range where the gradient is
+// near its end: the parts of it are held by half, the finished sums doubled.  The second part
+// is held 2^12 larger than that: 2^-11 of the first and less, it would sink into binary16's
+// subnormal numbers.  (At most 16 of a first part up to 37009, and so 2^16: cut to 65504, that
+// is 2^-22 of the whole.)
+constexpr float kDenseHold = 0.5f, kDenseLowScale = 4096.0f, kDenseMost16 = 65504.0f;
 struct DenseFew {
     const void *x, *w;          // [n_tokens][cols], [rows][cols]
     int x_dtype, w_dtype, n_tokens, rows, cols;
@@ -268,7 +271,7 @@ struct DenseProduct {
     int n_pairs;
     unsigned pairs;             // 4 bits each, the first lowest: part of A | part of B << 2
     int m_tiles, n_tiles;
-    float low_scale;            // of the sums of all pairs but the last
+    float low_scale, scale;     // of the sums of all pairs but the last; of all sums
     DenseOut o;                 // ld = M
     // K shares of a tile, each an own tile whose fp32 sums go to o.out + share * M * N
     // (joined by launch_dense_join); up to most_shares of them

@@ -13,8 +13,9 @@
 //   fp32 results: three bfloat16 parts, all 24 bits (what lies below 2^-133 is lost), and
 //     the products to 2^-24: 3 with a 16-bit operand, 6 of two fp32 ones.  (Two parts
 //     and three products leave 3e-6 to 4.5e-6 of a gradient's norm, a plain fp32 product
-//     about 1e-6.)  A slope of binary16: two binary16 parts, the second
-//     held 2^11 larger (22 bits, or 2^-36).
+//     about 1e-6.)  A gradient through a slope in binary16: two binary16 parts of its half (a
+//     slope of 1.13 takes it past binary16's range), the second held 2^12 larger (22 bits,
+//     or 2^-36).
 //   16-bit results: two parts; one for a large gradient's dz, which layers store in 16
 //     bits too: 2^-9 (2^-12) of each term next to the result's own rounding.
 // A gradient that is 16-bit itself, without a slope, goes as it is.  Measured (cold):
@@ -156,6 +157,11 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += v[j];
         if (PARTS) {
+            if constexpr (std::is_same<P, __half>::value) {
+                if (p.pre)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] *= kDenseHold;
+            }
             unsigned cut = 0;
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) {
@@ -172,7 +178,8 @@ __global__ void __launch_bounds__(256) dense_split_kernel(DenseSplit p, int bloc
                     const float left = v[j] - value<P>(o.v[j]);
                     // infinities and NaN are their first part
                     v[j] = isfinite(value<P>(o.v[j])) ? left : 0.0f;
-                    if constexpr (std::is_same<P, __half>::value) v[j] *= kDenseLowScale;
+                    if constexpr (std::is_same<P, __half>::value)
+                        v[j] = fminf(fmaxf(v[j] * kDenseLowScale, -kDenseMost16), kDenseMost16);
                 }
                 P *dst = (P *)p.parts + (p.by_row ? t * PARTS + q : (size_t)q * p.n_tokens + t) * p.ld;
                 if (WIDE) {

@@ -403,12 +403,12 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                     mbar_arrive_warp(acc_empty(buf), lane);
             }
             const int ml = quarter * 32 + lane, n0 = w.n0 + share * NC, m = w.m0 + side * kBM + ml;
-            const float bias = S == 1 && w.p->o.bias && m < w.p->M ? w.p->o.bias[m] : 0.0f;
+            const float bias = S == 1 && w.p->o.bias && m < w.p->M ? w.p->o.bias[m] : 0.0f, scale = w.p->scale;
             if (S > 1) {
                 // (all products of the CTA are done: its stages are free)
                 float *red = (float *)smem;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) red[(share * NC + c) * kBM + ml] = acc[c];
+                for (int c = 0; c < NC; ++c) red[(share * NC + c) * kBM + ml] = acc[c] * scale;
             } else if (w.p->fold) {
                 const dense::Epilogue e(w.p->o, w.p->M, w.m0 + side * kBM + quarter * 32 + (lane & 7) * 4, 0);
                 float *mine = (float *)(smem + C::STAGING) + (warp - kWEpi) * GROUP * 32;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
 #pragma unroll
                 for (int c = 0; c < NC; c += GROUP) {
 #pragma unroll
-                    for (int j = 0; j < GROUP; ++j) mine[j * 32 + lane] = acc[c + j] + bias;
+                    for (int j = 0; j < GROUP; ++j) mine[j * 32 + lane] = fmaf(acc[c + j], scale, bias);
                     __syncwarp();
                     e.store(mine, GROUP, n0 + c, w.p->N, lane);
                     __syncwarp();

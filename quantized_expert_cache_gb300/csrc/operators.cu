@@ -340,7 +340,7 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
     g.p[0].N = n_tokens;
     g.p[0].K = cols;
     g.p[0].bf16 = w_dtype == MOE_BF16;
-    g.p[0].low_scale = 1.0f;
+    g.p[0].low_scale = g.p[0].scale = 1.0f;
     g.p[0].o = out;
     if (x.parts > 1 && n_tokens <= moe::kDenseFold) {
         g.p[0].fold = 1;
@@ -470,6 +470,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     for (int i = 0; i < g.n_products; ++i) {
         g.p[i].bf16 = w_dtype == MOE_BF16;
         g.p[i].low_scale = w_dtype == MOE_F16 ? 1.0f / moe::kDenseLowScale : 1.0f;
+        g.p[i].scale = w_dtype == MOE_F16 && slope ? 1.0f / moe::kDenseHold : 1.0f;
         g.p[i].o.ld = cols;
         dense_pairs(g.p[i], a[i].parts, b[i].parts, g.p[i].o.dtype == MOE_F32 ? 2 : 1);
     }
