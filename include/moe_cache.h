@@ -626,9 +626,9 @@ int moe_token_logprobs_grad(moe_ctx *ctx, const void *d_logits, int dtype, const
  * fp32 rows enter with all their 24 bits (16 for a 16-bit result) but for what lies
  * below 2^-133.  Up to 2 tokens, and 3 or 4 on up to 2^22 weights, a plain fp32 sum,
  * others on the tensor cores: the bits of a token's result depend on the batch's size.
- * NaN and infinities spread as in the formulas.  A bounded wait that expires is
- * reported by the next cache_step or
- * miss_drain (MOE_ERR_FAULT).  d_ws: moe_dense_workspace's forward_bytes, the call's
+ * NaN and infinities spread as in the formulas, but for an infinity times what enters as
+ * zero (that below 2^-133), which is NaN.  A bounded wait that expires is reported by the
+ * next cache_step or miss_drain (MOE_ERR_FAULT).  d_ws: moe_dense_workspace's forward_bytes, the call's
  * own while it runs (0 bytes: NULL).  Asynchronous on `stream` (NULL: the context's),
  * any stream; capturable (a captured graph holds its buffers' addresses).  No output
  * and no workspace meets another buffer (MOE_ERR_ARG).  Errors: MOE_ERR_ARG,
@@ -651,7 +651,8 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
  * d_db sums dz in fp32.  dz and fp32 rows enter the products for an fp32 result with 24
  * bits (binary16 layers: 22, or 2^-36), for a 16-bit one with 16, but dz rounded to
  * w_dtype where n_tokens * rows * cols >= 2^32; a 16-bit dy without an activation goes as
- * it is.  The same call on the same inputs gives the same bits (those of
+ * it is.  (An infinite weight or row times a binary16 layer's dz of 2^-24 or less, through
+ * an activation, is NaN.)  The same call on the same inputs gives the same bits (those of
  * d_dx and d_dw depend on whether both are asked for).  d_ws:
  * moe_dense_workspace's backward_bytes.  Everything else as moe_dense_forward.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.

@@ -150,6 +150,11 @@ __device__ __forceinline__ void commit_warp(uint32_t bar, int ctas) {
         mma_commit_warp(bar);
 }
 
+// A finished sum of lower parts' products.  Not finite, it goes: an infinity times a lower
+// part that is zero or of the other sign is not what the formula has; the first parts'
+// product holds that infinity, or NaN, times a number of the value's own sign.
+__device__ __forceinline__ float lower_sum(float v) { return isfinite(v) ? v : 0.0f; }
+
 struct Tile {
     const DenseProduct *p;
     int m0, n0, kb, first, last;  // kb: steps of one pair of parts; [first, last): this CTA's
@@ -393,9 +398,9 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                     for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(v[j]);
                 }
                 // (the lower parts' products come first)
-                if (i < w.low && end == min(w.last, w.low) && w.p->low_scale != 1.0f)
+                if (i < w.low && end == min(w.last, w.low))
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) acc[c] *= w.p->low_scale;
+                    for (int c = 0; c < NC; ++c) acc[c] = lower_sum(acc[c]) * w.p->low_scale;
                 tc_fence_before();
                 if (PAIR)
                     arrive_cluster_warp(mapped(acc_empty(buf), leader), lane);
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
                     constexpr int TOKENS = NC / 4 < GROUP ? NC / 4 : GROUP;
 #pragma unroll
                     for (int j = 0; j < TOKENS; ++j)
-                        mine[j * 32 + lane] = (acc[c + 4 * j + 2] + acc[c + 4 * j + 1]) + acc[c + 4 * j] + bias;
+                        mine[j * 32 + lane] = lower_sum(acc[c + 4 * j + 2] + acc[c + 4 * j + 1]) + acc[c + 4 * j] + bias;
                     __syncwarp();
                     e.store(mine, TOKENS, (n0 + c) / 4, w.p->N / 4, lane);
                     __syncwarp();
@@ -455,7 +460,10 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::THREADS), 1) dense_gemm_kernel
             const int fold = w.p->fold ? 4 : 1, cols = min(BN, w.p->N - w.n0) / fold;
             for (int c = split * (C::THREADS / 32) + warp; c < cols; c += S * (C::THREADS / 32)) {
                 float sum[4] = {};
-                for (int f = fold - 1; f >= 0; --f) {  // (the lowest parts first)
+                for (int f = fold > 1 ? 2 : 0; f >= 0; --f) {  // (the lowest parts first, the fourth is zero)
+                    if (f == 0)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sum[j] = lower_sum(sum[j]);
                     float4 v[kMaxSplits];
 #pragma unroll
                     for (int s = 0; s < kMaxSplits; ++s)

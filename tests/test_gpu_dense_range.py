@@ -1,5 +1,6 @@
 """GPU tests of the 16-bit dense layers at the ends of their types' ranges, against plain
-64-bit implementations: gradients near binary16's largest numbers.
+64-bit implementations: gradients near binary16's largest numbers, infinities and NaN in every
+operand.
 
 Tolerances are those of tests/test_gpu_dense.py, in units of u = 2^-24; what a test adds
 to them is derived beside it.
@@ -11,7 +12,8 @@ import pytest
 import quantized_expert_cache_gb300 as qec
 
 torch = pytest.importorskip("torch")
-from test_gpu_dense import F16, F32, backward, check_backward, close_norm, gen, layer, rand, slope_ref  # noqa: E402
+from test_gpu_dense import (BF16, F16, F32, backward, check_backward, close_norm, forward, gen, layer,  # noqa: E402
+                            rand, slope_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +51,76 @@ def test_large_binary16_gradients(ctx, t, r, c, act, peak):
         if dw_dtype == F32 and t >= 64:
             # by norms: 42 u of the sums, 12 u (1 + |z|) of the slopes at |z| of 2.6, 2^-22 of the parts
             close_norm(got[1], dz.t() @ s["x"].double(), F32, "dw", 44 + 4)
+
+
+# ----------------------------------------------------------------- infinities, NaN
+def same_class(got, ref, what):
+    """Infinite where the definition is, of its sign; NaN where it is; finite elsewhere."""
+    got = got.double()
+    ok = torch.where(torch.isfinite(ref), torch.isfinite(got), (got == ref) | (torch.isnan(got) & torch.isnan(ref)))
+    assert ok.all(), (what, int((~ok).sum()), got[~ok][:6], ref[~ok][:6])
+
+
+def nonzero(v):
+    return torch.where(v == 0, torch.ones_like(v), v)
+
+
+@pytest.mark.parametrize("y", [F32, BF16])
+@pytest.mark.parametrize("x", [F32, BF16])
+@pytest.mark.parametrize("r,c", [(200, 264), (300, 4104)])
+@pytest.mark.parametrize("t", [1, 3, 5, 40, 64, 65, 300])
+def test_infinite_weights_and_rows(ctx, t, r, c, x, y):
+    types = (x, BF16, y)
+    s = layer(t, r, c, types, 50)
+    s["x"], s["w"] = nonzero(s["x"]), nonzero(s["w"])
+    s["x"][:, 2::3] = nonzero(s["x"][:, 2::3].to(BF16).to(x))  # (lower parts of zero)
+    inf = float("inf")
+    s["w"][3, 7], s["w"][5, 8], s["w"][6, 1] = inf, -inf, float("nan")
+    s["w"][8, 2], s["w"][8, 3] = inf, -inf
+    s["w"][r - 1, c - 1] = inf
+    if t > 2:
+        s["x"][1, 5], s["x"][2, 4] = inf, -inf
+        s["w"][9, 4] = inf
+    got, pre = forward(ctx, s, types, bias=True, pre=True)
+    ref = torch.empty(t, r, dtype=torch.float64, device="cuda")
+    for i in range(0, t, 25):  # (term by term: no product that the definition has not)
+        ref[i:i + 25] = torch.stack([(s["x"][i:i + 25].double() * w.double()).sum(1) for w in s["w"]], 1)
+    assert not torch.isfinite(ref).all()
+    same_class(pre, ref, "pre")
+    same_class(got, ref, "y")
+
+
+@pytest.mark.parametrize("types,act", [((F32, BF16, F32), qec.ACT_NONE), ((F32, BF16, F32), qec.ACT_SILU),
+                                       ((F32, BF16, BF16), qec.ACT_GELU), ((BF16, BF16, F32), qec.ACT_NONE),
+                                       ((BF16, BF16, BF16), qec.ACT_SILU), ((BF16, BF16, BF16), qec.ACT_NONE),
+                                       ((F16, F16, F16), qec.ACT_SILU)])
+@pytest.mark.parametrize("t,r,c", [(3, 72, 136), (40, 72, 136), (300, 200, 72), (1030, 72, 136)])
+def test_infinities_in_gradients(ctx, t, r, c, types, act):
+    s = layer(t, r, c, types, 51)
+    for k in ("x", "w", "dy"):
+        s[k] = nonzero(s[k])
+    s["pre"] = (s["pre"].abs() + 0.25).to(types[2])  # (slopes above 1/2)
+    # (no dz below binary16's smallest step, whose first part would be zero)
+    s["dy"] = torch.where(s["dy"].abs() < 1e-3, torch.ones_like(s["dy"]), s["dy"])
+    s["dy"][:, ::4] = s["dy"][:, ::4].to(BF16).to(types[2])
+    inf = float("inf")
+    clean = {k: s[k].clone() for k in ("x", "w", "dy")}
+
+    def run(plant):
+        for k in clean:
+            s[k] = clean[k].clone()
+        for k, at, v in plant:
+            s[k][at] = v
+        dz = s["dy"].double() * (slope_ref(s["pre"], act) if act else 1.0)
+        for dw_dtype in (F32, types[1]):
+            dx, dw, db = backward(ctx, s, types, act, dw_dtype)
+            x, w = s["x"].double(), s["w"].double()
+            for i in range(0, t, 100):
+                same_class(dx[i:i + 100], (dz[i:i + 100, :, None] * w[None]).sum(1), "dx")
+            same_class(dw, torch.stack([(dz[:, j, None] * x).sum(0) for j in range(r)]), "dw")
+            same_class(db, dz.sum(0), "db")
+
+    run([("w", (2, 7), inf), ("w", (r - 1, 8), -inf), ("w", (5, 9), float("nan"))])
+    run([("x", (1, 5), inf), ("x", (t - 1, c - 1), -inf)])
+    run([("dy", (0, 4), inf), ("dy", (1, 3), -inf), ("dy", (2, 9), float("nan"))])
+    run([("dy", (0, 4), inf), ("dy", (1, 4), -inf), ("w", (2, 7), inf), ("x", (2, 6), inf)])
