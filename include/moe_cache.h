@@ -649,12 +649,11 @@ int moe_dense_forward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_
  * any of them NULL, at least one wanted; d_x is read for d_dw only, d_w for d_dx only.
  * y_dtype MOE_F32 goes with MOE_BF16 weights.  Without tokens d_dw and d_db are zero.
  * d_db sums dz in fp32.  dz and fp32 rows enter the products for an fp32 result with 24
- * bits (binary16 layers: 22, or 2^-36), for a 16-bit one with 16, but dz rounded to
- * w_dtype where n_tokens * rows * cols >= 2^32; a 16-bit dy without an activation goes as
- * it is.  (An infinite weight or row times a binary16 layer's dz of 2^-24 or less, through
- * an activation, is NaN.)  The same call on the same inputs gives the same bits (those of
- * d_dx and d_dw depend on whether both are asked for).  d_ws:
- * moe_dense_workspace's backward_bytes.  Everything else as moe_dense_forward.
+ * bits (binary16 layers: 22, or 2^-36), for a 16-bit one with 16 (binary16: 22); a 16-bit
+ * dy without an activation goes as it is.  (An infinite weight or row times a binary16
+ * layer's dz of 2^-24 or less, through an activation, is NaN.)  The same call on the same
+ * inputs gives the same bits (those of d_dx and d_dw depend on whether both are asked for).
+ * d_ws: moe_dense_workspace's backward_bytes.  Everything else as moe_dense_forward.
  * Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */
 int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d_w, int w_dtype, const void *d_dy,

@@ -16,8 +16,7 @@
 //     about 1e-6.)  A gradient through a slope in binary16: two binary16 parts of its half (a
 //     slope of 1.13 takes it past binary16's range), the second held 2^12 larger (22 bits,
 //     or 2^-36).
-//   16-bit results: two parts; one for a large gradient's dz, which layers store in 16
-//     bits too: 2^-9 (2^-12) of each term next to the result's own rounding.
+//   16-bit results: two parts.
 // A gradient that is 16-bit itself, without a slope, goes as it is.  Measured (cold):
 // 4096 x 2048 fp32 in three parts 14 us for 84 MB; 1000 x 2880 fp16 with gelu's slope 10
 // us, latency.
@@ -332,12 +331,11 @@ int launch_few(const DenseFew &p, int n_sm, cudaStream_t st) {
 
 }  // namespace
 
-// (1 part of a 16-bit type: rounded slopes, or a copy with aligned rows; 0: sums alone)
+// (1 part of a 16-bit type: a copy with aligned rows; 0: sums alone)
 int launch_dense_split(const DenseSplit &p, cudaStream_t st) {
     using bf = __nv_bfloat16;
     switch (p.dtype * 4 + p.n_parts) {
         case 0: return launch_split<float, bf, 0>(p, st);
-        case 1: return launch_split<float, bf, 1>(p, st);
         case 2: return launch_split<float, bf, 2>(p, st);
         case 3: return launch_split<float, bf, 3>(p, st);
         case 4: return launch_split<__half, __half, 0>(p, st);

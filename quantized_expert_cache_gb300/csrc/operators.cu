@@ -74,14 +74,10 @@ int dense_sizes(moe_ctx *ctx, const char *what, int x_dtype, int w_dtype, int y_
 
 // Parts of an operand of the tensor cores (kernels_dense.cu says why).
 int row_parts(int x_dtype, bool f32_result) { return x_dtype != MOE_F32 ? 1 : f32_result ? 3 : 2; }
-int gradient_parts(int dtype, bool slope, bool f32_result, bool large) {
+int gradient_parts(int dtype, bool slope, bool f32_result) {
     if (dtype != MOE_F32 && !slope) return 1;
-    if (f32_result) return dtype == MOE_F16 ? 2 : 3;
-    return large ? 1 : 2;
+    return f32_result && dtype != MOE_F16 ? 3 : 2;
 }
-// Where a gradient's products bound its call, not its launches: 2^33 of them (4.6 us of
-// the measured bf16 rate for a pair of parts).
-bool large_gradient(int n_tokens, int rows, int cols) { return (double)n_tokens * rows * cols >= 1ll << 32; }
 // K shares of the weights' gradient: what 32 MB of sums hold.
 int weight_shares(int rows, int cols) { return (int)std::min<size_t>(8, ((size_t)32 << 20) / ((size_t)rows * cols * 4)); }
 
@@ -102,8 +98,7 @@ DenseSpace dense_space(bool backward, int x_dtype, int y_dtype, int act, int n_t
         return s;
     }
     if (x_dtype == MOE_F32) s.x_parts = take(t * cols * 3 * 2);
-    s.z_parts = take(t * round_up(rows, 8) * std::max(gradient_parts(y_dtype, act != MOE_ACT_NONE, true, false),
-                                                    gradient_parts(y_dtype, act != MOE_ACT_NONE, false, false)) * 2);
+    s.z_parts = take(t * round_up(rows, 8) * gradient_parts(y_dtype, act != MOE_ACT_NONE, true) * 2);
     s.sums = take((size_t)moe::dense_most_blocks(n_tokens) * rows * 4);
     if (weight_shares(rows, cols) > 1) s.shares = take((size_t)weight_shares(rows, cols) * rows * cols * 4);
     return s;
@@ -394,7 +389,7 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     const bool f32_result = (d_dx && x_dtype == MOE_F32) || (d_dw && dw_dtype == MOE_F32);
     // dz, as it is if it is 16-bit and its rows are aligned
     const bool product = d_dx || d_dw;
-    DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, gradient_parts(y_dtype, slope, f32_result, large_gradient(n_tokens, rows, cols))};
+    DenseMatrix dz{d_dy, (size_t)rows, t, (size_t)rows, gradient_parts(y_dtype, slope, f32_result)};
     const bool direct = !slope && y_dtype != MOE_F32 && rows % 8 == 0 && whole({d_dy}, 16);
     moe::DenseGemm g{};
     moe::DenseSplit s{};

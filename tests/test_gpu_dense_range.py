@@ -1,6 +1,6 @@
 """GPU tests of the 16-bit dense layers at the ends of their types' ranges, against plain
-64-bit implementations: gradients near binary16's largest numbers, infinities and NaN in every
-operand.
+64-bit implementations: gradients near binary16's largest numbers, infinities and NaN in
+every operand, and the digits that gradients keep whatever their size.
 
 Tolerances are those of tests/test_gpu_dense.py, in units of u = 2^-24; what a test adds
 to them is derived beside it.
@@ -12,8 +12,8 @@ import pytest
 import quantized_expert_cache_gb300 as qec
 
 torch = pytest.importorskip("torch")
-from test_gpu_dense import (BF16, F16, F32, backward, check_backward, close_norm, forward, gen, layer,  # noqa: E402
-                            rand, slope_ref)
+from test_gpu_dense import (BF16, F16, F32, U, backward, check_backward, close, close_norm, forward,  # noqa: E402
+                            gen, layer, rand, slope_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,39 @@ def test_infinities_in_gradients(ctx, t, r, c, types, act):
     run([("x", (1, 5), inf), ("x", (t - 1, c - 1), -inf)])
     run([("dy", (0, 4), inf), ("dy", (1, 3), -inf), ("dy", (2, 9), float("nan"))])
     run([("dy", (0, 4), inf), ("dy", (1, 4), -inf), ("w", (2, 7), inf), ("x", (2, 6), inf)])
+
+
+# ---------------------------------------------------- the same digits at every size
+@pytest.mark.parametrize("t,r,c", [(64, 256, 128), (1024, 2048, 2048)])
+@pytest.mark.parametrize("types", [(BF16, BF16, F32), (F32, BF16, F32)])
+def test_16_bit_gradients_of_fp32_ones_at_every_size(ctx, t, r, c, types):
+    # differences of neighbouring gradients 1 + j 2^-15 (two bfloat16 numbers to the bit): j 2^-15,
+    # j <= 127, is a bfloat16 number too, so the results are exact
+    s = layer(t, r, c, types, 60)
+    j = torch.randint(0, 128, (t, r), generator=gen(t, r), device="cuda")
+    s["dy"] = 1 + j.float() * 2.0 ** -15
+    s["w"][:], s["x"][:] = 0, 0
+    s["w"][0], s["w"][1], s["x"][0], s["x"][1] = 1, -1, 1, -1
+    dx, dw, _ = backward(ctx, s, types, qec.ACT_NONE, BF16)
+    dy = s["dy"].double()
+    assert torch.equal(dx.double(), (dy[:, 0] - dy[:, 1])[:, None].expand(t, c))
+    assert torch.equal(dw.double(), (dy[0] - dy[1])[:, None].expand(r, c))
+
+
+@pytest.mark.parametrize("t,r,c", [(64, 256, 128), (1024, 2048, 2048)])
+@pytest.mark.parametrize("act", [qec.ACT_SILU, qec.ACT_GELU])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_16_bit_gradients_through_slopes_at_every_size(ctx, t, r, c, act, dtype):
+    # differences of neighbouring slopes: two of 12 u (1 + |z|) and of the parts' 2^-22 (binary16)
+    # or 2^-16 (bfloat16), |z| <= 1.5 and slopes below 1.13; the sum of two terms is exact to 3 u
+    types = (dtype, dtype, dtype)
+    s = layer(t, r, c, types, 61)
+    s["dy"][:] = 1
+    s["pre"] = 0.5 + torch.rand(t, r, generator=gen(t, r, 62), device="cuda").to(dtype)
+    s["w"][:], s["x"][:] = 0, 0
+    s["w"][0], s["w"][1], s["x"][0], s["x"][1] = 1, -1, 1, -1
+    dx, dw, _ = backward(ctx, s, types, act, dtype)
+    dz = slope_ref(s["pre"], act)
+    tol = torch.tensor(2 * (30 * U + (2.0 ** -22 if dtype == F16 else 2.0 ** -16) * 1.13) + 3 * U, device="cuda")
+    for got, ref in ((dx, (dz[:, 0] - dz[:, 1])[:, None].expand(t, c)), (dw, (dz[0] - dz[1])[:, None].expand(r, c))):
+        close(got, ref, tol.double(), dtype)
