@@ -362,7 +362,8 @@ int moe_dense_backward(moe_ctx *ctx, const void *d_x, int x_dtype, const void *d
     const cudaStream_t st = stream ? (cudaStream_t)stream : c.stream;
     const size_t t = (size_t)n_tokens, xn = t * cols * size_of(x_dtype), wn = (size_t)rows * cols,
                  yn = t * rows * size_of(y_dtype), dwn = wn * size_of(dw_dtype), dbn = (size_t)rows * 4;
-    if (!apart({}, {{d_dw, dwn}, {d_db, dbn}}))
+    // (also where no token has anything written to d_dx or the workspace)
+    if (!apart({{d_dx ? d_w : nullptr, wn * 2}}, {{d_dw, dwn}, {d_db, dbn}}))
         return fail(ctx, MOE_ERR_ARG, "dense_backward: an output meets another buffer");
     const OnDevice on(c.device);
     if (n_tokens == 0) {
