@@ -570,7 +570,7 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
  *     and d_top_logp[t][..] their log probabilities
  *   d_stats[t] = (max x, log S), which moe_token_logprobs_grad reads
  * d_logits: [n_tokens][vocab] of dtype (MOE_F32, MOE_F16, MOE_BF16).  scale: one
- * over the temperature, positive.  d_targets: int32 [n_tokens], or NULL without
+ * over the temperature, positive, up to 2^127.  d_targets: int32 [n_tokens], or NULL without
  * d_logp; a target past the vocabulary is read as none and reported by the next
  * cache_step or miss_drain (MOE_ERR_FAULT).  Outputs are fp32 (d_top_idx int32),
  * any of them NULL, at least one wanted; n_top <= min(32, vocab), 0: no
@@ -580,8 +580,9 @@ int moe_router_loss(moe_ctx *ctx, const float *d_logits, const int32_t *d_idx, c
  * (-infinity, 0).  NaN and +infinity give NaN in their row; which alternatives a
  * row with a NaN has is unspecified.  Sums in fp32, without the largest terms,
  * which are counted: log probabilities near 0 keep their digits (terms below 2^-126
- * of the largest are left out).  The same inputs give the same bits.  Asynchronous on `stream` (NULL: the context's), any stream;
- * capturable; no workspace.  vocab <= 2^30; rows of any alignment take wide loads.
+ * of the largest are left out, and logits whose distance to it passes fp32's range).  The
+ * same inputs give the same bits.  Asynchronous on `stream` (NULL: the context's), any
+ * stream; capturable; no workspace.  vocab <= 2^30; rows of any alignment take wide loads.
  * No output meets another buffer (MOE_ERR_ARG).  Every pointer is aligned to its
  * elements.  Errors: MOE_ERR_ARG, MOE_ERR_CUDA.
  */

@@ -7,7 +7,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <cmath>
 #include <utility>
 
 namespace {
@@ -41,9 +40,10 @@ int launched(moe_ctx *ctx, const char *what, int rc) {
 // What both calls over the vocabulary ask of their sizes.
 int token_sizes(moe_ctx *ctx, const char *what, int dtype, int n_tokens, int vocab, float scale) {
     if (!known(dtype)) return fail(ctx, MOE_ERR_ARG, std::string(what) + ": dtype must be MOE_F32, MOE_F16 or MOE_BF16");
-    if (n_tokens < 0 || vocab < 1 || vocab > moe::kTokenMaxVocab || !(scale > 0.0f) || !std::isfinite(scale))
+    // (the kernels' scale / ln 2 is finite: the largest logit is 0 times it)
+    if (n_tokens < 0 || vocab < 1 || vocab > moe::kTokenMaxVocab || !(scale > 0.0f) || scale > 0x1p127f)
         return fail(ctx, MOE_ERR_ARG,
-                    std::string(what) + ": need n_tokens >= 0, 1 <= vocab <= 2^30, a positive finite scale");
+                    std::string(what) + ": need n_tokens >= 0, 1 <= vocab <= 2^30, a positive scale up to 2^127");
     return MOE_OK;
 }
 

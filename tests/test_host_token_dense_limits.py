@@ -1,8 +1,9 @@
 """Refusals of the token log probabilities and the 16-bit dense layers that guard their
 results, on the host over a stand-in for the CUDA runtime."""
 import ctypes
+import math
 
-from test_host_token_dense import BF16, F32, backward, ctx, lib  # noqa: F401
+from test_host_token_dense import BF16, F32, backward, ctx, grad, lib, logprobs  # noqa: F401
 
 
 def test_without_tokens_the_gradients_outputs_may_not_meet_the_weights(lib, ctx):  # noqa: F811
@@ -19,3 +20,13 @@ def test_without_tokens_the_gradients_outputs_may_not_meet_the_weights(lib, ctx)
             c.takes(["set"], w=w, dwd=dwd, **{out: w + at}, **other)
     # (weights that a call does not read are not looked at)
     c.takes(["set"], w=w, dx=None, dw=w, db=None)
+
+
+def test_scales_whose_binary_logarithm_passes_fp32(lib, ctx):  # noqa: F811
+    # scale / ln 2 has to be finite: the row's largest logit is 0 times it
+    for make in (logprobs, grad):
+        c = make(lib, ctx)
+        c.takes(scale=2.0 ** 127)
+        c.takes(scale=2.0 ** -149)
+        for scale in (math.nextafter(2.0 ** 127, math.inf) * (1 + 2.0 ** -23), 2.4e38, 3.4028234e38):
+            c.refuses(scale=scale)
