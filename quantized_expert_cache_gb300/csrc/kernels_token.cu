@@ -27,7 +27,7 @@
 //
 // Bound.  Many rows: HBM; 4096 x 65536 fp32 with 5 alternatives 176 us = 0.90 of a copy
 // (173 without: a row's second part, some 4 us long, behind other rows' reads), bf16
-// 148 = 0.53 (19 instructions an element), its gradient 161 = 0.98, fp32 308 = 1.02.  Few
+// 148 = 0.53 (19 instructions an element), its gradient 163 = 0.97, fp32 308 = 1.02.  Few
 // rows: latency; 1 x 65536 with 8 alternatives 5.6 us (3.8 without), 32 x 100003 bf16
 // with 20 9.6 (6.3), gradient of 33 x 32003 2.4.  A masked row with fewer tokens left
 // than alternatives wanted orders its many equal elements by lists: 31 us for 65536.
@@ -496,13 +496,12 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(TokenParams
 // ---- gradient: one read, one write, a row's scalars in every thread --------------
 struct GradRow {
     float top, log_sum, scale, by_log, by_one;
-    bool none;  // nothing but -infinity: zero
+    float at_zero;  // the factor without scale
     // -p (by_log log p + by_one): all of a logit's gradient but a target's own term.
     __device__ __forceinline__ float of(float x) const {
-        const float lp = fmaf(x - top, scale, -log_sum);
-        // (where p is 0 the clamped factor stays finite)
-        const float d = -exp2_neg(lp * kLog2e) * fmaf(by_log, fmaxf(lp, -150.0f), by_one);
-        return none ? 0.0f : d;
+        const float lp = fmaf(x - top, scale, -log_sum), p = exp2_neg(lp * kLog2e);
+        // (where p is 0, log p or scale may have taken the factor past fp32's range)
+        return -p * (p == 0.0f ? at_zero : fmaf(by_log, lp, by_one));
     }
 };
 
@@ -534,11 +533,14 @@ __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenGradParams p,
     w.top = p.stats[2 * row];
     w.log_sum = p.stats[2 * row + 1];
     w.scale = p.scale;
-    w.none = w.top == -kInf && w.log_sum == 0.0f;
     const float g = p.g_logp && target >= 0 ? p.g_logp[row] : 0.0f;
     const float gh = p.g_entropy ? p.g_entropy[row] : 0.0f, h = p.g_entropy ? p.entropy[row] : 0.0f;
     w.by_log = gh * p.scale;
-    w.by_one = fmaf(gh, h, g) * p.scale;
+    w.at_zero = fmaf(gh, h, g);
+    w.by_one = w.at_zero * p.scale;
+    // nothing but -infinity: every p is 0, and so are the gradients
+    const bool none = w.top == -kInf && w.log_sum == 0.0f;
+    if (none) w.top = w.at_zero = 0.0f;
     // the thread that has the target's pack: g (1 - p) by expm1, so that a likely target's
     // keeps its digits (read before the pack is stored over it)
     const int at = target < 0 ? -1 : (target + before) / N - pack0;
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenGradParams p,
 #pragma unroll 1
                 for (int i = max(e, 0); i < min(e + N, p.vocab); ++i) dx[i] = rounded<T>(w.of(value<T>(r.x[i])));
         }
-    if (mine && !w.none) dx[target] = rounded<T>(d_target);
+    if (mine && !none) dx[target] = rounded<T>(d_target);
 }
 
 template <typename K, typename... A>
