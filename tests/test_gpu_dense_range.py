@@ -12,8 +12,8 @@ import pytest
 import quantized_expert_cache_gb300 as qec
 
 torch = pytest.importorskip("torch")
-from test_gpu_dense import (BF16, F16, F32, U, backward, check_backward, close, close_norm, forward,  # noqa: E402
-                            gen, layer, rand, slope_ref)
+from test_gpu_dense import (ACTS, BF16, F16, F32, U, backward, check_backward, close, close_norm,  # noqa: E402
+                            forward, gen, layer, rand, slope_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +160,53 @@ def test_16_bit_gradients_through_slopes_at_every_size(ctx, t, r, c, act, dtype)
     tol = torch.tensor(2 * (30 * U + (2.0 ** -22 if dtype == F16 else 2.0 ** -16) * 1.13) + 3 * U, device="cuda")
     for got, ref in ((dx, (dz[:, 0] - dz[:, 1])[:, None].expand(t, c)), (dw, (dz[0] - dz[1])[:, None].expand(r, c))):
         close(got, ref, tol.double(), dtype)
+
+
+# ------------------------------------------------------------- digits of fp32 gradients
+@pytest.mark.parametrize("t,r,c", [(5, 8, 64), (64, 130, 264), (1030, 129, 640), (4096, 512, 2048)])
+def test_fp32_gradients_keep_their_digits(ctx, t, r, c):
+    # one weight: the rows' gradient is dy, all 24 bits of it; one row: the weights' is x times a
+    # power of two, or dy times one
+    types = (F32, BF16, F32)
+    s = layer(t, r, c, types, 70)
+    dy, x = s["dy"].clone(), s["x"].clone()
+    s["w"][:] = 0
+    s["w"][3, 11] = 1
+    s["x"][:] = 0
+    s["x"][4, 9] = 0.5
+    dx, dw, _ = backward(ctx, s, types, qec.ACT_NONE, F32)
+    assert torch.equal(dx[:, 11], dy[:, 3]) and not dx[:, :11].any() and not dx[:, 12:].any()
+    assert torch.equal(dw[:, 9], dy[4] / 2) and not dw[:, :9].any() and not dw[:, 10:].any()
+    s["x"], s["dy"] = x, torch.zeros_like(dy)
+    s["dy"][4, 2] = -2
+    _, dw, db = backward(ctx, s, types, qec.ACT_NONE, F32)
+    assert torch.equal(dw[2], -2 * x[4]) and not dw[:2].any() and not dw[3:].any()
+    assert float(db[2]) == -2 and not db[:2].any() and not db[3:].any()
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("t,r,c", [(40, 130, 264), (64, 512, 2048), (1030, 300, 640), (4096, 512, 2048)])
+def test_fp32_gradients_of_rows_by_norms(ctx, t, r, c, act):
+    # 42 u of the sums, at most 4 u of the additions between (r / 512 of half a step each); the
+    # lower parts' sums are 2^-8 of the whole's and take 171 u / 2^8 twice; no pair is left out (a
+    # weight is one part); slopes 12 u (1 + |z|), |z| of 1.5 in the mean
+    types = (F32, BF16, F32)
+    s = layer(t, r, c, types, 71)
+    dx, _, _ = backward(ctx, s, types, act, F32, "x")
+    dz = s["dy"].double() * (slope_ref(s["pre"], act) if act else 1.0)
+    close_norm(dx, dz @ s["w"].double(), F32, "dx", 4 + 2 + (30 if act else 0))
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (F32, BF16, F32), (F16, F16, F16)])
+@pytest.mark.parametrize("act", [qec.ACT_NONE, qec.ACT_GELU])
+@pytest.mark.parametrize("t,r", [(1, 33), (200, 136), (2049, 40), (4100, 129), (20000, 64)])
+def test_bias_gradients(ctx, t, r, act, types):
+    # a warp's chain over every eighth token of a block, eight warps, the blocks in four chains and
+    # two joins: additions on the longest way
+    s = layer(t, r, 8, types, 72)
+    _, _, db = backward(ctx, s, types, act, F32, "b")
+    block = 16 if t <= 2048 else ((t + 127) // 128 + 7) // 8 * 8
+    chain = block // 8 + 8 + ((t + block - 1) // block + 3) // 4 + 2
+    dz = s["dy"].double() * (slope_ref(s["pre"], act) if act else 1.0)
+    edz = 12 * U * (1 + s["pre"].double().abs()) * s["dy"].double().abs() if act else torch.zeros_like(dz)
+    close(db, dz.sum(0), (chain + (1 if act else 0)) * U * dz.abs().sum(0) + edz.sum(0), F32)
