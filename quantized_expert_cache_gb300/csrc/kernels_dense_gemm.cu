@@ -29,14 +29,19 @@
 // of CTAs and their sums joined through distributed shared memory, in order; or, in a
 // weights' gradient, over tiles of their own whose sums are joined in the workspace.
 //
-// Bound.  8192^3 bf16 605 us, 4096^3 99, 4096 x 8192 x 2048 87 (the library's product 545,
-// 80 and 74; all with a cold cache); both gradients of 4096^3 168 (1630 TFLOP/s, 0.85 of
-// the measured rate; tensor pipe active 76% of the time).  What a step takes in: by
-// count 64 KB for 1024 clocks of products, near what an SM draws from L2 (without
-// loads 8192^3 took 507 us, without products 564).  Activations and a second output add
-// their epilogue: 98 us with silu and pre-activations.  8 tokens on 65536 x 2048: HBM,
-// 45 us = 0.88 of a copy.  33 on 2887 x 2880 8.3 us: latency of the launch, one
-// round of steps and the join.
+// Bound.  8192^3 bf16 607 us, 4096^3 99, 4096 x 8192 x 2048 87, 4096 x 32000 x 2048 298 (the
+// library's product 550, 79, 72 and 282; all with a cold cache); both gradients of 4096^3
+// 171 (1610 TFLOP/s, 0.84 of the measured rate; tensor pipe active 77% of the time).
+// Neither the loads nor the products alone: without loads 8192^3 took 507 us, without
+// products 564 (64 KB a step for 1024 clocks of products); what is missing to the library,
+// which reads the same operands, is their overlap.  The tile of 256 columns spills 60 bytes
+// a thread (96 registers for 18 warps).  Activations and a second output add their
+// epilogue: 98 us with silu and pre-activations for 84, in a graph.  Rows that are no
+// multiple of 4 are stored one element a lane: 4096 x 32003 x 2048 486 us, 32000 298.
+// 8 tokens on 65536 x 2048: HBM, 45 us = 0.88 of a copy.  33 on 2887 x 2880 8.4 us: latency
+// of the launch, one round of steps and the join.  fp32 rows: 4096 x 2048 x 2048 87 us for an
+// fp32 result (54 for its three products of parts at the measured rate, the split before
+// them 16), 62 for a 16-bit one (two products, 36).
 #include <cuda.h>
 #include <cooperative_groups.h>
 
@@ -604,7 +609,10 @@ int clusters_at_once(int ctas, int device, int n_sm) {
 
 }  // namespace
 
-// The cheapest of the tiles and K splits, by the clocks of the longest CTA.
+// The cheapest of the tiles and K splits, by the clocks of the longest CTA.  (A model, right
+// where tiles fill the SMs and to 7% for few tokens; for split pairs it counts the join too
+// low: 512 tokens on 4096 x 4096 22.4 us with the 256p/2 it takes, 19.2 with 128p/1; 2048 on
+// 512 x 2048 12.5 with 128p/2, 10.3 with 64/1.)
 DensePlan dense_plan(const DenseProduct *p, int n_products, int device, int n_sm) {
     DensePlan best{};
     for (const Shape &f : kShapes) {

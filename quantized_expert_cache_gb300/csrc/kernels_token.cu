@@ -17,20 +17,25 @@
 // element, and units below it hold none of the n; the others, little more than n of
 // them, are read again (from L2).  What reaches the bound there, seldom more than a few
 // dozen elements, is put in order by counting what comes before each; where it is more
-// than kCand (ties, masked rows), lists of 32 sorted over a warp's lanes take it in and
-// are merged pairwise.  Keys hold the value over the inverted index, so order and ties
-// (the lowest index) are one comparison of whole numbers, whatever the order of work.
+// than kCand, lists of 32 sorted over a warp's lanes take it in and are merged pairwise.
+// That is so for ties and masked rows, and for rows of no more units than alternatives,
+// which leave no bound: with 32 of them fp32 rows up to 4096 logits and of 8200 to 16384
+// (their tiles are four times as large), 16-bit ones up to 8192.  Keys hold the value over
+// the inverted index, so order and ties (the lowest index) are one comparison of whole
+// numbers, whatever the order of work.
 //
 // A row takes a cluster of 1 to 8 CTAs.  They write their units' maxima into each other's
 // shared memory, their sums and candidates into the first one's: no workspace, any
 // stream, one launch.
 //
 // Bound.  Many rows: HBM; 4096 x 65536 fp32 with 5 alternatives 176 us = 0.90 of a copy
-// (173 without: a row's second part, some 4 us long, behind other rows' reads), bf16
-// 148 = 0.53 (19 instructions an element), its gradient 163 = 0.97, fp32 308 = 1.02.  Few
-// rows: latency; 1 x 65536 with 8 alternatives 5.6 us (3.8 without), 32 x 100003 bf16
-// with 20 9.6 (6.3), gradient of 33 x 32003 2.4.  A masked row with fewer tokens left
-// than alternatives wanted orders its many equal elements by lists: 31 us for 65536.
+// (158 without: a row's second part stands behind other rows' reads).  bf16 167 = 0.47
+// (147 without): issue, 19 instructions an element, which this form takes and the data do
+// not ask for.  Gradients: bf16 163 = 0.97, fp32 308 = 1.02.  Few rows: latency; 1 x 65536
+// with 8 alternatives 5.6 us (3.8 without), 32 x 100003 bf16 with 20 9.6 (6.3), gradient of
+// 33 x 32003 2.4.  Rows that go to the lists: 64 x 2000 fp32 with 20 alternatives 16.7 us
+// (6.1 with 8), 32 x 12000 with 32 34; a masked row of 65536 with fewer tokens left than
+// alternatives wanted 31.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -617,7 +622,7 @@ int launch_rows(const TokenParams &p, int n_sm, cudaStream_t st) {
 
 template <typename T>
 int launch_grad(const TokenGradParams &p, cudaStream_t st) {
-    // (64 bytes a thread: 4096 x 65536 bf16 166 us; 32 bytes 269, 128 173)
+    // (64 bytes a thread: 4096 x 65536 bf16 166 us with a cold cache; 32 bytes 269, 128 173)
     constexpr int N = 16 / (int)sizeof(T), PACKS = kTokenGradPacks;
     const int packs = (p.vocab + N - 1) / N + 1, chunks = (packs + kThreads * PACKS - 1) / (kThreads * PACKS);
     return launch(token_grad_kernel<T>, (size_t)p.n_tokens * chunks, 1, st, p, chunks,
